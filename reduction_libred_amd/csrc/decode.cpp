@@ -1,0 +1,275 @@
+// decode.cpp -- the C entry points of libred_decode.h: argument checks,
+// launch shapes, and the calls into the kernels.
+#include "decode.hpp"
+
+#include <initializer_list>
+
+#include "host.hpp"
+
+using libred::Heads;
+using libred::host_compute_units;
+using libred::host_fail;
+using libred::host_scratch;
+using libred::is_aligned;
+
+namespace {
+
+size_t type_bytes(int type) { return type == RED_F32 ? 4 : type == RED_F16 || type == RED_BF16 ? 2 : 1; }
+
+// Largest element offset a strided tensor may reach (the byte offset of an
+// 8-byte element still fits 63 bits).
+constexpr int64_t kMaxSpan = (int64_t)1 << 59;
+
+// Elements spanned by tokens x heads x dim at these strides; -1 if a stride
+// is negative or the span is out of range.
+int64_t span_of(const red_heads& h, size_t tokens, size_t dim) {
+    if (h.heads < 0 || h.token_stride < 0 || h.head_stride < 0) return -1;
+    if (h.heads == 0 || tokens == 0) return 0;
+    int64_t a, b, s;
+    if (__builtin_mul_overflow((int64_t)(tokens - 1), h.token_stride, &a) ||
+        __builtin_mul_overflow(h.heads - 1, h.head_stride, &b) || __builtin_add_overflow(a, b, &s) ||
+        __builtin_add_overflow(s, (int64_t)dim, &s) || s > kMaxSpan)
+        return -1;
+    return s;
+}
+
+// Rows of an output must lie apart from each other.
+bool rows_apart(const red_heads& h, size_t tokens, size_t dim) {
+    const int64_t d = (int64_t)dim, t = (int64_t)tokens;
+    if (h.heads == 0 || t == 0) return true;
+    if (h.heads > 1 && h.head_stride < d) return false;
+    if (t > 1 && h.token_stride < d) return false;
+    if (h.heads == 1 || t == 1) return true;
+    return h.token_stride >= (h.heads - 1) * h.head_stride + d || h.head_stride >= (t - 1) * h.token_stride + d;
+}
+
+bool heads_valid(const red_heads& h, size_t tokens, size_t dim, size_t esize) {
+    const int64_t s = span_of(h, tokens, dim);
+    if (s < 0) return false;
+    return s == 0 || (h.data != nullptr && is_aligned(h.data, esize));
+}
+
+bool spans_meet(const red_heads& a, const red_heads& b, size_t tokens, size_t dim, size_t esize) {
+    const uintptr_t as = (uintptr_t)span_of(a, tokens, dim) * esize, bs = (uintptr_t)span_of(b, tokens, dim) * esize;
+    const uintptr_t a0 = (uintptr_t)a.data, b0 = (uintptr_t)b.data;
+    return as && bs && a0 < b0 + bs && b0 < a0 + as;
+}
+
+bool same_place(const red_heads& a, const red_heads& b) {
+    return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride;
+}
+
+// An output over its own input: the same rows, or none of them.
+bool output_valid(const red_heads& out, const red_heads& in, size_t tokens, size_t dim, size_t esize) {
+    if (out.heads != in.heads || !heads_valid(out, tokens, dim, esize) || !rows_apart(out, tokens, dim)) return false;
+    return same_place(out, in) || !spans_meet(out, in, tokens, dim, esize);
+}
+
+Heads to_heads(const red_heads& h) { return Heads{h.data, h.token_stride, h.head_stride}; }
+
+// Whether rows can be read `bytes` at a time: rows start on such a boundary.
+bool rows_on(const red_heads& h, size_t tokens, size_t esize, size_t bytes) {
+    if (h.heads == 0) return true;
+    return is_aligned(h.data, bytes) && (tokens <= 1 || h.token_stride * (int64_t)esize % (int64_t)bytes == 0) &&
+           (h.heads == 1 || h.head_stride * (int64_t)esize % (int64_t)bytes == 0);
+}
+
+using QkNormLaunch = hipError_t (*)(int, int, const libred::QkNorm&, bool, int, hipStream_t);
+
+red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, const red_heads* dk, float* dqw,
+                        float* dkw, bool back, hipStream_t stream) {
+    if (a == nullptr || (back && (dq == nullptr || dk == nullptr))) return RED_ERR_INVALID_ARG;
+    if (a->type != RED_F32 && a->type != RED_F16 && a->type != RED_BF16) return RED_ERR_INVALID_ARG;
+    const size_t es = type_bytes(a->type), T = a->tokens, D = a->dim;
+    if (D < 1 || D > RED_HEAD_MAX_DIM || a->rot > D || a->rot % 2 != 0 || T > RED_MAX_N) return RED_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.f)) return RED_ERR_INVALID_ARG;
+    if (a->q.heads > 1 << 20 || a->k.heads > 1 << 20) return RED_ERR_INVALID_ARG;
+    if (!heads_valid(a->q, T, D, es) || !heads_valid(a->k, T, D, es)) return RED_ERR_INVALID_ARG;
+    if (!output_valid(a->q_out, a->q, T, D, es) || !output_valid(a->k_out, a->k, T, D, es)) return RED_ERR_INVALID_ARG;
+    if (!is_aligned(a->q_weight, es) || !is_aligned(a->k_weight, es)) return RED_ERR_INVALID_ARG;
+    if (!is_aligned(a->pos, 8) || !is_aligned(a->freq, 4)) return RED_ERR_INVALID_ARG;
+    if (back) {
+        if (dq->heads != a->q.heads || dk->heads != a->k.heads) return RED_ERR_INVALID_ARG;
+        if (!heads_valid(*dq, T, D, es) || !heads_valid(*dk, T, D, es)) return RED_ERR_INVALID_ARG;
+        if (!output_valid(a->q_out, *dq, T, D, es) || !output_valid(a->k_out, *dk, T, D, es)) return RED_ERR_INVALID_ARG;
+        if (!is_aligned(dqw, 4) || !is_aligned(dkw, 4)) return RED_ERR_INVALID_ARG;
+    }
+    const int rows = (int)(a->q.heads + a->k.heads);
+    const bool empty = T == 0 || rows == 0;
+    if (!empty && a->rot > 0 && (a->pos == nullptr || a->freq == nullptr)) return RED_ERR_INVALID_ARG;
+    const bool sums = back && (dqw != nullptr || dkw != nullptr);
+    if (empty && !sums) return RED_OK;
+
+    // Elements a lane holds: those of a 16-byte load where every row allows
+    // it, 4 elements where 8 bytes (16-bit types) do, else 1.
+    auto fits = [&](size_t v) {
+        const size_t b = v * es;
+        if (D % v != 0 || !rows_on(a->q, T, es, b) || !rows_on(a->k, T, es, b) || !rows_on(a->q_out, T, es, b) ||
+            !rows_on(a->k_out, T, es, b) || !is_aligned(a->q_weight, b) || !is_aligned(a->k_weight, b))
+            return false;
+        return !back || (rows_on(*dq, T, es, b) && rows_on(*dk, T, es, b));
+    };
+    int vec = (int)(16 / es);
+    if (!fits((size_t)vec)) vec = fits(4) ? 4 : 1;
+    int lanes = 4;
+    while (lanes < 64 && (size_t)(lanes * vec) < D) lanes *= 2;
+    if (vec == 1) lanes = 64;
+
+    int dev, cus;
+    red_status st = host_compute_units(&dev, &cus);
+    if (st != RED_OK) return st;
+    libred::QkNorm k = {};
+    k.q = to_heads(a->q), k.k = to_heads(a->k), k.q_out = to_heads(a->q_out), k.k_out = to_heads(a->k_out);
+    if (back) k.dq = to_heads(*dq), k.dk = to_heads(*dk);
+    k.q_weight = a->q_weight, k.k_weight = a->k_weight;
+    k.pos = a->pos, k.freq = a->freq;
+    k.tokens = (int64_t)T;
+    k.q_heads = (int)a->q.heads, k.k_heads = (int)a->k.heads, k.dim = (int)D;
+    k.rot = (int)a->rot, k.interleaved = a->interleaved != 0, k.eps = a->eps;
+    // Waves: a token's heads are shared by several where there are few tokens,
+    // until there are 16 waves a compute unit or a wave has one pass left.
+    const int passes = rows == 0 ? 1 : (rows + 64 / lanes - 1) / (64 / lanes);
+    const size_t want = (size_t)cus * 16;
+    size_t parts = T >= want || T == 0 ? 1 : (want + T - 1) / T;
+    if (parts > (size_t)passes) parts = passes;
+    k.parts = (int)parts;
+    const size_t items = T * parts;
+    size_t blocks = (items + libred::kQkNormWaves - 1) / libred::kQkNormWaves;
+    if (blocks == 0) blocks = 1;
+    const QkNormLaunch launch = a->type == RED_F32   ? libred::launch_qk_norm_f32
+                                : a->type == RED_F16 ? libred::launch_qk_norm_f16
+                                                     : libred::launch_qk_norm_bf16;
+    if (!back) {
+        if (blocks > 0x7fffffff) return RED_ERR_INVALID_ARG;
+        const hipError_t e = launch(vec, lanes, k, false, (int)blocks, stream);
+        return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+    }
+    const size_t cap = (size_t)cus * 4;
+    if (blocks > cap) blocks = cap;
+    void* partials = nullptr;
+    st = host_scratch(dev, stream, blocks * 2 * D * sizeof(float), &partials);
+    if (st != RED_OK) return st;
+    k.partials = static_cast<float*>(partials);
+    hipError_t e = launch(vec, lanes, k, true, (int)blocks, stream);
+    if (e == hipSuccess && sums) e = libred::launch_qk_norm_weights(k.partials, (int)blocks, (int)D, dqw, dkw, stream);
+    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+}
+
+// Elements (or scales) spanned by a paged tensor of these strides, -1 if
+// negative or out of range.
+int64_t paged_span(const red_paged_cache& c, int64_t page, int64_t head, int64_t place, size_t dim) {
+    if (page < 0 || head < 0 || place < 0) return -1;
+    int64_t a, b, d, s;
+    if (__builtin_mul_overflow((int64_t)c.pages - 1, page, &a) || __builtin_mul_overflow((int64_t)c.heads - 1, head, &b) ||
+        __builtin_mul_overflow((int64_t)c.places - 1, place, &d) || __builtin_add_overflow(a, b, &s) ||
+        __builtin_add_overflow(s, d, &s) || __builtin_add_overflow(s, (int64_t)dim, &s) || s > kMaxSpan)
+        return -1;
+    return s;
+}
+
+// A cache with at least one page, or one that holds nothing (pages 0).
+bool cache_valid(const red_paged_cache* c) {
+    if (c == nullptr) return false;
+    if (c->type != RED_F16 && c->type != RED_BF16 && c->type != RED_I8 && c->type != RED_E4M3) return false;
+    if (c->heads < 1 || c->heads > 1 << 20 || c->places < 1 || c->places > 1 << 20 || c->dim < 1 ||
+        c->dim > RED_HEAD_MAX_DIM || c->pages > (size_t)1 << 40)
+        return false;
+    if (c->pages == 0) return true;
+    const bool scaled = c->type == RED_I8 || c->type == RED_E4M3;
+    const size_t es = type_bytes(c->type);
+    if (c->k == nullptr || c->v == nullptr || !is_aligned(c->k, es) || !is_aligned(c->v, es)) return false;
+    if (paged_span(*c, c->page_stride, c->head_stride, c->place_stride, c->dim) < 0) return false;
+    if (!scaled) return c->k_scales == nullptr && c->v_scales == nullptr;
+    if (c->k_scales == nullptr || c->v_scales == nullptr || !is_aligned(c->k_scales, 4) || !is_aligned(c->v_scales, 4))
+        return false;
+    return paged_span(*c, c->scale_page_stride, c->scale_head_stride, c->scale_place_stride, 1) >= 0;
+}
+
+libred::PagedCache to_cache(const red_paged_cache& c) {
+    return libred::PagedCache{c.k,
+                              c.v,
+                              c.k_scales,
+                              c.v_scales,
+                              c.page_stride,
+                              c.head_stride,
+                              c.place_stride,
+                              c.scale_page_stride,
+                              c.scale_head_stride,
+                              c.scale_place_stride,
+                              (int64_t)c.pages,
+                              (int)c.heads,
+                              (int)c.places,
+                              (int)c.dim};
+}
+
+// Whether the cache's rows start on `bytes` boundaries.
+bool cache_rows_on(const red_paged_cache& c, size_t bytes) {
+    const int64_t es = (int64_t)type_bytes(c.type), b = (int64_t)bytes;
+    return is_aligned(c.k, bytes) && is_aligned(c.v, bytes) && (c.pages <= 1 || c.page_stride * es % b == 0) &&
+           (c.heads == 1 || c.head_stride * es % b == 0) && (c.places == 1 || c.place_stride * es % b == 0);
+}
+
+red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, const red_heads* v, const int64_t* slots,
+                      size_t tokens, bool write, hipStream_t stream) {
+    if (!cache_valid(c) || k == nullptr || v == nullptr) return RED_ERR_INVALID_ARG;
+    if (type != RED_F16 && type != RED_BF16) return RED_ERR_INVALID_ARG;
+    if ((c->type == RED_F16 || c->type == RED_BF16) && c->type != type) return RED_ERR_INVALID_ARG;
+    if (tokens > RED_MAX_N) return RED_ERR_INVALID_ARG;
+    const size_t D = c->dim;
+    for (const red_heads* h : {k, v}) {
+        if (h->heads != (int64_t)c->heads || !heads_valid(*h, tokens, D, 2)) return RED_ERR_INVALID_ARG;
+        if (!write && !rows_apart(*h, tokens, D)) return RED_ERR_INVALID_ARG;
+    }
+    if (tokens > 0 && (slots == nullptr || !is_aligned(slots, 8))) return RED_ERR_INVALID_ARG;
+    if (tokens == 0 || (write && c->pages == 0)) return RED_OK;
+    const size_t cb = type_bytes(c->type);
+    const int vec = D % 8 == 0 && rows_on(*k, tokens, 2, 16) && rows_on(*v, tokens, 2, 16) && cache_rows_on(*c, 8 * cb) ? 8 : 1;
+    int lanes = 8;
+    while ((size_t)(lanes * vec) < D) lanes *= 2;
+    if (vec == 1) lanes = 64;
+    int dev, cus;
+    const red_status st = host_compute_units(&dev, &cus);
+    if (st != RED_OK) return st;
+    libred::CacheRows a = {};
+    a.cache = to_cache(*c);
+    a.k = to_heads(*k), a.v = to_heads(*v);
+    a.slots = slots, a.tokens = (int64_t)tokens;
+    const size_t block_tokens = (size_t)(libred::kCacheWaves * 64 / lanes);
+    const size_t groups = (tokens + block_tokens - 1) / block_tokens;
+    if (groups > 0x7fffffff) return RED_ERR_INVALID_ARG;
+    // A block takes all heads of its tokens; where that makes too few blocks
+    // for 4 a compute unit the heads are shared, down to one row a group.
+    const size_t want = (size_t)cus * 4, pairs = 2 * c->heads;
+    size_t parts = groups >= want ? 1 : (want + groups - 1) / groups;
+    if (parts > pairs) parts = pairs;
+    if (parts > 65535) parts = 65535;
+    a.parts = (int)parts;
+    const hipError_t e = write ? libred::launch_cache_write(type, c->type, vec, lanes, a, (unsigned int)groups, stream)
+                               : libred::launch_cache_read(type, c->type, vec, lanes, a, (unsigned int)groups, stream);
+    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+}
+
+}  // namespace
+
+extern "C" {
+
+red_status red_qk_norm_rope(const red_qk_norm_rope_args* a, hipStream_t stream) {
+    return qk_norm_call(a, nullptr, nullptr, nullptr, nullptr, false, stream);
+}
+
+red_status red_qk_norm_rope_backward(const red_qk_norm_rope_args* a, const red_heads* dq, const red_heads* dk,
+                                     float* dq_weight, float* dk_weight, hipStream_t stream) {
+    return qk_norm_call(a, dq, dk, dq_weight, dk_weight, true, stream);
+}
+
+red_status red_cache_write(const red_paged_cache* cache, int type, const red_heads* k, const red_heads* v,
+                           const int64_t* slots, size_t tokens, hipStream_t stream) {
+    return cache_call(cache, type, k, v, slots, tokens, true, stream);
+}
+
+red_status red_cache_read(const red_paged_cache* cache, int type, const red_heads* k, const red_heads* v,
+                          const int64_t* slots, size_t tokens, hipStream_t stream) {
+    return cache_call(cache, type, k, v, slots, tokens, false, stream);
+}
+
+}  // extern "C"

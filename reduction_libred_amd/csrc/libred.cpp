@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "dispatch_table.hpp"
+#include "host.hpp"
 #include "launch.hpp"
 #include "libred.h"
 #include "libred_ablate.h"
@@ -1041,6 +1042,23 @@ red_status cols_call(const float* x, size_t rows, size_t cols, size_t ld, float*
 }
 
 }  // namespace
+
+namespace libred {
+
+red_status host_fail(hipError_t e, red_status code) { return fail(e, code); }
+
+red_status host_compute_units(int* dev, int* cu_count) {
+    DeviceInfo info;
+    const red_status st = current_device(dev, &info);
+    if (st == RED_OK) *cu_count = info.cu_count;
+    return st;
+}
+
+red_status host_scratch(int dev, hipStream_t stream, size_t bytes, void** out) {
+    return get_scratch(dev, stream, bytes, out);
+}
+
+}  // namespace libred
 
 extern "C" {
 

@@ -1,0 +1,10 @@
+// Norms of heads with the rotation: IEEE half.
+#include "qk_norm.hpp"
+
+namespace libred {
+
+hipError_t launch_qk_norm_f16(int vec, int lanes, const QkNorm& a, bool back, int blocks, hipStream_t stream) {
+    return launch_qk_norm_type<F16>(vec, lanes, a, back, blocks, stream);
+}
+
+}  // namespace libred
