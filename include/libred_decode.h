@@ -130,6 +130,93 @@ red_status red_cache_write(const red_paged_cache *cache, int type, const red_hea
 red_status red_cache_read(const red_paged_cache *cache, int type, const red_heads *k, const red_heads *v,
                           const int64_t *slots, size_t tokens, hipStream_t stream);
 
+#define RED_TREE_MAX_NODES 64
+
+/*
+ * Attention of drafted tokens over a paged cache. Sequence b holds lens[b]
+ * tokens and then the `nodes` drafted ones, whose keys and values are in the
+ * cache too: token t lies at place t % places of page table[b * table_stride
+ * + t / places]. Node i sees every token below lens[b], and of the nodes
+ * those whose bit is set in tree_mask[b * nodes + i] (bit j: node j; itself
+ * among them where it is to be seen), or, where tree_mask is NULL, nodes 0 ..
+ * i. Only the first node_count[b] nodes exist (NULL: all).
+ *
+ *   s = scale * q . k,  out = softmax(s) v,  lse = log sum exp(s)
+ *
+ * Query head h reads kv head h / (q_heads / cache heads). A row that sees
+ * nothing, and every row of a node that does not exist, gets out = 0 and
+ * lse = -inf; what lies in the cache behind a mask, infinities and NaN
+ * included, does not reach a result.
+ *
+ * type: RED_F16 or RED_BF16 of q and out, and of a 16-bit cache. q and out:
+ * (batch, nodes, q_heads, dim) with strides of their own, rows on 16-byte
+ * boundaries, the rows of out in that order; lse: batch * nodes * q_heads
+ * floats. The cache's dim is a multiple of 16 up to 256, its rows start on
+ * 16-byte boundaries. nodes <= 64, batch and q_heads <= 65535. max_len is the
+ * largest number of tokens, nodes included, that a sequence may have: it
+ * shapes the launch, and tokens from it on (or beyond table_cols pages) are
+ * not looked at. A page number outside the cache is not followed: its tokens
+ * read as zeros. Scales of an 8-bit cache are not negative; a scale below
+ * 2^-100 counts as that for values. Scores and sums are held in float32; in
+ * the product with V their exponentials are rounded to `type` (to float16
+ * with an 8-bit cache).
+ */
+typedef struct red_tree_attention_args {
+    int type;
+    float scale;
+    size_t batch, nodes, q_heads;
+    size_t max_len;
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_batch_stride, q_node_stride, q_head_stride;
+    int64_t out_batch_stride, out_node_stride, out_head_stride;
+    red_paged_cache cache;
+    const int32_t *table;
+    size_t table_cols;
+    int64_t table_stride;
+    const int32_t *lens;
+    const int64_t *tree_mask;
+    const int32_t *node_count;
+} red_tree_attention_args;
+
+red_status red_tree_attention(const red_tree_attention_args *a, hipStream_t stream);
+
+/*
+ * Verification of drafted tokens by given random numbers. p: (batch, drafts +
+ * 1, vocab), the target's probabilities after each prefix; q: (batch, drafts,
+ * vocab), the draft's, or NULL where its tokens were certain (q = 1 for the
+ * drafted token). Draft i of draft_count[b] (NULL: all) is accepted while
+ *
+ *   u[b][i] * q[b][i][d_i] < p[b][i][d_i],  d_i = drafted[b][i]
+ *
+ * (in float64; a token outside the vocabulary is refused), and accepted[b] = n
+ * counts those before the first refusal. tokens[b] (drafts + 1 of them) holds
+ * the n accepted tokens, then one drawn from the weights w by r[b] (0 <= r <
+ * 1), then -1. w = max(p[b][n] - q[b][n], 0) after a refusal, or p[b][n] where
+ * that is 0 everywhere or nothing was refused; the token is the first whose
+ * running sum of w (float64) exceeds r times the sum. -1 stands for it where
+ * w has no positive element or the sum is NaN; with r of 1 or more it is the
+ * last of positive weight. type: RED_F32, RED_F16 or RED_BF16 of p and q.
+ * drafted, u and tokens are contiguous. drafts may be 0.
+ */
+typedef struct red_verify_drafts_args {
+    int type;
+    size_t batch, drafts, vocab;
+    const void *p;
+    int64_t p_batch_stride, p_step_stride;
+    const void *q;
+    int64_t q_batch_stride, q_step_stride;
+    const int64_t *drafted;
+    const float *u;
+    const float *r;
+    const int32_t *draft_count;
+    int32_t *accepted;
+    int64_t *tokens;
+} red_verify_drafts_args;
+
+red_status red_verify_drafts(const red_verify_drafts_args *a, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -579,6 +579,7 @@ def red_version():
 
 from . import decode  # noqa: E402
 from .decode import (  # noqa: E402,F401
-    red_cache_read, red_cache_write, red_qk_norm_rope, red_qk_norm_rope_backward)
+    red_cache_read, red_cache_write, red_qk_norm_rope, red_qk_norm_rope_backward, red_tree_attention,
+    red_verify_drafts)
 
 SIGNATURES.update(decode.SIGNATURES)

@@ -31,7 +31,9 @@ MANIFEST = os.path.join(HERE, "libred_objects.json")
 
 SOURCES = ["libred.cpp", "flat_sum_f32.hip", "flat_ops.hip", "flat_fused.hip", "flat_argmax.hip", "flat_argmin.hip",
            "flat_wide.hip", "rows_sum.hip", "rows_max.hip", "cols_reduce.hip", "ablate.hip", "probe.hip", "read_probe.hip", "rows_narrow.hip",
-           "decode.cpp", "qk_norm_f32.hip", "qk_norm_f16.hip", "qk_norm_bf16.hip", "paged_cache.hip"]
+           "decode.cpp", "qk_norm_f32.hip", "qk_norm_f16.hip", "qk_norm_bf16.hip", "paged_cache.hip",
+           "attention_f16_16.hip", "attention_f16_i8.hip", "attention_f16_e4m3.hip", "attention_bf16_16.hip",
+           "attention_bf16_i8.hip", "attention_bf16_e4m3.hip", "attention_combine.hip", "verify_drafts.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,10 @@
+// Attention of drafted tokens: bf16 queries over a cache of the same type.
+#include "tree_attention.hpp"
+
+namespace libred {
+
+hipError_t launch_attention_bf16_16(const TreeAttention& a, hipStream_t stream) {
+    return launch_attention<BF16, Cached16>(a, stream);
+}
+
+}  // namespace libred

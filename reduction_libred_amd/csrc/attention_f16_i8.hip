@@ -1,0 +1,10 @@
+// Attention of drafted tokens: f16 queries over a cache of i8.
+#include "tree_attention.hpp"
+
+namespace libred {
+
+hipError_t launch_attention_f16_i8(const TreeAttention& a, hipStream_t stream) {
+    return launch_attention<F16, CachedI8>(a, stream);
+}
+
+}  // namespace libred

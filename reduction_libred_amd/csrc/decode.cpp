@@ -249,6 +249,123 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
 }
 
+red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) {
+    if (a == nullptr || !cache_valid(&a->cache)) return RED_ERR_INVALID_ARG;
+    const red_paged_cache& c = a->cache;
+    const int type = a->type;
+    if (type != RED_F16 && type != RED_BF16) return RED_ERR_INVALID_ARG;
+    if ((c.type == RED_F16 || c.type == RED_BF16) && c.type != type) return RED_ERR_INVALID_ARG;
+    const size_t D = c.dim, B = a->batch, N = a->nodes, H = a->q_heads, G = H / c.heads;
+    if (D % 16 != 0 || !cache_rows_on(c, 16)) return RED_ERR_INVALID_ARG;
+    if (N > RED_TREE_MAX_NODES || H % c.heads != 0 || H > 65535 || B > 65535) return RED_ERR_INVALID_ARG;
+    if (a->max_len > (size_t)1 << 30 || a->table_cols > (size_t)1 << 30 || a->table_stride < 0) return RED_ERR_INVALID_ARG;
+    if (a->table_stride > (int64_t)1 << 40 || !(a->scale - a->scale == 0.f)) return RED_ERR_INVALID_ARG;
+    if (B == 0 || N == 0 || H == 0) return RED_OK;
+    if (a->q == nullptr || a->out == nullptr || a->lse == nullptr || a->lens == nullptr) return RED_ERR_INVALID_ARG;
+    if (!is_aligned(a->q, 16) || !is_aligned(a->out, 16) || !is_aligned(a->lse, 4) || !is_aligned(a->lens, 4) ||
+        !is_aligned(a->table, 4) || !is_aligned(a->tree_mask, 8) || !is_aligned(a->node_count, 4))
+        return RED_ERR_INVALID_ARG;
+    const size_t tokens = a->table_cols * c.places < a->max_len ? a->table_cols * c.places : a->max_len;
+    if (tokens > 0 && a->table == nullptr) return RED_ERR_INVALID_ARG;
+    // (batch, node) pairs and heads: rows of q on 16-byte boundaries, rows of
+    // out as well and apart from each other.
+    const int64_t lim = (int64_t)1 << 40, d = (int64_t)D;
+    const int64_t qb = B > 1 ? a->q_batch_stride : 0, qn = N > 1 ? a->q_node_stride : 0, qh = H > 1 ? a->q_head_stride : 0;
+    const int64_t bs = B > 1 ? a->out_batch_stride : 0, ns = N > 1 ? a->out_node_stride : 0, hs = H > 1 ? a->out_head_stride : 0;
+    for (const int64_t s : {qb, qn, qh, bs, ns, hs})
+        if (s < 0 || s > lim || s % 8 != 0) return RED_ERR_INVALID_ARG;
+    const int64_t head_span = ((int64_t)H - 1) * hs + d, node_span = ((int64_t)N - 1) * ns + head_span;
+    if ((H > 1 && hs < d) || (N > 1 && ns < head_span) || (B > 1 && bs < node_span)) return RED_ERR_INVALID_ARG;
+    const red_heads q = {const_cast<void*>(a->q), (int64_t)B, 0, qb};
+    const red_heads o = {a->out, (int64_t)B, 0, bs};
+    const int64_t q_span = ((int64_t)N - 1) * qn + ((int64_t)H - 1) * qh + d;
+    const uintptr_t q0 = (uintptr_t)q.data, qe = q0 + 2 * (uintptr_t)span_of(q, 1, (size_t)q_span);
+    const uintptr_t o0 = (uintptr_t)o.data, oe = o0 + 2 * (uintptr_t)span_of(o, 1, (size_t)node_span);
+    if (q0 < oe && o0 < qe) return RED_ERR_INVALID_ARG;
+
+    int dev, cus;
+    red_status st = host_compute_units(&dev, &cus);
+    if (st != RED_OK) return st;
+    libred::TreeAttention k = {};
+    k.q = a->q, k.out = a->out, k.lse = a->lse;
+    k.q_batch = qb, k.q_node = qn, k.q_head = qh;
+    k.out_batch = bs, k.out_node = ns, k.out_head = hs;
+    k.cache = to_cache(c);
+    k.table = a->table, k.table_stride = a->table_stride;
+    k.lens = a->lens, k.mask = a->tree_mask, k.count = a->node_count;
+    k.batch = (int)B, k.nodes = (int)N, k.group = (int)G, k.max_tokens = c.pages == 0 ? 0 : (int)tokens;
+    k.scale = (a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
+    k.flip = a->scale < 0.f ? 0x80008000u : 0u;
+    const size_t M = N * G;
+    const libred::AttentionShape shape = libred::attention_shape((int)M);
+    k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());
+    if (c.heads * (size_t)k.row_blocks > 65535) return RED_ERR_INVALID_ARG;
+    // Chunks: enough blocks for the card, whole tiles each.
+    const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
+    const size_t base = B * c.heads * (size_t)k.row_blocks, want = (size_t)cus * 8;
+    size_t splits = (want + base - 1) / base;
+    if (splits > tiles) splits = tiles;
+    if (splits > (size_t)libred::kAttentionMaxSplits) splits = libred::kAttentionMaxSplits;
+    if (splits < 1) splits = 1;
+    const size_t per = tiles == 0 ? 1 : (tiles + splits - 1) / splits;
+    k.chunk = (int)(per * tile);
+    k.splits = tiles == 0 ? 1 : (int)((tiles + per - 1) / per);
+    if (k.splits > 1) {
+        const size_t rows = B * c.heads * (size_t)k.splits * M;
+        void* p = nullptr;
+        st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)), &p);
+        if (st != RED_OK) return st;
+        k.part_o = static_cast<float*>(p);
+        k.part_ml = reinterpret_cast<float2*>(k.part_o + rows * D);
+    }
+    hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
+    if (e == hipSuccess && k.splits > 1) e = libred::launch_attention_combine(type, k, stream);
+    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+}
+
+// Whether batch x steps rows of `vocab` elements at these strides stay in range.
+bool rows_in_range(int64_t batch_stride, int64_t step_stride, size_t batch, size_t steps, size_t vocab) {
+    const red_heads h = {nullptr, (int64_t)steps, batch_stride, step_stride};
+    return span_of(h, batch, vocab) >= 0;
+}
+
+red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
+    if (a == nullptr) return RED_ERR_INVALID_ARG;
+    if (a->type != RED_F32 && a->type != RED_F16 && a->type != RED_BF16) return RED_ERR_INVALID_ARG;
+    const size_t es = type_bytes(a->type), B = a->batch, K = a->drafts, V = a->vocab;
+    if (B > 65535 || K > 1 << 20 || V < 1 || V > (size_t)1 << 40) return RED_ERR_INVALID_ARG;
+    if (B == 0) return RED_OK;
+    if (a->p == nullptr || a->r == nullptr || a->accepted == nullptr || a->tokens == nullptr) return RED_ERR_INVALID_ARG;
+    if (K > 0 && (a->drafted == nullptr || a->u == nullptr)) return RED_ERR_INVALID_ARG;
+    if (!is_aligned(a->p, es) || !is_aligned(a->q, es) || !is_aligned(a->drafted, 8) || !is_aligned(a->u, 4) ||
+        !is_aligned(a->r, 4) || !is_aligned(a->draft_count, 4) || !is_aligned(a->accepted, 4) || !is_aligned(a->tokens, 8))
+        return RED_ERR_INVALID_ARG;
+    if (!rows_in_range(a->p_batch_stride, a->p_step_stride, B, K + 1, V)) return RED_ERR_INVALID_ARG;
+    if (a->q != nullptr && !rows_in_range(a->q_batch_stride, a->q_step_stride, B, K, V)) return RED_ERR_INVALID_ARG;
+    int dev, cus;
+    red_status st = host_compute_units(&dev, &cus);
+    if (st != RED_OK) return st;
+    libred::Verify k = {};
+    k.p = a->p, k.q = a->q;
+    k.p_batch = a->p_batch_stride, k.p_step = a->p_step_stride;
+    k.q_batch = a->q_batch_stride, k.q_step = a->q_step_stride;
+    k.drafted = a->drafted, k.u = a->u, k.r = a->r, k.count = a->draft_count;
+    k.accepted = a->accepted, k.tokens = a->tokens;
+    k.vocab = (int64_t)V, k.batch = (int)B, k.drafts = (int)K;
+    // Segments: 8 blocks a compute unit over the batch, of at least 1024 tokens.
+    size_t segs = ((size_t)cus * 8 + B - 1) / B;
+    if (segs > (V + 1023) / 1024) segs = (V + 1023) / 1024;
+    if (segs > (size_t)libred::kVerifyMaxSegs) segs = libred::kVerifyMaxSegs;
+    k.seg = (int64_t)((V + segs - 1) / segs);
+    k.segs = (int)((V + (size_t)k.seg - 1) / (size_t)k.seg);
+    void* sums = nullptr;
+    st = host_scratch(dev, stream, B * (size_t)k.segs * sizeof(double), &sums);
+    if (st != RED_OK) return st;
+    k.sums = static_cast<double*>(sums);
+    const hipError_t e = libred::launch_verify(a->type, k, stream);
+    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+}
+
 }  // namespace
 
 extern "C" {
@@ -271,5 +388,11 @@ red_status red_cache_read(const red_paged_cache* cache, int type, const red_head
                           const int64_t* slots, size_t tokens, hipStream_t stream) {
     return cache_call(cache, type, k, v, slots, tokens, false, stream);
 }
+
+red_status red_tree_attention(const red_tree_attention_args* a, hipStream_t stream) {
+    return attention_call(a, stream);
+}
+
+red_status red_verify_drafts(const red_verify_drafts_args* a, hipStream_t stream) { return verify_call(a, stream); }
 
 }  // extern "C"

@@ -68,4 +68,63 @@ hipError_t launch_cache_write(int type, int cache_type, int vec, int lanes, cons
 hipError_t launch_cache_read(int type, int cache_type, int vec, int lanes, const CacheRows& a, unsigned int groups,
                              hipStream_t stream);
 
+// Attention of drafted tokens. Rows of one kv head are numbered node * group +
+// query head of the group; a block takes `rows` of them (the shape's) and one
+// chunk of the cache's tokens.
+struct TreeAttention {
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_batch, q_node, q_head, out_batch, out_node, out_head;  // strides
+    PagedCache cache;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lens;
+    const int64_t* mask;   // null: a chain
+    const int32_t* count;  // null: all nodes
+    int batch, nodes, group, max_tokens, chunk, splits, row_blocks;
+    float scale;  // magnitude, times log2(e)
+    unsigned int flip;  // 0x80008000 where the scale is negative: the sign of q
+    float* part_o;   // per (batch, kv head, split, row): dim floats, and
+    float2* part_ml; // the running maximum and sum
+};
+
+// How waves share a block: `waves_m` groups of 32 * row_tiles rows times
+// `waves_t` parts of the tokens, `step` tokens a wave at a time.
+struct AttentionShape {
+    int row_tiles, waves_m, waves_t, step;
+    constexpr int rows() const { return 32 * row_tiles * waves_m; }
+    constexpr int tokens() const { return waves_t * step; }
+};
+constexpr AttentionShape kFewRows = {1, 1, 4, 32}, kManyRows = {1, 4, 1, 64};
+// The shape for `rows` rows of a kv head.
+constexpr AttentionShape attention_shape(int rows) { return rows <= 32 ? kFewRows : kManyRows; }
+constexpr int kAttentionMaxSplits = 256;
+// Joins the chunks of every row into the output.
+hipError_t launch_attention_combine(int type, const TreeAttention& a, hipStream_t stream);
+hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_f16_16(const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_f16_i8(const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_f16_e4m3(const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_bf16_16(const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_bf16_i8(const TreeAttention& a, hipStream_t stream);
+hipError_t launch_attention_bf16_e4m3(const TreeAttention& a, hipStream_t stream);
+
+// Verification of drafted tokens: a sequence's row is cut into `segs` segments
+// of `seg` tokens.
+struct Verify {
+    const void *p, *q;  // q null: the draft's tokens were certain
+    int64_t p_batch, p_step, q_batch, q_step;
+    const int64_t* drafted;
+    const float *u, *r;
+    const int32_t* count;
+    int32_t* accepted;
+    int64_t* tokens;
+    double* sums;  // batch * segs
+    int64_t vocab, seg;
+    int batch, drafts, segs;
+};
+constexpr int kVerifyMaxSegs = 256;
+hipError_t launch_verify(int type, const Verify& a, hipStream_t stream);
+
 }  // namespace libred

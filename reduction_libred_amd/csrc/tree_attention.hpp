@@ -1,0 +1,510 @@
+// tree_attention.hpp -- attention of drafted tokens over a paged cache.
+//
+// For row n (a node and a query head) over the tokens t it sees:
+//     s = scale q.k_t,  out = sum_t 2^(s' - M) v_t / sum_t 2^(s' - M),
+// s' = s log2(e), with the running maximum M and sum of an online softmax in
+// float32. All query heads of a kv head and all nodes are rows of one product,
+// so a tile of keys and values is read once for all of them.
+//
+// Products use the 32x32x16 matrix instruction, transposed: S^T = K Q^T puts
+// one row n in each lane column (lane % 32), 16 of 32 tokens in a lane and the
+// other 16 in lane ^ 32, so maxima and sums are lane-local but for one
+// exchange. The exponentials are then already the operand of O^T = V^T P^T: a
+// product does not mind the order of the tokens it sums over, so V^T is read
+// in the order that S^T left them in, with the transposing LDS load.
+//
+// A block walks its chunk of the tokens in tiles: while one tile is computed,
+// the next is on its way from memory into registers (rows looked up through
+// the page table a tile earlier), and is converted to 16 bits on its way into
+// the LDS, once for all waves. 8-bit elements stay whole: the scale of a key
+// multiplies its scores, and the scale of a value joins the exponent,
+//     w_t = 2^(s'_t + log2 c_t - M),  out = sum_t w_t code_t / sum_t w_t / c_t,
+// so that w stays in range whatever the scales are. P is rounded to the type
+// of V in the product (float16 for 8-bit caches, which hold those exactly):
+// relative 2^-11 or 2^-8 a term, the step of the output's own type.
+//
+// Long caches are split over blocks; their sums are joined by
+// combine_kernel in the order of the chunks.
+#pragma once
+
+#include "decode_common.hpp"
+
+namespace libred {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <class T>
+struct Mma;
+template <>
+struct Mma<F16> {
+    static __device__ __forceinline__ f32x16 dot(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+    }
+    static constexpr uint32_t kExponent = 0x7C00u;
+};
+template <>
+struct Mma<BF16> {
+    static __device__ __forceinline__ f32x16 dot(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+    }
+    static constexpr uint32_t kExponent = 0x7F80u;
+};
+
+// The elements of a cache: how many bytes, and 4 of them as 16-bit values.
+struct Cached16 {
+    static constexpr int kBytes = 2;
+};
+struct CachedI8 {
+    static constexpr int kBytes = 1;
+    template <class T>
+    static __device__ __forceinline__ u32x2 widen4(uint32_t w) {
+        if constexpr (std::is_same_v<T, F16>) {
+            // The biased byte as the low bits of 1024 + b, less 1152.
+            const uint32_t b = w ^ 0x80808080u;
+            const f16x2 c = {(_Float16)1152.f, (_Float16)1152.f};
+            return u32x2{__builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)) - c),
+                         __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)) - c)};
+        } else {
+            return u32x2{Mma<BF16>::pack((float)(int8_t)w, (float)(int8_t)(w >> 8)),
+                         Mma<BF16>::pack((float)(int8_t)(w >> 16), (float)(int8_t)(w >> 24))};
+        }
+    }
+};
+struct CachedE4M3 {
+    static constexpr int kBytes = 1;
+    template <class T>
+    static __device__ __forceinline__ u32x2 widen4(uint32_t w) {
+        if constexpr (std::is_same_v<T, F16>)
+            return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true))};
+        else
+            return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, false)),
+                         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true))};
+    }
+};
+
+// The larger (or the sum) of a value and lane ^ 32's.
+__device__ __forceinline__ float other_half(float v) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v), __builtin_bit_cast(unsigned, v), false, false);
+    return __builtin_bit_cast(float, threadIdx.x & 32 ? s[0] : s[1]);
+}
+
+constexpr float kLazy = 8.f;  // how far (in powers of 2) scores may pass M before M follows
+
+template <class C, int DP, int RT, int WM, int WT, int TS>
+struct AttentionTile {
+    static constexpr int kThreads = kWave * WM * WT;
+    static constexpr int kTokens = WT * TS;
+    static constexpr int kRows = 32 * RT * WM;
+    static constexpr int kPerLoad = 16 / C::kBytes;  // elements of a 16-byte load
+    static constexpr int kRowLoads = DP / kPerLoad;
+    static constexpr int kLoads = (kTokens * kRowLoads + kThreads - 1) / kThreads;
+    // Row pitches in the LDS (bytes): 16 times an odd number, so that 16-byte
+    // reads down a column of 8 rows meet all banks; 64 more than a multiple
+    // of 128, so that the transposing reads of 4 rows times 64 bytes do.
+    static constexpr int kPitchK = DP * 2 + 16;
+    static constexpr int kPitchV = (DP * 2) % 128 == 64 ? DP * 2 : DP * 2 + 64;
+    static constexpr int kTileBytes = kTokens * (kPitchK + kPitchV);
+    static constexpr int kPitchO = DP + 4;  // floats
+    static constexpr int kOutBytes = WT > 1 ? WM * WT * 32 * kPitchO * 4 : 0;
+    static constexpr int kBytes = kTileBytes > kOutBytes ? kTileBytes : kOutBytes;
+};
+
+template <class T, class C, int DP, int RT, int WM, int WT, int TS>
+__global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attention_kernel(TreeAttention a) {
+    using S = AttentionTile<C, DP, RT, WM, WT, TS>;
+    constexpr bool kScaled = C::kBytes == 1;
+    using VT = std::conditional_t<kScaled, F16, T>;
+    constexpr int TT = S::kTokens, KS = DP / 16, DT = DP / 32, SUB = TS / 32;
+    static_assert(RT == 1 || WT == 1, "waves that share rows join one row tile");
+    __shared__ __align__(16) char tile[S::kBytes];
+    __shared__ int64_t offs[3][TT];
+    __shared__ __align__(16) float kfac[kScaled ? TT : 4], vlog[kScaled ? TT : 4], vinv[kScaled ? TT : 4];
+    __shared__ float red[2][WM * WT][32];
+    __shared__ uint32_t bad[TT / 32];
+    char* const ldsk = tile;
+    char* const ldsv = tile + TT * S::kPitchK;
+
+    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, n = lane % 32, half = lane / 32;
+    const int wm = wave % WM, wt = wave / WM;
+    const int split = blockIdx.x, b = blockIdx.z;
+    const int h = blockIdx.y / a.row_blocks, rb = blockIdx.y - h * a.row_blocks;
+    const int D = a.cache.dim, group = a.group, M = a.nodes * group, heads = a.cache.heads;
+    const int count = a.count ? min(max(a.count[b], 0), a.nodes) : a.nodes;
+    const int len = max(a.lens[b], 0);
+    const int total = (int)min((int64_t)len + count, (int64_t)a.max_tokens);
+    const int first = split * a.chunk, last = min(first + a.chunk, total);
+    const bool direct = a.splits == 1;
+    const int row0 = (rb * WM + wm) * 32 * RT;
+    if (!direct && (first >= last || rb * S::kRows >= count * group)) return;
+
+    // This lane's rows.
+    int row[RT];
+    uint64_t seen[RT];  // the nodes it sees
+    u32x4 qf[RT][KS];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        row[r] = row0 + r * 32 + n;
+        const int node = row[r] / group, g = row[r] - node * group;
+        const bool live = row[r] < M && node < count;
+        const uint64_t upto = count >= 64 ? ~0ull : (1ull << count) - 1;
+        seen[r] = !live ? 0 : (a.mask ? (uint64_t)a.mask[(int64_t)b * a.nodes + node] : ~0ull >> (63 - node)) & upto;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch + node * a.q_node + (h * group + g) * a.q_head;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[r][s] = u32x4{0, 0, 0, 0};
+            if (live && s * 16 < D) qf[r][s] = *reinterpret_cast<const u32x4*>(q + s * 16 + half * 8) ^ a.flip;
+        }
+    }
+
+    f32x16 o[RT][DT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        m[r] = -__builtin_inff();
+        l[r] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
+    }
+
+    // Tiles are numbered from 0 at `first`. lookup() finds the page of this
+    // thread's token (tid < TT) of a tile; a page outside the cache is not
+    // followed, its tokens read as zeros.
+    const int64_t headk = (int64_t)h * a.cache.head_stride;
+    auto lookup = [&](int i) -> int {
+        const int t = first + i * TT + tid;
+        return tid < TT && t < last ? a.table[b * a.table_stride + t / a.cache.places] : -1;
+    };
+    auto offset = [&](int i, int page, int64_t* scale) -> int64_t {
+        const int t = first + i * TT + tid, at = t % a.cache.places;
+        *scale = -1;
+        if (page < 0 || page >= a.cache.pages) return -1;
+        *scale = (int64_t)page * a.cache.scale_page_stride + (int64_t)at * a.cache.scale_place_stride + (int64_t)h * a.cache.scale_head_stride;
+        return (int64_t)page * a.cache.page_stride + (int64_t)at * a.cache.place_stride + headk;
+    };
+    u32x4 rk[S::kLoads], rv[S::kLoads];
+    float sk = 0.f, sv = 1.f;
+    auto fetch = [&](int i, int64_t scale) {
+#pragma unroll
+        for (int j = 0; j < S::kLoads; ++j) {
+            const int e = j * S::kThreads + tid, t = e / S::kRowLoads, c = e % S::kRowLoads;
+            rk[j] = rv[j] = u32x4{0, 0, 0, 0};
+            if (e < TT * S::kRowLoads && c * S::kPerLoad < D) {
+                const int64_t off = offs[i % 3][t];
+                if (off >= 0) {
+                    const int64_t at = (off + c * S::kPerLoad) * C::kBytes;
+                    rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.k) + at);
+                    rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.v) + at);
+                }
+            }
+        }
+        if constexpr (kScaled) {
+            sk = 0.f, sv = 1.f;
+            if (tid < TT && scale >= 0) sk = a.cache.k_scales[scale], sv = a.cache.v_scales[scale];
+        }
+    };
+    // Elements of V that are no numbers, in the rows of nodes: set to 0 in the
+    // tile (0 times them would reach rows that do not see the node) and noted.
+    auto clean = [&](u32x4 v, int t) -> u32x4 {
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            constexpr uint32_t X = Mma<VT>::kExponent;
+            if ((v[w] & X) == X) v[w] &= 0xFFFF0000u, any = true;
+            if ((v[w] >> 16 & X) == X) v[w] &= 0x0000FFFFu, any = true;
+        }
+        if (any) atomicOr(&bad[t / 32], 1u << (t % 32));
+        return v;
+    };
+    auto store = [&](int i) {
+        const bool nodes_in = first + (i + 1) * TT > len;
+#pragma unroll
+        for (int j = 0; j < S::kLoads; ++j) {
+            const int e = j * S::kThreads + tid, t = e / S::kRowLoads, c = e % S::kRowLoads;
+            if (S::kLoads * S::kThreads != TT * S::kRowLoads && e >= TT * S::kRowLoads) break;
+            const bool node = nodes_in && first + i * TT + t >= len;
+            u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * (S::kPerLoad * 2));
+            u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
+            if constexpr (kScaled) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const u32x2 k0 = C::template widen4<T>(rk[j][2 * p]), k1 = C::template widen4<T>(rk[j][2 * p + 1]);
+                    const u32x2 v0 = C::template widen4<VT>(rv[j][2 * p]), v1 = C::template widen4<VT>(rv[j][2 * p + 1]);
+                    u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
+                    if (node) v = clean(v, t);
+                    dk[p] = u32x4{k0[0], k0[1], k1[0], k1[1]};
+                    dv[p] = v;
+                }
+            } else {
+                *dk = rk[j];
+                *dv = node ? clean(rv[j], t) : rv[j];
+            }
+        }
+        if constexpr (kScaled) {
+            if (tid < TT) {
+                // A scale of 0 (a row of zeros) is taken as 2^-100.
+                const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
+                kfac[tid] = sk * a.scale;
+                vlog[tid] = __builtin_amdgcn_logf(c);
+                vinv[tid] = 1.f / c;
+            }
+        }
+    };
+
+    const int tiles = last > first ? (last - first + TT - 1) / TT : 0;
+    int64_t scale0 = -1, scale1 = -1;
+    if (tiles > 0) {
+        const int64_t o0 = offset(0, lookup(0), &scale0), o1 = offset(1, lookup(1), &scale1);
+        if (tid < TT) offs[0][tid] = o0, offs[1][tid] = o1;
+        __syncthreads();
+        fetch(0, scale0);
+    }
+    for (int i = 0; i < tiles; ++i) {
+        if (i > 0) __syncthreads();  // the tile before has been read
+        const int base = first + i * TT;
+        if (base + TT > len) {
+            if (tid < TT / 32) bad[tid] = 0;
+            __syncthreads();
+        }
+        store(i);
+        __syncthreads();
+        const int page = lookup(i + 2);
+        if (i + 1 < tiles) fetch(i + 1, scale1);
+
+        // Scores of this wave's tokens.
+        const int t0 = wt * TS;
+        f32x16 sc[RT][SUB];
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) sc[r][s] = f32x16{};
+            const char* kp = ldsk + (t0 + s * 32 + n) * S::kPitchK + half * 16;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const u32x4 kf = *reinterpret_cast<const u32x4*>(kp + k * 32);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) sc[r][s] = Mma<T>::dot(kf, qf[r][k], sc[r][s]);
+            }
+        }
+        const bool masked = base + t0 + TS > min(len, total);
+        auto visible = [&](int r, int t) {  // t: number of the token in the sequence
+            const int j = t - len;
+            return t < total && (j < 0 || (j < 64 && (seen[r] >> (j & 63) & 1)));
+        };
+        uint32_t pf[RT][SUB][8];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int t = t0 + s * 32 + 8 * (x / 4) + 4 * half + x % 4;
+                    float v = sc[r][s][x];
+                    if constexpr (kScaled) v = v * kfac[t] + vlog[t];
+                    if (masked && !visible(r, base + t)) v = -__builtin_inff();
+                    sc[r][s][x] = v;
+                    top = fmaxf(top, v);
+                }
+            top = fmaxf(top, other_half(top));
+            if constexpr (!kScaled) top *= a.scale;
+            if (__any(top > m[r] + kLazy)) {
+                const float to = top > m[r] + kLazy ? top : m[r];
+                const float f = to == m[r] ? 1.f : __builtin_amdgcn_exp2f(m[r] - to);
+                m[r] = to;
+                l[r] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[r][d] *= f;
+            }
+            const float ms = m[r] == -__builtin_inff() ? 0.f : m[r];
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int t = t0 + s * 32 + 8 * (x / 4) + 4 * half + x % 4;
+                    float v;
+                    if constexpr (kScaled) {
+                        v = __builtin_amdgcn_exp2f(sc[r][s][x] - ms);
+                        const float p = v * vinv[t];
+                        l[r] += masked && !visible(r, base + t) ? 0.f : p;
+                    } else {
+                        v = __builtin_amdgcn_exp2f(sc[r][s][x] * a.scale - ms);
+                        if (masked && !visible(r, base + t)) v = 0.f;  // also where the scale is 0
+                        l[r] += v;
+                    }
+                    sc[r][s][x] = v;
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) pf[r][s][x] = Mma<VT>::pack(sc[r][s][2 * x], sc[r][s][2 * x + 1]);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                // 16 lanes read 4 tokens times 16 columns; lane % 16 picks a column.
+                const char* vp = ldsv + (t0 + s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
+                                 (lane / 16 % 2) * 32 + (lane % 4) * 8;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    using L = __attribute__((address_space(3))) s16x4*;
+                    const u32x2 v0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + d * 64)));
+                    const u32x2 v1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + d * 64 + 8 * S::kPitchV)));
+                    const u32x4 vf = {v0[0], v0[1], v1[0], v1[1]};
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const u32x4 p = {pf[r][s][4 * k], pf[r][s][4 * k + 1], pf[r][s][4 * k + 2], pf[r][s][4 * k + 3]};
+                        o[r][d] = Mma<VT>::dot(vf, p, o[r][d]);
+                    }
+                }
+            }
+        // Values of nodes that are no numbers reach the rows that see them.
+        if (base + TT > len) {
+            for (int t = t0; t < t0 + TS; ++t) {
+                if (!(bad[t / 32] >> (t % 32) & 1)) continue;
+                const int64_t off = offs[i % 3][t];
+                const int u = t - t0, x = (u % 32) / 8 * 4 + u % 4, from = n + 32 * (u / 4 % 2);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                        for (int y = 0; y < 16; ++y)
+                            if (s == u / 32 && y == x) w = sc[r][s][y];
+                    w = __shfl(w, from);
+                    if (off < 0 || !visible(r, base + t)) continue;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            const int c = d * 32 + 8 * (y / 4) + 4 * half + y % 4;
+                            if (c >= D) continue;
+                            float v;
+                            if constexpr (kScaled)
+                                v = F16::widen((uint16_t)C::template widen4<F16>(static_cast<const uint8_t*>(a.cache.v)[off + c])[0]);
+                            else
+                                v = T::widen(static_cast<const uint16_t*>(a.cache.v)[off + c]);
+                            if (!(__builtin_fabsf(v) < __builtin_inff())) o[r][d][y] += w * v;
+                        }
+                }
+            }
+        }
+        int64_t scale2;
+        const int64_t next = offset(i + 2, page, &scale2);
+        if (tid < TT) offs[(i + 2) % 3][tid] = next;
+        scale1 = scale2;
+    }
+
+    // Where a row's sums go: to the output, or to the partials of this chunk.
+    const int64_t prow0 = (((int64_t)b * heads + h) * a.splits + split) * M;
+    auto out_of = [&](int rw) {
+        const int node = rw / group, g = rw - node * group;
+        return static_cast<uint16_t*>(a.out) + b * a.out_batch + node * a.out_node + (h * group + g) * a.out_head;
+    };
+    auto put_stats = [&](int rw, float mm, float ll) {
+        if (direct) {
+            const int node = rw / group, g = rw - node * group;
+            if (node >= count) ll = 0.f;
+            a.lse[((int64_t)b * a.nodes + node) * (heads * group) + h * group + g] =
+                ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * 0.69314718055994531f : -__builtin_inff();
+        } else {
+            a.part_ml[prow0 + rw] = make_float2(mm, ll);
+        }
+    };
+    auto put4 = [&](int rw, int c, f32x4 v, float ll) {
+        if (direct) {
+            const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+            u32x2 w = {Mma<T>::pack(v[0] * inv, v[1] * inv), Mma<T>::pack(v[2] * inv, v[3] * inv)};
+            if (ll == 0.f || rw >= count * group) w = u32x2{0, 0};
+            *reinterpret_cast<u32x2*>(out_of(rw) + c) = w;
+        } else {
+            *reinterpret_cast<f32x4*>(a.part_o + (prow0 + rw) * D + c) = v;
+        }
+    };
+    if constexpr (WT == 1) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const float ll = l[r] + other_half(l[r]);
+            if (row[r] >= M) continue;
+            if (half == 0) put_stats(row[r], m[r], ll);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int y = 0; y < 16; y += 4) {
+                    const int c = d * 32 + 2 * y + 4 * half;
+                    if (c < D) put4(row[r], c, f32x4{o[r][d][y], o[r][d][y + 1], o[r][d][y + 2], o[r][d][y + 3]}, ll);
+                }
+        }
+    } else {
+        float ll = l[0] + other_half(l[0]);
+        if (half == 0) red[0][wave][n] = m[0];
+        __syncthreads();
+        float mm = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < WT; ++w) mm = fmaxf(mm, red[0][wm + w * WM][n]);
+        const float f = m[0] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[0] - mm);
+        if (half == 0) red[1][wave][n] = ll * f;
+        float* ob = reinterpret_cast<float*>(tile) + (wave * 32 + n) * S::kPitchO;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 16; y += 4)
+                *reinterpret_cast<f32x4*>(ob + d * 32 + 2 * y + 4 * half) =
+                    f32x4{o[0][d][y], o[0][d][y + 1], o[0][d][y + 2], o[0][d][y + 3]} * f;
+        __syncthreads();
+        for (int e = tid; e < WM * 32 * (DP / 4); e += S::kThreads) {
+            const int rr = e / (DP / 4), c = e % (DP / 4) * 4, w0 = rr / 32, rn = rr % 32, rw = rb * S::kRows + rr;
+            if (c >= D || rw >= M) continue;
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            float lsum = 0.f, mx = -__builtin_inff();
+#pragma unroll
+            for (int w = 0; w < WT; ++w) {
+                v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(tile) + ((w0 + w * WM) * 32 + rn) * S::kPitchO + c);
+                lsum += red[1][w0 + w * WM][rn];
+                mx = fmaxf(mx, red[0][w0 + w * WM][rn]);
+            }
+            if (c == 0) put_stats(rw, mx, lsum);
+            put4(rw, c, v, lsum);
+        }
+    }
+}
+
+template <class T, class C, int DP, int RT, int WM, int WT, int TS>
+hipError_t launch_attention_shape(const TreeAttention& a, hipStream_t stream) {
+    const dim3 grid((unsigned)a.splits, (unsigned)(a.cache.heads * a.row_blocks), (unsigned)a.batch);
+    tree_attention_kernel<T, C, DP, RT, WM, WT, TS><<<grid, kWave * WM * WT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <class T, class C, int DP>
+hipError_t launch_attention_dim(const TreeAttention& a, hipStream_t stream) {
+    if (a.nodes * a.group <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 1, 1, 4, 32>(a, stream);
+    return launch_attention_shape<T, C, DP, 1, 4, 1, 64>(a, stream);
+}
+
+template <class T, class C>
+hipError_t launch_attention(const TreeAttention& a, hipStream_t stream) {
+    const int d = a.cache.dim;
+    if (d <= 64) return launch_attention_dim<T, C, 64>(a, stream);
+    if (d <= 96) return launch_attention_dim<T, C, 96>(a, stream);
+    if (d <= 128) return launch_attention_dim<T, C, 128>(a, stream);
+    if (d <= 192) return launch_attention_dim<T, C, 192>(a, stream);
+    return launch_attention_dim<T, C, 256>(a, stream);
+}
+
+}  // namespace libred

@@ -36,7 +36,25 @@ class PagedCache(ctypes.Structure):
                 ("scale_page_stride", _L), ("scale_head_stride", _L), ("scale_place_stride", _L)]
 
 
+class TreeAttentionArgs(ctypes.Structure):
+    _fields_ = [("type", _I), ("scale", _F), ("batch", _Z), ("nodes", _Z), ("q_heads", _Z), ("max_len", _Z),
+                ("q", _P), ("out", _P), ("lse", _P),
+                ("q_batch_stride", _L), ("q_node_stride", _L), ("q_head_stride", _L),
+                ("out_batch_stride", _L), ("out_node_stride", _L), ("out_head_stride", _L),
+                ("cache", PagedCache), ("table", _P), ("table_cols", _Z), ("table_stride", _L),
+                ("lens", _P), ("tree_mask", _P), ("node_count", _P)]
+
+
+class VerifyDraftsArgs(ctypes.Structure):
+    _fields_ = [("type", _I), ("batch", _Z), ("drafts", _Z), ("vocab", _Z),
+                ("p", _P), ("p_batch_stride", _L), ("p_step_stride", _L),
+                ("q", _P), ("q_batch_stride", _L), ("q_step_stride", _L),
+                ("drafted", _P), ("u", _P), ("r", _P), ("draft_count", _P), ("accepted", _P), ("tokens", _P)]
+
+
 SIGNATURES = {
+    "red_verify_drafts": (_I, [ctypes.POINTER(VerifyDraftsArgs), _P]),
+    "red_tree_attention": (_I, [ctypes.POINTER(TreeAttentionArgs), _P]),
     "red_qk_norm_rope": (_I, [ctypes.POINTER(QkNormRopeArgs), _P]),
     "red_qk_norm_rope_backward": (_I, [ctypes.POINTER(QkNormRopeArgs), ctypes.POINTER(Heads), ctypes.POINTER(Heads),
                                        _P, _P, _P]),
@@ -197,3 +215,79 @@ def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None,
                                   _stream_handle(stream, device))
     _check(name, st)
     return k_out, v_out
+
+
+def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tree_mask=None, node_count=None,
+                       k_scales=None, v_scales=None, out=None, stream=None):
+    """Attention of drafted tokens q (batch, nodes, q heads, dim; float16 or
+    bfloat16; at most 64 nodes) over a paged cache (see red_cache_write).
+    Sequence b has lens[b] tokens (int32) and then its nodes, whose keys and
+    values are in the cache as well; token t lies in page table[b, t // places]
+    (int32). Node i sees all tokens below lens[b] and the nodes whose bits are
+    set in tree_mask[b, i] (int64; None: nodes 0 .. i); node_count (int32)
+    says how many nodes there are (None: all). max_len: the most tokens, nodes
+    included, of a sequence (None: what the table holds). -> (out like q, lse
+    (batch, nodes, q heads) float32); rows that see nothing hold 0 and -inf."""
+    name = "red_tree_attention"
+    c = _cache(name, k_pages, v_pages, k_scales, v_scales)
+    device = k_pages.device
+    _tensor(name, "q", q, _FLOATS[1:], device)
+    if q.dim() != 4 or q.shape[3] != c.dim:
+        raise ValueError(f"{name}: q must be (batch, nodes, q heads, {c.dim})")
+    batch, nodes, heads, dim = q.shape
+    _tensor(name, "table", table, torch.int32, device)
+    if table.dim() != 2 or table.shape[0] != batch:
+        raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
+    out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else \
+        _tensor(name, "out", out, q.dtype, device, q.shape)
+    lse = torch.empty((batch, nodes, heads), dtype=torch.float32, device=device)
+    cols = table.shape[1]
+    a = TreeAttentionArgs(TYPES[q.dtype], scale, batch, nodes, heads, cols * c.places if max_len is None else max_len,
+                          q.data_ptr(), out.data_ptr(), lse.data_ptr(), *q.stride()[:3], *out.stride()[:3], c,
+                          table.data_ptr(), cols, table.stride(0), _vector(name, "lens", lens, torch.int32, device, batch))
+    if tree_mask is not None:
+        _tensor(name, "tree_mask", tree_mask, torch.int64, device, (batch, nodes))
+        if not tree_mask.is_contiguous():
+            raise ValueError(f"{name}: tree_mask must be contiguous")
+        a.tree_mask = tree_mask.data_ptr()
+    if node_count is not None:
+        a.node_count = _vector(name, "node_count", node_count, torch.int32, device, batch)
+    with torch.cuda.device(device):
+        st = lib().red_tree_attention(ctypes.byref(a), _stream_handle(stream, device))
+    _check(name, st)
+    return out, lse
+
+
+def red_verify_drafts(p, q, drafted, u, r, draft_count=None, stream=None):
+    """Which drafted tokens (batch, drafts; int64) the target's probabilities p
+    (batch, drafts + 1, vocab) accept against the draft's q (batch, drafts,
+    vocab; None: its tokens were certain), by the random numbers u (batch,
+    drafts) and r (batch; both float32), and the token drawn after them.
+    draft_count (int32): how many drafts a sequence has (None: all).
+    -> (accepted (batch) int32, tokens (batch, drafts + 1) int64: the accepted
+    ones, the drawn one, then -1)."""
+    name = "red_verify_drafts"
+    _tensor(name, "p", p, _FLOATS, None)
+    device = p.device
+    if p.dim() != 3 or p.shape[1] < 1:
+        raise ValueError(f"{name}: p must be (batch, drafts + 1, vocab)")
+    batch, drafts, vocab = p.shape[0], p.shape[1] - 1, p.shape[2]
+    a = VerifyDraftsArgs(TYPES[p.dtype], batch, drafts, vocab, p.data_ptr(), *p.stride()[:2])
+    if q is not None:
+        _tensor(name, "q", q, p.dtype, device, (batch, drafts, vocab))
+        a.q, a.q_batch_stride, a.q_step_stride = q.data_ptr(), *q.stride()[:2]
+    for what, x, dtype in (("drafted", drafted, torch.int64), ("u", u, torch.float32)):
+        _tensor(name, what, x, dtype, device, (batch, drafts))
+        if not x.is_contiguous():
+            raise ValueError(f"{name}: {what} must be contiguous")
+        setattr(a, what, x.data_ptr())
+    a.r = _vector(name, "r", r, torch.float32, device, batch)
+    if draft_count is not None:
+        a.draft_count = _vector(name, "draft_count", draft_count, torch.int32, device, batch)
+    accepted = torch.empty(batch, dtype=torch.int32, device=device)
+    tokens = torch.empty((batch, drafts + 1), dtype=torch.int64, device=device)
+    a.accepted, a.tokens = accepted.data_ptr(), tokens.data_ptr()
+    with torch.cuda.device(device):
+        st = lib().red_verify_drafts(ctypes.byref(a), _stream_handle(stream, device))
+    _check(name, st)
+    return accepted, tokens

@@ -241,6 +241,281 @@ def test_cache_write_and_read(case):
         assert torch.equal(now, was)
 
 
+# ---------------------------------------------------------------------------
+# Attention over the cache
+# ---------------------------------------------------------------------------
+ATTEND = [  # lens, nodes, q heads, kv heads, dim, places, tree, counts, dtype, cache, cache layout
+    ([300], 1, 4, 1, 128, 16, False, None, F16, F16, "own"), ([1], 1, 2, 2, 64, 1, False, None, BF16, BF16, "own"),
+    ([0, 5, 130], 4, 4, 2, 64, 24, True, [4, 0, 3], BF16, I8, "own"), ([127, 128, 129, 1000], 8, 8, 2, 128, 64, True, [8, 5, 8, 1], BF16, I8, "own"),
+    ([500, 20], 64, 2, 1, 80, 8, True, [64, 33], F16, E4M3, "own"), ([77, 640], 63, 8, 1, 128, 32, True, None, BF16, BF16, "own"),
+    ([64, 1, 2], 17, 6, 2, 96, 16, True, None, F16, I8, "places first"), ([900], 5, 3, 3, 256, 24, False, None, F16, F16, "own"),
+    ([333], 40, 4, 1, 256, 128, True, None, BF16, E4M3, "own"), ([258, 31], 3, 8, 1, 192, 16, True, None, BF16, I8, "own"),
+    ([200], 33, 2, 1, 192, 16, False, [20], F16, F16, "places first"), ([100, 0], 2, 16, 2, 16, 8, True, None, F16, I8, "own"),
+    ([90], 9, 4, 1, 112, 1, True, None, BF16, E4M3, "own"), ([0], 64, 8, 1, 48, 128, True, None, BF16, BF16, "own"),
+    ([0, 0], 1, 1, 1, 64, 16, False, [0, 1], F16, F16, "own"), ([2500, 3, 1700], 2, 4, 2, 64, 16, True, None, F16, E4M3, "own"),
+    ([700, 1400] * 32, 1, 8, 8, 64, 32, False, None, BF16, I8, "own"), ([260, 1100] * 4, 64, 8, 4, 64, 64, True, None, F16, F16, "own"),
+]
+
+
+def attend_inputs(case, seed, scale_of_v=1.0):
+    lens, nodes, hq, hk, dim, places, tree, counts, dt, kind, layout = case
+    g = gen(seed)
+    b = len(lens)
+    per = -(-(max(lens) + nodes) // places) + 1
+    pages = b * per + 2
+    pg, sc = empty_cache(pages, hk, places, dim, kind, layout, g)
+    for i in range(2):
+        x = torch.randn(pages, hk, places, dim, generator=g)
+        if kind == I8:
+            pg[i].copy_((x * 36).clamp(-127, 127).round().to(I8))
+        elif kind == E4M3:
+            pg[i].view(I8).copy_((x * 120).clamp(-448, 448).to(E4M3).view(I8))
+        else:
+            pg[i].copy_(x.to(kind))
+        sc[i].copy_((0.5 + torch.rand(pages, hk, places, generator=g)) / (36 if kind == I8 else 120) * (scale_of_v if i else 1.0))
+    table = (torch.randperm(pages - 2, generator=g)[:b * per] + 1).to(torch.int32).view(b, per)
+    q = (1.5 * torch.randn(b, nodes, hq, dim, generator=g)).to(dt)
+    mask = None
+    if tree:
+        mask = torch.zeros(b, nodes, dtype=torch.int64)
+        for i in range(b):
+            for j in range(nodes):
+                parent = int(torch.randint(-1, j, (1,), generator=g)) if j else -1
+                word = ((int(mask[i, parent]) & (2 ** 64 - 1)) if parent >= 0 else 0) | 1 << j
+                mask[i, j] = word - 2 ** 64 if word >= 2 ** 63 else word
+    return pg, sc, table, q, mask
+
+
+def check_attend(case, pg, sc, table, q, mask, scale, out, lse, pages_ok=None):
+    lens, nodes, hq, hk, dim, places, tree, counts, dt, kind, layout = case
+    group, scaled = hq // hk, kind in R.TOP
+    hp = R.step(F16 if scaled else dt)
+    code = [(p.view(I8).cpu().view(E4M3) if kind == E4M3 else p.cpu()).float() for p in pg]
+    c = [s.cpu() if scaled else torch.ones(code[0].shape[:3]) for s in sc]
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert not out[~lse.isfinite() & (lse < 0)].any()
+    for b, n in enumerate(lens):
+        count = nodes if counts is None else counts[b]
+        total = n + count
+        seen = R.visible(n, nodes, mask[b] if tree else None, count, total).repeat_interleave(group, 0)
+        t = torch.arange(total)
+        page, at = table[b, t // places].long().cpu(), t % places
+        ok = (page >= 0) & (page < code[0].shape[0])
+        page = torch.where(ok, page, 0)
+        for h in range(hk):
+            k, v = (torch.where(ok[:, None], x[page, h, at], 0.0) for x in code)
+            kc, vc = (torch.where(ok, x[page, h, at], 1.0) for x in c)
+            rows = q[b, :, h * group:(h + 1) * group].reshape(nodes * group, dim)
+            want, wlse, weights, size = R.tree_attention(rows, k.double() * kc.double()[:, None], v.double() * vc.double()[:, None], seen, scale)
+            got = out[b, :, h * group:(h + 1) * group].reshape(nodes * group, dim)
+            glse = lse[b, :, h * group:(h + 1) * group].reshape(-1)
+            for i in range(nodes * group):
+                if not seen[i].any():
+                    assert glse[i] == -math.inf and not got[i].any(), (b, h, i)
+                    continue
+                p, vs, cs = weights[i][:, None], v[seen[i]].double(), vc[seen[i]].double()[:, None]
+                es = (dim + 8) * U * size[i] + 16 * U * (1 + cs.log2().abs().max())
+                terms = (p * cs * vs).nan_to_num(0.0, 0.0, 0.0)
+                # rounded exponentials: 3.5 half steps of the root of the sum of
+                # squares (6 standard deviations), and half the spacing of
+                # subnormals where P is float16; then float32 sums
+                sub = 2.0 ** -25 * (p * cs).max() * vs.nan_to_num(0.0, 0.0, 0.0).square().sum(0).sqrt() * 3.5
+                allowed = (R.step(dt) * want[i].abs() + 3.5 * hp * terms.square().sum(0).sqrt() + sub +
+                           ((len(p) + 32) * U + 2 * es) * terms.abs().sum(0) + R.tiny(dt))
+                same = (got[i] == want[i]) | (got[i].isnan() & want[i].isnan())
+                assert (same | ((got[i] - want[i]).abs() <= allowed)).all(), (b, h, i, (got[i] - want[i]).abs().max())
+                assert abs(glse[i] - wlse[i]) <= es + (len(p) + 32) * U + 4 * U * wlse[i].abs(), (b, h, i, glse[i], wlse[i])
+
+
+def attend(case, pg, sc, table, q, mask, scale, **kw):
+    lens, counts, kind = case[0], case[7], case[9]
+    if kind in R.TOP:
+        kw.update(k_scales=sc[0], v_scales=sc[1])
+    return rl.red_tree_attention(q.to(DEV) if q.device.type == "cpu" else q, pg[0], pg[1], table.to(DEV),
+                                 torch.tensor(lens, dtype=torch.int32, device=DEV), scale,
+                                 tree_mask=mask.to(DEV) if mask is not None else None,
+                                 node_count=torch.tensor(counts, dtype=torch.int32, device=DEV) if counts is not None else None, **kw)
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=str)
+def test_tree_attention(case):
+    say(case)
+    pg, sc, table, q, mask = attend_inputs(case, 11)
+    scale = case[4] ** -0.5
+    out, lse = attend(case, pg, sc, table, q, mask, scale, max_len=max(case[0]) + case[1])
+    check_attend(case, pg, sc, table, q, mask, scale, out, lse)
+    again = attend(case, pg, sc, table, q, mask, scale, max_len=max(case[0]) + case[1])
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("case", [ATTEND[3], ATTEND[5], ATTEND[15]], ids=str)
+@pytest.mark.parametrize("scale_of_v, scale", [(1e-20, 0.3), (1e15, -0.1), (1.0, 0.0)])
+def test_tree_attention_scales(case, scale_of_v, scale):
+    say(case, scale_of_v, scale)
+    if case[3] is F16 and case[9] is E4M3 or case[8] is F16:
+        scale_of_v = min(max(scale_of_v, 1e-3), 10.0)      # the output has to be in range
+    pg, sc, table, q, mask = attend_inputs(case, 12, scale_of_v)
+    out, lse = attend(case, pg, sc, table, q, mask, scale)
+    check_attend(case, pg, sc, table, q, mask, scale, out, lse)
+
+
+@pytest.mark.parametrize("case", [
+    ([150, 40], 8, 4, 2, 64, 16, True, [8, 6], F16, F16, "own"), ([150, 40], 8, 4, 2, 64, 16, True, [8, 6], BF16, E4M3, "own"),
+    ([150, 40], 64, 2, 1, 128, 16, True, [60, 50], BF16, BF16, "own"), ([150, 40], 8, 4, 2, 64, 16, True, [8, 6], F16, I8, "own")], ids=str)
+def test_tree_attention_masked_places(case):
+    """Infinities and NaN where no row, or not every row, sees them."""
+    say(case)
+    lens, nodes, counts, places, kind = case[0], case[1], case[7], case[5], case[9]
+    pg, sc, table, q, mask = attend_inputs(case, 13)
+    used = torch.zeros(pg[0].shape[0], places, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        t = torch.arange(n + counts[b])
+        used[table[b, t // places].long(), t % places] = True
+    free = (~used).nonzero().to(DEV)
+    bad = float("nan")
+    for x in pg:
+        if kind == I8:
+            x[free[:, 0], :, free[:, 1]] = 127
+        elif kind == E4M3:
+            x.view(I8)[free[:, 0], :, free[:, 1]] = 127            # NaN
+        else:
+            x[free[:, 0], :, free[:, 1]] = bad
+    for x in sc:
+        x[free[:, 0], :, free[:, 1]] = bad
+    for b, n in enumerate(lens):                       # two nodes hold what is no number
+        for j, value in ((1, float("inf")), (3, bad)):
+            p, at = int(table[b, (n + j) // places]), (n + j) % places
+            if kind == I8:
+                sc[0][p, :, at] = sc[1][p, :, at] = bad
+            elif kind == E4M3:
+                pg[0].view(I8)[p, :, at, 2] = 127
+                pg[1].view(I8)[p, 0, at, 5] = 127
+            else:
+                pg[0][p, :, at, 2] = 1.0
+                pg[1][p, 0, at, 5] = value
+                pg[1][p, 0, at, 6] = -value
+    scale = 0.2
+    out, lse = attend(case, pg, sc, table, q, mask, scale)
+    if kind in (F16, BF16):
+        check_attend(case, pg, sc, table, q, mask, scale, out, lse)
+        return
+    # rows that see one of them are NaN, the others as if those nodes were not there
+    clean = [x.clone() for x in sc]
+    cp = [x.clone() for x in pg]
+    for b, n in enumerate(lens):
+        for j in (1, 3):
+            p, at = int(table[b, (n + j) // places]), (n + j) % places
+            for x in clean:
+                x[p, :, at] = 1.0
+            for x in cp:
+                x.view(I8)[p, :, at] = 0
+    sees = ((mask >> 1 | mask >> 3) & 1).bool()
+    for b in range(len(lens)):
+        for i in range(counts[b]):
+            if sees[b, i]:
+                assert lse[b, i].isnan().all() and out[b, i].isnan().all()
+    out, lse = out.cpu(), lse.cpu()
+    ref_out, ref_lse = (x.cpu() for x in attend(case, cp, clean, table, q, mask, scale))
+    blind = ~sees & (torch.arange(nodes) < torch.tensor(counts)[:, None])
+    assert torch.equal(out[blind], ref_out[blind]) and torch.equal(lse[blind], ref_lse[blind])
+
+
+def test_tree_attention_bad_pages_and_lengths():
+    """Pages outside the cache read as zeros; lengths beyond max_len or the
+    table are cut; q and out with strides of their own."""
+    case = ([200, 50], 4, 4, 2, 64, 16, False, None, F16, F16, "own")
+    pg, sc, table, q, mask = attend_inputs(case, 14)
+    table[0, 3], table[0, 7], table[1, 1] = -5, 1 << 30, pg[0].shape[0]
+    out, lse = attend(case, pg, sc, table, q, mask, 0.125)
+    check_attend(case, pg, sc, table, q, mask, 0.125, out, lse)
+    cut = ([100, 50], *case[1:])
+    a = attend(([100, 50], *case[1:7], [0, 4], *case[8:]), pg, sc, table, q, mask, 0.125)
+    wide = torch.zeros(2, 4, 9, 64, dtype=F16, device=DEV)[:, :, 3:7]
+    wide.copy_(q)
+    to = torch.full((2, 4, 6, 64), 7.0, dtype=F16, device=DEV)
+    b = attend(cut, pg, sc, table, wide, mask, 0.125, out=to[:, :, 1:5])
+    assert torch.equal(a[0][1], b[0][1]) and torch.equal(a[1][1], b[1][1]) and (to[:, :, 0] == 7).all() and (to[:, :, 5] == 7).all()
+    # 100 tokens of the 200 (and none of the nodes) where max_len is 100
+    full = ([100], 4, 4, 2, 64, 16, True, [4], F16, F16, "own")
+    none = torch.zeros(1, 4, dtype=torch.int64)
+    c = attend(([200], 4, 4, 2, 64, 16, False, None, F16, F16, "own"), pg, sc, table[:1], q[:1], None, 0.125, max_len=100)
+    d = attend(full, pg, sc, table[:1], q[:1], none, 0.125)
+    assert torch.equal(c[0], d[0]) and torch.equal(c[1], d[1])
+    e = attend(([200], 4, 4, 2, 64, 16, False, None, F16, F16, "own"), pg, sc, table[:1, :0], q[:1], None, 0.125)
+    assert not e[0].any() and (e[1] == -math.inf).all()
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens
+# ---------------------------------------------------------------------------
+VERIFY = [  # batch, drafts, vocab, dtype, given, sharpness, layout
+    (1, 4, 32000, F32, True, 2.5, "own"), (5, 6, 1001, F32, True, 2.5, "own"), (3, 10, 4099, BF16, True, 2.0, "own"),
+    (7, 3, 2048, F16, False, 4.0, "own"), (2, 70, 300, F32, True, 1.0, "own"), (9, 1, 1, F32, True, 1.0, "own"),
+    (4, 0, 777, F32, False, 1.0, "own"), (33, 5, 131071, F32, True, 2.5, "own"), (6, 4, 5003, BF16, False, 6.0, "odd"),
+    (6, 4, 1023, F32, True, 2.5, "odd"), (300, 2, 50, F16, True, 2.0, "own"), (0, 2, 50, F16, True, 2.0, "own"),
+]
+
+
+def verify_inputs(case, seed=21):
+    b, k, v, dt, given, sharp, layout = case
+    g = gen(seed)
+    x = sharp * torch.randn(b, k + 1, v, generator=g)
+    p = torch.softmax(x, -1).to(dt)
+    y = x[:, :k] + 0.7 * torch.randn(b, k, v, generator=g)
+    q = torch.softmax(y, -1).to(dt) if given else None
+    drafted = (y + torch.empty(b, k, v).exponential_(generator=g).log_().neg_()).argmax(-1) if k else torch.zeros(b, 0, dtype=torch.int64)
+    if not given and k:
+        drafted = p[:, :k].float().argmax(-1)          # certain drafts: the likeliest
+    u, r = torch.rand(b, k, generator=g), torch.rand(b, generator=g)
+    count = torch.randint(0, k + 1, (b,), generator=g).to(torch.int32)
+    return p, q, drafted, u, r, count
+
+
+def check_verify(p, q, drafted, u, r, count, got, layout="own"):
+    n, tokens = (x.cpu() for x in got)
+    for b in range(p.shape[0]):
+        want = R.verify(p[b], q[b] if q is not None else None, drafted[b], u[b], r[b], int(count[b]) if count is not None else p.shape[1] - 1)
+        assert (int(n[b]), tokens[b].tolist()) == want, b
+
+
+@pytest.mark.parametrize("case", VERIFY, ids=str)
+def test_verify_drafts(case):
+    say(case)
+    p, q, drafted, u, r, count = verify_inputs(case)
+    pd, qd = (place(x, case[6]) if x is not None else None for x in (p, q))
+    d = [x.to(DEV) for x in (drafted, u, r, count)]
+    check_verify(p, q, drafted, u, r, count, rl.red_verify_drafts(pd, qd, *d[:3], draft_count=d[3]))
+    check_verify(p, q, drafted, u, r, None, rl.red_verify_drafts(pd, qd, *d[:3]))
+    low, high = torch.zeros_like(d[2]), torch.full_like(d[2], 1 - 2.0 ** -24)
+    for e in (low, high):
+        check_verify(p, q, drafted, u, e.cpu(), count, rl.red_verify_drafts(pd, qd, *d[:2], e, draft_count=d[3]))
+
+
+def test_verify_drafts_corners():
+    b, k, v = 8, 3, 3001
+    p, q, drafted, u, r, _ = verify_inputs((b, k, v, F32, True, 2.0, "own"), 22)
+    q[0], u[0] = p[0, :k], 1.0                          # refused, and p - q is 0 everywhere
+    drafted[1] = torch.tensor([-1, 5, 6])               # outside the vocabulary
+    drafted[2, 1] = v
+    u[2, 0] = 0.0
+    p[3] = 0.0                                          # no weight at all
+    p[4, 0, 7] = float("nan")
+    drafted[4, 0], u[4, 0] = 7, 0.5
+    p[5, :, : v // 2] = 0.0                             # weight in the second half only
+    r[5], r[6] = 0.0, 1.0                               # r of 1: the last of positive weight
+    u[6], p[6, 0, -5:] = 1.0, 0.0
+    u[7] = 0.0                                          # everything accepted
+    p[7] = p[7] + 1e-30
+    args = [x.to(DEV) for x in (p, q, drafted, u, r)]
+    got = rl.red_verify_drafts(*args)
+    check_verify(p, q, drafted, u, r, None, got)
+    assert int(got[0][0]) == 0 and int(got[0][7]) == k and got[1][3].tolist() == [-1] * 4 and int(got[1][4, 0]) == -1
+    # counts out of range are cut
+    count = torch.tensor([-4, 0, 99, 2, 2, 1, 3, 1 << 30], dtype=torch.int32)
+    got = rl.red_verify_drafts(*args, draft_count=count.to(DEV))
+    check_verify(p, q, drafted, u, r, count.clamp(0, k), got)
+
+
 def test_python_refusals():
     q, k = torch.zeros(3, 4, 64, device=DEV), torch.zeros(3, 2, 64, device=DEV)
     pos, freq = torch.zeros(3, dtype=torch.int64, device=DEV), R.frequencies(64).to(DEV)
@@ -268,3 +543,27 @@ def test_python_refusals():
             w(*args, **kw)
     with pytest.raises(TypeError):
         rl.red_cache_read(pg, pg, slots, F32, k_scales=sc, v_scales=sc)
+    probs, d = torch.zeros(2, 4, 9, device=DEV), torch.zeros(2, 3, dtype=torch.int64, device=DEV)
+    u, r = torch.zeros(2, 3, device=DEV), torch.zeros(2, device=DEV)
+    f = rl.red_verify_drafts
+    for args, kw, error in (((probs.double(), None, d, u, r), {}, TypeError), ((probs[0], None, d, u, r), {}, ValueError),
+                            ((probs, probs, d, u, r), {}, ValueError), ((probs, None, d.int(), u, r), {}, TypeError),
+                            ((probs, None, d, u[:, :2], r), {}, ValueError), ((probs, None, d, u, u), {}, ValueError),
+                            ((probs, None, d, u, r), dict(draft_count=d[:, 0]), TypeError),
+                            ((probs, probs[:, :3].half(), d, u, r), {}, TypeError)):
+        with pytest.raises(error):
+            f(*args, **kw)
+    q4, pg = torch.zeros(2, 3, 4, 64, dtype=F16, device=DEV), torch.zeros(5, 2, 8, 64, dtype=F16, device=DEV)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    f = rl.red_tree_attention
+    for args, kw, error in (((q4.float(), pg, pg, table, lens, 1.0), {}, TypeError), ((q4.bfloat16(), pg, pg, table, lens, 1.0), {}, rl.RedError),
+                            ((q4[..., :32], pg, pg, table, lens, 1.0), {}, ValueError), ((q4, pg, pg, table.long(), lens, 1.0), {}, TypeError),
+                            ((q4, pg, pg, table[:1], lens, 1.0), {}, ValueError), ((q4, pg, pg, table, lens[:1], 1.0), {}, ValueError),
+                            ((q4, pg, pg[:, :1], table, lens, 1.0), {}, ValueError), ((q4, pg, pg, table, lens, float("nan")), {}, rl.RedError),
+                            ((q4[:, :, :3], pg, pg, table, lens, 1.0), {}, rl.RedError),
+                            ((q4, pg, pg, table, lens, 1.0), dict(tree_mask=torch.zeros(2, 4, dtype=torch.int64, device=DEV)), ValueError),
+                            ((q4, pg, pg, table, lens, 1.0), dict(node_count=lens.long()), TypeError),
+                            ((q4, pg, pg, table, lens, 1.0), dict(out=q4), rl.RedError),
+                            ((torch.zeros(2, 65, 4, 64, dtype=F16, device=DEV), pg, pg, table, lens, 1.0), {}, rl.RedError)):
+        with pytest.raises(error):
+            f(*args, **kw)
