@@ -294,7 +294,8 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     k.table = a->table, k.table_stride = a->table_stride;
     k.lens = a->lens, k.mask = a->tree_mask, k.count = a->node_count;
     k.batch = (int)B, k.nodes = (int)N, k.group = (int)G, k.max_tokens = c.pages == 0 ? 0 : (int)tokens;
-    k.scale = (a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
+    k.keep = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
+    k.scale = (a->scale == 0.f ? 1.f : a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
     k.flip = a->scale < 0.f ? 0x80008000u : 0u;
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M);

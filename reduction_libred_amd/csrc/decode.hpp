@@ -85,6 +85,7 @@ struct TreeAttention {
     int batch, nodes, group, max_tokens, chunk, splits, row_blocks;
     float scale;  // magnitude, times log2(e)
     unsigned int flip;  // 0x80008000 where the scale is negative: the sign of q
+    unsigned int keep;  // 0 where the scale is 0 (q is then, and scale is that of 1)
     float* part_o;   // per (batch, kv head, split, row): dim floats, and
     float2* part_ml; // the running maximum and sum
 };

@@ -132,10 +132,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     constexpr int TT = S::kTokens, KS = DP / 16, DT = DP / 32, SUB = TS / 32;
     static_assert(RT == 1 || WT == 1, "waves that share rows join one row tile");
     __shared__ __align__(16) char tile[S::kBytes];
-    __shared__ int64_t offs[3][TT];
+    __shared__ int64_t offs[2][TT];
     __shared__ __align__(16) float kfac[kScaled ? TT : 4], vlog[kScaled ? TT : 4], vinv[kScaled ? TT : 4];
     __shared__ float red[2][WM * WT][32];
-    __shared__ uint32_t bad[TT / 32];
+    __shared__ int odd;
     char* const ldsk = tile;
     char* const ldsv = tile + TT * S::kPitchK;
 
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             qf[r][s] = u32x4{0, 0, 0, 0};
-            if (live && s * 16 < D) qf[r][s] = *reinterpret_cast<const u32x4*>(q + s * 16 + half * 8) ^ a.flip;
+            if (live && s * 16 < D) qf[r][s] = (*reinterpret_cast<const u32x4*>(q + s * 16 + half * 8) ^ a.flip) & a.keep;
         }
     }
 
@@ -197,41 +197,49 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         return (int64_t)page * a.cache.page_stride + (int64_t)at * a.cache.place_stride + headk;
     };
     u32x4 rk[S::kLoads], rv[S::kLoads];
+    uint32_t there = 0;  // bit j: load j is of a token in the cache
     float sk = 0.f, sv = 1.f;
     auto fetch = [&](int i, int64_t scale) {
+        int64_t off[S::kLoads];
 #pragma unroll
         for (int j = 0; j < S::kLoads; ++j) {
-            const int e = j * S::kThreads + tid, t = e / S::kRowLoads, c = e % S::kRowLoads;
-            rk[j] = rv[j] = u32x4{0, 0, 0, 0};
-            if (e < TT * S::kRowLoads && c * S::kPerLoad < D) {
-                const int64_t off = offs[i % 3][t];
-                if (off >= 0) {
-                    const int64_t at = (off + c * S::kPerLoad) * C::kBytes;
-                    rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.k) + at);
-                    rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.v) + at);
-                }
-            }
+            const int e = j * S::kThreads + tid;
+            off[j] = offs[i % 2][min(e / S::kRowLoads, TT - 1)];
+        }
+        there = 0;
+#pragma unroll
+        for (int j = 0; j < S::kLoads; ++j) {
+            const int c = (j * S::kThreads + tid) % S::kRowLoads * S::kPerLoad;
+            there |= (off[j] >= 0 && c < D ? 1u : 0u) << j;
+            const int64_t at = ((off[j] >= 0 ? off[j] : 0) + (c < D ? c : 0)) * C::kBytes;
+            rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.k) + at);
+            rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.v) + at);
         }
         if constexpr (kScaled) {
             sk = 0.f, sv = 1.f;
             if (tid < TT && scale >= 0) sk = a.cache.k_scales[scale], sv = a.cache.v_scales[scale];
         }
     };
-    // Elements of V that are no numbers, in the rows of nodes: set to 0 in the
-    // tile (0 times them would reach rows that do not see the node) and noted.
-    auto clean = [&](u32x4 v, int t) -> u32x4 {
-        bool any = false;
+    // Infinities and NaN in the values of nodes are left out of the products
+    // (0 times them would reach rows that do not see the node) and noted;
+    // strange() gives them to the rows that do.
+    auto clean = [&](u32x4 v) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             constexpr uint32_t X = Mma<VT>::kExponent;
-            if ((v[w] & X) == X) v[w] &= 0xFFFF0000u, any = true;
-            if ((v[w] >> 16 & X) == X) v[w] &= 0x0000FFFFu, any = true;
+            const uint32_t keep = ((v[w] & X) == X ? 0u : 0xFFFFu) | ((v[w] >> 16 & X) == X ? 0u : 0xFFFF0000u);
+            if (keep != ~0u) odd = 1;
+            v[w] &= keep;
         }
-        if (any) atomicOr(&bad[t / 32], 1u << (t % 32));
         return v;
     };
     auto store = [&](int i) {
         const bool nodes_in = first + (i + 1) * TT > len;
+        if (there != (1u << S::kLoads) - 1) {
+#pragma unroll
+            for (int j = 0; j < S::kLoads; ++j)
+                if (!(there >> j & 1)) rk[j] = rv[j] = u32x4{0, 0, 0, 0};
+        }
 #pragma unroll
         for (int j = 0; j < S::kLoads; ++j) {
             const int e = j * S::kThreads + tid, t = e / S::kRowLoads, c = e % S::kRowLoads;
@@ -245,13 +253,13 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                     const u32x2 k0 = C::template widen4<T>(rk[j][2 * p]), k1 = C::template widen4<T>(rk[j][2 * p + 1]);
                     const u32x2 v0 = C::template widen4<VT>(rv[j][2 * p]), v1 = C::template widen4<VT>(rv[j][2 * p + 1]);
                     u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
-                    if (node) v = clean(v, t);
+                    if (node) v = clean(v);
                     dk[p] = u32x4{k0[0], k0[1], k1[0], k1[1]};
                     dv[p] = v;
                 }
             } else {
                 *dk = rk[j];
-                *dv = node ? clean(rv[j], t) : rv[j];
+                *dv = node ? clean(rv[j]) : rv[j];
             }
         }
         if constexpr (kScaled) {
@@ -260,13 +268,16 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                 const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
                 kfac[tid] = sk * a.scale;
                 vlog[tid] = __builtin_amdgcn_logf(c);
-                vinv[tid] = 1.f / c;
+                // 1 where the scale is no number (the exponent says so), so
+                // that a row that does not see the token adds 0 times it.
+                vinv[tid] = c < __builtin_inff() ? 1.f / c : 1.f;
             }
         }
     };
 
     const int tiles = last > first ? (last - first + TT - 1) / TT : 0;
     int64_t scale0 = -1, scale1 = -1;
+    if (tid == 0) odd = 0;
     if (tiles > 0) {
         const int64_t o0 = offset(0, lookup(0), &scale0), o1 = offset(1, lookup(1), &scale1);
         if (tid < TT) offs[0][tid] = o0, offs[1][tid] = o1;
@@ -276,10 +287,6 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     for (int i = 0; i < tiles; ++i) {
         if (i > 0) __syncthreads();  // the tile before has been read
         const int base = first + i * TT;
-        if (base + TT > len) {
-            if (tid < TT / 32) bad[tid] = 0;
-            __syncthreads();
-        }
         store(i);
         __syncthreads();
         const int page = lookup(i + 2);
@@ -300,11 +307,35 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                 for (int r = 0; r < RT; ++r) sc[r][s] = Mma<T>::dot(kf, qf[r][k], sc[r][s]);
             }
         }
-        const bool masked = base + t0 + TS > min(len, total);
-        auto visible = [&](int r, int t) {  // t: number of the token in the sequence
-            const int j = t - len;
-            return t < total && (j < 0 || (j < 64 && (seen[r] >> (j & 63) & 1)));
-        };
+        if constexpr (kScaled) {
+#pragma unroll
+            for (int s = 0; s < SUB; ++s)
+#pragma unroll
+                for (int x = 0; x < 16; x += 4) {
+                    const int t = t0 + s * 32 + 2 * x + 4 * half;
+                    const f32x4 kf = *reinterpret_cast<const f32x4*>(kfac + t), vl = *reinterpret_cast<const f32x4*>(vlog + t);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) sc[r][s][x + y] = sc[r][s][x + y] * kf[y] + vl[y];
+                }
+        }
+        if (base + t0 + TS > min(len, total)) {
+            // Bit t of a word: whether this lane's row sees token t of 32.
+#pragma unroll
+            for (int s = 0; s < SUB; ++s) {
+                const int from = base + t0 + s * 32, j = from - len, left = total - from;
+                const uint32_t there = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    uint32_t sees = j <= -32 ? ~0u : j >= 64 ? 0u : j >= 0 ? (uint32_t)(seen[r] >> j) : (uint32_t)(seen[r] << -j) | ((1u << -j) - 1);
+                    sees = (sees & there) >> (4 * half);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        if (!(sees & 1u << (8 * (x / 4) + x % 4))) sc[r][s][x] = -__builtin_inff();
+                }
+            }
+        }
         uint32_t pf[RT][SUB][8];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -312,14 +343,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
             for (int s = 0; s < SUB; ++s)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int t = t0 + s * 32 + 8 * (x / 4) + 4 * half + x % 4;
-                    float v = sc[r][s][x];
-                    if constexpr (kScaled) v = v * kfac[t] + vlog[t];
-                    if (masked && !visible(r, base + t)) v = -__builtin_inff();
-                    sc[r][s][x] = v;
-                    top = fmaxf(top, v);
-                }
+                for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[r][s][x]);
             top = fmaxf(top, other_half(top));
             if constexpr (!kScaled) top *= a.scale;
             if (__any(top > m[r] + kLazy)) {
@@ -334,79 +358,45 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int t = t0 + s * 32 + 8 * (x / 4) + 4 * half + x % 4;
-                    float v;
-                    if constexpr (kScaled) {
-                        v = __builtin_amdgcn_exp2f(sc[r][s][x] - ms);
-                        const float p = v * vinv[t];
-                        l[r] += masked && !visible(r, base + t) ? 0.f : p;
-                    } else {
-                        v = __builtin_amdgcn_exp2f(sc[r][s][x] * a.scale - ms);
-                        if (masked && !visible(r, base + t)) v = 0.f;  // also where the scale is 0
-                        l[r] += v;
-                    }
-                    sc[r][s][x] = v;
-                }
+                for (int x = 0; x < 16; x += 4) {
+                    f32x4 vi;
+                    if constexpr (kScaled) vi = *reinterpret_cast<const f32x4*>(vinv + t0 + s * 32 + 2 * x + 4 * half);
+                    float w[4];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) pf[r][s][x] = Mma<VT>::pack(sc[r][s][2 * x], sc[r][s][2 * x + 1]);
+                    for (int y = 0; y < 4; ++y) {
+                        w[y] = __builtin_amdgcn_exp2f(kScaled ? sc[r][s][x + y] - ms : sc[r][s][x + y] * a.scale - ms);
+                        l[r] += kScaled ? w[y] * vi[y] : w[y];
+                    }
+                    pf[r][s][x / 2] = Mma<VT>::pack(w[0], w[1]);
+                    pf[r][s][x / 2 + 1] = Mma<VT>::pack(w[2], w[3]);
+                }
             }
         }
+        // 8 tokens of a column: 16 lanes read 4 tokens times 16 columns; lane % 16 picks a column.
+        auto values = [&](int s, int k, int d) -> u32x4 {
+            const char* vp = ldsv + (t0 + s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
+                             (lane / 16 % 2) * 32 + (lane % 4) * 8 + d * 64;
+            using L = __attribute__((address_space(3))) s16x4*;
+            const u32x2 v0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)vp));
+            const u32x2 v1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + 8 * S::kPitchV)));
+            return u32x4{v0[0], v0[1], v1[0], v1[1]};
+        };
+        auto weights = [&](int r, int s, int k) -> u32x4 {
+            return u32x4{pf[r][s][4 * k], pf[r][s][4 * k + 1], pf[r][s][4 * k + 2], pf[r][s][4 * k + 3]};
+        };
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                // 16 lanes read 4 tokens times 16 columns; lane % 16 picks a column.
-                const char* vp = ldsv + (t0 + s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
-                                 (lane / 16 % 2) * 32 + (lane % 4) * 8;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    using L = __attribute__((address_space(3))) s16x4*;
-                    const u32x2 v0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + d * 64)));
-                    const u32x2 v1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + d * 64 + 8 * S::kPitchV)));
-                    const u32x4 vf = {v0[0], v0[1], v1[0], v1[1]};
+                    const u32x4 v = values(s, k, d);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const u32x4 p = {pf[r][s][4 * k], pf[r][s][4 * k + 1], pf[r][s][4 * k + 2], pf[r][s][4 * k + 3]};
-                        o[r][d] = Mma<VT>::dot(vf, p, o[r][d]);
-                    }
+                    for (int r = 0; r < RT; ++r) o[r][d] = Mma<VT>::dot(v, weights(r, s, k), o[r][d]);
                 }
-            }
-        // Values of nodes that are no numbers reach the rows that see them.
-        if (base + TT > len) {
-            for (int t = t0; t < t0 + TS; ++t) {
-                if (!(bad[t / 32] >> (t % 32) & 1)) continue;
-                const int64_t off = offs[i % 3][t];
-                const int u = t - t0, x = (u % 32) / 8 * 4 + u % 4, from = n + 32 * (u / 4 % 2);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    float w = 0.f;
-#pragma unroll
-                    for (int s = 0; s < SUB; ++s)
-#pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            if (s == u / 32 && y == x) w = sc[r][s][y];
-                    w = __shfl(w, from);
-                    if (off < 0 || !visible(r, base + t)) continue;
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const int c = d * 32 + 8 * (y / 4) + 4 * half + y % 4;
-                            if (c >= D) continue;
-                            float v;
-                            if constexpr (kScaled)
-                                v = F16::widen((uint16_t)C::template widen4<F16>(static_cast<const uint8_t*>(a.cache.v)[off + c])[0]);
-                            else
-                                v = T::widen(static_cast<const uint16_t*>(a.cache.v)[off + c]);
-                            if (!(__builtin_fabsf(v) < __builtin_inff())) o[r][d][y] += w * v;
-                        }
-                }
-            }
-        }
         int64_t scale2;
         const int64_t next = offset(i + 2, page, &scale2);
-        if (tid < TT) offs[(i + 2) % 3][tid] = next;
+        if (tid < TT) offs[i % 2][tid] = next;
         scale1 = scale2;
     }
 
@@ -425,6 +415,30 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         } else {
             a.part_ml[prow0 + rw] = make_float2(mm, ll);
         }
+    };
+    // The infinities and NaN in columns c .. c + 3 of the nodes of this chunk
+    // that row rw sees: their weights do not matter.
+    auto strange = [&](int rw, int c) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        const int node = rw / group;
+        if (node >= count) return v;
+        const uint64_t word = a.mask ? (uint64_t)a.mask[(int64_t)b * a.nodes + node] : ~0ull >> (63 - node);
+#pragma unroll 1
+        for (int t = max(first, len); t < last; ++t) {
+            const int page = a.table[b * a.table_stride + t / a.cache.places];
+            if (!(word >> (t - len) & 1) || page < 0 || page >= a.cache.pages) continue;
+            const int64_t at = (int64_t)page * a.cache.page_stride + (int64_t)(t % a.cache.places) * a.cache.place_stride + headk + c;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                float f;
+                if constexpr (kScaled)
+                    f = F16::widen((uint16_t)C::template widen4<F16>(static_cast<const uint8_t*>(a.cache.v)[at + y])[0]);
+                else
+                    f = T::widen(static_cast<const uint16_t*>(a.cache.v)[at + y]);
+                if (!(__builtin_fabsf(f) < __builtin_inff())) v[y] += f;
+            }
+        }
+        return v;
     };
     auto put4 = [&](int rw, int c, f32x4 v, float ll) {
         if (direct) {
@@ -480,6 +494,19 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             }
             if (c == 0) put_stats(rw, mx, lsum);
             put4(rw, c, v, lsum);
+        }
+    }
+    __syncthreads();
+    if (odd) {
+        for (int e = tid; e < S::kRows * (DP / 4); e += S::kThreads) {
+            const int c = e % (DP / 4) * 4, rw = rb * S::kRows + e / (DP / 4);
+            if (c >= D || rw >= M) continue;
+            const f32x4 v = strange(rw, c);
+            for (int y = 0; y < 4; ++y) {
+                if (v[y] == 0.f) continue;
+                if (direct) out_of(rw)[c + y] = T::narrow(v[y]);
+                else a.part_o[(prow0 + rw) * D + c + y] = v[y];
+            }
         }
     }
 }
