@@ -1,6 +1,7 @@
-// Attention of drafted tokens over a split cache: joins the chunks of a row,
+// Attention of drafted tokens over a shared-out cache: joins the pieces of a
+// row,
 //     out = sum_c 2^(M_c - M) O_c / sum_c 2^(M_c - M) l_c,  M = max M_c,
-// in the order of the chunks, and the choice of the kernel by types.
+// in their order, and the choice of the kernel by types.
 #include "decode_common.hpp"
 
 namespace libred {
@@ -12,44 +13,80 @@ constexpr int kThreads = 256;
 struct MaxOp {
     __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
+struct AddOp {
+    __device__ float operator()(float a, float b) const { return a + b; }
+};
 
-// One block a row: first the weight of every chunk, then the chunks in
-// kThreads / LANES slices, each lane with 4 neighbouring columns.
-template <class T, int LANES>
-__global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a) {
-    constexpr int kSlices = kThreads / LANES;
-    __shared__ float weight[kAttentionMaxSplits], red[2][kThreads / kWave];
-    __shared__ f32x4 sums[kThreads];
+// A row is joined by `waves` waves of the block (1, or all where there are few
+// rows). Its pieces are taken 64 at a time: their weights first, then their
+// sums, LANES lanes with 4 neighbouring columns each.
+template <class T, int LANES, int WAVES>
+__global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a, int rows_a_block) {
+    constexpr int kRowsHere = kThreads / kWave / WAVES, kSlices = WAVES * kWave / LANES;
+    __shared__ f32x4 sums[WAVES > 1 ? kThreads : 1];
     const int D = a.cache.dim, group = a.group, M = a.nodes * group, heads = a.cache.heads;
-    const int tid = threadIdx.x, rw = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x % (WAVES * kWave), wl = threadIdx.x % kWave;
+    const int64_t all_rows = (int64_t)a.batch * heads * M;
+    const int64_t id = (int64_t)blockIdx.x * kRowsHere + threadIdx.x / (WAVES * kWave);
+    if (id >= all_rows) return;  // whole waves; with several waves a row, whole blocks
+    const int rw = (int)(id % M), h = (int)(id / M % heads), b = (int)(id / M / heads);
     const int node = rw / group, g = rw - node * group;
-    const int count = a.count ? min(max(a.count[b], 0), a.nodes) : a.nodes;
-    const int64_t lenb = max(a.lens[b], 0);
-    const int total = (int)min(lenb + count, (int64_t)a.max_tokens);
-    const int chunks = node < count ? (total + a.chunk - 1) / a.chunk : 0;
-    const int64_t row0 = ((int64_t)b * heads + h) * a.splits * M + rw;  // of chunk c: + c * M
-    float2 ml = make_float2(-__builtin_inff(), 0.f);
-    if (tid < chunks) ml = a.part_ml[row0 + (int64_t)tid * M];
-    float m = group_combine<kWave>(ml.x, MaxOp());
-    if (tid % kWave == 0) red[0][tid / kWave] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float w = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(ml.x - m);
-    weight[tid] = w;
-    const float lw = group_sum<kWave>(w * ml.y);
-    if (tid % kWave == 0) red[1][tid / kWave] = lw;
-    __syncthreads();
-    const float l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    int count;
+    sequence_tokens(a, b, &count);
+    const int64_t per = a.plan[a.batch + 1], start = a.plan[b];
+    const int seg_tiles = a.plan[b + 1] - (int)start, per_seq = heads * a.row_blocks;
+    const int rb = rw / rows_a_block, seg = h * a.row_blocks + rb;
+    const int64_t first = start * per_seq + (int64_t)seg * seg_tiles;
+    int pieces = 0;
+    int64_t slot = 0;
+    if (node < count && seg_tiles > 0) {
+        const int64_t w0 = first / per, w1 = (first + seg_tiles - 1) / per;
+        pieces = (int)(w1 - w0) + 1;
+        slot = w0 + (int64_t)b * per_seq + seg;
+    }
+    const int64_t row0 = slot * rows_a_block + (rw - rb * rows_a_block);
     const int lane = tid % LANES, slice = tid / LANES, c = lane * 4;
+    float m = -__builtin_inff(), l = 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (c < D)
-        for (int k = slice; k < chunks; k += kSlices)
-            v += weight[k] * *reinterpret_cast<const f32x4*>(a.part_o + (row0 + (int64_t)k * M) * D + c);
-    sums[tid] = v;
-    __syncthreads();
-    if (slice == 0 && c < D) {
+    for (int k0 = 0; k0 < pieces; k0 += kWave) {
+        float2 ml = make_float2(-__builtin_inff(), 0.f);
+        if (k0 + wl < pieces) ml = a.part_ml[row0 + (int64_t)(k0 + wl) * rows_a_block];
+        const float to = fmaxf(m, group_combine<kWave>(ml.x, MaxOp()));
+        const float f = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - to);
+        const float w = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(ml.x - to);
+        l = l * f + group_combine<kWave>(w * ml.y, AddOp());
+        v *= f;
+        m = to;
+        const int here = min(pieces - k0, kWave);
+        for (int k1 = 0; k1 < here; k1 += 4 * kSlices) {
+            f32x4 x[4];
+            float wk[4];
 #pragma unroll
-        for (int s = 1; s < kSlices; ++s) v += sums[s * LANES + lane];
+            for (int u = 0; u < 4; ++u) {
+                const int k = k1 + u * kSlices + slice, kk = min(k, here - 1);
+                wk[u] = __shfl(w, kk);
+                x[u] = *reinterpret_cast<const f32x4*>(a.part_o + (row0 + (int64_t)(k0 + kk) * rows_a_block) * D + (c < D ? c : 0));
+                if (k >= here) x[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v += wk[u] * x[u];
+        }
+    }
+    // Slices: those of a wave, then those of the block's waves.
+    if constexpr (LANES < kWave) {
+#pragma unroll
+        for (int o = LANES; o < kWave; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], o);
+    }
+    if constexpr (WAVES > 1) {
+        sums[threadIdx.x] = v;
+        __syncthreads();
+        if (tid >= LANES) return;
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v += sums[w * kWave + lane];
+    }
+    if (tid < LANES && c < D) {
         const bool empty = l == 0.f;
         const float inv = empty ? 0.f : 1.f / l;
         typename Vec<T, 4>::type out;
@@ -63,22 +100,27 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a) {
     }
 }
 
-template <class T>
-hipError_t combine(const TreeAttention& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.nodes * a.group), (unsigned)a.cache.heads, (unsigned)a.batch);
-    if (a.cache.dim <= 64)
-        combine_kernel<T, 16><<<grid, kThreads, 0, stream>>>(a);
-    else if (a.cache.dim <= 128)
-        combine_kernel<T, 32><<<grid, kThreads, 0, stream>>>(a);
+template <class T, int LANES>
+hipError_t combine_lanes(const TreeAttention& a, int rows_a_block, hipStream_t stream) {
+    const int64_t rows = (int64_t)a.batch * a.cache.heads * a.nodes * a.group;
+    if (rows < 2048)
+        combine_kernel<T, LANES, 4><<<(unsigned)rows, kThreads, 0, stream>>>(a, rows_a_block);
     else
-        combine_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
+        combine_kernel<T, LANES, 1><<<(unsigned)((rows + 3) / 4), kThreads, 0, stream>>>(a, rows_a_block);
     return hipGetLastError();
+}
+
+template <class T>
+hipError_t combine(const TreeAttention& a, int rows_a_block, hipStream_t stream) {
+    if (a.cache.dim <= 64) return combine_lanes<T, 16>(a, rows_a_block, stream);
+    if (a.cache.dim <= 128) return combine_lanes<T, 32>(a, rows_a_block, stream);
+    return combine_lanes<T, 64>(a, rows_a_block, stream);
 }
 
 }  // namespace
 
-hipError_t launch_attention_combine(int type, const TreeAttention& a, hipStream_t stream) {
-    return type == RED_F16 ? combine<F16>(a, stream) : combine<BF16>(a, stream);
+hipError_t launch_attention_combine(int type, const TreeAttention& a, int rows_a_block, hipStream_t stream) {
+    return type == RED_F16 ? combine<F16>(a, rows_a_block, stream) : combine<BF16>(a, rows_a_block, stream);
 }
 
 hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream) {

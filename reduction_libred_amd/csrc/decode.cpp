@@ -300,27 +300,25 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());
-    if (c.heads * (size_t)k.row_blocks > 65535) return RED_ERR_INVALID_ARG;
-    // Chunks: enough blocks for the card, whole tiles each.
+    // One block a segment where none has more than one tile; else as many as
+    // the card holds at once (two of 4 waves a compute unit), or one a tile.
     const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
-    const size_t base = B * c.heads * (size_t)k.row_blocks, want = (size_t)cus * 8;
-    size_t splits = (want + base - 1) / base;
-    if (splits > tiles) splits = tiles;
-    if (splits > (size_t)libred::kAttentionMaxSplits) splits = libred::kAttentionMaxSplits;
-    if (splits < 1) splits = 1;
-    const size_t per = tiles == 0 ? 1 : (tiles + splits - 1) / splits;
-    k.chunk = (int)(per * tile);
-    k.splits = tiles == 0 ? 1 : (int)((tiles + per - 1) / per);
-    if (k.splits > 1) {
-        const size_t rows = B * c.heads * (size_t)k.splits * M;
+    const size_t segments = B * c.heads * (size_t)k.row_blocks;
+    if (segments > 0x7fffffff || (int64_t)(B * tiles) > 0x7fffffff) return RED_ERR_INVALID_ARG;
+    if (tiles > 1) {
+        const size_t hold = (size_t)cus * 2;
+        const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
+        k.blocks = (int)blocks;
+        const size_t rows = (blocks + segments) * (size_t)shape.rows(), plan = (B + 2 + 3) / 4 * 4;
         void* p = nullptr;
-        st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)), &p);
+        st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)) + plan * sizeof(int), &p);
         if (st != RED_OK) return st;
         k.part_o = static_cast<float*>(p);
         k.part_ml = reinterpret_cast<float2*>(k.part_o + rows * D);
+        k.plan = reinterpret_cast<int*>(k.part_ml + rows);
     }
     hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
-    if (e == hipSuccess && k.splits > 1) e = libred::launch_attention_combine(type, k, stream);
+    if (e == hipSuccess && k.blocks > 0) e = libred::launch_attention_combine(type, k, shape.rows(), stream);
     return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
 }
 

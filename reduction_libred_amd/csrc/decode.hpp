@@ -69,8 +69,9 @@ hipError_t launch_cache_read(int type, int cache_type, int vec, int lanes, const
                              hipStream_t stream);
 
 // Attention of drafted tokens. Rows of one kv head are numbered node * group +
-// query head of the group; a block takes `rows` of them (the shape's) and one
-// chunk of the cache's tokens.
+// query head of the group; a block takes `rows` of them (the shape's) at a
+// time. Sequence, kv head and block of rows make a segment; the tiles of all
+// segments, one after the other, are shared out evenly over `blocks` blocks.
 struct TreeAttention {
     const void* q;
     void* out;
@@ -82,12 +83,16 @@ struct TreeAttention {
     const int32_t* lens;
     const int64_t* mask;   // null: a chain
     const int32_t* count;  // null: all nodes
-    int batch, nodes, group, max_tokens, chunk, splits, row_blocks;
+    int batch, nodes, group, max_tokens, row_blocks;
+    int blocks;  // 0: one block a segment, of at most one tile, that writes the output
     float scale;  // magnitude, times log2(e)
     unsigned int flip;  // 0x80008000 where the scale is negative: the sign of q
     unsigned int keep;  // 0 where the scale is 0 (q is then, and scale is that of 1)
-    float* part_o;   // per (batch, kv head, split, row): dim floats, and
-    float2* part_ml; // the running maximum and sum
+    // The sums of a segment's piece in block w are number w + segment, `rows`
+    // rows of `dim` floats, and a maximum and a sum a row.
+    float* part_o;
+    float2* part_ml;
+    int* plan;  // batch + 2: tiles of a segment before sequence b (block 0 writes it), tiles a block
 };
 
 // How waves share a block: `waves_m` groups of 32 * row_tiles rows times
@@ -100,9 +105,8 @@ struct AttentionShape {
 constexpr AttentionShape kFewRows = {1, 1, 4, 32}, kManyRows = {1, 4, 1, 64};
 // The shape for `rows` rows of a kv head.
 constexpr AttentionShape attention_shape(int rows) { return rows <= 32 ? kFewRows : kManyRows; }
-constexpr int kAttentionMaxSplits = 256;
-// Joins the chunks of every row into the output.
-hipError_t launch_attention_combine(int type, const TreeAttention& a, hipStream_t stream);
+// Joins the pieces of every row into the output (rows_a_block: the shape's).
+hipError_t launch_attention_combine(int type, const TreeAttention& a, int rows_a_block, hipStream_t stream);
 hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream);
 hipError_t launch_attention_f16_16(const TreeAttention& a, hipStream_t stream);
 hipError_t launch_attention_f16_i8(const TreeAttention& a, hipStream_t stream);

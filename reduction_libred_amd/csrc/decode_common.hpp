@@ -69,4 +69,11 @@ __device__ __forceinline__ float group_sum(float v) {
     return group_combine<G>(v, [](float a, float b) { return a + b; });
 }
 
+// Tokens of sequence b, nodes included, and how many nodes it has.
+__device__ __forceinline__ int sequence_tokens(const TreeAttention& a, int b, int* nodes) {
+    const int count = a.count ? min(max(a.count[b], 0), a.nodes) : a.nodes;
+    *nodes = count;
+    return (int)min((int64_t)max(a.lens[b], 0) + count, (int64_t)a.max_tokens);
+}
+
 }  // namespace libred

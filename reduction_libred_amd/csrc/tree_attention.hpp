@@ -23,11 +23,16 @@
 // of V in the product (float16 for 8-bit caches, which hold those exactly):
 // relative 2^-11 or 2^-8 a term, the step of the output's own type.
 //
-// Long caches are split over blocks; their sums are joined by
-// combine_kernel in the order of the chunks.
+// The tiles of all sequences, heads and blocks of rows are shared out evenly
+// over as many blocks as the card holds at once, whatever the lengths: a block
+// takes a run of tiles, which may end one segment and begin the next, and
+// writes the sums of every piece; combine_kernel joins a segment's pieces in
+// order. (With a fixed grid of chunks instead, 32 sequences of 1500 to 16384
+// tokens kept the compute units half busy: 231 us.)
 #pragma once
 
 #include "decode_common.hpp"
+#include "launch.hpp"
 
 namespace libred {
 
@@ -103,6 +108,12 @@ __device__ __forceinline__ float other_half(float v) {
     return __builtin_bit_cast(float, threadIdx.x & 32 ? s[0] : s[1]);
 }
 
+// A value that is the same in all lanes, as one the compiler knows to be.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 constexpr float kLazy = 8.f;  // how far (in powers of 2) scores may pass M before M follows
 
 template <class C, int DP, int RT, int WM, int WT, int TS>
@@ -139,18 +150,74 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     char* const ldsk = tile;
     char* const ldsv = tile + TT * S::kPitchK;
 
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave, n = lane % 32, half = lane / 32;
+    const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = lane % 32, half = lane / 32;
     const int wm = wave % WM, wt = wave / WM;
-    const int split = blockIdx.x, b = blockIdx.z;
-    const int h = blockIdx.y / a.row_blocks, rb = blockIdx.y - h * a.row_blocks;
     const int D = a.cache.dim, group = a.group, M = a.nodes * group, heads = a.cache.heads;
-    const int count = a.count ? min(max(a.count[b], 0), a.nodes) : a.nodes;
-    const int len = max(a.lens[b], 0);
-    const int total = (int)min((int64_t)len + count, (int64_t)a.max_tokens);
-    const int first = split * a.chunk, last = min(first + a.chunk, total);
-    const bool direct = a.splits == 1;
+    const bool direct = a.blocks == 0;
+    const int per_seq = heads * a.row_blocks;  // segments of a sequence
+
+    // This block's share of the tiles: [now, end) of all segments' tiles.
+    int b = 0, seg = 0, skip = 0;  // sequence, segment in it, tiles of that segment that are another's
+    int64_t now = 0, end = 1;
+    // Blocks are dealt to the XCDs in turn; each XCD takes a run of shares, so
+    // that the blocks of rows of one head read its tokens through one L2.
+    const int share = direct || gridDim.x % kXcds ? blockIdx.x : blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    if (direct) {
+        b = blockIdx.x / per_seq, seg = blockIdx.x % per_seq;
+    } else {
+        auto tiles_of = [&](int q) {
+            int nodes;
+            const int t = q < a.batch ? sequence_tokens(a, q, &nodes) : 0;
+            return q < a.batch && nodes > 0 ? (t + TT - 1) / TT : 0;
+        };
+        int64_t all = 0;
+        for (int q = 0; q < a.batch; q += kWave) all += group_combine<kWave>(tiles_of(q + lane), [](int x, int y) { return x + y; });
+        all *= per_seq;
+        const int64_t per = (all + gridDim.x - 1) / gridDim.x;
+        now = share * per, end = min(now + per, all);
+        const bool planner = share == 0 && wave == 0;
+        if (now >= end && !planner) return;
+        // The sequence that holds tile `now`.
+        const int64_t want = now / per_seq;  // as tiles of one segment of each sequence
+        int64_t before = 0;
+        bool found = false;
+        for (int q = 0; q < a.batch && (planner || !found); q += kWave) {
+            int upto = tiles_of(q + lane);
+            const int own = upto;
+            for (int o = 1; o < kWave; o <<= 1) {
+                const int x = __shfl_up(upto, o);
+                if (lane >= o) upto += x;
+            }
+            if (planner && q + lane < a.batch) a.plan[q + lane] = (int)(before + upto - own);
+            const uint64_t past = __ballot(before + upto > want);
+            if (past && !found) {
+                found = true;
+                const int at = __ffsll((unsigned long long)past) - 1;
+                b = q + at;
+                const int64_t rest = now - (before + __shfl(upto - own, at)) * per_seq;
+                const int each = __shfl(own, at);
+                seg = (int)(rest / each);
+                skip = (int)(rest - (int64_t)seg * each);
+            }
+            before += __shfl(upto, kWave - 1);
+        }
+        if (planner && lane == 0) a.plan[a.batch] = (int)before, a.plan[a.batch + 1] = (int)per;
+        b = uniform(b), seg = uniform(seg), skip = uniform(skip);
+        now = uniform64(now), end = uniform64(end);
+    }
+
+    while (now < end) {
+    int nodes_in_b;
+    const int total = uniform(sequence_tokens(a, b, &nodes_in_b)), len = uniform(max(a.lens[b], 0)), count = uniform(nodes_in_b);
+    const int h = seg / a.row_blocks, rb = seg - h * a.row_blocks;
+    const int64_t slot = direct ? 0 : share + (int64_t)b * per_seq + seg;
+    const int seg_tiles = count > 0 ? (total + TT - 1) / TT : 0;
+    // No rows in this block of rows (the nodes it would hold do not exist).
+    const bool rows_in = rb * S::kRows < count * group;
+    const int mine = direct ? seg_tiles : (int)min((int64_t)(seg_tiles - skip), end - now);
+    const int first = skip * TT, last = min(total, first + mine * TT);
     const int row0 = (rb * WM + wm) * 32 * RT;
-    if (!direct && (first >= last || rb * S::kRows >= count * group)) return;
+    if (rows_in || direct) {
 
     // This lane's rows.
     int row[RT];
@@ -275,8 +342,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         }
     };
 
-    const int tiles = last > first ? (last - first + TT - 1) / TT : 0;
+    const int tiles = rows_in && last > first ? (last - first + TT - 1) / TT : 0;
     int64_t scale0 = -1, scale1 = -1;
+    __syncthreads();  // the segment before is done with the LDS
     if (tid == 0) odd = 0;
     if (tiles > 0) {
         const int64_t o0 = offset(0, lookup(0), &scale0), o1 = offset(1, lookup(1), &scale1);
@@ -401,7 +469,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     }
 
     // Where a row's sums go: to the output, or to the partials of this chunk.
-    const int64_t prow0 = (((int64_t)b * heads + h) * a.splits + split) * M;
+    const int64_t prow0 = slot * S::kRows - rb * S::kRows;
     auto out_of = [&](int rw) {
         const int node = rw / group, g = rw - node * group;
         return static_cast<uint16_t*>(a.out) + b * a.out_batch + node * a.out_node + (h * group + g) * a.out_head;
@@ -509,11 +577,26 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             }
         }
     }
+    }
+    now += direct ? 1 : mine;
+    skip = 0;
+    if (now < end) {  // the next segment that has tiles
+        int nodes = count;
+        int t = total;
+        do {
+            if (++seg == per_seq) {
+                seg = 0, ++b;
+                t = uniform(sequence_tokens(a, b, &nodes));
+                nodes = uniform(nodes);
+            }
+        } while (t == 0 || nodes == 0);
+    }
+    }
 }
 
 template <class T, class C, int DP, int RT, int WM, int WT, int TS>
 hipError_t launch_attention_shape(const TreeAttention& a, hipStream_t stream) {
-    const dim3 grid((unsigned)a.splits, (unsigned)(a.cache.heads * a.row_blocks), (unsigned)a.batch);
+    const unsigned int grid = a.blocks ? (unsigned)a.blocks : (unsigned)(a.batch * a.cache.heads * a.row_blocks);
     tree_attention_kernel<T, C, DP, RT, WM, WT, TS><<<grid, kWave * WM * WT, 0, stream>>>(a);
     return hipGetLastError();
 }
