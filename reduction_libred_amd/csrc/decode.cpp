@@ -297,6 +297,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     k.keep = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
     k.scale = (a->scale == 0.f ? 1.f : a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
     k.flip = a->scale < 0.f ? 0x80008000u : 0u;
+    k.inv_places = 1.0 / (double)c.places;
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());

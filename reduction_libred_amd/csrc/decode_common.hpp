@@ -69,6 +69,13 @@ __device__ __forceinline__ float group_sum(float v) {
     return group_combine<G>(v, [](float a, float b) { return a + b; });
 }
 
+// A wave's LDS writes are seen by its own later reads (the LDS serves a wave
+// in order); this keeps the compiler from moving them past each other.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Tokens of sequence b, nodes included, and how many nodes it has.
 __device__ __forceinline__ int sequence_tokens(const TreeAttention& a, int b, int* nodes) {
     const int count = a.count ? min(max(a.count[b], 0), a.nodes) : a.nodes;

@@ -21,13 +21,6 @@
 
 namespace libred {
 
-// A wave's LDS writes are seen by its own later reads (the LDS serves a wave
-// in order); this keeps the compiler from moving them past each other.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // cos and sin of 2 pi t from t in turns. Quarter turns come off exactly, the
 // rest is at most an eighth of a turn, where the Taylor sums to the 14th power
 // are off by less than 1e-15.

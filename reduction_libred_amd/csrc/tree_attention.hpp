@@ -13,10 +13,11 @@
 // product does not mind the order of the tokens it sums over, so V^T is read
 // in the order that S^T left them in, with the transposing LDS load.
 //
-// A block walks its chunk of the tokens in tiles: while one tile is computed,
-// the next is on its way from memory into registers (rows looked up through
-// the page table a tile earlier), and is converted to 16 bits on its way into
-// the LDS, once for all waves. 8-bit elements stay whole: the scale of a key
+// A team of waves walks its tokens in tiles: while one tile is computed, the
+// next is on its way from memory into registers (rows looked up through the
+// page table a tile earlier), and is converted to 16 bits on its way into the
+// LDS, once for all its waves. Up to 32 rows a team is one wave and needs no
+// barrier; the block's waves take tiles in turn and join at the end. 8-bit elements stay whole: the scale of a key
 // multiplies its scores, and the scale of a value joins the exponent,
 //     w_t = 2^(s'_t + log2 c_t - M),  out = sum_t w_t code_t / sum_t w_t / c_t,
 // so that w stays in range whatever the scales are. P is rounded to the type
@@ -123,16 +124,23 @@ struct AttentionTile {
     static constexpr int kRows = 32 * RT * WM;
     static constexpr int kPerLoad = 16 / C::kBytes;  // elements of a 16-byte load
     static constexpr int kRowLoads = DP / kPerLoad;
-    static constexpr int kLoads = (kTokens * kRowLoads + kThreads - 1) / kThreads;
+    // A team of waves shares a tile of TS tokens: the waves_m waves of
+    // different rows, or one wave, which then needs no barriers.
+    static constexpr int kTeam = kWave * WM;
+    static constexpr int kLoads = (TS * kRowLoads + kTeam - 1) / kTeam;
+    // Tiles a team holds in the LDS: with barriers two, so that one is written
+    // while the other is read and there is one barrier a tile.
+    static constexpr int kHeld = WM > 1 ? 2 : 1;
     // Row pitches in the LDS (bytes): 16 times an odd number, so that 16-byte
     // reads down a column of 8 rows meet all banks; 64 more than a multiple
     // of 128, so that the transposing reads of 4 rows times 64 bytes do.
     static constexpr int kPitchK = DP * 2 + 16;
     static constexpr int kPitchV = (DP * 2) % 128 == 64 ? DP * 2 : DP * 2 + 64;
-    static constexpr int kTileBytes = kTokens * (kPitchK + kPitchV);
+    static constexpr int kTileBytes = TS * (kPitchK + kPitchV);
     static constexpr int kPitchO = DP + 4;  // floats
     static constexpr int kOutBytes = WT > 1 ? WM * WT * 32 * kPitchO * 4 : 0;
-    static constexpr int kBytes = kTileBytes > kOutBytes ? kTileBytes : kOutBytes;
+    static constexpr int kAllTiles = WT * kHeld * kTileBytes;
+    static constexpr int kBytes = kAllTiles > kOutBytes ? kAllTiles : kOutBytes;
 };
 
 template <class T, class C, int DP, int RT, int WM, int WT, int TS>
@@ -141,17 +149,20 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     constexpr bool kScaled = C::kBytes == 1;
     using VT = std::conditional_t<kScaled, F16, T>;
     constexpr int TT = S::kTokens, KS = DP / 16, DT = DP / 32, SUB = TS / 32;
+    static_assert(WM == 1 || WT == 1, "a team is a wave or the block");
     static_assert(RT == 1 || WT == 1, "waves that share rows join one row tile");
+    constexpr int HELD = S::kHeld, NL = S::kLoads;
     __shared__ __align__(16) char tile[S::kBytes];
-    __shared__ int64_t offs[2][TT];
-    __shared__ __align__(16) float kfac[kScaled ? TT : 4], vlog[kScaled ? TT : 4], vinv[kScaled ? TT : 4];
+    __shared__ int64_t offs_all[WT][2][TS];
+    __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
     __shared__ float red[2][WM * WT][32];
     __shared__ int odd;
-    char* const ldsk = tile;
-    char* const ldsv = tile + TT * S::kPitchK;
 
     const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = lane % 32, half = lane / 32;
     const int wm = wave % WM, wt = wave / WM;
+    const int tm = WM == 1 ? lane : tid;  // in the team
+    char* const tiles_lds = tile + wt * HELD * S::kTileBytes;
+    auto& offs = offs_all[wt];
     const int D = a.cache.dim, group = a.group, M = a.nodes * group, heads = a.cache.heads;
     const bool direct = a.blocks == 0;
     const int per_seq = heads * a.row_blocks;  // segments of a sequence
@@ -233,8 +244,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch + node * a.q_node + (h * group + g) * a.q_head;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            qf[r][s] = u32x4{0, 0, 0, 0};
-            if (live && s * 16 < D) qf[r][s] = (*reinterpret_cast<const u32x4*>(q + s * 16 + half * 8) ^ a.flip) & a.keep;
+            const bool in = live && s * 16 < D;
+            const u32x4 x = *reinterpret_cast<const u32x4*>(in ? q + s * 16 + half * 8 : static_cast<const uint16_t*>(a.q));
+            qf[r][s] = (x ^ a.flip) & (in ? a.keep : 0u);
         }
     }
 
@@ -248,35 +260,35 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
     }
 
-    // Tiles are numbered from 0 at `first`. lookup() finds the page of this
-    // thread's token (tid < TT) of a tile; a page outside the cache is not
-    // followed, its tokens read as zeros.
-    const int64_t headk = (int64_t)h * a.cache.head_stride;
+    // The team's tiles are numbered from 0 at `origin`, TT tokens apart.
+    // lookup() finds the page of this thread's token (tm < TS) of a tile; a
+    // page outside the cache is not followed, its tokens read as zeros.
+    const int origin = first + wt * TS;
+    const int64_t headk = (int64_t)h * a.cache.head_stride, heads_k = (int64_t)h * a.cache.scale_head_stride;
+    const int32_t* pages = a.table + b * a.table_stride;
+    auto page_of = [&](int t) { return (int)(((double)t + 0.5) * a.inv_places); };
     auto lookup = [&](int i) -> int {
-        const int t = first + i * TT + tid;
-        return tid < TT && t < last ? a.table[b * a.table_stride + t / a.cache.places] : -1;
+        const int t = origin + i * TT + tm;
+        return tm < TS && t < last ? pages[page_of(t)] : -1;
     };
     auto offset = [&](int i, int page, int64_t* scale) -> int64_t {
-        const int t = first + i * TT + tid, at = t % a.cache.places;
+        const int t = origin + i * TT + tm, at = t - page_of(t) * a.cache.places;
         *scale = -1;
         if (page < 0 || page >= a.cache.pages) return -1;
-        *scale = (int64_t)page * a.cache.scale_page_stride + (int64_t)at * a.cache.scale_place_stride + (int64_t)h * a.cache.scale_head_stride;
+        *scale = (int64_t)page * a.cache.scale_page_stride + (int64_t)at * a.cache.scale_place_stride + heads_k;
         return (int64_t)page * a.cache.page_stride + (int64_t)at * a.cache.place_stride + headk;
     };
-    u32x4 rk[S::kLoads], rv[S::kLoads];
+    u32x4 rk[NL], rv[NL];
     uint32_t there = 0;  // bit j: load j is of a token in the cache
     float sk = 0.f, sv = 1.f;
     auto fetch = [&](int i, int64_t scale) {
-        int64_t off[S::kLoads];
+        int64_t off[NL];
 #pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) {
-            const int e = j * S::kThreads + tid;
-            off[j] = offs[i % 2][min(e / S::kRowLoads, TT - 1)];
-        }
+        for (int j = 0; j < NL; ++j) off[j] = offs[i % 2][min((j * S::kTeam + tm) / S::kRowLoads, TS - 1)];
         there = 0;
 #pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) {
-            const int c = (j * S::kThreads + tid) % S::kRowLoads * S::kPerLoad;
+        for (int j = 0; j < NL; ++j) {
+            const int c = (j * S::kTeam + tm) % S::kRowLoads * S::kPerLoad;
             there |= (off[j] >= 0 && c < D ? 1u : 0u) << j;
             const int64_t at = ((off[j] >= 0 ? off[j] : 0) + (c < D ? c : 0)) * C::kBytes;
             rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.k) + at);
@@ -284,7 +296,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         }
         if constexpr (kScaled) {
             sk = 0.f, sv = 1.f;
-            if (tid < TT && scale >= 0) sk = a.cache.k_scales[scale], sv = a.cache.v_scales[scale];
+            if (tm < TS && scale >= 0) sk = a.cache.k_scales[scale], sv = a.cache.v_scales[scale];
         }
     };
     // Infinities and NaN in the values of nodes are left out of the products
@@ -301,17 +313,20 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         return v;
     };
     auto store = [&](int i) {
-        const bool nodes_in = first + (i + 1) * TT > len;
-        if (there != (1u << S::kLoads) - 1) {
+        char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
+        char* const ldsv = ldsk + TS * S::kPitchK;
+        const int base = origin + i * TT;
+        const bool nodes_in = base + TS > len;
+        if (there != (1u << NL) - 1) {
 #pragma unroll
-            for (int j = 0; j < S::kLoads; ++j)
+            for (int j = 0; j < NL; ++j)
                 if (!(there >> j & 1)) rk[j] = rv[j] = u32x4{0, 0, 0, 0};
         }
 #pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) {
-            const int e = j * S::kThreads + tid, t = e / S::kRowLoads, c = e % S::kRowLoads;
-            if (S::kLoads * S::kThreads != TT * S::kRowLoads && e >= TT * S::kRowLoads) break;
-            const bool node = nodes_in && first + i * TT + t >= len;
+        for (int j = 0; j < NL; ++j) {
+            const int e = j * S::kTeam + tm, t = e / S::kRowLoads, c = e % S::kRowLoads;
+            if (NL * S::kTeam != TS * S::kRowLoads && e >= TS * S::kRowLoads) break;
+            const bool node = nodes_in && base + t >= len;
             u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * (S::kPerLoad * 2));
             u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
             if constexpr (kScaled) {
@@ -330,44 +345,71 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             }
         }
         if constexpr (kScaled) {
-            if (tid < TT) {
+            if (tm < TS) {
                 // A scale of 0 (a row of zeros) is taken as 2^-100.
                 const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
-                kfac[tid] = sk * a.scale;
-                vlog[tid] = __builtin_amdgcn_logf(c);
+                auto& f = factors[wt][i % HELD];
+                f[0][tm] = sk * a.scale;
+                f[1][tm] = __builtin_amdgcn_logf(c);
                 // 1 where the scale is no number (the exponent says so), so
                 // that a row that does not see the token adds 0 times it.
-                vinv[tid] = c < __builtin_inff() ? 1.f / c : 1.f;
+                f[2][tm] = c < __builtin_inff() ? 1.f / c : 1.f;
             }
         }
     };
+    auto team_sync = [&]() {
+        if constexpr (WM > 1) __syncthreads();
+        else wave_lds_fence();
+    };
 
-    const int tiles = rows_in && last > first ? (last - first + TT - 1) / TT : 0;
-    int64_t scale0 = -1, scale1 = -1;
+    const int tiles = rows_in && last > origin ? (last - origin + TT - 1) / TT : 0;
+    int64_t scale_next = -1;  // of the tile after the one whose loads were issued last
     __syncthreads();  // the segment before is done with the LDS
     if (tid == 0) odd = 0;
+    __syncthreads();
     if (tiles > 0) {
-        const int64_t o0 = offset(0, lookup(0), &scale0), o1 = offset(1, lookup(1), &scale1);
-        if (tid < TT) offs[0][tid] = o0, offs[1][tid] = o1;
-        __syncthreads();
+        int64_t scale0;
+        const int p0 = lookup(0), p1 = lookup(1), p2 = HELD == 2 ? lookup(2) : -1;
+        const int64_t o0 = offset(0, p0, &scale0), o1 = offset(1, p1, &scale_next);
+        if (tm < TS) offs[0][tm] = o0, offs[1][tm] = o1;
+        team_sync();
         fetch(0, scale0);
+        if constexpr (HELD == 2) {
+            __syncthreads();
+            int64_t scale2;
+            const int64_t o2 = offset(2, p2, &scale2);
+            if (tm < TS) offs[0][tm] = o2;
+            store(0);
+            if (1 < tiles) fetch(1, scale_next);
+            scale_next = scale2;
+            __syncthreads();
+        }
     }
     for (int i = 0; i < tiles; ++i) {
-        if (i > 0) __syncthreads();  // the tile before has been read
-        const int base = first + i * TT;
-        store(i);
-        __syncthreads();
-        const int page = lookup(i + 2);
-        if (i + 1 < tiles) fetch(i + 1, scale1);
+        const int base = origin + i * TT;
+        // Where a tile is written and the next is asked for: with one tile in
+        // the LDS before the products, with two beside them.
+        constexpr int AHEAD = HELD;  // of the tile asked for here
+        const int page = lookup(i + AHEAD + 1);
+        if constexpr (HELD == 1) {
+            wave_lds_fence();
+            store(i);
+            wave_lds_fence();
+            if (i + 1 < tiles) fetch(i + 1, scale_next);
+        }
+        const char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
+        const char* const ldsv = ldsk + TS * S::kPitchK;
+        auto& kfac = factors[wt][i % HELD][0];
+        auto& vlog = factors[wt][i % HELD][1];
+        auto& vinv = factors[wt][i % HELD][2];
 
         // Scores of this wave's tokens.
-        const int t0 = wt * TS;
         f32x16 sc[RT][SUB];
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
 #pragma unroll
             for (int r = 0; r < RT; ++r) sc[r][s] = f32x16{};
-            const char* kp = ldsk + (t0 + s * 32 + n) * S::kPitchK + half * 16;
+            const char* kp = ldsk + (s * 32 + n) * S::kPitchK + half * 16;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const u32x4 kf = *reinterpret_cast<const u32x4*>(kp + k * 32);
@@ -375,12 +417,16 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                 for (int r = 0; r < RT; ++r) sc[r][s] = Mma<T>::dot(kf, qf[r][k], sc[r][s]);
             }
         }
+        if constexpr (HELD == 2) {
+            if (i + 1 < tiles) store(i + 1);
+            if (i + 2 < tiles) fetch(i + 2, scale_next);
+        }
         if constexpr (kScaled) {
 #pragma unroll
             for (int s = 0; s < SUB; ++s)
 #pragma unroll
                 for (int x = 0; x < 16; x += 4) {
-                    const int t = t0 + s * 32 + 2 * x + 4 * half;
+                    const int t = s * 32 + 2 * x + 4 * half;
                     const f32x4 kf = *reinterpret_cast<const f32x4*>(kfac + t), vl = *reinterpret_cast<const f32x4*>(vlog + t);
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
@@ -388,11 +434,11 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                         for (int y = 0; y < 4; ++y) sc[r][s][x + y] = sc[r][s][x + y] * kf[y] + vl[y];
                 }
         }
-        if (base + t0 + TS > min(len, total)) {
+        if (base + TS > min(len, total)) {
             // Bit t of a word: whether this lane's row sees token t of 32.
 #pragma unroll
             for (int s = 0; s < SUB; ++s) {
-                const int from = base + t0 + s * 32, j = from - len, left = total - from;
+                const int from = base + s * 32, j = from - len, left = total - from;
                 const uint32_t there = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
@@ -407,11 +453,12 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         uint32_t pf[RT][SUB][8];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            float top = -__builtin_inff();
+            float top4[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
 #pragma unroll
             for (int s = 0; s < SUB; ++s)
 #pragma unroll
-                for (int x = 0; x < 16; ++x) top = fmaxf(top, sc[r][s][x]);
+                for (int x = 0; x < 16; ++x) top4[x % 4] = fmaxf(top4[x % 4], sc[r][s][x]);
+            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             top = fmaxf(top, other_half(top));
             if constexpr (!kScaled) top *= a.scale;
             if (__any(top > m[r] + kLazy)) {
@@ -428,7 +475,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
                 for (int x = 0; x < 16; x += 4) {
                     f32x4 vi;
-                    if constexpr (kScaled) vi = *reinterpret_cast<const f32x4*>(vinv + t0 + s * 32 + 2 * x + 4 * half);
+                    if constexpr (kScaled) vi = *reinterpret_cast<const f32x4*>(vinv + s * 32 + 2 * x + 4 * half);
                     float w[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
@@ -442,7 +489,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         }
         // 8 tokens of a column: 16 lanes read 4 tokens times 16 columns; lane % 16 picks a column.
         auto values = [&](int s, int k, int d) -> u32x4 {
-            const char* vp = ldsv + (t0 + s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
+            const char* vp = ldsv + (s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
                              (lane / 16 % 2) * 32 + (lane % 4) * 8 + d * 64;
             using L = __attribute__((address_space(3))) s16x4*;
             const u32x2 v0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)vp));
@@ -463,9 +510,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                     for (int r = 0; r < RT; ++r) o[r][d] = Mma<VT>::dot(v, weights(r, s, k), o[r][d]);
                 }
         int64_t scale2;
-        const int64_t next = offset(i + 2, page, &scale2);
-        if (tid < TT) offs[i % 2][tid] = next;
-        scale1 = scale2;
+        const int64_t next = offset(i + AHEAD + 1, page, &scale2);
+        if (tm < TS) offs[(i + AHEAD + 1) % 2][tm] = next;
+        scale_next = scale2;
+        if constexpr (HELD == 2) __syncthreads();
     }
 
     // Where a row's sums go: to the output, or to the partials of this chunk.
