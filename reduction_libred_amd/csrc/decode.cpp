@@ -269,6 +269,11 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     if (tokens > 0 && a->table == nullptr) return RED_ERR_INVALID_ARG;
     // (batch, node) pairs and heads: rows of q on 16-byte boundaries, rows of
     // out as well and apart from each other.
+    // Rows are found by 32-bit numbers of 16 bytes from the head's first.
+    const int64_t es = (int64_t)type_bytes(c.type), unit = 16 / es;
+    const int64_t rows_span = c.pages == 0 ? 0 : paged_span(c, c.page_stride, 0, c.place_stride, D) / unit;
+    if (rows_span > 0xFFFFFFFFll || c.scale_page_stride > 0xFFFFFFFFll || c.scale_place_stride > 0xFFFFFFFFll)
+        return RED_ERR_INVALID_ARG;
     const int64_t lim = (int64_t)1 << 40, d = (int64_t)D;
     const int64_t qb = B > 1 ? a->q_batch_stride : 0, qn = N > 1 ? a->q_node_stride : 0, qh = H > 1 ? a->q_head_stride : 0;
     const int64_t bs = B > 1 ? a->out_batch_stride : 0, ns = N > 1 ? a->out_node_stride : 0, hs = H > 1 ? a->out_head_stride : 0;
@@ -297,6 +302,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     k.keep = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
     k.scale = (a->scale == 0.f ? 1.f : a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
     k.flip = a->scale < 0.f ? 0x80008000u : 0u;
+    k.page16 = (uint32_t)(c.pages > 1 ? c.page_stride / unit : 0), k.place16 = (uint32_t)(c.places > 1 ? c.place_stride / unit : 0);
     k.inv_places = 1.0 / (double)c.places;
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M);
@@ -305,7 +311,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     // the card holds at once (two of 4 waves a compute unit), or one a tile.
     const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
     const size_t segments = B * c.heads * (size_t)k.row_blocks;
-    if (segments > 0x7fffffff || (int64_t)(B * tiles) > 0x7fffffff) return RED_ERR_INVALID_ARG;
+    if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;
     if (tiles > 1) {
         const size_t hold = (size_t)cus * 2;
         const size_t blocks = segments * tiles < hold ? segments * tiles : hold;

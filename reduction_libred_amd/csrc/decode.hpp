@@ -86,6 +86,7 @@ struct TreeAttention {
     int batch, nodes, group, max_tokens, row_blocks;
     int blocks;  // 0: one block a segment, of at most one tile, that writes the output
     float scale;  // magnitude, times log2(e)
+    uint32_t page16, place16;  // strides of the cache's pages and places in units of 16 bytes
     double inv_places;  // 1 / places: (t + 0.5) * that, cut, is the page of token t below 2^30 exactly
     unsigned int flip;  // 0x80008000 where the scale is negative: the sign of q
     unsigned int keep;  // 0 where the scale is 0 (q is then, and scale is that of 1)

@@ -115,6 +115,16 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
+// The kernel's arguments, as memory that the compiler has not seen yet: what is
+// needed at the two ends of a segment is loaded there and holds no registers in
+// between.
+typedef const __attribute__((address_space(4))) TreeAttention* Arguments;
+__device__ __forceinline__ Arguments arguments_again() {
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return (Arguments)p;
+}
+
 constexpr float kLazy = 8.f;  // how far (in powers of 2) scores may pass M before M follows
 
 template <class C, int DP, int RT, int WM, int WT, int TS>
@@ -153,11 +163,16 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     static_assert(RT == 1 || WT == 1, "waves that share rows join one row tile");
     constexpr int HELD = S::kHeld, NL = S::kLoads;
     __shared__ __align__(16) char tile[S::kBytes];
-    __shared__ int64_t offs_all[WT][2][TS];
+    __shared__ uint32_t offs_all[WT][2][TS];  // where the rows of a tile's tokens start, in 16 bytes
+    __shared__ uint64_t held[WT][4];           // which of them are in the cache
     __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
     __shared__ float red[2][WM * WT][32];
     __shared__ int odd;
 
+    // One argument of every 64-byte line, so that all lines are asked for at
+    // once: fetched one after the other as they are met, the arguments alone
+    // take several microseconds of a small call.
+    asm volatile("" ::"s"(a.q), "s"(a.q_head), "s"(a.cache.k), "s"(a.cache.scale_head_stride), "s"(a.lens), "s"(a.blocks), "s"(a.plan));
     const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = lane % 32, half = lane / 32;
     const int wm = wave % WM, wt = wave / WM;
     const int tm = WM == 1 ? lane : tid;  // in the team
@@ -167,136 +182,129 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     const bool direct = a.blocks == 0;
     const int per_seq = heads * a.row_blocks;  // segments of a sequence
 
-    // This block's share of the tiles: [now, end) of all segments' tiles.
+    // This block's share of the tiles: [now, end) of all segments' tiles
+    // (below 2^31, which the entry point checks).
     int b = 0, seg = 0, skip = 0;  // sequence, segment in it, tiles of that segment that are another's
-    int64_t now = 0, end = 1;
+    int now = 0, end = 1;
+    int len, count;  // of sequence b
     // Blocks are dealt to the XCDs in turn; each XCD takes a run of shares, so
     // that the blocks of rows of one head read its tokens through one L2.
     const int share = direct || gridDim.x % kXcds ? blockIdx.x : blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    auto load_sequence = [&](int q, int* q_len, int* q_count) {
+        const int c = a.count ? min(max(a.count[q], 0), a.nodes) : a.nodes;
+        *q_len = max(a.lens[q], 0);
+        *q_count = c;
+    };
+    auto tokens_of = [&](int q_len, int q_count) { return (int)min((int64_t)q_len + q_count, (int64_t)a.max_tokens); };
     if (direct) {
         b = blockIdx.x / per_seq, seg = blockIdx.x % per_seq;
+        load_sequence(b, &len, &count);
     } else {
-        auto tiles_of = [&](int q) {
-            int nodes;
-            const int t = q < a.batch ? sequence_tokens(a, q, &nodes) : 0;
-            return q < a.batch && nodes > 0 ? (t + TT - 1) / TT : 0;
+        // 64 sequences at a time, one a lane; `upto` is the running sum of
+        // their tiles.
+        int at_len = 0, at_count = 0, own = 0, upto = 0;
+        auto group_of = [&](int q) {
+            at_len = at_count = own = 0;
+            if (q + lane < a.batch) {
+                load_sequence(q + lane, &at_len, &at_count);
+                own = at_count > 0 ? (tokens_of(at_len, at_count) + TT - 1) / TT : 0;
+            }
+            upto = own;
+            upto += dpp_move<0x111, 0xF>(0, upto);  // shifted by 1, 2, 4 and 8 in rows of 16
+            upto += dpp_move<0x112, 0xF>(0, upto);
+            upto += dpp_move<0x114, 0xF>(0, upto);
+            upto += dpp_move<0x118, 0xF>(0, upto);
+            upto += dpp_move<0x142, 0xA>(0, upto);  // rows 0 and 2 into 1 and 3
+            upto += dpp_move<0x143, 0xC>(0, upto);  // the first half into the second
         };
-        int64_t all = 0;
-        for (int q = 0; q < a.batch; q += kWave) all += group_combine<kWave>(tiles_of(q + lane), [](int x, int y) { return x + y; });
+        int all = 0;
+        for (int q = 0; q < a.batch; q += kWave) {
+            group_of(q);
+            all += read_lane(upto, kWave - 1);
+        }
         all *= per_seq;
-        const int64_t per = (all + gridDim.x - 1) / gridDim.x;
-        now = share * per, end = min(now + per, all);
+        const int per = (all + (int)gridDim.x - 1) / (int)gridDim.x;
         const bool planner = share == 0 && wave == 0;
+        now = (int)min(share * (int64_t)per, (int64_t)all), end = min(now + per, all);
         if (now >= end && !planner) return;
         // The sequence that holds tile `now`.
-        const int64_t want = now / per_seq;  // as tiles of one segment of each sequence
-        int64_t before = 0;
+        const int want = now / per_seq;  // as tiles of one segment of each sequence
+        int before = 0;
         bool found = false;
         for (int q = 0; q < a.batch && (planner || !found); q += kWave) {
-            int upto = tiles_of(q + lane);
-            const int own = upto;
-            for (int o = 1; o < kWave; o <<= 1) {
-                const int x = __shfl_up(upto, o);
-                if (lane >= o) upto += x;
-            }
-            if (planner && q + lane < a.batch) a.plan[q + lane] = (int)(before + upto - own);
+            if (a.batch > kWave) group_of(q);
+            if (planner && q + lane < a.batch) a.plan[q + lane] = before + upto - own;
             const uint64_t past = __ballot(before + upto > want);
             if (past && !found) {
                 found = true;
                 const int at = __ffsll((unsigned long long)past) - 1;
                 b = q + at;
-                const int64_t rest = now - (before + __shfl(upto - own, at)) * per_seq;
-                const int each = __shfl(own, at);
-                seg = (int)(rest / each);
-                skip = (int)(rest - (int64_t)seg * each);
+                len = read_lane(at_len, at), count = read_lane(at_count, at);
+                const int rest = now - (before + read_lane(upto - own, at)) * per_seq, each = read_lane(own, at);
+                seg = rest / each;
+                skip = rest - seg * each;
             }
-            before += __shfl(upto, kWave - 1);
+            before += read_lane(upto, kWave - 1);
         }
-        if (planner && lane == 0) a.plan[a.batch] = (int)before, a.plan[a.batch + 1] = (int)per;
-        b = uniform(b), seg = uniform(seg), skip = uniform(skip);
-        now = uniform64(now), end = uniform64(end);
+        if (planner && lane == 0) a.plan[a.batch] = before, a.plan[a.batch + 1] = per;
+        b = uniform(b), seg = uniform(seg), skip = uniform(skip), now = uniform(now), end = uniform(end);
     }
 
     while (now < end) {
-    int nodes_in_b;
-    const int total = uniform(sequence_tokens(a, b, &nodes_in_b)), len = uniform(max(a.lens[b], 0)), count = uniform(nodes_in_b);
-    const int h = seg / a.row_blocks, rb = seg - h * a.row_blocks;
+    const Arguments A = arguments_again();
+    len = uniform(len), count = uniform(count);
+    const int total = tokens_of(len, count);
+    const int h = seg / A->row_blocks, rb = seg - h * A->row_blocks;
     const int64_t slot = direct ? 0 : share + (int64_t)b * per_seq + seg;
     const int seg_tiles = count > 0 ? (total + TT - 1) / TT : 0;
     // No rows in this block of rows (the nodes it would hold do not exist).
     const bool rows_in = rb * S::kRows < count * group;
-    const int mine = direct ? seg_tiles : (int)min((int64_t)(seg_tiles - skip), end - now);
+    const int mine = direct ? seg_tiles : min(seg_tiles - skip, end - now);
     const int first = skip * TT, last = min(total, first + mine * TT);
     const int row0 = (rb * WM + wm) * 32 * RT;
     if (rows_in || direct) {
 
-    // This lane's rows.
-    int row[RT];
-    uint64_t seen[RT];  // the nodes it sees
-    u32x4 qf[RT][KS];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        row[r] = row0 + r * 32 + n;
-        const int node = row[r] / group, g = row[r] - node * group;
-        const bool live = row[r] < M && node < count;
-        const uint64_t upto = count >= 64 ? ~0ull : (1ull << count) - 1;
-        seen[r] = !live ? 0 : (a.mask ? (uint64_t)a.mask[(int64_t)b * a.nodes + node] : ~0ull >> (63 - node)) & upto;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + b * a.q_batch + node * a.q_node + (h * group + g) * a.q_head;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const bool in = live && s * 16 < D;
-            const u32x4 x = *reinterpret_cast<const u32x4*>(in ? q + s * 16 + half * 8 : static_cast<const uint16_t*>(a.q));
-            qf[r][s] = (x ^ a.flip) & (in ? a.keep : 0u);
-        }
-    }
-
-    f32x16 o[RT][DT];
-    float m[RT], l[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        m[r] = -__builtin_inff();
-        l[r] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
-    }
-
-    // The team's tiles are numbered from 0 at `origin`, TT tokens apart.
-    // lookup() finds the page of this thread's token (tm < TS) of a tile; a
-    // page outside the cache is not followed, its tokens read as zeros.
+    // The team's tiles are numbered from 0 at `origin`, TT tokens apart. A tile
+    // goes through three steps: lookup() asks for the page of this thread's
+    // token (tm < TS); settle() notes where the token's rows start; fetch()
+    // asks for the rows. A page outside the cache is not followed: its tokens
+    // read as zeros, as those from `last` on do.
     const int origin = first + wt * TS;
-    const int64_t headk = (int64_t)h * a.cache.head_stride, heads_k = (int64_t)h * a.cache.scale_head_stride;
-    const int32_t* pages = a.table + b * a.table_stride;
-    auto page_of = [&](int t) { return (int)(((double)t + 0.5) * a.inv_places); };
+    const int32_t* pages = A->table + b * A->table_stride;
+    auto page_of = [&](int t) { return (int)(((double)t + 0.5) * A->inv_places); };
     auto lookup = [&](int i) -> int {
         const int t = origin + i * TT + tm;
         return tm < TS && t < last ? pages[page_of(t)] : -1;
     };
-    auto offset = [&](int i, int page, int64_t* scale) -> int64_t {
-        const int t = origin + i * TT + tm, at = t - page_of(t) * a.cache.places;
-        *scale = -1;
-        if (page < 0 || page >= a.cache.pages) return -1;
-        *scale = (int64_t)page * a.cache.scale_page_stride + (int64_t)at * a.cache.scale_place_stride + heads_k;
-        return (int64_t)page * a.cache.page_stride + (int64_t)at * a.cache.place_stride + headk;
-    };
-    u32x4 rk[NL], rv[NL];
-    uint32_t there = 0;  // bit j: load j is of a token in the cache
-    float sk = 0.f, sv = 1.f;
-    auto fetch = [&](int i, int64_t scale) {
-        int64_t off[NL];
-#pragma unroll
-        for (int j = 0; j < NL; ++j) off[j] = offs[i % 2][min((j * S::kTeam + tm) / S::kRowLoads, TS - 1)];
-        there = 0;
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int c = (j * S::kTeam + tm) % S::kRowLoads * S::kPerLoad;
-            there |= (off[j] >= 0 && c < D ? 1u : 0u) << j;
-            const int64_t at = ((off[j] >= 0 ? off[j] : 0) + (c < D ? c : 0)) * C::kBytes;
-            rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.k) + at);
-            rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.cache.v) + at);
+    auto settle = [&](int i, int page) -> int64_t {
+        const int t = origin + i * TT + tm, at = t - page_of(t) * A->cache.places;
+        const bool in = page >= 0 && page < A->cache.pages;
+        const uint64_t all = __ballot(in);
+        if (tm < TS) {
+            offs[i % 2][tm] = in ? (uint32_t)page * A->page16 + (uint32_t)at * A->place16 : 0;
+            if (tm == 0) held[wt][i % 4] = TS == 64 ? all : all & 0xFFFFFFFFu;
         }
+        return in ? (int64_t)((uint64_t)(uint32_t)page * (uint32_t)A->cache.scale_page_stride + (uint64_t)(uint32_t)at * (uint32_t)A->cache.scale_place_stride) : -1;
+    };
+    constexpr uint64_t kAllIn = TS == 64 ? ~0ull : 0xFFFFFFFFull;
+    const char* const kh = static_cast<const char*>(A->cache.k) + h * A->cache.head_stride * C::kBytes;
+    const char* const vh = static_cast<const char*>(A->cache.v) + h * A->cache.head_stride * C::kBytes;
+    const float* const ksh = A->cache.k_scales + h * A->cache.scale_head_stride;
+    const float* const vsh = A->cache.v_scales + h * A->cache.scale_head_stride;
+    u32x4 rk[NL], rv[NL];
+    float sk = 0.f, sv = 1.f;
+    auto row_at = [&](int j) { return min((j * S::kTeam + tm) / S::kRowLoads, TS - 1); };
+    auto column_at = [&](int j) { return (j * S::kTeam + tm) % S::kRowLoads * S::kPerLoad; };
+    auto fetch_one = [&](int j, uint32_t off) {
+        const int c = column_at(j);
+        const uint64_t at = (uint64_t)off * 16 + (c < D ? c : 0) * C::kBytes;
+        rk[j] = *reinterpret_cast<const u32x4*>(kh + at);
+        rv[j] = *reinterpret_cast<const u32x4*>(vh + at);
+    };
+    auto fetch_scales = [&](int64_t scale) {
         if constexpr (kScaled) {
             sk = 0.f, sv = 1.f;
-            if (tm < TS && scale >= 0) sk = a.cache.k_scales[scale], sv = a.cache.v_scales[scale];
+            if (tm < TS && scale >= 0) sk = ksh[scale], sv = vsh[scale];
         }
     };
     // Infinities and NaN in the values of nodes are left out of the products
@@ -312,48 +320,62 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         }
         return v;
     };
+    auto fetch = [&](int i, int64_t scale) {
+        uint32_t off[NL];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) off[j] = offs[i % 2][row_at(j)];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) fetch_one(j, off[j]);
+        fetch_scales(scale);
+    };
     auto store = [&](int i) {
         char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
         char* const ldsv = ldsk + TS * S::kPitchK;
         const int base = origin + i * TT;
-        const bool nodes_in = base + TS > len;
-        if (there != (1u << NL) - 1) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j)
-                if (!(there >> j & 1)) rk[j] = rv[j] = u32x4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int e = j * S::kTeam + tm, t = e / S::kRowLoads, c = e % S::kRowLoads;
-            if (NL * S::kTeam != TS * S::kRowLoads && e >= TS * S::kRowLoads) break;
-            const bool node = nodes_in && base + t >= len;
-            u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * (S::kPerLoad * 2));
-            u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
-            if constexpr (kScaled) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const u32x2 k0 = C::template widen4<T>(rk[j][2 * p]), k1 = C::template widen4<T>(rk[j][2 * p + 1]);
-                    const u32x2 v0 = C::template widen4<VT>(rv[j][2 * p]), v1 = C::template widen4<VT>(rv[j][2 * p + 1]);
-                    u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
-                    if (node) v = clean(v);
-                    dk[p] = u32x4{k0[0], k0[1], k1[0], k1[1]};
-                    dv[p] = v;
-                }
-            } else {
-                *dk = rk[j];
-                *dv = node ? clean(rv[j]) : rv[j];
-            }
-        }
+        const uint64_t in = held[wt][i % 4];
+        const bool part = uniform((int)(in != kAllIn)) || DP != D;
         if constexpr (kScaled) {
             if (tm < TS) {
                 // A scale of 0 (a row of zeros) is taken as 2^-100.
                 const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
                 auto& f = factors[wt][i % HELD];
-                f[0][tm] = sk * a.scale;
+                f[0][tm] = sk * A->scale;
                 f[1][tm] = __builtin_amdgcn_logf(c);
                 // 1 where the scale is no number (the exponent says so), so
                 // that a row that does not see the token adds 0 times it.
                 f[2][tm] = c < __builtin_inff() ? 1.f / c : 1.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int e = j * S::kTeam + tm, t = e / S::kRowLoads, c = e % S::kRowLoads;
+            __builtin_amdgcn_sched_barrier(0);  // one row's conversion at a time: registers
+            if (NL * S::kTeam == TS * S::kRowLoads || e < TS * S::kRowLoads) {
+                if (part && !((in >> t & 1) && c * S::kPerLoad < D)) rk[j] = rv[j] = u32x4{0, 0, 0, 0};
+                u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * (S::kPerLoad * 2));
+                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
+                if constexpr (kScaled) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const u32x2 k0 = C::template widen4<T>(rk[j][2 * p]), k1 = C::template widen4<T>(rk[j][2 * p + 1]);
+                        const u32x2 v0 = C::template widen4<VT>(rv[j][2 * p]), v1 = C::template widen4<VT>(rv[j][2 * p + 1]);
+                        dk[p] = u32x4{k0[0], k0[1], k1[0], k1[1]};
+                        dv[p] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+                    }
+                } else {
+                    *dk = rk[j];
+                    *dv = rv[j];
+                }
+            }
+        }
+        if (!std::is_same_v<C, CachedI8> && base + TS > len) {  // what this thread wrote of nodes
+#pragma unroll 1
+            for (int j = 0; j < NL; ++j) {
+                const int e = j * S::kTeam + tm, t = e / S::kRowLoads, c = e % S::kRowLoads;
+                if (e >= TS * S::kRowLoads || base + t < len) continue;
+                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
+#pragma unroll 1
+                for (int p = 0; p < S::kPerLoad / 8; ++p) dv[p] = clean(dv[p]);
             }
         }
     };
@@ -363,34 +385,61 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     };
 
     const int tiles = rows_in && last > origin ? (last - origin + TT - 1) / TT : 0;
-    int64_t scale_next = -1;  // of the tile after the one whose loads were issued last
+    int64_t scale_next = -1;  // of the tile to be asked for next
+    const int p0 = lookup(0), p1 = lookup(1), p2 = HELD == 2 ? lookup(2) : -1;
+    // This lane's rows, looked at while the pages are on their way.
+    int row[RT];
+    uint64_t seen[RT];  // the nodes it sees
+    u32x4 qf[RT][KS];
+    {
+        const uint64_t upto = count >= 64 ? ~0ull : (1ull << count) - 1;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            row[r] = row0 + r * 32 + n;
+            const int node = row[r] / group, g = row[r] - node * group;
+            const bool live = row[r] < M && node < count;
+            seen[r] = ~0ull >> (63 - min(node, 63));
+            if (A->mask) seen[r] = (uint64_t)A->mask[(int64_t)b * A->nodes + (live ? node : 0)];
+            seen[r] = live ? seen[r] & upto : 0;
+            const uint16_t* q = static_cast<const uint16_t*>(A->q);
+            if (live) q += b * A->q_batch + node * A->q_node + (h * group + g) * A->q_head;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                qf[r][s] = *reinterpret_cast<const u32x4*>(q + (s * 16 < D ? s * 16 + half * 8 : 0));
+                qf[r][s] = (qf[r][s] ^ A->flip) & (live && s * 16 < D ? A->keep : 0u);
+            }
+        }
+    }
+
     __syncthreads();  // the segment before is done with the LDS
     if (tid == 0) odd = 0;
+    const int64_t scale0 = settle(0, p0);
+    scale_next = settle(1, p1);
     __syncthreads();
-    if (tiles > 0) {
-        int64_t scale0;
-        const int p0 = lookup(0), p1 = lookup(1), p2 = HELD == 2 ? lookup(2) : -1;
-        const int64_t o0 = offset(0, p0, &scale0), o1 = offset(1, p1, &scale_next);
-        if (tm < TS) offs[0][tm] = o0, offs[1][tm] = o1;
-        team_sync();
-        fetch(0, scale0);
-        if constexpr (HELD == 2) {
-            __syncthreads();
-            int64_t scale2;
-            const int64_t o2 = offset(2, p2, &scale2);
-            if (tm < TS) offs[0][tm] = o2;
-            store(0);
-            if (1 < tiles) fetch(1, scale_next);
-            scale_next = scale2;
-            __syncthreads();
-        }
+    if (tiles > 0) fetch(0, scale0);
+    f32x16 o[RT][DT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        m[r] = -__builtin_inff();
+        l[r] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
+    }
+
+    if constexpr (HELD == 2) {
+        __syncthreads();
+        const int64_t scale2 = settle(2, p2);
+        if (tiles > 0) store(0);
+        if (tiles > 1) fetch(1, scale_next);
+        scale_next = scale2;
+        __syncthreads();
     }
     for (int i = 0; i < tiles; ++i) {
         const int base = origin + i * TT;
-        // Where a tile is written and the next is asked for: with one tile in
-        // the LDS before the products, with two beside them.
-        constexpr int AHEAD = HELD;  // of the tile asked for here
-        const int page = lookup(i + AHEAD + 1);
+        // With one tile in the LDS it is written before its products, with
+        // two the next is written beside them.
+        const int page = lookup(i + HELD + 1);
         if constexpr (HELD == 1) {
             wave_lds_fence();
             store(i);
@@ -460,7 +509,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                 for (int x = 0; x < 16; ++x) top4[x % 4] = fmaxf(top4[x % 4], sc[r][s][x]);
             float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             top = fmaxf(top, other_half(top));
-            if constexpr (!kScaled) top *= a.scale;
+            if constexpr (!kScaled) top *= A->scale;
             if (__any(top > m[r] + kLazy)) {
                 const float to = top > m[r] + kLazy ? top : m[r];
                 const float f = to == m[r] ? 1.f : __builtin_amdgcn_exp2f(m[r] - to);
@@ -479,7 +528,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
                     float w[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        w[y] = __builtin_amdgcn_exp2f(kScaled ? sc[r][s][x + y] - ms : sc[r][s][x + y] * a.scale - ms);
+                        w[y] = __builtin_amdgcn_exp2f(kScaled ? sc[r][s][x + y] - ms : sc[r][s][x + y] * A->scale - ms);
                         l[r] += kScaled ? w[y] * vi[y] : w[y];
                     }
                     pf[r][s][x / 2] = Mma<VT>::pack(w[0], w[1]);
@@ -509,27 +558,25 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
                     for (int r = 0; r < RT; ++r) o[r][d] = Mma<VT>::dot(v, weights(r, s, k), o[r][d]);
                 }
-        int64_t scale2;
-        const int64_t next = offset(i + AHEAD + 1, page, &scale2);
-        if (tm < TS) offs[(i + AHEAD + 1) % 2][tm] = next;
-        scale_next = scale2;
-        if constexpr (HELD == 2) __syncthreads();
+        scale_next = settle(i + HELD + 1, page);
+        team_sync();
     }
 
+    const Arguments E = arguments_again();
     // Where a row's sums go: to the output, or to the partials of this chunk.
     const int64_t prow0 = slot * S::kRows - rb * S::kRows;
     auto out_of = [&](int rw) {
         const int node = rw / group, g = rw - node * group;
-        return static_cast<uint16_t*>(a.out) + b * a.out_batch + node * a.out_node + (h * group + g) * a.out_head;
+        return static_cast<uint16_t*>(E->out) + b * E->out_batch + node * E->out_node + (h * group + g) * E->out_head;
     };
     auto put_stats = [&](int rw, float mm, float ll) {
         if (direct) {
             const int node = rw / group, g = rw - node * group;
             if (node >= count) ll = 0.f;
-            a.lse[((int64_t)b * a.nodes + node) * (heads * group) + h * group + g] =
+            E->lse[((int64_t)b * E->nodes + node) * (heads * group) + h * group + g] =
                 ll > 0.f || ll != ll ? (mm + __builtin_amdgcn_logf(ll)) * 0.69314718055994531f : -__builtin_inff();
         } else {
-            a.part_ml[prow0 + rw] = make_float2(mm, ll);
+            E->part_ml[prow0 + rw] = make_float2(mm, ll);
         }
     };
     // The infinities and NaN in columns c .. c + 3 of the nodes of this chunk
@@ -538,19 +585,19 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         const int node = rw / group;
         if (node >= count) return v;
-        const uint64_t word = a.mask ? (uint64_t)a.mask[(int64_t)b * a.nodes + node] : ~0ull >> (63 - node);
+        const uint64_t word = E->mask ? (uint64_t)E->mask[(int64_t)b * E->nodes + node] : ~0ull >> (63 - node);
 #pragma unroll 1
         for (int t = max(first, len); t < last; ++t) {
-            const int page = a.table[b * a.table_stride + t / a.cache.places];
-            if (!(word >> (t - len) & 1) || page < 0 || page >= a.cache.pages) continue;
-            const int64_t at = (int64_t)page * a.cache.page_stride + (int64_t)(t % a.cache.places) * a.cache.place_stride + headk + c;
+            const int page = E->table[b * E->table_stride + t / E->cache.places];
+            if (!(word >> (t - len) & 1) || page < 0 || page >= E->cache.pages) continue;
+            const int64_t at = (int64_t)page * E->cache.page_stride + (int64_t)(t % E->cache.places) * E->cache.place_stride + h * E->cache.head_stride + c;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 float f;
                 if constexpr (kScaled)
-                    f = F16::widen((uint16_t)C::template widen4<F16>(static_cast<const uint8_t*>(a.cache.v)[at + y])[0]);
+                    f = F16::widen((uint16_t)C::template widen4<F16>(static_cast<const uint8_t*>(E->cache.v)[at + y])[0]);
                 else
-                    f = T::widen(static_cast<const uint16_t*>(a.cache.v)[at + y]);
+                    f = T::widen(static_cast<const uint16_t*>(E->cache.v)[at + y]);
                 if (!(__builtin_fabsf(f) < __builtin_inff())) v[y] += f;
             }
         }
@@ -563,7 +610,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             if (ll == 0.f || rw >= count * group) w = u32x2{0, 0};
             *reinterpret_cast<u32x2*>(out_of(rw) + c) = w;
         } else {
-            *reinterpret_cast<f32x4*>(a.part_o + (prow0 + rw) * D + c) = v;
+            *reinterpret_cast<f32x4*>(E->part_o + (prow0 + rw) * D + c) = v;
         }
     };
     if constexpr (WT == 1) {
@@ -621,7 +668,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             for (int y = 0; y < 4; ++y) {
                 if (v[y] == 0.f) continue;
                 if (direct) out_of(rw)[c + y] = T::narrow(v[y]);
-                else a.part_o[(prow0 + rw) * D + c + y] = v[y];
+                else E->part_o[(prow0 + rw) * D + c + y] = v[y];
             }
         }
     }
@@ -629,15 +676,13 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     now += direct ? 1 : mine;
     skip = 0;
     if (now < end) {  // the next segment that has tiles
-        int nodes = count;
-        int t = total;
         do {
             if (++seg == per_seq) {
                 seg = 0, ++b;
-                t = uniform(sequence_tokens(a, b, &nodes));
-                nodes = uniform(nodes);
+                load_sequence(b, &len, &count);
+                len = uniform(len), count = uniform(count);
             }
-        } while (t == 0 || nodes == 0);
+        } while (count == 0 || tokens_of(len, count) == 0);
     }
     }
 }
