@@ -97,16 +97,18 @@ struct TreeAttention {
     int* plan;  // batch + 2: tiles of a segment before sequence b (block 0 writes it), tiles a block
 };
 
-// How waves share a block: `waves_m` groups of 32 * row_tiles rows times
+// How waves share a block: `waves_m` groups of `wave_rows` rows times
 // `waves_t` parts of the tokens, `step` tokens a wave at a time.
 struct AttentionShape {
-    int row_tiles, waves_m, waves_t, step;
-    constexpr int rows() const { return 32 * row_tiles * waves_m; }
+    int wave_rows, waves_m, waves_t, step;
+    constexpr int rows() const { return wave_rows * waves_m; }
     constexpr int tokens() const { return waves_t * step; }
 };
-constexpr AttentionShape kFewRows = {1, 1, 4, 32}, kManyRows = {1, 4, 1, 64};
+constexpr AttentionShape kFewestRows = {16, 1, 4, 32}, kFewRows = {32, 1, 4, 32}, kManyRows = {32, 4, 1, 64};
 // The shape for `rows` rows of a kv head.
-constexpr AttentionShape attention_shape(int rows) { return rows <= 32 ? kFewRows : kManyRows; }
+constexpr AttentionShape attention_shape(int rows) {
+    return rows <= kFewestRows.rows() ? kFewestRows : rows <= kFewRows.rows() ? kFewRows : kManyRows;
+}
 // Joins the pieces of every row into the output (rows_a_block: the shape's).
 hipError_t launch_attention_combine(int type, const TreeAttention& a, int rows_a_block, hipStream_t stream);
 hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream);

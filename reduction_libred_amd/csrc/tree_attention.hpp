@@ -6,8 +6,9 @@
 // float32. All query heads of a kv head and all nodes are rows of one product,
 // so a tile of keys and values is read once for all of them.
 //
-// Products use the 32x32x16 matrix instruction, transposed: S^T = K Q^T puts
-// one row n in each lane column (lane % 32), 16 of 32 tokens in a lane and the
+// Products use the 32x32x16 matrix instruction (16x16x32 for up to 16 rows,
+// with half the registers and exponentials), transposed: S^T = K Q^T puts one
+// row n in each lane column (lane % 32), 16 of 32 tokens in a lane and the
 // other 16 in lane ^ 32, so maxima and sums are lane-local but for one
 // exchange. The exponentials are then already the operand of O^T = V^T P^T: a
 // product does not mind the order of the tokens it sums over, so V^T is read
@@ -53,6 +54,10 @@ struct Mma<F16> {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
     }
+    static __device__ __forceinline__ f32x4 dot(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
+                                                      0, 0);
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
     }
@@ -62,6 +67,10 @@ template <>
 struct Mma<BF16> {
     static __device__ __forceinline__ f32x16 dot(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x4 dot(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                        0, 0, 0);
     }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -103,10 +112,23 @@ struct CachedE4M3 {
     }
 };
 
-// The larger (or the sum) of a value and lane ^ 32's.
-__device__ __forceinline__ float other_half(float v) {
-    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v), __builtin_bit_cast(unsigned, v), false, false);
-    return __builtin_bit_cast(float, threadIdx.x & 32 ? s[0] : s[1]);
+// Combine the values of the lanes that share a row: lane ^ 32, and lane ^ 16
+// where a row of the tile is spread over four. Every lane gets the result.
+template <int PARTS, class F>
+__device__ __forceinline__ float join_parts(float v, F op) {
+    const unsigned a = __builtin_bit_cast(unsigned, v);
+    const auto s = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    // Elements of a vector go through variables: a bit cast of s[1] itself
+    // reads element 0.
+    const unsigned s0 = s[0], s1 = s[1];
+    v = op(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
+    if constexpr (PARTS == 4) {
+        const unsigned c = __builtin_bit_cast(unsigned, v);
+        const auto q = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+        const unsigned q0 = q[0], q1 = q[1];
+        v = op(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1));
+    }
+    return v;
 }
 
 // A value that is the same in all lanes, as one the compiler knows to be.
@@ -127,11 +149,13 @@ __device__ __forceinline__ Arguments arguments_again() {
 
 constexpr float kLazy = 8.f;  // how far (in powers of 2) scores may pass M before M follows
 
-template <class C, int DP, int RT, int WM, int WT, int TS>
+// RW rows a wave (the side of its matrix instruction), WM waves of different
+// rows, WT of different tokens, TS tokens a tile.
+template <class C, int DP, int RW, int WM, int WT, int TS>
 struct AttentionTile {
     static constexpr int kThreads = kWave * WM * WT;
     static constexpr int kTokens = WT * TS;
-    static constexpr int kRows = 32 * RT * WM;
+    static constexpr int kRows = RW * WM;
     static constexpr int kPerLoad = 16 / C::kBytes;  // elements of a 16-byte load
     static constexpr int kRowLoads = DP / kPerLoad;
     // A team of waves shares a tile of TS tokens: the waves_m waves of
@@ -148,32 +172,36 @@ struct AttentionTile {
     static constexpr int kPitchV = (DP * 2) % 128 == 64 ? DP * 2 : DP * 2 + 64;
     static constexpr int kTileBytes = TS * (kPitchK + kPitchV);
     static constexpr int kPitchO = DP + 4;  // floats
-    static constexpr int kOutBytes = WT > 1 ? WM * WT * 32 * kPitchO * 4 : 0;
+    static constexpr int kOutBytes = WT > 1 ? WM * WT * RW * kPitchO * 4 : 0;
     static constexpr int kAllTiles = WT * kHeld * kTileBytes;
     static constexpr int kBytes = kAllTiles > kOutBytes ? kAllTiles : kOutBytes;
 };
 
-template <class T, class C, int DP, int RT, int WM, int WT, int TS>
+template <class T, class C, int DP, int RW, int WM, int WT, int TS>
 __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attention_kernel(TreeAttention a) {
-    using S = AttentionTile<C, DP, RT, WM, WT, TS>;
+    using S = AttentionTile<C, DP, RW, WM, WT, TS>;
     constexpr bool kScaled = C::kBytes == 1;
     using VT = std::conditional_t<kScaled, F16, T>;
-    constexpr int TT = S::kTokens, KS = DP / 16, DT = DP / 32, SUB = TS / 32;
+    // A row lies in PARTS lanes (RW apart), which hold X of 32 tokens each, in
+    // fours: value x is of token 4 PARTS (x / 4) + 4 part + x % 4. One product
+    // takes KD elements of q and k, and XP = 8 values a lane of P.
+    constexpr int PARTS = kWave / RW, X = 32 / PARTS, KD = 8 * PARTS;
+    constexpr int TT = S::kTokens, KS = DP / KD, DT = DP / RW, SUB = TS / 32, OX = RW * RW / kWave;
+    using Acc = std::conditional_t<RW == 32, f32x16, f32x4>;
     static_assert(WM == 1 || WT == 1, "a team is a wave or the block");
-    static_assert(RT == 1 || WT == 1, "waves that share rows join one row tile");
     constexpr int HELD = S::kHeld, NL = S::kLoads;
     __shared__ __align__(16) char tile[S::kBytes];
     __shared__ uint32_t offs_all[WT][2][TS];  // where the rows of a tile's tokens start, in 16 bytes
     __shared__ uint64_t held[WT][4];           // which of them are in the cache
     __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
-    __shared__ float red[2][WM * WT][32];
+    __shared__ float red[2][WM * WT][RW];
     __shared__ int odd;
 
     // One argument of every 64-byte line, so that all lines are asked for at
     // once: fetched one after the other as they are met, the arguments alone
     // take several microseconds of a small call.
     asm volatile("" ::"s"(a.q), "s"(a.q_head), "s"(a.cache.k), "s"(a.cache.scale_head_stride), "s"(a.lens), "s"(a.blocks), "s"(a.plan));
-    const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = lane % 32, half = lane / 32;
+    const int tid = threadIdx.x, wave = uniform(tid / kWave), lane = tid % kWave, n = lane % RW, part = lane / RW;
     const int wm = wave % WM, wt = wave / WM;
     const int tm = WM == 1 ? lane : tid;  // in the team
     char* const tiles_lds = tile + wt * HELD * S::kTileBytes;
@@ -261,7 +289,6 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     const bool rows_in = rb * S::kRows < count * group;
     const int mine = direct ? seg_tiles : min(seg_tiles - skip, end - now);
     const int first = skip * TT, last = min(total, first + mine * TT);
-    const int row0 = (rb * WM + wm) * 32 * RT;
     if (rows_in || direct) {
 
     // The team's tiles are numbered from 0 at `origin`, TT tokens apart. A tile
@@ -387,27 +414,23 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     const int tiles = rows_in && last > origin ? (last - origin + TT - 1) / TT : 0;
     int64_t scale_next = -1;  // of the tile to be asked for next
     const int p0 = lookup(0), p1 = lookup(1), p2 = HELD == 2 ? lookup(2) : -1;
-    // This lane's rows, looked at while the pages are on their way.
-    int row[RT];
-    uint64_t seen[RT];  // the nodes it sees
-    u32x4 qf[RT][KS];
+    // This lane's row, looked at while the pages are on their way.
+    const int row = (rb * WM + wm) * RW + n;
+    uint64_t seen;  // the nodes it sees
+    u32x4 qf[KS];
     {
-        const uint64_t upto = count >= 64 ? ~0ull : (1ull << count) - 1;
+        const int node = row / group, g = row - node * group;
+        const bool live = row < M && node < count;
+        seen = ~0ull >> (63 - min(node, 63));
+        if (A->mask) seen = (uint64_t)A->mask[(int64_t)b * A->nodes + (live ? node : 0)];
+        seen = live ? seen & (count >= 64 ? ~0ull : (1ull << count) - 1) : 0;
+        const uint16_t* q = static_cast<const uint16_t*>(A->q);
+        if (live) q += b * A->q_batch + node * A->q_node + (h * group + g) * A->q_head;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            row[r] = row0 + r * 32 + n;
-            const int node = row[r] / group, g = row[r] - node * group;
-            const bool live = row[r] < M && node < count;
-            seen[r] = ~0ull >> (63 - min(node, 63));
-            if (A->mask) seen[r] = (uint64_t)A->mask[(int64_t)b * A->nodes + (live ? node : 0)];
-            seen[r] = live ? seen[r] & upto : 0;
-            const uint16_t* q = static_cast<const uint16_t*>(A->q);
-            if (live) q += b * A->q_batch + node * A->q_node + (h * group + g) * A->q_head;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                qf[r][s] = *reinterpret_cast<const u32x4*>(q + (s * 16 < D ? s * 16 + half * 8 : 0));
-                qf[r][s] = (qf[r][s] ^ A->flip) & (live && s * 16 < D ? A->keep : 0u);
-            }
+        for (int s = 0; s < KS; ++s) {
+            const int d = s * KD + part * 8;
+            qf[s] = *reinterpret_cast<const u32x4*>(q + (d < D ? d : 0));
+            qf[s] = (qf[s] ^ A->flip) & (live && d < D ? A->keep : 0u);
         }
     }
 
@@ -417,15 +440,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     scale_next = settle(1, p1);
     __syncthreads();
     if (tiles > 0) fetch(0, scale0);
-    f32x16 o[RT][DT];
-    float m[RT], l[RT];
+    Acc o[DT];
+    float m = -__builtin_inff(), l = 0.f;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        m[r] = -__builtin_inff();
-        l[r] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[r][d] = f32x16{};
-    }
+    for (int d = 0; d < DT; ++d) o[d] = Acc{};
 
     if constexpr (HELD == 2) {
         __syncthreads();
@@ -453,19 +471,16 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         auto& vinv = factors[wt][i % HELD][2];
 
         // Scores of this wave's tokens.
-        f32x16 sc[RT][SUB];
+        Acc sc[SUB * X / OX];  // OX values each
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) {
+        for (int s = 0; s < SUB * X / OX; ++s) {
+            sc[s] = Acc{};
+            const char* kp = ldsk + (s * RW + n) * S::kPitchK + part * 16;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) sc[r][s] = f32x16{};
-            const char* kp = ldsk + (s * 32 + n) * S::kPitchK + half * 16;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const u32x4 kf = *reinterpret_cast<const u32x4*>(kp + k * 32);
-#pragma unroll
-                for (int r = 0; r < RT; ++r) sc[r][s] = Mma<T>::dot(kf, qf[r][k], sc[r][s]);
-            }
+            for (int k = 0; k < KS; ++k) sc[s] = Mma<T>::dot(*reinterpret_cast<const u32x4*>(kp + k * KD * 2), qf[k], sc[s]);
         }
+        // Value x of 32 tokens.
+        auto score = [&](int s, int x) -> auto& { return sc[(s * X + x) / OX]; };
         if constexpr (HELD == 2) {
             if (i + 1 < tiles) store(i + 1);
             if (i + 2 < tiles) fetch(i + 2, scale_next);
@@ -474,13 +489,11 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
             for (int s = 0; s < SUB; ++s)
 #pragma unroll
-                for (int x = 0; x < 16; x += 4) {
-                    const int t = s * 32 + 2 * x + 4 * half;
+                for (int x = 0; x < X; x += 4) {
+                    const int t = s * 32 + PARTS * x + 4 * part;
                     const f32x4 kf = *reinterpret_cast<const f32x4*>(kfac + t), vl = *reinterpret_cast<const f32x4*>(vlog + t);
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) sc[r][s][x + y] = sc[r][s][x + y] * kf[y] + vl[y];
+                    for (int y = 0; y < 4; ++y) score(s, x)[(x + y) % OX] = score(s, x)[(x + y) % OX] * kf[y] + vl[y];
                 }
         }
         if (base + TS > min(len, total)) {
@@ -489,75 +502,64 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             for (int s = 0; s < SUB; ++s) {
                 const int from = base + s * 32, j = from - len, left = total - from;
                 const uint32_t there = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
+                uint32_t sees = j <= -32 ? ~0u : j >= 64 ? 0u : j >= 0 ? (uint32_t)(seen >> j) : (uint32_t)(seen << -j) | ((1u << -j) - 1);
+                sees = (sees & there) >> (4 * part);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    uint32_t sees = j <= -32 ? ~0u : j >= 64 ? 0u : j >= 0 ? (uint32_t)(seen[r] >> j) : (uint32_t)(seen[r] << -j) | ((1u << -j) - 1);
-                    sees = (sees & there) >> (4 * half);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        if (!(sees & 1u << (8 * (x / 4) + x % 4))) sc[r][s][x] = -__builtin_inff();
-                }
+                for (int x = 0; x < X; ++x)
+                    if (!(sees & 1u << (4 * PARTS * (x / 4) + x % 4))) score(s, x)[x % OX] = -__builtin_inff();
             }
         }
-        uint32_t pf[RT][SUB][8];
+        float top4[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            float top4[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+        for (int s = 0; s < SUB; ++s)
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
+            for (int x = 0; x < X; ++x) top4[x % 4] = fmaxf(top4[x % 4], score(s, x)[x % OX]);
+        float top = join_parts<PARTS>(fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])), [](float x, float y) { return fmaxf(x, y); });
+        if constexpr (!kScaled) top *= A->scale;
+        if (__any(top > m + kLazy)) {
+            const float to = top > m + kLazy ? top : m;
+            const float f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
 #pragma unroll
-                for (int x = 0; x < 16; ++x) top4[x % 4] = fmaxf(top4[x % 4], sc[r][s][x]);
-            float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-            top = fmaxf(top, other_half(top));
-            if constexpr (!kScaled) top *= A->scale;
-            if (__any(top > m[r] + kLazy)) {
-                const float to = top > m[r] + kLazy ? top : m[r];
-                const float f = to == m[r] ? 1.f : __builtin_amdgcn_exp2f(m[r] - to);
-                m[r] = to;
-                l[r] *= f;
+            for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+        const float ms = m == -__builtin_inff() ? 0.f : m;
+        uint32_t pf[SUB][X / 2];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) o[r][d] *= f;
-            }
-            const float ms = m[r] == -__builtin_inff() ? 0.f : m[r];
+        for (int s = 0; s < SUB; ++s) {
 #pragma unroll
-            for (int s = 0; s < SUB; ++s) {
+            for (int x = 0; x < X; x += 4) {
+                f32x4 vi;
+                if constexpr (kScaled) vi = *reinterpret_cast<const f32x4*>(vinv + s * 32 + PARTS * x + 4 * part);
+                float w[4];
 #pragma unroll
-                for (int x = 0; x < 16; x += 4) {
-                    f32x4 vi;
-                    if constexpr (kScaled) vi = *reinterpret_cast<const f32x4*>(vinv + s * 32 + 2 * x + 4 * half);
-                    float w[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        w[y] = __builtin_amdgcn_exp2f(kScaled ? sc[r][s][x + y] - ms : sc[r][s][x + y] * A->scale - ms);
-                        l[r] += kScaled ? w[y] * vi[y] : w[y];
-                    }
-                    pf[r][s][x / 2] = Mma<VT>::pack(w[0], w[1]);
-                    pf[r][s][x / 2 + 1] = Mma<VT>::pack(w[2], w[3]);
+                for (int y = 0; y < 4; ++y) {
+                    const float v = score(s, x)[(x + y) % OX];
+                    w[y] = __builtin_amdgcn_exp2f(kScaled ? v - ms : v * A->scale - ms);
+                    l += kScaled ? w[y] * vi[y] : w[y];
                 }
+                pf[s][x / 2] = Mma<VT>::pack(w[0], w[1]);
+                pf[s][x / 2 + 1] = Mma<VT>::pack(w[2], w[3]);
             }
         }
-        // 8 tokens of a column: 16 lanes read 4 tokens times 16 columns; lane % 16 picks a column.
+        // 8 tokens of a column, those of values 8k .. 8k + 7: 16 lanes read 4
+        // tokens times 16 columns, twice; lane % 16 picks a column.
         auto values = [&](int s, int k, int d) -> u32x4 {
-            const char* vp = ldsv + (s * 32 + k * 16 + 4 * half + (lane % 16) / 4) * S::kPitchV +
-                             (lane / 16 % 2) * 32 + (lane % 4) * 8 + d * 64;
+            const char* vp = ldsv + (s * 32 + k * 8 * PARTS + 4 * part + (lane % 16) / 4) * S::kPitchV +
+                             (lane % RW / 16) * 32 + (lane % 4) * 8 + d * RW * 2;
             using L = __attribute__((address_space(3))) s16x4*;
             const u32x2 v0 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)vp));
-            const u32x2 v1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + 8 * S::kPitchV)));
+            const u32x2 v1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(vp + 4 * PARTS * S::kPitchV)));
             return u32x4{v0[0], v0[1], v1[0], v1[1]};
-        };
-        auto weights = [&](int r, int s, int k) -> u32x4 {
-            return u32x4{pf[r][s][4 * k], pf[r][s][4 * k + 1], pf[r][s][4 * k + 2], pf[r][s][4 * k + 3]};
         };
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < X / 8; ++k)
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const u32x4 v = values(s, k, d);
-#pragma unroll
-                    for (int r = 0; r < RT; ++r) o[r][d] = Mma<VT>::dot(v, weights(r, s, k), o[r][d]);
-                }
+                for (int d = 0; d < DT; ++d)
+                    o[d] = Mma<VT>::dot(values(s, k, d), u32x4{pf[s][4 * k], pf[s][4 * k + 1], pf[s][4 * k + 2], pf[s][4 * k + 3]}, o[d]);
         scale_next = settle(i + HELD + 1, page);
         team_sync();
     }
@@ -613,47 +615,44 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
             *reinterpret_cast<f32x4*>(E->part_o + (prow0 + rw) * D + c) = v;
         }
     };
+    const float ll = join_parts<PARTS>(l, [](float x, float y) { return x + y; });
+    // Columns of an accumulator, in fours: 4 PARTS (y / 4) + 4 part.
     if constexpr (WT == 1) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float ll = l[r] + other_half(l[r]);
-            if (row[r] >= M) continue;
-            if (half == 0) put_stats(row[r], m[r], ll);
+        if (row < M) {
+            if (part == 0) put_stats(row, m, ll);
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int y = 0; y < 16; y += 4) {
-                    const int c = d * 32 + 2 * y + 4 * half;
-                    if (c < D) put4(row[r], c, f32x4{o[r][d][y], o[r][d][y + 1], o[r][d][y + 2], o[r][d][y + 3]}, ll);
+                for (int y = 0; y < OX; y += 4) {
+                    const int c = d * RW + PARTS * y + 4 * part;
+                    if (c < D) put4(row, c, f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]}, ll);
                 }
         }
     } else {
-        float ll = l[0] + other_half(l[0]);
-        if (half == 0) red[0][wave][n] = m[0];
+        if (part == 0) red[0][wave][n] = m;
         __syncthreads();
         float mm = -__builtin_inff();
 #pragma unroll
-        for (int w = 0; w < WT; ++w) mm = fmaxf(mm, red[0][wm + w * WM][n]);
-        const float f = m[0] == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m[0] - mm);
-        if (half == 0) red[1][wave][n] = ll * f;
-        float* ob = reinterpret_cast<float*>(tile) + (wave * 32 + n) * S::kPitchO;
+        for (int w = 0; w < WT; ++w) mm = fmaxf(mm, red[0][w][n]);
+        const float f = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - mm);
+        if (part == 0) red[1][wave][n] = ll * f;
+        float* ob = reinterpret_cast<float*>(tile) + (wave * RW + n) * S::kPitchO;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int y = 0; y < 16; y += 4)
-                *reinterpret_cast<f32x4*>(ob + d * 32 + 2 * y + 4 * half) =
-                    f32x4{o[0][d][y], o[0][d][y + 1], o[0][d][y + 2], o[0][d][y + 3]} * f;
+            for (int y = 0; y < OX; y += 4)
+                *reinterpret_cast<f32x4*>(ob + d * RW + PARTS * y + 4 * part) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]} * f;
         __syncthreads();
-        for (int e = tid; e < WM * 32 * (DP / 4); e += S::kThreads) {
-            const int rr = e / (DP / 4), c = e % (DP / 4) * 4, w0 = rr / 32, rn = rr % 32, rw = rb * S::kRows + rr;
+        for (int e = tid; e < RW * (DP / 4); e += S::kThreads) {
+            const int rn = e / (DP / 4), c = e % (DP / 4) * 4, rw = rb * S::kRows + rn;
             if (c >= D || rw >= M) continue;
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
             float lsum = 0.f, mx = -__builtin_inff();
 #pragma unroll
             for (int w = 0; w < WT; ++w) {
-                v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(tile) + ((w0 + w * WM) * 32 + rn) * S::kPitchO + c);
-                lsum += red[1][w0 + w * WM][rn];
-                mx = fmaxf(mx, red[0][w0 + w * WM][rn]);
+                v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(tile) + (w * RW + rn) * S::kPitchO + c);
+                lsum += red[1][w][rn];
+                mx = fmaxf(mx, red[0][w][rn]);
             }
             if (c == 0) put_stats(rw, mx, lsum);
             put4(rw, c, v, lsum);
@@ -687,17 +686,19 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     }
 }
 
-template <class T, class C, int DP, int RT, int WM, int WT, int TS>
+template <class T, class C, int DP, int RW, int WM, int WT, int TS>
 hipError_t launch_attention_shape(const TreeAttention& a, hipStream_t stream) {
     const unsigned int grid = a.blocks ? (unsigned)a.blocks : (unsigned)(a.batch * a.cache.heads * a.row_blocks);
-    tree_attention_kernel<T, C, DP, RT, WM, WT, TS><<<grid, kWave * WM * WT, 0, stream>>>(a);
+    tree_attention_kernel<T, C, DP, RW, WM, WT, TS><<<grid, kWave * WM * WT, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <class T, class C, int DP>
 hipError_t launch_attention_dim(const TreeAttention& a, hipStream_t stream) {
-    if (a.nodes * a.group <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 1, 1, 4, 32>(a, stream);
-    return launch_attention_shape<T, C, DP, 1, 4, 1, 64>(a, stream);
+    const int rows = a.nodes * a.group;
+    if (rows <= kFewestRows.rows()) return launch_attention_shape<T, C, DP, 16, 1, 4, 32>(a, stream);
+    if (rows <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 32, 1, 4, 32>(a, stream);
+    return launch_attention_shape<T, C, DP, 32, 4, 1, 64>(a, stream);
 }
 
 template <class T, class C>
