@@ -3,12 +3,17 @@
 Like the rest of the binding, each function has the name of the C entry point
 it calls and only marshals arguments. Tensors are taken with the strides they
 have, as long as their last dimension is contiguous.
+
+A decoding step makes these calls with little work in each, so the way to the
+C call is kept short: one look at a tensor where it is as it should be (what is
+wrong is found out afterwards), and argument structs packed in one go.
 """
 import ctypes
+import struct
 
 import torch
 
-from . import _check, _stream_handle, lib
+from . import RedError, _stream_handle, lib
 
 _P = ctypes.c_void_p
 _Z = ctypes.c_size_t
@@ -19,6 +24,8 @@ _F = ctypes.c_float
 TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
 
 
+# The structs of libred_decode.h, each with a packer that takes their fields
+# one after the other.
 class Heads(ctypes.Structure):
     _fields_ = [("data", _P), ("heads", _L), ("token_stride", _L), ("head_stride", _L)]
 
@@ -52,65 +59,112 @@ class VerifyDraftsArgs(ctypes.Structure):
                 ("drafted", _P), ("u", _P), ("r", _P), ("draft_count", _P), ("accepted", _P), ("tokens", _P)]
 
 
+def _packer(cls):
+    codes = {_P: "Q", _Z: "Q", _L: "q", _I: "i", _F: "f"}
+
+    def fields(c):
+        return "".join(codes[t] if t in codes else "0Q" + fields(t) + "0Q" for _, t in c._fields_)
+
+    p = struct.Struct("@" + fields(cls) + "0Q")
+    assert p.size == ctypes.sizeof(cls)
+    return p.pack
+
+
+_pack_heads, _pack_qk_norm, _pack_cache = _packer(Heads), _packer(QkNormRopeArgs), _packer(PagedCache)
+_pack_attention, _pack_verify = _packer(TreeAttentionArgs), _packer(VerifyDraftsArgs)
+
 SIGNATURES = {
-    "red_verify_drafts": (_I, [ctypes.POINTER(VerifyDraftsArgs), _P]),
-    "red_tree_attention": (_I, [ctypes.POINTER(TreeAttentionArgs), _P]),
-    "red_qk_norm_rope": (_I, [ctypes.POINTER(QkNormRopeArgs), _P]),
-    "red_qk_norm_rope_backward": (_I, [ctypes.POINTER(QkNormRopeArgs), ctypes.POINTER(Heads), ctypes.POINTER(Heads),
-                                       _P, _P, _P]),
-    "red_cache_write": (_I, [ctypes.POINTER(PagedCache), _I, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _P, _Z, _P]),
-    "red_cache_read": (_I, [ctypes.POINTER(PagedCache), _I, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _P, _Z, _P]),
+    "red_qk_norm_rope": (_I, [_P, _P]),
+    "red_qk_norm_rope_backward": (_I, [_P, _P, _P, _P, _P, _P]),
+    "red_cache_write": (_I, [_P, _I, _P, _P, _P, _Z, _P]),
+    "red_cache_read": (_I, [_P, _I, _P, _P, _P, _Z, _P]),
+    "red_tree_attention": (_I, [_P, _P]),
+    "red_verify_drafts": (_I, [_P, _P]),
 }
 
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
+_HALVES = _FLOATS[1:]
+_CACHES = (torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn)
+_INT32, _INT64, _FLOAT32 = torch.int32, torch.int64, torch.float32
 
-def _tensor(name, what, x, dtype, device, shape=None):
-    """Refuse what is not a tensor of this type (a type or a tuple of them),
-    on this device (None: any ROCm device), of this shape, with a contiguous
-    last dimension."""
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+
+def _refuse(name, what, x, dtype, device, shape, contiguous=False):
+    """Raise what is wrong with x."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name}: {what} must be a tensor on a ROCm device")
-    if device is not None and x.device != device:
-        raise ValueError(f"{name}: {what} must be on {device}")
-    if x.dtype != dtype and not (isinstance(dtype, tuple) and x.dtype in dtype):
+    if device is not None and x.get_device() != device:
+        raise ValueError(f"{name}: {what} must be on cuda:{device}")
+    if x.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name}: {what} must be {dtype}, got {x.dtype}")
-    if shape is not None and x.shape != shape:
+    if x.shape != shape:
         raise ValueError(f"{name}: {what} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.dim() and x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dimension of {what} must be contiguous")
+    raise ValueError(f"{name}: {'' if contiguous else 'the last dimension of '}{what} must be contiguous")
+
+
+def _any(name, what, x, dtypes, dims, layout):
+    """The first tensor of a call, of one of these types and `dims`
+    dimensions; -> its device."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in dtypes:
+        _refuse(name, what, x, dtypes, None, None)
+    if x.dim() != dims:
+        raise ValueError(f"{name}: {what} must be {layout}")
+    if x.stride(-1) != 1 and x.shape[-1] > 1:
+        _refuse(name, what, x, dtypes, None, x.shape)
+    return x.get_device()
+
+
+def _rows(name, what, x, dtype, device, shape):
+    """A tensor of this shape with a contiguous last dimension."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == device and x.shape == shape and
+            (x.stride(-1) == 1 or shape[-1] <= 1)):
+        _refuse(name, what, x, dtype, device, shape)
     return x
 
 
-def _vector(name, what, x, dtype, device, n):
-    _tensor(name, what, x, dtype, device, (n,))
+def _whole(name, what, x, dtype, device, shape):
+    """The address of a contiguous tensor of this shape."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == device and x.shape == shape and
+            x.is_contiguous()):
+        _refuse(name, what, x, dtype, device, shape, True)
     return x.data_ptr()
 
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(name, device, stream, *args):
+    """lib().name(*args, stream) with `device` current."""
+    if _current_device() != device:
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    handle = _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream, device)
+    st = getattr(lib(), name)(*args, handle)
+    if st:
+        raise RedError(name, st, lib().red_last_hip_error())
+
+
+def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
+    device = _any(name, "q", q, _FLOATS, 3, "(tokens, q heads, dim)")
+    dtype, (tokens, heads, dim) = q.dtype, q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError(f"{name}: k must be (tokens, k heads, dim)")
+    _rows(name, "k", k, dtype, device, (tokens, k.shape[1], dim))
+    half = freq.shape[0] if isinstance(freq, torch.Tensor) and freq.dim() == 1 else -1
+    q_out = q.new_empty(q.shape) if q_out is None else _rows(name, "q_out", q_out, dtype, device, q.shape)
+    k_out = k.new_empty(k.shape) if k_out is None else _rows(name, "k_out", k_out, dtype, device, k.shape)
+    pos, freq = _whole(name, "pos", pos, _INT64, device, (tokens,)), _whole(name, "freq", freq, _FLOAT32, device, (half,))
+    qw = 0 if q_weight is None else _whole(name, "q_weight", q_weight, dtype, device, (dim,))
+    kw = 0 if k_weight is None else _whole(name, "k_weight", k_weight, dtype, device, (dim,))
+    kh = k.shape[1]
+    return device, q_out, k_out, _pack_qk_norm(
+        TYPES[dtype], 1 if interleaved else 0, tokens, dim, 2 * half, eps, q.data_ptr(), heads, *q.stride()[:2],
+        k.data_ptr(), kh, *k.stride()[:2], q_out.data_ptr(), heads, *q_out.stride()[:2], k_out.data_ptr(), kh,
+        *k_out.stride()[:2], qw, kw, pos, freq)
+
+
 def _heads(x):
-    return Heads(x.data_ptr(), x.shape[1], x.stride(0), x.stride(1))
-
-
-_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
-
-
-def _qk_norm_args(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
-    _tensor(name, "q", q, _FLOATS, None)
-    if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError(f"{name}: q and k must be (tokens, heads, dim)")
-    tokens, _, dim = q.shape
-    _tensor(name, "k", k, q.dtype, q.device, (tokens, k.shape[1], dim))
-    args = QkNormRopeArgs(TYPES[q.dtype], 1 if interleaved else 0, tokens, dim, 2 * freq.numel(), eps, _heads(q), _heads(k))
-    args.pos = _vector(name, "pos", pos, torch.int64, q.device, tokens)
-    args.freq = _vector(name, "freq", freq, torch.float32, q.device, freq.numel())
-    if q_weight is not None:
-        args.q_weight = _vector(name, "q_weight", q_weight, q.dtype, q.device, dim)
-    if k_weight is not None:
-        args.k_weight = _vector(name, "k_weight", k_weight, q.dtype, q.device, dim)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else \
-        _tensor(name, "q_out", q_out, q.dtype, q.device, q.shape)
-    k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k_out is None else \
-        _tensor(name, "k_out", k_out, q.dtype, q.device, k.shape)
-    args.q_out, args.k_out = _heads(q_out), _heads(k_out)
-    return args, q_out, k_out
+    return _pack_heads(x.data_ptr(), x.shape[1], *x.stride()[:2])
 
 
 def red_qk_norm_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
@@ -121,10 +175,8 @@ def red_qk_norm_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps=1e-6, in
     apart, or neighbours if `interleaved`. float32, float16 or bfloat16; pos
     int64, freq float32. q_out and k_out may be q and k. -> (q_out, k_out)."""
     name = "red_qk_norm_rope"
-    args, q_out, k_out = _qk_norm_args(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
-    with torch.cuda.device(q.device):
-        st = lib().red_qk_norm_rope(ctypes.byref(args), _stream_handle(stream, q.device))
-    _check(name, st)
+    device, q_out, k_out, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    _call(name, device, stream, args)
     return q_out, k_out
 
 
@@ -134,43 +186,41 @@ def red_qk_norm_rope_backward(dq, dk, q, k, pos, freq, q_weight=None, k_weight=N
     -> (gradient of q, of k, of q_weight, of k_weight), the weights' in float32
     (also where the weight is None, that is ones)."""
     name = "red_qk_norm_rope_backward"
-    args, q_grad, k_grad = _qk_norm_args(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
-    _tensor(name, "dq", dq, q.dtype, q.device, q.shape)
-    _tensor(name, "dk", dk, q.dtype, q.device, k.shape)
-    dqw, dkw = torch.empty((2, q.shape[2]), dtype=torch.float32, device=q.device).unbind(0)
-    hq, hk = _heads(dq), _heads(dk)
-    with torch.cuda.device(q.device):
-        st = lib().red_qk_norm_rope_backward(ctypes.byref(args), ctypes.byref(hq), ctypes.byref(hk), dqw.data_ptr(),
-                                             dkw.data_ptr(), _stream_handle(stream, q.device))
-    _check(name, st)
+    device, q_grad, k_grad, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
+    _rows(name, "dq", dq, q.dtype, device, q.shape)
+    _rows(name, "dk", dk, q.dtype, device, k.shape)
+    dqw, dkw = torch.empty((2, q.shape[2]), dtype=_FLOAT32, device=q.device).unbind(0)
+    _call(name, device, stream, args, _heads(dq), _heads(dk), dqw.data_ptr(), dkw.data_ptr())
     return q_grad, k_grad, dqw, dkw
 
 
-_CACHES = (torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn)
-
-
 def _cache(name, k_pages, v_pages, k_scales, v_scales):
-    _tensor(name, "k_pages", k_pages, _CACHES, None)
-    if k_pages.dim() != 4:
-        raise ValueError(f"{name}: k_pages must be (pages, heads, places, dim)")
-    _tensor(name, "v_pages", v_pages, k_pages.dtype, k_pages.device, k_pages.shape)
-    strides = k_pages.stride()
+    """-> (device, the fields of a PagedCache)"""
+    device = _any(name, "k_pages", k_pages, _CACHES, 4, "(pages, heads, places, dim)")
+    dtype, shape, strides = k_pages.dtype, k_pages.shape, k_pages.stride()
+    _rows(name, "v_pages", v_pages, dtype, device, shape)
     if v_pages.stride() != strides:
         raise ValueError(f"{name}: k_pages and v_pages must have the same strides")
-    c = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), None, None, TYPES[k_pages.dtype], *k_pages.shape, *strides[:3])
-    scaled = c.type >= 3
+    kind = TYPES[dtype]
+    scaled = kind >= 3
     if scaled != (k_scales is not None) or scaled != (v_scales is not None):
         raise ValueError(f"{name}: 8-bit caches take k_scales and v_scales, 16-bit ones do not")
+    ks = vs = 0
+    scale_strides = (0, 0, 0)
     if scaled:
         for what, x in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if not isinstance(x, torch.Tensor) or x.dtype != torch.float32 or x.device != k_pages.device or \
-                    x.shape != k_pages.shape[:3]:
-                raise ValueError(f"{name}: {what} must be float32 {tuple(k_pages.shape[:3])} on {k_pages.device}")
-        if k_scales.stride() != v_scales.stride():
+            if not isinstance(x, torch.Tensor) or x.dtype is not _FLOAT32 or x.get_device() != device or x.shape != shape[:3]:
+                raise ValueError(f"{name}: {what} must be float32 {tuple(shape[:3])} on cuda:{device}")
+        scale_strides = k_scales.stride()
+        if v_scales.stride() != scale_strides:
             raise ValueError(f"{name}: k_scales and v_scales must have the same strides")
-        c.k_scales, c.v_scales = k_scales.data_ptr(), v_scales.data_ptr()
-        c.scale_page_stride, c.scale_head_stride, c.scale_place_stride = k_scales.stride()
-    return c
+        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    return device, (k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, kind, *shape, *strides[:3], *scale_strides)
+
+
+def _slots(name, slots, k_pages, device):
+    n = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
+    return _whole(name, "slots", slots, _INT64, device, (n,)), n, (n, k_pages.shape[1], k_pages.shape[3])
 
 
 def red_cache_write(k, v, slots, k_pages, v_pages, k_scales=None, v_scales=None, stream=None):
@@ -180,18 +230,12 @@ def red_cache_write(k, v, slots, k_pages, v_pages, k_scales=None, v_scales=None,
     are skipped). int8 and float8_e4m3fn caches take one scale a row in
     k_scales, v_scales (pages, heads, places; float32)."""
     name = "red_cache_write"
-    c = _cache(name, k_pages, v_pages, k_scales, v_scales)
-    device = k_pages.device
-    _tensor(name, "k", k, _FLOATS[1:], device)
-    shape = (slots.shape[0], k_pages.shape[1], k_pages.shape[3])
-    _tensor(name, "k", k, k.dtype, device, shape)
-    _tensor(name, "v", v, k.dtype, device, shape)
-    sl = _vector(name, "slots", slots, torch.int64, device, shape[0])
-    hk, hv = _heads(k), _heads(v)
-    with torch.cuda.device(device):
-        st = lib().red_cache_write(ctypes.byref(c), TYPES[k.dtype], ctypes.byref(hk), ctypes.byref(hv), sl, shape[0],
-                                   _stream_handle(stream, device))
-    _check(name, st)
+    device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
+    at, tokens, shape = _slots(name, slots, k_pages, device)
+    _any(name, "k", k, _HALVES, 3, "(tokens, heads, dim)")
+    _rows(name, "k", k, k.dtype, device, shape)
+    _rows(name, "v", v, k.dtype, device, shape)
+    _call(name, device, stream, _pack_cache(*c), TYPES[k.dtype], _heads(k), _heads(v), at, tokens)
 
 
 def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None, k_out=None, v_out=None, stream=None):
@@ -199,21 +243,13 @@ def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None,
     bfloat16. A slot outside the cache reads as zeros. -> (k, v), each (tokens,
     heads, dim)."""
     name = "red_cache_read"
-    c = _cache(name, k_pages, v_pages, k_scales, v_scales)
-    device = k_pages.device
-    if dtype not in _FLOATS[1:]:
+    device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
+    if dtype not in _HALVES:
         raise TypeError(f"{name}: dtype must be torch.float16 or torch.bfloat16")
-    shape = (slots.shape[0], k_pages.shape[1], k_pages.shape[3])
-    sl = _vector(name, "slots", slots, torch.int64, device, shape[0])
-    k_out = torch.empty(shape, dtype=dtype, device=device) if k_out is None else \
-        _tensor(name, "k_out", k_out, dtype, device, shape)
-    v_out = torch.empty(shape, dtype=dtype, device=device) if v_out is None else \
-        _tensor(name, "v_out", v_out, dtype, device, shape)
-    hk, hv = _heads(k_out), _heads(v_out)
-    with torch.cuda.device(device):
-        st = lib().red_cache_read(ctypes.byref(c), TYPES[dtype], ctypes.byref(hk), ctypes.byref(hv), sl, shape[0],
-                                  _stream_handle(stream, device))
-    _check(name, st)
+    at, tokens, shape = _slots(name, slots, k_pages, device)
+    k_out = k_pages.new_empty(shape, dtype=dtype) if k_out is None else _rows(name, "k_out", k_out, dtype, device, shape)
+    v_out = k_pages.new_empty(shape, dtype=dtype) if v_out is None else _rows(name, "v_out", v_out, dtype, device, shape)
+    _call(name, device, stream, _pack_cache(*c), TYPES[dtype], _heads(k_out), _heads(v_out), at, tokens)
     return k_out, v_out
 
 
@@ -229,32 +265,25 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     included, of a sequence (None: what the table holds). -> (out like q, lse
     (batch, nodes, q heads) float32); rows that see nothing hold 0 and -inf."""
     name = "red_tree_attention"
-    c = _cache(name, k_pages, v_pages, k_scales, v_scales)
-    device = k_pages.device
-    _tensor(name, "q", q, _FLOATS[1:], device)
-    if q.dim() != 4 or q.shape[3] != c.dim:
-        raise ValueError(f"{name}: q must be (batch, nodes, q heads, {c.dim})")
-    batch, nodes, heads, dim = q.shape
-    _tensor(name, "table", table, torch.int32, device)
-    if table.dim() != 2 or table.shape[0] != batch:
+    device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
+    _any(name, "q", q, _HALVES, 4, "(batch, nodes, q heads, dim)")
+    dtype, shape = q.dtype, q.shape
+    batch, nodes, heads, dim = shape
+    if dim != k_pages.shape[3]:
+        raise ValueError(f"{name}: q must be (batch, nodes, q heads, {k_pages.shape[3]})")
+    _rows(name, "q", q, dtype, device, shape)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
-    out = torch.empty(q.shape, dtype=q.dtype, device=device) if out is None else \
-        _tensor(name, "out", out, q.dtype, device, q.shape)
-    lse = torch.empty((batch, nodes, heads), dtype=torch.float32, device=device)
     cols = table.shape[1]
-    a = TreeAttentionArgs(TYPES[q.dtype], scale, batch, nodes, heads, cols * c.places if max_len is None else max_len,
-                          q.data_ptr(), out.data_ptr(), lse.data_ptr(), *q.stride()[:3], *out.stride()[:3], c,
-                          table.data_ptr(), cols, table.stride(0), _vector(name, "lens", lens, torch.int32, device, batch))
-    if tree_mask is not None:
-        _tensor(name, "tree_mask", tree_mask, torch.int64, device, (batch, nodes))
-        if not tree_mask.is_contiguous():
-            raise ValueError(f"{name}: tree_mask must be contiguous")
-        a.tree_mask = tree_mask.data_ptr()
-    if node_count is not None:
-        a.node_count = _vector(name, "node_count", node_count, torch.int32, device, batch)
-    with torch.cuda.device(device):
-        st = lib().red_tree_attention(ctypes.byref(a), _stream_handle(stream, device))
-    _check(name, st)
+    _rows(name, "table", table, _INT32, device, (batch, cols))
+    out = q.new_empty(shape) if out is None else _rows(name, "out", out, dtype, device, shape)
+    lse = q.new_empty((batch, nodes, heads), dtype=_FLOAT32)
+    mask = 0 if tree_mask is None else _whole(name, "tree_mask", tree_mask, _INT64, device, (batch, nodes))
+    count = 0 if node_count is None else _whole(name, "node_count", node_count, _INT32, device, (batch,))
+    _call(name, device, stream, _pack_attention(
+        TYPES[dtype], scale, batch, nodes, heads, cols * k_pages.shape[2] if max_len is None else max_len, q.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), *q.stride()[:3], *out.stride()[:3], *c, table.data_ptr(), cols, table.stride(0),
+        _whole(name, "lens", lens, _INT32, device, (batch,)), mask, count))
     return out, lse
 
 
@@ -267,27 +296,18 @@ def red_verify_drafts(p, q, drafted, u, r, draft_count=None, stream=None):
     -> (accepted (batch) int32, tokens (batch, drafts + 1) int64: the accepted
     ones, the drawn one, then -1)."""
     name = "red_verify_drafts"
-    _tensor(name, "p", p, _FLOATS, None)
-    device = p.device
-    if p.dim() != 3 or p.shape[1] < 1:
+    device = _any(name, "p", p, _FLOATS, 3, "(batch, drafts + 1, vocab)")
+    dtype, (batch, steps, vocab) = p.dtype, p.shape
+    if steps < 1:
         raise ValueError(f"{name}: p must be (batch, drafts + 1, vocab)")
-    batch, drafts, vocab = p.shape[0], p.shape[1] - 1, p.shape[2]
-    a = VerifyDraftsArgs(TYPES[p.dtype], batch, drafts, vocab, p.data_ptr(), *p.stride()[:2])
+    drafts = steps - 1
+    qp = q0 = q1 = 0
     if q is not None:
-        _tensor(name, "q", q, p.dtype, device, (batch, drafts, vocab))
-        a.q, a.q_batch_stride, a.q_step_stride = q.data_ptr(), *q.stride()[:2]
-    for what, x, dtype in (("drafted", drafted, torch.int64), ("u", u, torch.float32)):
-        _tensor(name, what, x, dtype, device, (batch, drafts))
-        if not x.is_contiguous():
-            raise ValueError(f"{name}: {what} must be contiguous")
-        setattr(a, what, x.data_ptr())
-    a.r = _vector(name, "r", r, torch.float32, device, batch)
-    if draft_count is not None:
-        a.draft_count = _vector(name, "draft_count", draft_count, torch.int32, device, batch)
-    accepted = torch.empty(batch, dtype=torch.int32, device=device)
-    tokens = torch.empty((batch, drafts + 1), dtype=torch.int64, device=device)
-    a.accepted, a.tokens = accepted.data_ptr(), tokens.data_ptr()
-    with torch.cuda.device(device):
-        st = lib().red_verify_drafts(ctypes.byref(a), _stream_handle(stream, device))
-    _check(name, st)
+        qp, (q0, q1, _) = _rows(name, "q", q, dtype, device, (batch, drafts, vocab)).data_ptr(), q.stride()
+    at = _whole(name, "drafted", drafted, _INT64, device, (batch, drafts))
+    up, rp = _whole(name, "u", u, _FLOAT32, device, (batch, drafts)), _whole(name, "r", r, _FLOAT32, device, (batch,))
+    count = 0 if draft_count is None else _whole(name, "draft_count", draft_count, _INT32, device, (batch,))
+    accepted, tokens = p.new_empty(batch, dtype=_INT32), p.new_empty((batch, steps), dtype=_INT64)
+    _call(name, device, stream, _pack_verify(TYPES[dtype], batch, drafts, vocab, p.data_ptr(), *p.stride()[:2], qp, q0, q1,
+                                             at, up, rp, count, accepted.data_ptr(), tokens.data_ptr()))
     return accepted, tokens
