@@ -113,12 +113,14 @@ __device__ __forceinline__ void turn(float (&f)[NV][VEC], const float (&c)[NV][V
     }
 }
 
-// Cosines and signed sines of this lane's columns for token position `p`.
-// back: the rotation the other way.
+// Cosines and signed sines of this lane's columns for token t. BACK: the
+// rotation the other way.
 template <int VEC, int G, int NV, bool BACK>
-__device__ __forceinline__ void token_turns(float (&c)[NV][VEC], float (&g)[NV][VEC], int64_t p, const float* freq,
-                                            int rot, int interleaved, int lane, float2* table) {
+__device__ __forceinline__ void token_turns(float (&c)[NV][VEC], float (&g)[NV][VEC], const int64_t* pos, int64_t t,
+                                            const float* freq, int rot, int interleaved, int lane, float2* table) {
+    if (rot == 0) return;
     const int half = rot / 2;
+    const int64_t p = pos[t];
     wave_lds_fence();
     for (int i = threadIdx.x % kWave; i < half; i += kWave) {
         const double a = (double)p * (double)freq[i] * 0.15915494309189533577;  // turns
@@ -158,71 +160,105 @@ __device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const void* p, 
     }
 }
 
-// Address of row r (queries first, then keys) of token t.
-template <class T>
-__device__ __forceinline__ typename T::bits* row_of(const Heads& q, const Heads& k, int q_heads, int64_t t, int r) {
-    const bool isq = r < q_heads;
-    typename T::bits* p = static_cast<typename T::bits*>(isq ? q.p : k.p);
-    return p + t * (isq ? q.ts : k.ts) + (isq ? r : r - q_heads) * (isq ? q.hs : k.hs);
+// A token's rows are taken in passes of R heads, those of q first; a pass is of
+// q or of k, so that which weight to use is the same for the whole wave.
+template <class T, int R>
+struct Passes {
+    const QkNorm& a;
+    int64_t t;
+    int group;
+    __device__ int of_q() const { return (a.q_heads + R - 1) / R; }
+    __device__ int all() const { return of_q() + (a.k_heads + R - 1) / R; }
+    __device__ bool is_q(int p) const { return p < of_q(); }
+    __device__ int head(int p) const { return (is_q(p) ? p : p - of_q()) * R + group; }
+    __device__ bool there(int p) const { return head(p) < (is_q(p) ? a.q_heads : a.k_heads); }
+    // Row of this group in pass p, in the tensors of q or k.
+    __device__ typename T::bits* row(int p, const Heads& q, const Heads& k) const {
+        const Heads& h = is_q(p) ? q : k;
+        return static_cast<typename T::bits*>(h.p) + t * h.ts + (there(p) ? head(p) : 0) * h.hs;
+    }
+};
+
+// Loads are made without a branch (around one the compiler would not know how
+// many are on their way, and would wait for all of them at each use): lanes
+// beyond the row read its first elements, and keep() drops them.
+template <class T, int VEC, int G, int NV>
+__device__ __forceinline__ void load_row(typename Vec<T, VEC>::type (&x)[NV], const typename T::bits* p, int dim, int lane) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int u = lane + v * G;
+        x[v] = reinterpret_cast<const typename Vec<T, VEC>::type*>(p)[u * VEC < dim ? u : 0];
+    }
+}
+template <int VEC, int G, int NV>
+__device__ __forceinline__ void keep(float (&f)[NV][VEC], bool there, int dim, int lane) {
+    if (__all(there) && dim == G * VEC * NV) return;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[v][j] = there && (lane + v * G) * VEC < dim ? f[v][j] : 0.f;
+}
+template <class T, int VEC, int G, int NV>
+__device__ __forceinline__ void store_row(typename T::bits* p, const float (&y)[NV][VEC], bool there, int dim, int lane) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (there && (lane + v * G) * VEC < dim)
+            reinterpret_cast<typename Vec<T, VEC>::type*>(p)[lane + v * G] = narrow_vec<T, VEC>(y[v]);
 }
 
 template <class T, int VEC, int G, int NV>
 __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) {
     using V = typename Vec<T, VEC>::type;
-    constexpr int R = kWave / G;  // rows at a time
-    constexpr int U = NV == 1 ? 4 : 1;  // of which loads are in flight
+    constexpr int R = kWave / G;        // rows at a time
+    constexpr int U = NV == 1 ? 4 : 1;  // passes whose loads are in flight
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % G, group = (threadIdx.x % kWave) / G;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % G;
+    const int group = (threadIdx.x % kWave) / G;
     const int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave;
-    const int64_t t = id / a.parts;
+    const int64_t t = a.parts == 1 ? id : id / a.parts;
     if (t >= a.tokens) return;
-    const int part = (int)(id - t * a.parts), rows = a.q_heads + a.k_heads;
-    const int passes = (rows + R - 1) / R, per = (passes + a.parts - 1) / a.parts;
-    const int first = part * per, last = min(passes, first + per);
+    const Passes<T, R> rows = {a, t, group};
+    const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
+    const int first = part * per, last = min(rows.all(), first + per);
+    V x[U][NV];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            load_row<T, VEC, G, NV>(x[u], rows.row(min(p0 + u, last - 1), a.q, a.k), a.dim, lane);
+    };
+    if (first >= last) return;
+    load(first);  // before the angles, which take as long
     float wq[NV][VEC], wk[NV][VEC], c[NV][VEC], g[NV][VEC];
     load_weight<T, VEC, G, NV>(wq, a.q_weight, a.dim, lane);
     load_weight<T, VEC, G, NV>(wk, a.k_weight, a.dim, lane);
     const int mode = turn_mode<VEC>(a.rot, a.interleaved);
-    token_turns<VEC, G, NV, false>(c, g, a.pos[t], a.freq, a.rot, a.interleaved, lane,
-                                   reinterpret_cast<float2*>(lds[wave]));
+    token_turns<VEC, G, NV, false>(c, g, a.pos, t, a.freq, a.rot, a.interleaved, lane, reinterpret_cast<float2*>(lds[wave]));
     float* row = lds[wave] + group * (G * VEC * NV);
     const float inv = 1.f / (float)a.dim;
+    auto norm = [&](const V(&in)[NV], const float(&w)[NV][VEC], int p) {
+        float y[NV][VEC], sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) widen_vec<T, VEC>(in[v], y[v]);
+        keep<VEC, G, NV>(y, rows.there(p), a.dim, lane);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sum += y[v][j] * y[v][j];
+        const float rn = rsqrtf(group_sum<G>(sum) * inv + a.eps);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) y[v][j] *= rn * w[v][j];
+        turn<VEC, G, NV>(y, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
+        store_row<T, VEC, G, NV>(rows.row(p, a.q_out, a.k_out), y, rows.there(p), a.dim, lane);
+    };
     for (int p0 = first; p0 < last; p0 += U) {
-        V x[U][NV];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = (p0 + u) * R + group;
-            const V* src = reinterpret_cast<const V*>(row_of<T>(a.q, a.k, a.q_heads, t, r < rows ? r : 0));
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                x[u][v] = V{};
-                if (p0 + u < last && r < rows && (lane + v * G) * VEC < a.dim) x[u][v] = src[lane + v * G];
-            }
-        }
+        if (p0 > first) load(p0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (p0 + u >= last) break;
-            const int r = (p0 + u) * R + group;
-            float y[NV][VEC], sum = 0.f;
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                widen_vec<T, VEC>(x[u][v], y[v]);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) sum += y[v][j] * y[v][j];
-            }
-            const float rn = rsqrtf(group_sum<G>(sum) * inv + a.eps);
-            const bool isq = r < a.q_heads;
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) y[v][j] *= rn * (isq ? wq[v][j] : wk[v][j]);
-            turn<VEC, G, NV>(y, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
-            if (r < rows) {
-                V* dst = reinterpret_cast<V*>(row_of<T>(a.q_out, a.k_out, a.q_heads, t, r));
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if ((lane + v * G) * VEC < a.dim) dst[lane + v * G] = narrow_vec<T, VEC>(y[v]);
-            }
+            if (rows.is_q(p0 + u)) norm(x[u], wq, p0 + u);
+            else norm(x[u], wk, p0 + u);
         }
     }
 }
@@ -237,9 +273,8 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     constexpr int R = kWave / G;
     constexpr int U = NV == 1 ? 2 : 1;
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % G, group = (threadIdx.x % kWave) / G;
-    const int rows = a.q_heads + a.k_heads;
-    const int passes = (rows + R - 1) / R, per = (passes + a.parts - 1) / a.parts;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % G;
+    const int group = (threadIdx.x % kWave) / G;
     float wq[NV][VEC], wk[NV][VEC], c[NV][VEC], g[NV][VEC], aq[NV][VEC], ak[NV][VEC];
     load_weight<T, VEC, G, NV>(wq, a.q_weight, a.dim, lane);
     load_weight<T, VEC, G, NV>(wk, a.k_weight, a.dim, lane);
@@ -252,63 +287,68 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     const float inv = 1.f / (float)a.dim;
     const int64_t items = a.tokens * a.parts;
     for (int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave; id < items; id += (int64_t)gridDim.x * kQkNormWaves) {
-        const int64_t t = id / a.parts;
-        const int part = (int)(id - t * a.parts);
-        const int first = part * per, last = min(passes, first + per);
-        token_turns<VEC, G, NV, true>(c, g, a.pos[t], a.freq, a.rot, a.interleaved, lane,
-                                      reinterpret_cast<float2*>(lds[wave]));
-        for (int p0 = first; p0 < last; p0 += U) {
-            V x[U][NV], e[U][NV];
+        const int64_t t = a.parts == 1 ? id : id / a.parts;
+        const Passes<T, R> rows = {a, t, group};
+        const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
+        const int first = part * per, last = min(rows.all(), first + per);
+        V x[2][U][NV], e[2][U][NV];  // the rows at hand, and those on their way
+        auto load = [&](int p0, V(&x)[U][NV], V(&e)[U][NV]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = (p0 + u) * R + group, rr = r < rows ? r : 0;
-                const V* sx = reinterpret_cast<const V*>(row_of<T>(a.q, a.k, a.q_heads, t, rr));
-                const V* se = reinterpret_cast<const V*>(row_of<T>(a.dq, a.dk, a.q_heads, t, rr));
+            for (int u = 0; u < U; ++u)
+            {
+                const int p = min(p0 + u, last - 1);
+                load_row<T, VEC, G, NV>(x[u], rows.row(p, a.q, a.k), a.dim, lane);
+                load_row<T, VEC, G, NV>(e[u], rows.row(p, a.dq, a.dk), a.dim, lane);
+            }
+        };
+        if (first >= last) continue;
+        load(first, x[0], e[0]);
+        token_turns<VEC, G, NV, true>(c, g, a.pos, t, a.freq, a.rot, a.interleaved, lane, reinterpret_cast<float2*>(lds[wave]));
+        auto back = [&](const V(&in)[NV], const V(&dy)[NV], const float(&w)[NV][VEC], float(&dw)[NV][VEC], int p) {
+            float f[NV][VEC], d[NV][VEC], o[NV][VEC], xx = 0.f, hx = 0.f;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    x[u][v] = e[u][v] = V{};
-                    if (p0 + u < last && r < rows && (lane + v * G) * VEC < a.dim) {
-                        x[u][v] = sx[lane + v * G];
-                        e[u][v] = se[lane + v * G];
-                    }
+            for (int v = 0; v < NV; ++v) {
+                widen_vec<T, VEC>(dy[v], d[v]);
+                widen_vec<T, VEC>(in[v], f[v]);
+            }
+            const bool there = rows.there(p);
+            keep<VEC, G, NV>(d, there, a.dim, lane);
+            keep<VEC, G, NV>(f, there, a.dim, lane);
+            turn<VEC, G, NV>(d, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    xx += f[v][j] * f[v][j];
+                    o[v][j] = d[v][j] * w[v][j];
+                    hx += o[v][j] * f[v][j];
                 }
             }
+            const float rn = rsqrtf(group_sum<G>(xx) * inv + a.eps);
+            const float m = rn * rn * (group_sum<G>(hx) * inv);
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    o[v][j] = rn * (o[v][j] - f[v][j] * m);
+                    // A row that is not there is zeros, but eps may be 0.
+                    dw[v][j] += there ? d[v][j] * (f[v][j] * rn) : 0.f;
+                }
+            store_row<T, VEC, G, NV>(rows.row(p, a.q_out, a.k_out), o, there, a.dim, lane);
+        };
+        auto some = [&](int p0, const V(&x)[U][NV], const V(&e)[U][NV]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p0 + u >= last) break;
-                const int r = (p0 + u) * R + group;
-                float f[NV][VEC], d[NV][VEC], xx = 0.f, hx = 0.f;
-                const bool isq = r < a.q_heads;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) widen_vec<T, VEC>(e[u][v], d[v]);
-                turn<VEC, G, NV>(d, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    widen_vec<T, VEC>(x[u][v], f[v]);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        xx += f[v][j] * f[v][j];
-                        hx += d[v][j] * (isq ? wq[v][j] : wk[v][j]) * f[v][j];
-                    }
-                }
-                const float rn = rsqrtf(group_sum<G>(xx) * inv + a.eps);
-                const float m = rn * rn * (group_sum<G>(hx) * inv);
-                if (r < rows) {
-                    V* dst = reinterpret_cast<V*>(row_of<T>(a.q_out, a.k_out, a.q_heads, t, r));
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        float o[VEC];
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            o[j] = rn * (d[v][j] * (isq ? wq[v][j] : wk[v][j]) - f[v][j] * m);
-                            const float dw = d[v][j] * f[v][j] * rn;
-                            if (isq) aq[v][j] += dw;
-                            else ak[v][j] += dw;
-                        }
-                        if ((lane + v * G) * VEC < a.dim) dst[lane + v * G] = narrow_vec<T, VEC>(o);
-                    }
-                }
+                if (rows.is_q(p0 + u)) back(x[u], e[u], wq, aq, p0 + u);
+                else back(x[u], e[u], wk, ak, p0 + u);
             }
+        };
+        for (int p0 = first; p0 < last; p0 += 2 * U) {
+            load(p0 + U, x[1], e[1]);
+            some(p0, x[0], e[0]);
+            load(p0 + 2 * U, x[0], e[0]);
+            some(p0 + U, x[1], e[1]);
         }
     }
     // Partials: groups of the wave, then waves of the block, in a fixed order.

@@ -17,8 +17,20 @@ __global__ __launch_bounds__(kWeightWaves* kWave) void qk_norm_weights_kernel(co
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int col = blockIdx.x * kWave + lane;
     double s = 0.0;
-    if (col < 2 * dim)
-        for (int b = wave; b < blocks; b += kWeightWaves) s += (double)partials[(size_t)b * 2 * dim + col];
+    if (col < 2 * dim) {
+        // 16 loads in flight: the sum is short and all latency.
+        constexpr int U = 16;
+        for (int b0 = wave; b0 < blocks; b0 += kWeightWaves * U) {
+            float x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int b = b0 + u * kWeightWaves;
+                x[u] = partials[(size_t)min(b, blocks - 1) * 2 * dim + col];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += b0 + u * kWeightWaves < blocks ? (double)x[u] : 0.0;
+        }
+    }
     sums[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && col < 2 * dim) {
