@@ -111,6 +111,9 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     };
     int vec = (int)(16 / es);
     if (!fits((size_t)vec)) vec = fits(4) ? 4 : 1;
+    // Rows that a wave takes at once lie within 2 GiB, else it takes one.
+    for (const red_heads* h : {&a->q, &a->k, &a->q_out, &a->k_out, dq, dk})
+        if (h != nullptr && h->heads > 1 && h->head_stride > (int64_t)1 << 25) vec = 1;
     int lanes = 4;
     while (lanes < 64 && (size_t)(lanes * vec) < D) lanes *= 2;
     if (vec == 1) lanes = 64;

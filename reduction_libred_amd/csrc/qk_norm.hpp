@@ -51,131 +51,177 @@ constexpr int kHeadMax = RED_HEAD_MAX_DIM;
 // LDS of a wave: cosines and sines of a token, or the rows that change halves.
 constexpr int kWaveFloats = 64 * 8;
 
-// How the two elements of a pair meet.
-enum { kTurnNone = 0, kTurnInside = 1, kTurnVectors = 2, kTurnElements = 3 };
+// How the two elements of a pair meet: in a lane's own vector (neighbours as
+// pairs), as whole vectors of two lanes (halves, at vector boundaries), or
+// element by element (anything, nothing turned included). The kernels are
+// built for each: chosen at run time, the branches alone doubled their
+// instructions.
+enum { kTurnInside = 0, kTurnVectors = 1, kTurnElements = 2 };
 
-template <int VEC>
-__device__ __forceinline__ int turn_mode(int rot, int interleaved) {
-    if (rot == 0) return kTurnNone;
-    if (interleaved) return VEC > 1 ? kTurnInside : kTurnElements;
-    return (rot / 2) % VEC == 0 && VEC > 1 ? kTurnVectors : kTurnElements;
+inline int turn_mode(int vec, int rot, int interleaved) {
+    if (vec == 1 || rot == 0 || rot % vec != 0) return kTurnElements;
+    return interleaved ? kTurnInside : rot / 2 % vec == 0 ? kTurnVectors : kTurnElements;
 }
 
-// f <- f c + partner g for the elements of this lane; `row` is the row's part
-// of the wave's LDS (dim floats), u0 this lane's first element.
-template <int VEC, int G, int NV>
-__device__ __forceinline__ void turn(float (&f)[NV][VEC], const float (&c)[NV][VEC], const float (&g)[NV][VEC],
-                                     int mode, int interleaved, int lane, int dim, int rot, float* row) {
-    if (mode == kTurnNone) return;
-    if constexpr (VEC > 1) {
-        if (mode == kTurnInside) {
+template <class T, int VEC>
+using RowVec = typename Vec<T, VEC>::type;
+
+// The element that shares a pair with element d.
+__device__ __forceinline__ int partner_of(int d, int rot, int interleaved) {
+    if (d >= rot) return d;
+    const int half = rot / 2;
+    return interleaved ? d ^ 1 : (d < half ? d + half : d - half);
+}
+
+// The partners of this lane's elements, through the wave's LDS as they are;
+// `row` is the row's part of it (rot elements). 0 where nothing turns.
+template <class T, int VEC, int G, int NV, int MODE>
+__device__ __forceinline__ void partners(float (&f)[NV][VEC], const RowVec<T, VEC> (&x)[NV], int interleaved, int lane,
+                                         int rot, typename T::bits* row) {
+    using V = RowVec<T, VEC>;
+    if constexpr (MODE == kTurnInside) {
+        float y[VEC];
+        widen_vec<T, VEC>(x[0], y);
+        const bool turns = lane * VEC < rot;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[0][j] = turns ? y[j ^ 1] : 0.f;
+    } else {
+        wave_lds_fence();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int u = lane + v * G;
+            if (u * VEC < rot) reinterpret_cast<V*>(row)[u] = x[v];
+        }
+        wave_lds_fence();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int d = (lane + v * G) * VEC;
+            if constexpr (MODE == kTurnVectors) {
+                V y = V{};
+                if (d < rot) y = *reinterpret_cast<const V*>(row + (d < rot / 2 ? d + rot / 2 : d - rot / 2));
+                widen_vec<T, VEC>(y, f[v]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) f[v][j] = d + j < rot ? T::widen(row[partner_of(d + j, rot, interleaved)]) : 0.f;
+            }
+        }
+    }
+}
+
+// The angles of token t as cosines and sines in the wave's LDS.
+__device__ __forceinline__ void token_angles(const int64_t* pos, int64_t t, const float* freq, int rot, float* cosines,
+                                             float* sines) {
+    if (rot == 0) return;
+    const int64_t p = pos[t];
+    wave_lds_fence();
+    for (int i = threadIdx.x % kWave; i < rot / 2; i += kWave) {
+        const double a = (double)p * (double)freq[i] * 0.15915494309189533577;  // turns
+        const float2 cs = cos_sin_turns(a - rint(a));
+        cosines[i] = cs.x;
+        sines[i] = cs.y;
+    }
+    wave_lds_fence();
+}
+
+// Cosines and signed sines of this lane's columns: (x, partner) -> x c +
+// partner g; c = 1, g = 0 beyond the rotated part. BACK: the rotation the
+// other way.
+template <int VEC, int G, int NV, int MODE, bool BACK>
+__device__ __forceinline__ void lane_turns(float (&c)[NV][VEC], float (&g)[NV][VEC], int rot, int interleaved, int lane,
+                                           const float* cosines, const float* sines) {
+    const int half = rot / 2;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int d = (lane + v * G) * VEC;
+        if constexpr (MODE == kTurnVectors) {
+            const bool turns = d < rot, first = d < half;
+            const int i = turns ? (first ? d : d - half) : 0;
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4) {
+                const f32x4 cs = *reinterpret_cast<const f32x4*>(cosines + i + j), sn = *reinterpret_cast<const f32x4*>(sines + i + j);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    c[v][j + y] = turns ? cs[y] : 1.f;
+                    g[v][j + y] = turns ? (first != BACK ? -sn[y] : sn[y]) : 0.f;
+                }
+            }
+        } else if constexpr (MODE == kTurnInside) {
+            const bool turns = d < rot;
 #pragma unroll
             for (int j = 0; j < VEC; j += 2) {
-                const float a = f[0][j], b = f[0][j + 1];
-                f[0][j] = a * c[0][j] + b * g[0][j];
-                f[0][j + 1] = b * c[0][j + 1] + a * g[0][j + 1];
+                const float cs = cosines[turns ? (d + j) / 2 : 0], sn = sines[turns ? (d + j) / 2 : 0];
+                c[v][j] = c[v][j + 1] = turns ? cs : 1.f;
+                g[v][j] = turns ? (BACK ? sn : -sn) : 0.f;
+                g[v][j + 1] = -g[v][j];
             }
-            return;
-        }
-    }
-    const int half = rot / 2;
-    wave_lds_fence();
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int d = (lane + v * G) * VEC;
-        if (d >= rot) continue;
-        if constexpr (VEC >= 4) {
-#pragma unroll
-            for (int j = 0; j < VEC; j += 4)
-                *reinterpret_cast<f32x4*>(row + d + j) = f32x4{f[v][j], f[v][j + 1], f[v][j + 2], f[v][j + 3]};
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) row[d + j] = f[v][j];
-        }
-    }
-    wave_lds_fence();
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int d = (lane + v * G) * VEC;
-        if (d >= rot) continue;
-        if (VEC > 1 && mode == kTurnVectors) {
-            const f32x4* o = reinterpret_cast<const f32x4*>(row + (d < half ? d + half : d - half));
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) f[v][j] = f[v][j] * c[v][j] + o[j / 4][j % 4] * g[v][j];
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 const int e = d + j;
-                const int o = interleaved ? e ^ 1 : (e < half ? e + half : e - half);
-                if (e < rot) f[v][j] = f[v][j] * c[v][j] + row[o] * g[v][j];
+                const bool turns = e < rot, first = interleaved ? !(e & 1) : e < half;
+                const int i = interleaved ? e >> 1 : (first ? e : e - half);
+                c[v][j] = turns ? cosines[i] : 1.f;
+                g[v][j] = turns ? (first != BACK ? -sines[i] : sines[i]) : 0.f;
             }
-        }
-    }
-}
-
-// Cosines and signed sines of this lane's columns for token t. BACK: the
-// rotation the other way.
-template <int VEC, int G, int NV, bool BACK>
-__device__ __forceinline__ void token_turns(float (&c)[NV][VEC], float (&g)[NV][VEC], const int64_t* pos, int64_t t,
-                                            const float* freq, int rot, int interleaved, int lane, float2* table) {
-    if (rot == 0) return;
-    const int half = rot / 2;
-    const int64_t p = pos[t];
-    wave_lds_fence();
-    for (int i = threadIdx.x % kWave; i < half; i += kWave) {
-        const double a = (double)p * (double)freq[i] * 0.15915494309189533577;  // turns
-        table[i] = cos_sin_turns(a - rint(a));
-    }
-    wave_lds_fence();
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int d = (lane + v * G) * VEC + j;
-            float2 cs = make_float2(1.f, 0.f);
-            bool first = true;
-            if (d < rot) {
-                first = interleaved ? !(d & 1) : d < half;
-                cs = table[interleaved ? d >> 1 : (first ? d : d - half)];
-            }
-            c[v][j] = cs.x;
-            g[v][j] = first != BACK ? -cs.y : cs.y;
         }
     }
     wave_lds_fence();
 }
 
+// A weight at this lane's columns, or at their partners.
 template <class T, int VEC, int G, int NV>
 __device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const void* p, int dim, int lane) {
-    using V = typename Vec<T, VEC>::type;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int u = lane + v * G;
-        if (p != nullptr && u * VEC < dim) {
-            widen_vec<T, VEC>(static_cast<const V*>(p)[u], w[v]);
+        if (p != nullptr) {
+            widen_vec<T, VEC>(static_cast<const RowVec<T, VEC>*>(p)[u * VEC < dim ? u : 0], w[v]);
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) w[v][j] = 1.f;
         }
     }
 }
+template <class T, int VEC, int G, int NV, int MODE>
+__device__ __forceinline__ void load_partner_weight(float (&w)[NV][VEC], const float (&own)[NV][VEC], const void* p, int dim,
+                                                    int rot, int interleaved, int lane) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int d = (lane + v * G) * VEC;
+        if constexpr (MODE == kTurnInside) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[v][j] = own[v][j ^ 1];
+        } else if (p == nullptr) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[v][j] = 1.f;
+        } else if constexpr (MODE == kTurnVectors) {
+            const int o = d < rot ? (d < rot / 2 ? d + rot / 2 : d - rot / 2) : 0;
+            widen_vec<T, VEC>(*reinterpret_cast<const RowVec<T, VEC>*>(static_cast<const typename T::bits*>(p) + o), w[v]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                w[v][j] = T::widen(static_cast<const typename T::bits*>(p)[d + j < dim ? partner_of(d + j, rot, interleaved) : 0]);
+        }
+    }
+}
 
 // A token's rows are taken in passes of R heads, those of q first; a pass is of
-// q or of k, so that which weight to use is the same for the whole wave.
-template <class T, int R>
+// q or of k, so that which weight to use is the same for the whole wave. A row
+// is found as an address that is the wave's and an offset below 4 GiB that is
+// the lane's (the entry point sees to that), which costs one instruction.
+template <class T, int R, int VEC>
 struct Passes {
     const QkNorm& a;
-    int64_t t;
-    int group;
+    int group, lane;
     __device__ int of_q() const { return (a.q_heads + R - 1) / R; }
     __device__ int all() const { return of_q() + (a.k_heads + R - 1) / R; }
     __device__ bool is_q(int p) const { return p < of_q(); }
-    __device__ int head(int p) const { return (is_q(p) ? p : p - of_q()) * R + group; }
-    __device__ bool there(int p) const { return head(p) < (is_q(p) ? a.q_heads : a.k_heads); }
-    // Row of this group in pass p, in the tensors of q or k.
-    __device__ typename T::bits* row(int p, const Heads& q, const Heads& k) const {
-        const Heads& h = is_q(p) ? q : k;
-        return static_cast<typename T::bits*>(h.p) + t * h.ts + (there(p) ? head(p) : 0) * h.hs;
+    __device__ int head0(int p) const { return (is_q(p) ? p : p - of_q()) * R; }
+    __device__ bool there(int p) const { return head0(p) + group < (is_q(p) ? a.q_heads : a.k_heads); }
+    // Of this lane's group in a tensor of heads, in bytes.
+    __device__ uint32_t offset(const Heads& h) const { return (uint32_t)group * (uint32_t)h.hs * (uint32_t)sizeof(typename T::bits); }
+    __device__ char* base(int p, int64_t t, const Heads& h) const {
+        return static_cast<char*>(h.p) + (t * h.ts + head0(p) * h.hs) * (int64_t)sizeof(typename T::bits);
     }
 };
 
@@ -183,11 +229,11 @@ struct Passes {
 // many are on their way, and would wait for all of them at each use): lanes
 // beyond the row read its first elements, and keep() drops them.
 template <class T, int VEC, int G, int NV>
-__device__ __forceinline__ void load_row(typename Vec<T, VEC>::type (&x)[NV], const typename T::bits* p, int dim, int lane) {
+__device__ __forceinline__ void load_row(RowVec<T, VEC> (&x)[NV], const char* base, uint32_t offset, int dim, int lane) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int u = lane + v * G;
-        x[v] = reinterpret_cast<const typename Vec<T, VEC>::type*>(p)[u * VEC < dim ? u : 0];
+        x[v] = *reinterpret_cast<const RowVec<T, VEC>*>(base + (uint32_t)(offset + (u * VEC < dim ? u : 0) * (uint32_t)sizeof(RowVec<T, VEC>)));
     }
 }
 template <int VEC, int G, int NV>
@@ -199,16 +245,22 @@ __device__ __forceinline__ void keep(float (&f)[NV][VEC], bool there, int dim, i
         for (int j = 0; j < VEC; ++j) f[v][j] = there && (lane + v * G) * VEC < dim ? f[v][j] : 0.f;
 }
 template <class T, int VEC, int G, int NV>
-__device__ __forceinline__ void store_row(typename T::bits* p, const float (&y)[NV][VEC], bool there, int dim, int lane) {
+__device__ __forceinline__ void store_row(char* base, uint32_t offset, const float (&y)[NV][VEC], bool there, int dim,
+                                          int lane) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-        if (there && (lane + v * G) * VEC < dim)
-            reinterpret_cast<typename Vec<T, VEC>::type*>(p)[lane + v * G] = narrow_vec<T, VEC>(y[v]);
+    for (int v = 0; v < NV; ++v) {
+        const int u = lane + v * G;
+        if (there && u * VEC < dim)
+            *reinterpret_cast<RowVec<T, VEC>*>(base + (uint32_t)(offset + u * (uint32_t)sizeof(RowVec<T, VEC>))) = narrow_vec<T, VEC>(y[v]);
+    }
 }
 
-template <class T, int VEC, int G, int NV>
+// With the weight folded into cosine and sine, an element of the result is
+//     r (x (w c) + partner (w_partner g)),
+// so the exchange of partners does not wait for the row's sum.
+template <class T, int VEC, int G, int NV, int MODE>
 __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) {
-    using V = typename Vec<T, VEC>::type;
+    using V = RowVec<T, VEC>;
     constexpr int R = kWave / G;        // rows at a time
     constexpr int U = NV == 1 ? 4 : 1;  // passes whose loads are in flight
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
@@ -217,26 +269,43 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) 
     const int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave;
     const int64_t t = a.parts == 1 ? id : id / a.parts;
     if (t >= a.tokens) return;
-    const Passes<T, R> rows = {a, t, group};
+    const Passes<T, R, VEC> rows = {a, group, lane};
     const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
     const int first = part * per, last = min(rows.all(), first + per);
+    if (first >= last) return;
+    const uint32_t in_q = rows.offset(a.q), in_k = rows.offset(a.k), out_q = rows.offset(a.q_out), out_k = rows.offset(a.k_out);
     V x[U][NV];
     auto load = [&](int p0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            load_row<T, VEC, G, NV>(x[u], rows.row(min(p0 + u, last - 1), a.q, a.k), a.dim, lane);
+        for (int u = 0; u < U; ++u) {
+            const int p = min(p0 + u, last - 1);
+            const bool q = rows.is_q(p);
+            load_row<T, VEC, G, NV>(x[u], rows.base(p, t, q ? a.q : a.k), rows.there(p) ? (q ? in_q : in_k) : 0, a.dim, lane);
+        }
     };
-    if (first >= last) return;
     load(first);  // before the angles, which take as long
-    float wq[NV][VEC], wk[NV][VEC], c[NV][VEC], g[NV][VEC];
-    load_weight<T, VEC, G, NV>(wq, a.q_weight, a.dim, lane);
-    load_weight<T, VEC, G, NV>(wk, a.k_weight, a.dim, lane);
-    const int mode = turn_mode<VEC>(a.rot, a.interleaved);
-    token_turns<VEC, G, NV, false>(c, g, a.pos, t, a.freq, a.rot, a.interleaved, lane, reinterpret_cast<float2*>(lds[wave]));
-    float* row = lds[wave] + group * (G * VEC * NV);
+    float aq[NV][VEC], bq[NV][VEC], ak[NV][VEC], bk[NV][VEC];
+    {
+        float c[NV][VEC], g[NV][VEC];
+        load_weight<T, VEC, G, NV>(aq, a.q_weight, a.dim, lane);
+        load_weight<T, VEC, G, NV>(ak, a.k_weight, a.dim, lane);
+        load_partner_weight<T, VEC, G, NV, MODE>(bq, aq, a.q_weight, a.dim, a.rot, a.interleaved, lane);
+        load_partner_weight<T, VEC, G, NV, MODE>(bk, ak, a.k_weight, a.dim, a.rot, a.interleaved, lane);
+        token_angles(a.pos, t, a.freq, a.rot, lds[wave], lds[wave] + kHeadMax / 2);
+        lane_turns<VEC, G, NV, MODE, false>(c, g, a.rot, a.interleaved, lane, lds[wave], lds[wave] + kHeadMax / 2);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                aq[v][j] *= c[v][j], ak[v][j] *= c[v][j];
+                bq[v][j] *= g[v][j], bk[v][j] *= g[v][j];
+            }
+    }
+    typename T::bits* row = reinterpret_cast<typename T::bits*>(lds[wave]) + group * (G * VEC * NV);
     const float inv = 1.f / (float)a.dim;
-    auto norm = [&](const V(&in)[NV], const float(&w)[NV][VEC], int p) {
-        float y[NV][VEC], sum = 0.f;
+    auto norm = [&](const V(&in)[NV], const float(&wc)[NV][VEC], const float(&wg)[NV][VEC], int p, const Heads& to, uint32_t at) {
+        float y[NV][VEC], o[NV][VEC], sum = 0.f;
+        partners<T, VEC, G, NV, MODE>(o, in, a.interleaved, lane, a.rot, row);
 #pragma unroll
         for (int v = 0; v < NV; ++v) widen_vec<T, VEC>(in[v], y[v]);
         keep<VEC, G, NV>(y, rows.there(p), a.dim, lane);
@@ -248,17 +317,16 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) 
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) y[v][j] *= rn * w[v][j];
-        turn<VEC, G, NV>(y, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
-        store_row<T, VEC, G, NV>(rows.row(p, a.q_out, a.k_out), y, rows.there(p), a.dim, lane);
+            for (int j = 0; j < VEC; ++j) y[v][j] = rn * (y[v][j] * wc[v][j] + o[v][j] * wg[v][j]);
+        store_row<T, VEC, G, NV>(rows.base(p, t, to), at, y, rows.there(p), a.dim, lane);
     };
     for (int p0 = first; p0 < last; p0 += U) {
         if (p0 > first) load(p0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (p0 + u >= last) break;
-            if (rows.is_q(p0 + u)) norm(x[u], wq, p0 + u);
-            else norm(x[u], wk, p0 + u);
+            if (rows.is_q(p0 + u)) norm(x[u], aq, bq, p0 + u, a.q_out, out_q);
+            else norm(x[u], ak, bk, p0 + u, a.k_out, out_k);
         }
     }
 }
@@ -267,9 +335,9 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) 
 // add up the weight gradients of its columns in registers; they are added over
 // the wave's groups, then over the block's waves, and one row of 2 dim
 // partials a block goes to memory (qk_norm_weights_kernel adds those).
-template <class T, int VEC, int G, int NV>
+template <class T, int VEC, int G, int NV, int MODE>
 __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(QkNorm a) {
-    using V = typename Vec<T, VEC>::type;
+    using V = RowVec<T, VEC>;
     constexpr int R = kWave / G;
     constexpr int U = NV == 1 ? 2 : 1;
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
@@ -282,66 +350,69 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) aq[v][j] = ak[v][j] = 0.f;
-    const int mode = turn_mode<VEC>(a.rot, a.interleaved);
-    float* row = lds[wave] + group * (G * VEC * NV);
+    typename T::bits* row = reinterpret_cast<typename T::bits*>(lds[wave]) + group * (G * VEC * NV);
     const float inv = 1.f / (float)a.dim;
+    const Passes<T, R, VEC> rows = {a, group, lane};
+    const uint32_t x_q = rows.offset(a.q), x_k = rows.offset(a.k), d_q = rows.offset(a.dq), d_k = rows.offset(a.dk);
+    const uint32_t out_q = rows.offset(a.q_out), out_k = rows.offset(a.k_out);
     const int64_t items = a.tokens * a.parts;
     for (int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave; id < items; id += (int64_t)gridDim.x * kQkNormWaves) {
         const int64_t t = a.parts == 1 ? id : id / a.parts;
-        const Passes<T, R> rows = {a, t, group};
         const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
         const int first = part * per, last = min(rows.all(), first + per);
+        if (first >= last) continue;
         V x[2][U][NV], e[2][U][NV];  // the rows at hand, and those on their way
         auto load = [&](int p0, V(&x)[U][NV], V(&e)[U][NV]) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-            {
+            for (int u = 0; u < U; ++u) {
                 const int p = min(p0 + u, last - 1);
-                load_row<T, VEC, G, NV>(x[u], rows.row(p, a.q, a.k), a.dim, lane);
-                load_row<T, VEC, G, NV>(e[u], rows.row(p, a.dq, a.dk), a.dim, lane);
+                const bool q = rows.is_q(p), there = rows.there(p);
+                load_row<T, VEC, G, NV>(x[u], rows.base(p, t, q ? a.q : a.k), there ? (q ? x_q : x_k) : 0, a.dim, lane);
+                load_row<T, VEC, G, NV>(e[u], rows.base(p, t, q ? a.dq : a.dk), there ? (q ? d_q : d_k) : 0, a.dim, lane);
             }
         };
-        if (first >= last) continue;
         load(first, x[0], e[0]);
-        token_turns<VEC, G, NV, true>(c, g, a.pos, t, a.freq, a.rot, a.interleaved, lane, reinterpret_cast<float2*>(lds[wave]));
-        auto back = [&](const V(&in)[NV], const V(&dy)[NV], const float(&w)[NV][VEC], float(&dw)[NV][VEC], int p) {
+        token_angles(a.pos, t, a.freq, a.rot, lds[wave], lds[wave] + kHeadMax / 2);
+        lane_turns<VEC, G, NV, MODE, true>(c, g, a.rot, a.interleaved, lane, lds[wave], lds[wave] + kHeadMax / 2);
+        auto back = [&](const V(&in)[NV], const V(&dy)[NV], const float(&w)[NV][VEC], float(&dw)[NV][VEC], int p, const Heads& to, uint32_t at) {
             float f[NV][VEC], d[NV][VEC], o[NV][VEC], xx = 0.f, hx = 0.f;
+            partners<T, VEC, G, NV, MODE>(o, dy, a.interleaved, lane, a.rot, row);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 widen_vec<T, VEC>(dy[v], d[v]);
                 widen_vec<T, VEC>(in[v], f[v]);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) d[v][j] = d[v][j] * c[v][j] + o[v][j] * g[v][j];
             }
             const bool there = rows.there(p);
             keep<VEC, G, NV>(d, there, a.dim, lane);
             keep<VEC, G, NV>(f, there, a.dim, lane);
-            turn<VEC, G, NV>(d, c, g, mode, a.interleaved, lane, a.dim, a.rot, row);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     xx += f[v][j] * f[v][j];
                     o[v][j] = d[v][j] * w[v][j];
                     hx += o[v][j] * f[v][j];
                 }
-            }
-            const float rn = rsqrtf(group_sum<G>(xx) * inv + a.eps);
+            // The root of a row that is not there may be infinite.
+            const float rn = there ? rsqrtf(group_sum<G>(xx) * inv + a.eps) : 0.f;
             const float m = rn * rn * (group_sum<G>(hx) * inv);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     o[v][j] = rn * (o[v][j] - f[v][j] * m);
-                    // A row that is not there is zeros, but eps may be 0.
-                    dw[v][j] += there ? d[v][j] * (f[v][j] * rn) : 0.f;
+                    dw[v][j] += d[v][j] * (f[v][j] * rn);
                 }
-            store_row<T, VEC, G, NV>(rows.row(p, a.q_out, a.k_out), o, there, a.dim, lane);
+            store_row<T, VEC, G, NV>(rows.base(p, t, to), at, o, there, a.dim, lane);
         };
         auto some = [&](int p0, const V(&x)[U][NV], const V(&e)[U][NV]) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p0 + u >= last) break;
-                if (rows.is_q(p0 + u)) back(x[u], e[u], wq, aq, p0 + u);
-                else back(x[u], e[u], wk, ak, p0 + u);
+                if (rows.is_q(p0 + u)) back(x[u], e[u], wq, aq, p0 + u, a.q_out, out_q);
+                else back(x[u], e[u], wk, ak, p0 + u, a.k_out, out_k);
             }
         };
         for (int p0 = first; p0 < last; p0 += 2 * U) {
@@ -372,30 +443,39 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     }
 }
 
-template <class T, int VEC, int G, int NV>
-hipError_t launch_qk_norm_shape(const QkNorm& a, bool back, int blocks, hipStream_t stream) {
+template <class T, int VEC, int G, int NV, int MODE>
+hipError_t launch_qk_norm_mode(const QkNorm& a, bool back, int blocks, hipStream_t stream) {
     if (back)
-        qk_norm_backward_kernel<T, VEC, G, NV><<<blocks, kQkNormWaves * kWave, 0, stream>>>(a);
+        qk_norm_backward_kernel<T, VEC, G, NV, MODE><<<blocks, kQkNormWaves * kWave, 0, stream>>>(a);
     else
-        qk_norm_kernel<T, VEC, G, NV><<<blocks, kQkNormWaves * kWave, 0, stream>>>(a);
+        qk_norm_kernel<T, VEC, G, NV, MODE><<<blocks, kQkNormWaves * kWave, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <class T, int VEC, int G>
+hipError_t launch_qk_norm_lanes(const QkNorm& a, bool back, int blocks, hipStream_t stream) {
+    switch (turn_mode(VEC, a.rot, a.interleaved)) {
+        case kTurnInside: return launch_qk_norm_mode<T, VEC, G, 1, kTurnInside>(a, back, blocks, stream);
+        case kTurnVectors: return launch_qk_norm_mode<T, VEC, G, 1, kTurnVectors>(a, back, blocks, stream);
+        default: return launch_qk_norm_mode<T, VEC, G, 1, kTurnElements>(a, back, blocks, stream);
+    }
 }
 
 template <class T, int VEC>
 hipError_t launch_qk_norm_vec(int lanes, const QkNorm& a, bool back, int blocks, hipStream_t stream) {
     switch (lanes) {
-        case 4: return launch_qk_norm_shape<T, VEC, 4, 1>(a, back, blocks, stream);
-        case 8: return launch_qk_norm_shape<T, VEC, 8, 1>(a, back, blocks, stream);
-        case 16: return launch_qk_norm_shape<T, VEC, 16, 1>(a, back, blocks, stream);
-        case 32: return launch_qk_norm_shape<T, VEC, 32, 1>(a, back, blocks, stream);
-        case 64: return launch_qk_norm_shape<T, VEC, 64, 1>(a, back, blocks, stream);
+        case 4: return launch_qk_norm_lanes<T, VEC, 4>(a, back, blocks, stream);
+        case 8: return launch_qk_norm_lanes<T, VEC, 8>(a, back, blocks, stream);
+        case 16: return launch_qk_norm_lanes<T, VEC, 16>(a, back, blocks, stream);
+        case 32: return launch_qk_norm_lanes<T, VEC, 32>(a, back, blocks, stream);
+        case 64: return launch_qk_norm_lanes<T, VEC, 64>(a, back, blocks, stream);
         default: return hipErrorInvalidValue;
     }
 }
 
 template <class T>
 hipError_t launch_qk_norm_type(int vec, int lanes, const QkNorm& a, bool back, int blocks, hipStream_t stream) {
-    if (vec == 1) return launch_qk_norm_shape<T, 1, 64, 4>(a, back, blocks, stream);
+    if (vec == 1) return launch_qk_norm_mode<T, 1, 64, 4, kTurnElements>(a, back, blocks, stream);
     if (vec == 4) return launch_qk_norm_vec<T, 4>(lanes, a, back, blocks, stream);
     if constexpr (sizeof(typename T::bits) == 2)
         if (vec == 8) return launch_qk_norm_vec<T, 8>(lanes, a, back, blocks, stream);
