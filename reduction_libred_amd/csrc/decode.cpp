@@ -147,7 +147,7 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
         const hipError_t e = launch(vec, lanes, k, false, (int)blocks, stream);
         return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
     }
-    const size_t cap = (size_t)cus * 4;
+    const size_t cap = (size_t)cus * 6;
     if (blocks > cap) blocks = cap;
     void* partials = nullptr;
     st = host_scratch(dev, stream, blocks * 2 * D * sizeof(float), &partials);

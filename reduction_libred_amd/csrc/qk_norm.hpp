@@ -233,7 +233,7 @@ __device__ __forceinline__ void load_row(RowVec<T, VEC> (&x)[NV], const char* ba
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int u = lane + v * G;
-        x[v] = *reinterpret_cast<const RowVec<T, VEC>*>(base + (uint32_t)(offset + (u * VEC < dim ? u : 0) * (uint32_t)sizeof(RowVec<T, VEC>)));
+        x[v] = load_vec<true>(reinterpret_cast<const RowVec<T, VEC>*>(base + (uint32_t)(offset + (u * VEC < dim ? u : 0) * (uint32_t)sizeof(RowVec<T, VEC>))));
     }
 }
 template <int VEC, int G, int NV>
@@ -251,7 +251,7 @@ __device__ __forceinline__ void store_row(char* base, uint32_t offset, const flo
     for (int v = 0; v < NV; ++v) {
         const int u = lane + v * G;
         if (there && u * VEC < dim)
-            *reinterpret_cast<RowVec<T, VEC>*>(base + (uint32_t)(offset + u * (uint32_t)sizeof(RowVec<T, VEC>))) = narrow_vec<T, VEC>(y[v]);
+            store_vec<false>(reinterpret_cast<RowVec<T, VEC>*>(base + (uint32_t)(offset + u * (uint32_t)sizeof(RowVec<T, VEC>))), narrow_vec<T, VEC>(y[v]));
     }
 }
 
@@ -262,7 +262,7 @@ template <class T, int VEC, int G, int NV, int MODE>
 __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) {
     using V = RowVec<T, VEC>;
     constexpr int R = kWave / G;        // rows at a time
-    constexpr int U = NV == 1 ? 4 : 1;  // passes whose loads are in flight
+    constexpr int U = NV == 1 ? 5 : 1;  // passes whose loads are in flight
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % G;
     const int group = (threadIdx.x % kWave) / G;
