@@ -28,7 +28,7 @@ struct QkNorm {
     float* partials;  // backward: 2 * dim floats a block
     int64_t tokens;
     int q_heads, k_heads, dim, rot, interleaved;
-    int parts;  // waves that share a token's heads
+    int parts;  // waves that share a token's heads; above 1 only where tokens * parts is below 2^31
     float eps;
 };
 

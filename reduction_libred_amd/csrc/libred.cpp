@@ -1048,9 +1048,15 @@ namespace libred {
 red_status host_fail(hipError_t e, red_status code) { return fail(e, code); }
 
 red_status host_compute_units(int* dev, int* cu_count) {
+    // The device of this thread's last call, most of the time.
+    static thread_local int last = -1, last_units = 0;
+    if (last >= 0 && hipGetDevice(dev) == hipSuccess && *dev == last) {
+        *cu_count = last_units;
+        return RED_OK;
+    }
     DeviceInfo info;
     const red_status st = current_device(dev, &info);
-    if (st == RED_OK) *cu_count = info.cu_count;
+    if (st == RED_OK) *cu_count = last_units = info.cu_count, last = *dev;
     return st;
 }
 

@@ -255,6 +255,11 @@ __device__ __forceinline__ void store_row(char* base, uint32_t offset, const flo
     }
 }
 
+// One argument of every 64-byte line, so that all lines are asked for at once.
+__device__ __forceinline__ void ask_for_arguments(const QkNorm& a) {
+    asm volatile("" ::"s"(a.q.p), "s"(a.k_out.p), "s"(a.q_weight), "s"(a.tokens));
+}
+
 // With the weight folded into cosine and sine, an element of the result is
 //     r (x (w c) + partner (w_partner g)),
 // so the exchange of partners does not wait for the row's sum.
@@ -264,10 +269,11 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) 
     constexpr int R = kWave / G;        // rows at a time
     constexpr int U = NV == 1 ? 5 : 1;  // passes whose loads are in flight
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
+    ask_for_arguments(a);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % G;
     const int group = (threadIdx.x % kWave) / G;
     const int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave;
-    const int64_t t = a.parts == 1 ? id : id / a.parts;
+    const int64_t t = a.parts == 1 ? id : (uint32_t)id / (uint32_t)a.parts;
     if (t >= a.tokens) return;
     const Passes<T, R, VEC> rows = {a, group, lane};
     const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
@@ -341,6 +347,7 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     constexpr int R = kWave / G;
     constexpr int U = NV == 1 ? 2 : 1;
     __shared__ __align__(16) float lds[kQkNormWaves][kWaveFloats];
+    ask_for_arguments(a);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % G;
     const int group = (threadIdx.x % kWave) / G;
     float wq[NV][VEC], wk[NV][VEC], c[NV][VEC], g[NV][VEC], aq[NV][VEC], ak[NV][VEC];
@@ -357,7 +364,7 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_backward_kernel(Q
     const uint32_t out_q = rows.offset(a.q_out), out_k = rows.offset(a.k_out);
     const int64_t items = a.tokens * a.parts;
     for (int64_t id = (int64_t)blockIdx.x * kQkNormWaves + wave; id < items; id += (int64_t)gridDim.x * kQkNormWaves) {
-        const int64_t t = a.parts == 1 ? id : id / a.parts;
+        const int64_t t = a.parts == 1 ? id : (uint32_t)id / (uint32_t)a.parts;
         const int part = (int)(id - t * a.parts), per = (rows.all() + a.parts - 1) / a.parts;
         const int first = part * per, last = min(rows.all(), first + per);
         if (first >= last) continue;

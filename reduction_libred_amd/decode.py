@@ -133,13 +133,19 @@ _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_functions = {}
+
+
 def _call(name, device, stream, *args):
     """lib().name(*args, stream) with `device` current."""
     if _current_device() != device:
         with torch.cuda.device(device):
             return _call(name, device, stream, *args)
     handle = _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream, device)
-    st = getattr(lib(), name)(*args, handle)
+    f = _functions.get(name)
+    if f is None:
+        f = _functions[name] = getattr(lib(), name)
+    st = f(*args, handle)
     if st:
         raise RedError(name, st, lib().red_last_hip_error())
 
