@@ -361,11 +361,9 @@ red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
     k.drafted = a->drafted, k.u = a->u, k.r = a->r, k.count = a->draft_count;
     k.accepted = a->accepted, k.tokens = a->tokens;
     k.vocab = (int64_t)V, k.batch = (int)B, k.drafts = (int)K;
-    // Segments: 8 blocks a compute unit over the batch, of at least 1024 tokens.
-    size_t segs = ((size_t)cus * 8 + B - 1) / B;
-    if (segs > (V + 1023) / 1024) segs = (V + 1023) / 1024;
-    if (segs > (size_t)libred::kVerifyMaxSegs) segs = libred::kVerifyMaxSegs;
-    k.seg = (int64_t)((V + segs - 1) / segs);
+    // Segments of 1024 tokens, or as many times that as leave at most 256.
+    const size_t least = (V + libred::kVerifyMaxSegs - 1) / libred::kVerifyMaxSegs;
+    k.seg = (int64_t)((least + 1023) / 1024 * 1024);
     k.segs = (int)((V + (size_t)k.seg - 1) / (size_t)k.seg);
     void* sums = nullptr;
     st = host_scratch(dev, stream, B * (size_t)k.segs * sizeof(double), &sums);

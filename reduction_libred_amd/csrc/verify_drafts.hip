@@ -6,11 +6,13 @@
 //     w = p_n                where all were accepted:
 // the first token whose running sum of w passes r sum(w).
 //
-// Only row n of p and q is read as a whole: once for the sum, by `segs` blocks
-// a sequence (each finds n for itself, from at most two gathers a draft), and
-// once more in the one segment where the running sum passes its border, by a
-// second launch. Sums run in float64: float32 inputs differ exactly there, and
-// a border is then missed by less than 2^-40 of the sum whatever the order.
+// Only row n of p and q is read as a whole: once for its sums, a wave a
+// segment of 1024 tokens (each wave finds n for itself, from at most two
+// gathers a draft), and once more in the one segment where the running sum
+// passes its border, by a second launch, a block a sequence with 4 tokens a
+// thread. Sums run in float64: float32 inputs differ exactly there, and a
+// border is then missed by less than 2^-40 of the sum whatever the order.
+// Memory bounds the first launch, latency the second.
 #include "decode_common.hpp"
 
 namespace libred {
@@ -65,7 +67,6 @@ struct Verifier {
 // What a row's weights are made of.
 enum { kAll = 0, kLessRow = 1, kLessToken = 2 };
 
-template <class T>
 __device__ __forceinline__ double weight(float p, float q, int kind, bool token) {
     double w = (double)p;
     if (kind == kLessRow) w -= (double)q;
@@ -73,95 +74,102 @@ __device__ __forceinline__ double weight(float p, float q, int kind, bool token)
     return w < 0.0 ? 0.0 : w;  // a NaN stays one
 }
 
-// Sum over the block in a fixed order; every thread gets it.
-__device__ __forceinline__ double block_sum(double v, double* lds) {
-    v = group_combine<kWave>(v, AddF64());
-    __syncthreads();
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
-    __syncthreads();
-    double s = lds[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += lds[w];
-    return s;
-}
+constexpr int kStep = 1024;  // tokens of a wave at a time in the first launch, of a block in the second
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
     using V = Verifier<T>;
-    constexpr int N = V::kVec;
-    __shared__ double lds[kWaves];
+    constexpr int N = V::kVec, U = kStep / (kWave * N);
+    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));  // one argument of every 64-byte line
     const V v(a, blockIdx.y);
+    const int lane = threadIdx.x % kWave, seg = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (seg >= a.segs) return;
     const int n = v.accepted();
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.accepted[v.b] = n;
+    if (seg == 0 && lane == 0) a.accepted[v.b] = n;
     const int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
     const typename V::B *p = v.row_p(n), *q = kind == kLessRow ? v.row_q(n) : p;
-    const int64_t first = (int64_t)blockIdx.x * a.seg, last = min(first + a.seg, a.vocab);
+    const int64_t first = (int64_t)seg * a.seg, last = min(first + a.seg, a.vocab);
     double sum = 0.0;
-    int64_t i = first + threadIdx.x * N;
-    for (; i + N <= last; i += kThreads * N) {
-        const typename V::Vector x = *reinterpret_cast<const typename V::Vector*>(p + i);
-        typename V::Vector y = x;
-        if (kind == kLessRow) y = *reinterpret_cast<const typename V::Vector*>(q + i);
+    for (int64_t i0 = first; i0 < last; i0 += kStep) {
+        if (i0 + kStep <= last) {
+            typename V::Vector x[U], y[U];
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum += weight<T>(T::widen(x[j]), T::widen(y[j]), kind, i + j == token);
+            for (int u = 0; u < U; ++u) {
+                x[u] = *reinterpret_cast<const typename V::Vector*>(p + i0 + (u * kWave + lane) * N);
+                y[u] = *reinterpret_cast<const typename V::Vector*>(q + i0 + (u * kWave + lane) * N);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    sum += weight(T::widen(x[u][j]), T::widen(y[u][j]), kind, i0 + (u * kWave + lane) * N + j == token);
+        } else {
+            for (int64_t i = i0 + lane; i < last; i += kWave) sum += weight(T::widen(p[i]), T::widen(q[i]), kind, i == token);
+        }
     }
-    for (; i < last; ++i) {  // of one thread: the end of the segment
-        sum += weight<T>(T::widen(p[i]), T::widen(q[i]), kind, i == token);
-    }
-    sum = block_sum(sum, lds);
-    if (threadIdx.x == 0) a.sums[(int64_t)v.b * a.segs + blockIdx.x] = sum;
+    sum = group_combine<kWave>(sum, AddF64());
+    if (lane == 0) a.sums[(int64_t)v.b * a.segs + seg] = sum;
 }
 
-// Running sum over the threads of the block, this thread's value included.
-__device__ __forceinline__ double block_scan(double v, double* lds) {
+// Running sum over the threads of the block, this thread's value included; and
+// the whole sum. In a fixed order.
+__device__ __forceinline__ double block_scan(double v, double* lds, double* total) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    for (int o = 1; o < kWave; o <<= 1) {
-        const double x = __shfl_up(v, o);
-        if (lane >= o) v += x;
-    }
+    v += dpp_move<0x111, 0xF>(0.0, v);  // shifted by 1, 2, 4 and 8 in rows of 16
+    v += dpp_move<0x112, 0xF>(0.0, v);
+    v += dpp_move<0x114, 0xF>(0.0, v);
+    v += dpp_move<0x118, 0xF>(0.0, v);
+    v += dpp_move<0x142, 0xA>(0.0, v);  // rows 0 and 2 into 1 and 3
+    v += dpp_move<0x143, 0xC>(0.0, v);  // the first half into the second
     __syncthreads();
     if (lane == kWave - 1) lds[wave] = v;
     __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < wave; ++w) before += lds[w];
+    double before = 0.0, all = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) before = all;
+        all += lds[w];
+    }
+    *total = all;
     return before + v;
 }
 
-__device__ __forceinline__ int64_t block_min(int64_t v, int64_t* lds) {
-    for (int o = 1; o < kWave; o <<= 1) v = min(v, (int64_t)__shfl_xor((long long)v, o));
+// The first (or last) thread for which `is` holds, -1 if none.
+__device__ __forceinline__ int block_find(bool is, bool last, int* lds) {
+    const uint64_t mask = __ballot(is);
+    const int wave = threadIdx.x / kWave;
     __syncthreads();
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
+    if (threadIdx.x % kWave == 0)
+        lds[wave] = !mask ? -1 : wave * kWave + (last ? 63 - __clzll((long long)mask) : __ffsll((unsigned long long)mask) - 1);
     __syncthreads();
-    v = lds[0];
-    for (int w = 1; w < kWaves; ++w) v = min(v, lds[w]);
-    return v;
+    int found = -1;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        if (lds[w] >= 0 && (last || found < 0)) found = lds[w];
+    return found;
 }
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
     using V = Verifier<T>;
-    __shared__ double lds[kWaves];
-    __shared__ int64_t ids[kWaves];
-    __shared__ double before_seg;
+    constexpr int N = kStep / kThreads;  // tokens of a thread at a time
+    __shared__ double lds[kWaves], start;
+    __shared__ int ids[kWaves];
+    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));
     const V v(a, blockIdx.x);
-    const int n = a.accepted[v.b], tid = threadIdx.x;
+    const int tid = threadIdx.x;
+    double mine = tid < a.segs ? a.sums[(int64_t)v.b * a.segs + tid] : 0.0;
+    const int n = a.accepted[v.b];
+    const double r = (double)a.r[v.b];
     int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
     const typename V::B *p = v.row_p(n), *q = kind == kLessRow ? v.row_q(n) : p;
-    auto at = [&](int64_t i) { return weight<T>(T::widen(p[i]), T::widen(q[i]), kind, i == token); };
-    auto range_sum = [&](int64_t first, int64_t last) {  // of this thread's share of a segment
-        double s = 0.0;
-        for (int64_t i = first; i < last; ++i) s += at(i);
-        return s;
-    };
+    auto at = [&](int64_t i) { return weight(T::widen(p[i]), T::widen(q[i]), kind, i == token); };
 
     // The segment in which the running sum passes r times the whole.
-    double mine = tid < a.segs ? a.sums[(int64_t)v.b * a.segs + tid] : 0.0;
-    double run = block_scan(mine, lds);
-    if (tid == kThreads - 1) before_seg = run;
-    __syncthreads();
-    double total = before_seg;
+    double total, all;
+    double run = block_scan(mine, lds, &total);
     if (!(total > 0.0)) {
         // p is nowhere above q: the weights are p itself.
         kind = kAll;
@@ -170,45 +178,55 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
             const int64_t f = s * a.seg, e = min(f + a.seg, a.vocab);
             double x = 0.0;
             for (int64_t i = f + tid; i < e; i += kThreads) x += at(i);
-            x = block_sum(x, lds);
-            if (tid == s) mine = x;
+            block_scan(x, lds, &all);
+            if (tid == s) mine = all;
         }
-        __syncthreads();
-        run = block_scan(mine, lds);
-        __syncthreads();
-        if (tid == kThreads - 1) before_seg = run;
-        __syncthreads();
-        total = before_seg;
+        run = block_scan(mine, lds, &total);
     }
-    const double border = (double)a.r[v.b] * total;
-    constexpr int64_t kNone = INT64_MAX;
-    int64_t seg = block_min(tid < a.segs && mine > 0.0 && run > border ? tid : kNone, ids);
+    const double border = r * total;
+    const bool some = tid < a.segs && mine > 0.0;
+    int seg = block_find(some && run > border, false, ids);
     // No segment passes the border where r is 1 or more: the last with weight.
-    const bool past = seg == kNone;
-    if (past) seg = -block_min(tid < a.segs && mine > 0.0 ? -tid : kNone, ids);
+    const bool past = seg < 0;
+    if (past) seg = block_find(some, true, ids);
     int64_t pick = -1;
     if (seg >= 0 && total > 0.0) {
+        if (tid == seg) start = seg == 0 ? 0.0 : run - mine;
         __syncthreads();
-        if (tid == seg) before_seg = run - mine;
-        if (tid == 0 && seg == 0) before_seg = 0.0;
-        __syncthreads();
-        const int64_t f = seg * a.seg, e = min(f + a.seg, a.vocab), share = (e - f + kThreads - 1) / kThreads;
-        const int64_t i0 = min(f + tid * share, e), i1 = min(i0 + share, e);
-        const double own = range_sum(i0, i1);
-        double s = before_seg + (block_scan(own, lds) - own);
-        int64_t hit = kNone, top = kNone;
-        for (int64_t i = i0; i < i1; ++i) {
-            const double w = at(i);
-            s += w;
-            if (w > 0.0) {
-                top = -i;
-                if (hit == kNone && s > border) hit = i;
+        double before = start;
+        const int64_t f = seg * a.seg, e = min(f + a.seg, a.vocab);
+        for (int64_t i0 = f; i0 < e; i0 += kStep) {
+            double w[N], own = 0.0;
+            const int64_t i = i0 + tid * N;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                w[j] = at(min(i + j, e - 1));
+                if (i + j >= e) w[j] = 0.0;
+                own += w[j];
             }
+            double s = before + (block_scan(own, lds, &all) - own);
+            int hit = -1, top = -1;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                s += w[j];
+                if (w[j] > 0.0) {
+                    top = j;
+                    if (hit < 0 && s > border) hit = j;
+                }
+            }
+            // Of the last element with weight so far in case none passes: the
+            // two orders of summation may round the border apart.
+            const int who = past ? -1 : block_find(hit >= 0, false, ids);
+            const int end = who >= 0 ? who : block_find(top >= 0, true, ids);
+            if (end >= 0) {
+                if (tid == end) ids[0] = who >= 0 ? hit : top;
+                __syncthreads();
+                pick = i0 + end * N + ids[0];
+                __syncthreads();
+            }
+            if (who >= 0) break;
+            before += all;
         }
-        hit = past ? kNone : block_min(hit, ids);
-        // None where the two orders of summation round the border apart.
-        const int64_t end = block_min(top, ids);
-        pick = hit != kNone ? hit : end != kNone ? -end : -1;
     }
     for (int i = tid; i <= a.drafts; i += kThreads)
         a.tokens[(int64_t)v.b * (a.drafts + 1) + i] = i < n ? v.drafted(i) : i == n ? pick : -1;
@@ -216,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
 
 template <class T>
 hipError_t verify(const Verify& a, hipStream_t stream) {
-    verify_sum_kernel<T><<<dim3((unsigned)a.segs, (unsigned)a.batch), kThreads, 0, stream>>>(a);
+    verify_sum_kernel<T><<<dim3((unsigned)(a.segs + kWaves - 1) / kWaves, (unsigned)a.batch), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     verify_pick_kernel<T><<<(unsigned)a.batch, kThreads, 0, stream>>>(a);
