@@ -365,6 +365,10 @@ red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
     const size_t least = (V + libred::kVerifyMaxSegs - 1) / libred::kVerifyMaxSegs;
     k.seg = (int64_t)((least + 1023) / 1024 * 1024);
     k.segs = (int)((V + (size_t)k.seg - 1) / (size_t)k.seg);
+    // Waves: 32 a compute unit over the batch, each with segments in turn (192
+    // rows of 131071: 33 us; 16 and 48 a compute unit 35, a wave a segment 40).
+    const size_t waves = ((size_t)cus * 32 + B - 1) / B, all = ((size_t)k.segs + 3) / 4;
+    k.blocks = (int)(all < (waves + 3) / 4 ? all : (waves + 3) / 4);
     void* sums = nullptr;
     st = host_scratch(dev, stream, B * (size_t)k.segs * sizeof(double), &sums);
     if (st != RED_OK) return st;

@@ -82,13 +82,15 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
     constexpr int N = V::kVec, U = kStep / (kWave * N);
     asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));  // one argument of every 64-byte line
     const V v(a, blockIdx.y);
-    const int lane = threadIdx.x % kWave, seg = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave;
+    int seg = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (seg >= a.segs) return;
     const int n = v.accepted();
     if (seg == 0 && lane == 0) a.accepted[v.b] = n;
     const int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
     const typename V::B *p = v.row_p(n), *q = kind == kLessRow ? v.row_q(n) : p;
+    for (; seg < a.segs; seg += gridDim.x * kWaves) {
     const int64_t first = (int64_t)seg * a.seg, last = min(first + a.seg, a.vocab);
     double sum = 0.0;
     for (int64_t i0 = first; i0 < last; i0 += kStep) {
@@ -96,8 +98,8 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
             typename V::Vector x[U], y[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                x[u] = *reinterpret_cast<const typename V::Vector*>(p + i0 + (u * kWave + lane) * N);
-                y[u] = *reinterpret_cast<const typename V::Vector*>(q + i0 + (u * kWave + lane) * N);
+                x[u] = __builtin_nontemporal_load(reinterpret_cast<const typename V::Vector*>(p + i0 + (u * kWave + lane) * N));
+                y[u] = __builtin_nontemporal_load(reinterpret_cast<const typename V::Vector*>(q + i0 + (u * kWave + lane) * N));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -110,6 +112,7 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
     }
     sum = group_combine<kWave>(sum, AddF64());
     if (lane == 0) a.sums[(int64_t)v.b * a.segs + seg] = sum;
+    }
 }
 
 // Running sum over the threads of the block, this thread's value included; and
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
 
 template <class T>
 hipError_t verify(const Verify& a, hipStream_t stream) {
-    verify_sum_kernel<T><<<dim3((unsigned)(a.segs + kWaves - 1) / kWaves, (unsigned)a.batch), kThreads, 0, stream>>>(a);
+    verify_sum_kernel<T><<<dim3((unsigned)a.blocks, (unsigned)a.batch), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     verify_pick_kernel<T><<<(unsigned)a.batch, kThreads, 0, stream>>>(a);
