@@ -237,6 +237,12 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     a.cache = to_cache(*c);
     a.k = to_heads(*k), a.v = to_heads(*v);
     a.slots = slots, a.tokens = (int64_t)tokens;
+    if (c->pages == 0) {
+        // A read of nothing: no slot is inside, but the kernel's loads are made
+        // all the same (and dropped), so they get memory to read.
+        a.cache.k = k->data, a.cache.v = v->data;
+        a.cache.k_scales = a.cache.v_scales = reinterpret_cast<float*>(const_cast<int64_t*>(slots));
+    }
     const size_t block_tokens = (size_t)(libred::kCacheWaves * 64 / lanes);
     const size_t groups = (tokens + block_tokens - 1) / block_tokens;
     if (groups > 0x7fffffff) return RED_ERR_INVALID_ARG;

@@ -99,8 +99,8 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_write_kernel(CacheRo
                                                       (isk ? p : p - c.heads) * s.hs);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                x[u][v] = V{};
-                if ((lane + v * G) * VEC < c.dim) x[u][v] = src[lane + v * G];
+                const int at = lane + v * G;
+                x[u][v] = load_vec<true>(src + (at * VEC < c.dim ? at : 0));
             }
         }
 #pragma unroll
@@ -121,6 +121,7 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_write_kernel(CacheRo
                 uint32_t top = 0;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
+                    // Lanes beyond the row hold its first elements again.
                     widen_vec<T, VEC>(x[u][v], f[v]);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j)
@@ -177,18 +178,22 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_read_kernel(CacheRow
             const bool isk = p < c.heads;
             const int h = isk ? p : p - c.heads;
             const typename C::bits* src = static_cast<const typename C::bits*>(isk ? c.k : c.v) + row + h * c.head_stride;
-            s[u] = 0.f;
-            if constexpr (C::kScaled)
-                if (inside) s[u] = (isk ? c.k_scales : c.v_scales)[scale + h * c.scale_head_stride];
-            w[u] = u32x2{0, 0};
+            if constexpr (C::kScaled) s[u] = (isk ? c.k_scales : c.v_scales)[scale + h * c.scale_head_stride];
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                x[u][v] = V{};
-                b[u][v] = 0;
-                if (!inside || (lane + v * G) * VEC >= c.dim) continue;
-                if constexpr (!C::kScaled) x[u][v] = reinterpret_cast<const V*>(src)[lane + v * G];
-                else if constexpr (VEC == 8) w[u] = reinterpret_cast<const u32x2*>(src)[lane];
-                else b[u][v] = src[lane + v * G];
+                const int at = (lane + v * G) * VEC < c.dim ? lane + v * G : 0;
+                if constexpr (!C::kScaled) x[u][v] = reinterpret_cast<const V*>(src)[at];
+                else if constexpr (VEC == 8) w[u] = reinterpret_cast<const u32x2*>(src)[at];
+                else b[u][v] = src[at];
+            }
+        }
+        if (!inside) {  // the loads were of the cache's first row: zeros instead
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u] = 0.f;
+                w[u] = u32x2{0, 0};
+#pragma unroll
+                for (int v = 0; v < NV; ++v) x[u][v] = V{}, b[u][v] = 0;
             }
         }
 #pragma unroll
@@ -202,14 +207,14 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_read_kernel(CacheRow
             for (int v = 0; v < NV; ++v) {
                 if ((lane + v * G) * VEC >= c.dim) continue;
                 if constexpr (!C::kScaled) {
-                    dst[lane + v * G] = x[u][v];
+                    store_vec<true>(dst + lane + v * G, x[u][v]);
                 } else if constexpr (VEC == 8) {
                     float f[8];
                     C::unpack4(w[u][0], f);
                     C::unpack4(w[u][1], f + 4);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] *= s[u];
-                    dst[lane] = narrow_vec<T, 8>(f);
+                    store_vec<true>(dst + lane, narrow_vec<T, 8>(f));
                 } else {
                     float f[4];
                     C::unpack4(b[u][v], f);

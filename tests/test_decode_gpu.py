@@ -241,6 +241,20 @@ def test_cache_write_and_read(case):
         assert torch.equal(now, was)
 
 
+@pytest.mark.parametrize("kind", [I8, E4M3, F16])
+def test_cache_without_pages(kind):
+    pg = torch.empty(0, 2, 4, 64, dtype=kind, device=DEV)
+    sc = dict(k_scales=torch.empty(0, 2, 4, device=DEV), v_scales=torch.empty(0, 2, 4, device=DEV)) if kind in R.TOP else {}
+    slots = torch.tensor([0, -1, 5], device=DEV)
+    kv = torch.ones(3, 2, 64, dtype=F16, device=DEV)
+    rl.red_cache_write(kv, kv, slots, pg, pg, **sc)
+    for x in rl.red_cache_read(pg, pg, slots, F16, k_out=kv, **sc):
+        assert x.shape == (3, 2, 64) and not x.any()
+    table, lens = torch.zeros(1, 3, dtype=torch.int32, device=DEV), torch.tensor([7], dtype=torch.int32, device=DEV)
+    out, lse = rl.red_tree_attention(torch.ones(1, 2, 2, 64, dtype=F16, device=DEV), pg, pg, table, lens, 1.0, **sc)
+    assert not out.any() and (lse == -math.inf).all()
+
+
 # ---------------------------------------------------------------------------
 # Attention over the cache
 # ---------------------------------------------------------------------------
