@@ -312,7 +312,8 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     k.scale = (a->scale == 0.f ? 1.f : a->scale < 0.f ? -a->scale : a->scale) * 1.4426950408889634f;
     k.flip = a->scale < 0.f ? 0x80008000u : 0u;
     k.page16 = (uint32_t)(c.pages > 1 ? c.page_stride / unit : 0), k.place16 = (uint32_t)(c.places > 1 ? c.place_stride / unit : 0);
-    k.inv_places = 1.0 / (double)c.places;
+    while ((size_t)1 << k.places_shift < c.places) ++k.places_shift;
+    k.places_factor = (uint32_t)(((uint64_t)1 << (30 + k.places_shift)) / c.places + 1);
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());

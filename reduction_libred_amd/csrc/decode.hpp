@@ -87,7 +87,10 @@ struct TreeAttention {
     int blocks;  // 0: one block a segment, of at most one tile, that writes the output
     float scale;  // magnitude, times log2(e)
     uint32_t page16, place16;  // strides of the cache's pages and places in units of 16 bytes
-    double inv_places;  // 1 / places: (t + 0.5) * that, cut, is the page of token t below 2^30 exactly
+    // Token t < 2^30 is in page (4 t factor >> 32) >> shift of its sequence:
+    // shift = ceil(log2 places), factor = 2^(30 + shift) / places cut, plus 1.
+    uint32_t places_factor;
+    int places_shift;
     unsigned int flip;  // 0x80008000 where the scale is negative: the sign of q
     unsigned int keep;  // 0 where the scale is 0 (q is then, and scale is that of 1)
     // The sums of a segment's piece in block w are number w + segment, `rows`

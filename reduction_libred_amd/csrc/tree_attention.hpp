@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     static_assert(WM == 1 || WT == 1, "a team is a wave or the block");
     constexpr int HELD = S::kHeld, NL = S::kLoads;
     __shared__ __align__(16) char tile[S::kBytes];
-    __shared__ uint32_t offs_all[WT][2][TS];  // where the rows of a tile's tokens start, in 16 bytes
+    __shared__ uint32_t offs_all[WT][4][TS];  // where the rows of a tile's tokens start, in 16 bytes
     __shared__ uint64_t held[WT][4];           // which of them are in the cache
     __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
     __shared__ float red[2][WM * WT][RW];
@@ -292,26 +292,33 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     if (rows_in || direct) {
 
     // The team's tiles are numbered from 0 at `origin`, TT tokens apart. A tile
-    // goes through three steps: lookup() asks for the page of this thread's
-    // token (tm < TS); settle() notes where the token's rows start; fetch()
-    // asks for the rows. A page outside the cache is not followed: its tokens
+    // goes through three steps: lookup() asks for the page of a lane's token;
+    // settle() notes where the token's rows start; fetch() asks for the rows. A page outside the cache is not followed: its tokens
     // read as zeros, as those from `last` on do.
     const int origin = first + wt * TS;
     const int32_t* pages = A->table + b * A->table_stride;
-    auto page_of = [&](int t) { return (int)(((double)t + 0.5) * A->inv_places); };
-    auto lookup = [&](int i) -> int {
-        const int t = origin + i * TT + tm;
-        return tm < TS && t < last ? pages[page_of(t)] : -1;
+    // Up to 64 tokens at once: AT_ONCE tiles, a lane a token, by one wave.
+    constexpr int AT_ONCE = kWave / TS;
+    const int ahead = lane / TS, mine_t = lane % TS;  // this lane's tile of them, and token
+    const bool looks = WM == 1 || wm == 0;
+    int page = -1, at = 0;
+    auto lookup = [&](int i) {
+        if (!looks) return;
+        const int t = origin + (i + ahead) * TT + mine_t;
+        const int number = __umulhi((uint32_t)t << 2, A->places_factor) >> A->places_shift;
+        at = t - number * A->cache.places;
+        page = t < last ? pages[number] : -1;
     };
-    auto settle = [&](int i, int page) -> int64_t {
-        const int t = origin + i * TT + tm, at = t - page_of(t) * A->cache.places;
+    int64_t scale_at = -1;  // of this lane's token in the tiles settled last
+    auto settle = [&](int i) {
+        if (!looks) return;
         const bool in = page >= 0 && page < A->cache.pages;
         const uint64_t all = __ballot(in);
-        if (tm < TS) {
-            offs[i % 2][tm] = in ? (uint32_t)page * A->page16 + (uint32_t)at * A->place16 : 0;
-            if (tm == 0) held[wt][i % 4] = TS == 64 ? all : all & 0xFFFFFFFFu;
-        }
-        return in ? (int64_t)((uint64_t)(uint32_t)page * (uint32_t)A->cache.scale_page_stride + (uint64_t)(uint32_t)at * (uint32_t)A->cache.scale_place_stride) : -1;
+        const int slot = (i + ahead) % 4;
+        offs[slot][mine_t] = in ? (uint32_t)page * A->page16 + (uint32_t)at * A->place16 : 0;
+        if (mine_t == 0) held[wt][slot] = TS == 64 ? all : all >> (32 * ahead) & 0xFFFFFFFFu;
+        if constexpr (kScaled)
+            scale_at = in ? (int64_t)((uint64_t)(uint32_t)page * (uint32_t)A->cache.scale_page_stride + (uint64_t)(uint32_t)at * (uint32_t)A->cache.scale_place_stride) : -1;
     };
     constexpr uint64_t kAllIn = TS == 64 ? ~0ull : 0xFFFFFFFFull;
     const char* const kh = static_cast<const char*>(A->cache.k) + h * A->cache.head_stride * C::kBytes;
@@ -328,10 +335,13 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         rk[j] = *reinterpret_cast<const u32x4*>(kh + at);
         rv[j] = *reinterpret_cast<const u32x4*>(vh + at);
     };
-    auto fetch_scales = [&](int64_t scale) {
+    // Of tile i, by the lanes that looked its tokens up.
+    auto fetch_scales = [&](int i) {
         if constexpr (kScaled) {
-            sk = 0.f, sv = 1.f;
-            if (tm < TS && scale >= 0) sk = ksh[scale], sv = vsh[scale];
+            if (looks && ahead == i % AT_ONCE) {
+                sk = 0.f, sv = 1.f;
+                if (scale_at >= 0) sk = ksh[scale_at], sv = vsh[scale_at];
+            }
         }
     };
     // Infinities and NaN in the values of nodes are left out of the products
@@ -347,13 +357,13 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         }
         return v;
     };
-    auto fetch = [&](int i, int64_t scale) {
+    auto fetch = [&](int i) {
         uint32_t off[NL];
 #pragma unroll
-        for (int j = 0; j < NL; ++j) off[j] = offs[i % 2][row_at(j)];
+        for (int j = 0; j < NL; ++j) off[j] = offs[i % 4][row_at(j)];
 #pragma unroll
         for (int j = 0; j < NL; ++j) fetch_one(j, off[j]);
-        fetch_scales(scale);
+        fetch_scales(i);
     };
     auto store = [&](int i) {
         char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
@@ -362,15 +372,15 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         const uint64_t in = held[wt][i % 4];
         const bool part = uniform((int)(in != kAllIn)) || DP != D;
         if constexpr (kScaled) {
-            if (tm < TS) {
+            if (looks && ahead == i % AT_ONCE) {
                 // A scale of 0 (a row of zeros) is taken as 2^-100.
                 const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
                 auto& f = factors[wt][i % HELD];
-                f[0][tm] = sk * A->scale;
-                f[1][tm] = __builtin_amdgcn_logf(c);
+                f[0][mine_t] = sk * A->scale;
+                f[1][mine_t] = __builtin_amdgcn_logf(c);
                 // 1 where the scale is no number (the exponent says so), so
                 // that a row that does not see the token adds 0 times it.
-                f[2][tm] = c < __builtin_inff() ? 1.f / c : 1.f;
+                f[2][mine_t] = c < __builtin_inff() ? 1.f / c : 1.f;
             }
         }
 #pragma unroll
@@ -412,8 +422,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     };
 
     const int tiles = rows_in && last > origin ? (last - origin + TT - 1) / TT : 0;
-    int64_t scale_next = -1;  // of the tile to be asked for next
-    const int p0 = lookup(0), p1 = lookup(1), p2 = HELD == 2 ? lookup(2) : -1;
+    lookup(0);
     // This lane's row, looked at while the pages are on their way.
     const int row = (rb * WM + wm) * RW + n;
     uint64_t seen;  // the nodes it sees
@@ -436,33 +445,38 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 
     __syncthreads();  // the segment before is done with the LDS
     if (tid == 0) odd = 0;
-    const int64_t scale0 = settle(0, p0);
-    scale_next = settle(1, p1);
+    settle(0);
     __syncthreads();
-    if (tiles > 0) fetch(0, scale0);
+    if (tiles > 0) fetch(0);
     Acc o[DT];
     float m = -__builtin_inff(), l = 0.f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = Acc{};
 
     if constexpr (HELD == 2) {
-        __syncthreads();
-        const int64_t scale2 = settle(2, p2);
+        lookup(1);
+        settle(1);
         if (tiles > 0) store(0);
-        if (tiles > 1) fetch(1, scale_next);
-        scale_next = scale2;
+        lookup(2);
+        __syncthreads();
+        if (tiles > 1) fetch(1);
+        settle(2);
         __syncthreads();
     }
     for (int i = 0; i < tiles; ++i) {
         const int base = origin + i * TT;
         // With one tile in the LDS it is written before its products, with
-        // two the next is written beside them.
-        const int page = lookup(i + HELD + 1);
+        // two the next is written beside them. The pages of tiles to come are
+        // looked up here and settled at the end, before they are fetched in
+        // the next turn.
+        const bool look = HELD == 2 || i % 2 == 0;
+        constexpr int TO_COME = HELD == 2 ? 3 : 2;
+        if (look) lookup(i + TO_COME);
         if constexpr (HELD == 1) {
             wave_lds_fence();
             store(i);
             wave_lds_fence();
-            if (i + 1 < tiles) fetch(i + 1, scale_next);
+            if (i + 1 < tiles) fetch(i + 1);
         }
         const char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
         const char* const ldsv = ldsk + TS * S::kPitchK;
@@ -483,7 +497,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
         auto score = [&](int s, int x) -> auto& { return sc[(s * X + x) / OX]; };
         if constexpr (HELD == 2) {
             if (i + 1 < tiles) store(i + 1);
-            if (i + 2 < tiles) fetch(i + 2, scale_next);
+            if (i + 2 < tiles) fetch(i + 2);
         }
         if constexpr (kScaled) {
 #pragma unroll
@@ -560,7 +574,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] = Mma<VT>::dot(values(s, k, d), u32x4{pf[s][4 * k], pf[s][4 * k + 1], pf[s][4 * k + 2], pf[s][4 * k + 3]}, o[d]);
-        scale_next = settle(i + HELD + 1, page);
+        if (look) settle(i + TO_COME);
         team_sync();
     }
 
