@@ -332,8 +332,8 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     auto fetch_one = [&](int j, uint32_t off) {
         const int c = column_at(j);
         const uint64_t at = (uint64_t)off * 16 + (c < D ? c : 0) * C::kBytes;
-        rk[j] = *reinterpret_cast<const u32x4*>(kh + at);
-        rv[j] = *reinterpret_cast<const u32x4*>(vh + at);
+        rk[j] = load_vec<HELD == 1>(reinterpret_cast<const u32x4*>(kh + at));
+        rv[j] = load_vec<HELD == 1>(reinterpret_cast<const u32x4*>(vh + at));
     };
     // Of tile i, by the lanes that looked its tokens up.
     auto fetch_scales = [&](int i) {
