@@ -24,24 +24,22 @@ template <class T, int LANES, int WAVES>
 __global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a, int rows_a_block) {
     constexpr int kRowsHere = kThreads / kWave / WAVES, kSlices = WAVES * kWave / LANES;
     __shared__ f32x4 sums[WAVES > 1 ? kThreads : 1];
+    asm volatile("" ::"s"(a.out), "s"(a.out_batch), "s"(a.cache.dim), "s"(a.lens), "s"(a.plan));  // one of every 64-byte line
     const int D = a.cache.dim, group = a.group, M = a.nodes * group, heads = a.cache.heads;
     const int tid = threadIdx.x % (WAVES * kWave), wl = threadIdx.x % kWave;
-    const int64_t all_rows = (int64_t)a.batch * heads * M;
-    const int64_t id = (int64_t)blockIdx.x * kRowsHere + threadIdx.x / (WAVES * kWave);
-    if (id >= all_rows) return;  // whole waves; with several waves a row, whole blocks
-    const int rw = (int)(id % M), h = (int)(id / M % heads), b = (int)(id / M / heads);
+    const int rw = blockIdx.x * kRowsHere + __builtin_amdgcn_readfirstlane(threadIdx.x / (WAVES * kWave)), h = blockIdx.y, b = blockIdx.z;
+    if (rw >= M) return;  // whole waves; with several waves a row, whole blocks
     const int node = rw / group, g = rw - node * group;
     int count;
     sequence_tokens(a, b, &count);
-    const int64_t per = a.plan[a.batch + 1], start = a.plan[b];
-    const int seg_tiles = a.plan[b + 1] - (int)start, per_seq = heads * a.row_blocks;
+    const int per = a.plan[a.batch + 1], start = a.plan[b], seg_tiles = a.plan[b + 1] - start, per_seq = heads * a.row_blocks;
     const int rb = rw / rows_a_block, seg = h * a.row_blocks + rb;
-    const int64_t first = start * per_seq + (int64_t)seg * seg_tiles;
+    const int first = start * per_seq + seg * seg_tiles;
     int pieces = 0;
     int64_t slot = 0;
     if (node < count && seg_tiles > 0) {
-        const int64_t w0 = first / per, w1 = (first + seg_tiles - 1) / per;
-        pieces = (int)(w1 - w0) + 1;
+        const int w0 = first / per, w1 = (first + seg_tiles - 1) / per;
+        pieces = w1 - w0 + 1;
         slot = w0 + (int64_t)b * per_seq + seg;
     }
     const int64_t row0 = slot * rows_a_block + (rw - rb * rows_a_block);
@@ -49,27 +47,33 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a, int 
     float m = -__builtin_inff(), l = 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < pieces; k0 += kWave) {
-        float2 ml = make_float2(-__builtin_inff(), 0.f);
-        if (k0 + wl < pieces) ml = a.part_ml[row0 + (int64_t)(k0 + wl) * rows_a_block];
+        const int here = min(pieces - k0, kWave);
+        // The first sums are asked for together with the weights.
+        f32x4 x[4];
+        auto load = [&](int k1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = k0 + min(k1 + u * kSlices + slice, here - 1);
+                x[u] = *reinterpret_cast<const f32x4*>(a.part_o + (row0 + (int64_t)k * rows_a_block) * D + (c < D ? c : 0));
+            }
+        };
+        float2 ml = a.part_ml[row0 + (int64_t)(k0 + min(wl, here - 1)) * rows_a_block];
+        load(0);
+        if (wl >= here) ml = make_float2(-__builtin_inff(), 0.f);
         const float to = fmaxf(m, group_combine<kWave>(ml.x, MaxOp()));
         const float f = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - to);
         const float w = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(ml.x - to);
         l = l * f + group_combine<kWave>(w * ml.y, AddOp());
         v *= f;
         m = to;
-        const int here = min(pieces - k0, kWave);
         for (int k1 = 0; k1 < here; k1 += 4 * kSlices) {
-            f32x4 x[4];
-            float wk[4];
+            if (k1 > 0) load(k1);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int k = k1 + u * kSlices + slice, kk = min(k, here - 1);
-                wk[u] = __shfl(w, kk);
-                x[u] = *reinterpret_cast<const f32x4*>(a.part_o + (row0 + (int64_t)(k0 + kk) * rows_a_block) * D + (c < D ? c : 0));
-                if (k >= here) x[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                const int k = k1 + u * kSlices + slice;
+                const float wk = __shfl(w, min(k, here - 1));
+                if (k < here) v += wk * x[u];
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v += wk[u] * x[u];
         }
     }
     // Slices: those of a wave, then those of the block's waves.
@@ -103,10 +107,13 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a, int 
 template <class T, int LANES>
 hipError_t combine_lanes(const TreeAttention& a, int rows_a_block, hipStream_t stream) {
     const int64_t rows = (int64_t)a.batch * a.cache.heads * a.nodes * a.group;
-    if (rows < 2048)
-        combine_kernel<T, LANES, 4><<<(unsigned)rows, kThreads, 0, stream>>>(a, rows_a_block);
+    const unsigned int M = (unsigned)(a.nodes * a.group);
+    const bool few = rows < 2048;
+    const dim3 grid(few ? M : (M + 3) / 4, (unsigned)a.cache.heads, (unsigned)a.batch);
+    if (few)
+        combine_kernel<T, LANES, 4><<<grid, kThreads, 0, stream>>>(a, rows_a_block);
     else
-        combine_kernel<T, LANES, 1><<<(unsigned)((rows + 3) / 4), kThreads, 0, stream>>>(a, rows_a_block);
+        combine_kernel<T, LANES, 1><<<grid, kThreads, 0, stream>>>(a, rows_a_block);
     return hipGetLastError();
 }
 
