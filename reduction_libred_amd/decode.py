@@ -150,23 +150,52 @@ def _call(name, device, stream, *args):
         raise RedError(name, st, lib().red_last_hip_error())
 
 
-def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
+def _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out):
+    """Raise what is wrong with the arguments, if anything is."""
     device = _any(name, "q", q, _FLOATS, 3, "(tokens, q heads, dim)")
-    dtype, (tokens, heads, dim) = q.dtype, q.shape
+    dtype, (tokens, _, dim) = q.dtype, q.shape
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError(f"{name}: k must be (tokens, k heads, dim)")
     _rows(name, "k", k, dtype, device, (tokens, k.shape[1], dim))
-    half = freq.shape[0] if isinstance(freq, torch.Tensor) and freq.dim() == 1 else -1
-    q_out = q.new_empty(q.shape) if q_out is None else _rows(name, "q_out", q_out, dtype, device, q.shape)
-    k_out = k.new_empty(k.shape) if k_out is None else _rows(name, "k_out", k_out, dtype, device, k.shape)
-    pos, freq = _whole(name, "pos", pos, _INT64, device, (tokens,)), _whole(name, "freq", freq, _FLOAT32, device, (half,))
-    qw = 0 if q_weight is None else _whole(name, "q_weight", q_weight, dtype, device, (dim,))
-    kw = 0 if k_weight is None else _whole(name, "k_weight", k_weight, dtype, device, (dim,))
-    kh = k.shape[1]
+    for what, x, shape in (("q_out", q_out, q.shape), ("k_out", k_out, k.shape)):
+        if x is not None:
+            _rows(name, what, x, dtype, device, shape)
+    _whole(name, "pos", pos, _INT64, device, (tokens,))
+    _whole(name, "freq", freq, _FLOAT32, device, (freq.shape[0] if isinstance(freq, torch.Tensor) and freq.dim() == 1 else -1,))
+    for what, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if x is not None:
+            _whole(name, what, x, dtype, device, (dim,))
+
+
+def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
+    try:
+        dtype, device, (tokens, heads, dim) = q.dtype, q.get_device(), q.shape
+        k_tokens, kh, k_dim = k.shape
+        half, = freq.shape
+        fine = (device >= 0 and dtype in _FLOATS and k.dtype is dtype and k.get_device() == device and k_tokens == tokens and
+                k_dim == dim and pos.dtype is _INT64 and pos.shape == (tokens,) and pos.get_device() == device and
+                pos.is_contiguous() and freq.dtype is _FLOAT32 and freq.get_device() == device and freq.is_contiguous())
+        q0, q1, q2 = q.stride()
+        k0, k1, k2 = k.stride()
+        fine = fine and (q2 == k2 == 1 or dim <= 1)
+        for w in (q_weight, k_weight):
+            if w is not None:
+                fine = fine and w.dtype is dtype and w.shape == (dim,) and w.get_device() == device and w.is_contiguous()
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine or q_out is not None or k_out is not None:
+        _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None:
+        k_out = torch.empty_like(k)
+    a0, a1, _ = q_out.stride()
+    b0, b1, _ = k_out.stride()
     return device, q_out, k_out, _pack_qk_norm(
-        TYPES[dtype], 1 if interleaved else 0, tokens, dim, 2 * half, eps, q.data_ptr(), heads, *q.stride()[:2],
-        k.data_ptr(), kh, *k.stride()[:2], q_out.data_ptr(), heads, *q_out.stride()[:2], k_out.data_ptr(), kh,
-        *k_out.stride()[:2], qw, kw, pos, freq)
+        TYPES[dtype], 1 if interleaved else 0, tokens, dim, 2 * half, eps, q.data_ptr(), heads, q0, q1, k.data_ptr(), kh, k0,
+        k1, q_out.data_ptr(), heads, a0, a1, k_out.data_ptr(), kh, b0, b1,
+        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(), pos.data_ptr(),
+        freq.data_ptr())
 
 
 def _heads(x):
@@ -195,38 +224,62 @@ def red_qk_norm_rope_backward(dq, dk, q, k, pos, freq, q_weight=None, k_weight=N
     device, q_grad, k_grad, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
     _rows(name, "dq", dq, q.dtype, device, q.shape)
     _rows(name, "dk", dk, q.dtype, device, k.shape)
-    dqw, dkw = torch.empty((2, q.shape[2]), dtype=_FLOAT32, device=q.device).unbind(0)
+    dqw = torch.empty(q.shape[2], dtype=_FLOAT32, device=q.device)
+    dkw = torch.empty_like(dqw)
     _call(name, device, stream, args, _heads(dq), _heads(dk), dqw.data_ptr(), dkw.data_ptr())
     return q_grad, k_grad, dqw, dkw
 
 
-def _cache(name, k_pages, v_pages, k_scales, v_scales):
-    """-> (device, the fields of a PagedCache)"""
+def _cache_check(name, k_pages, v_pages, k_scales, v_scales):
+    """Raise what is wrong with a cache, if anything is."""
     device = _any(name, "k_pages", k_pages, _CACHES, 4, "(pages, heads, places, dim)")
-    dtype, shape, strides = k_pages.dtype, k_pages.shape, k_pages.stride()
+    dtype, shape = k_pages.dtype, k_pages.shape
     _rows(name, "v_pages", v_pages, dtype, device, shape)
-    if v_pages.stride() != strides:
+    if v_pages.stride() != k_pages.stride():
         raise ValueError(f"{name}: k_pages and v_pages must have the same strides")
-    kind = TYPES[dtype]
-    scaled = kind >= 3
+    scaled = TYPES[dtype] >= 3
     if scaled != (k_scales is not None) or scaled != (v_scales is not None):
         raise ValueError(f"{name}: 8-bit caches take k_scales and v_scales, 16-bit ones do not")
-    ks = vs = 0
-    scale_strides = (0, 0, 0)
     if scaled:
         for what, x in (("k_scales", k_scales), ("v_scales", v_scales)):
             if not isinstance(x, torch.Tensor) or x.dtype is not _FLOAT32 or x.get_device() != device or x.shape != shape[:3]:
                 raise ValueError(f"{name}: {what} must be float32 {tuple(shape[:3])} on cuda:{device}")
-        scale_strides = k_scales.stride()
-        if v_scales.stride() != scale_strides:
+        if k_scales.stride() != v_scales.stride():
             raise ValueError(f"{name}: k_scales and v_scales must have the same strides")
-        ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+
+
+_NO_SCALES = (0, 0, 0)
+
+
+def _cache(name, k_pages, v_pages, k_scales, v_scales):
+    """-> (device, the fields of a PagedCache)"""
+    try:
+        dtype, device, shape, strides = k_pages.dtype, k_pages.get_device(), k_pages.shape, k_pages.stride()
+        kind = TYPES.get(dtype, 0)
+        fine = (device >= 0 and kind > 0 and len(shape) == 4 and v_pages.dtype is dtype and v_pages.get_device() == device and
+                v_pages.shape == shape and v_pages.stride() == strides and strides[3] == 1)
+        ks = vs = 0
+        scale_strides = _NO_SCALES
+        if kind >= 3:
+            scale_strides = k_scales.stride()
+            ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+            fine = (fine and k_scales.dtype is v_scales.dtype is _FLOAT32 and k_scales.get_device() == device and
+                    v_scales.get_device() == device and k_scales.shape == v_scales.shape == shape[:3] and
+                    v_scales.stride() == scale_strides)
+        else:
+            fine = fine and k_scales is v_scales is None
+    except AttributeError:
+        fine = False
+    if not fine:
+        _cache_check(name, k_pages, v_pages, k_scales, v_scales)
     return device, (k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, kind, *shape, *strides[:3], *scale_strides)
 
 
 def _slots(name, slots, k_pages, device):
+    """-> (address of the slots, how many, the shape of their rows)"""
     n = slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else -1
-    return _whole(name, "slots", slots, _INT64, device, (n,)), n, (n, k_pages.shape[1], k_pages.shape[3])
+    _, heads, _, dim = k_pages.shape
+    return _whole(name, "slots", slots, _INT64, device, (n,)), n, (n, heads, dim)
 
 
 def red_cache_write(k, v, slots, k_pages, v_pages, k_scales=None, v_scales=None, stream=None):
@@ -238,10 +291,16 @@ def red_cache_write(k, v, slots, k_pages, v_pages, k_scales=None, v_scales=None,
     name = "red_cache_write"
     device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
     at, tokens, shape = _slots(name, slots, k_pages, device)
-    _any(name, "k", k, _HALVES, 3, "(tokens, heads, dim)")
-    _rows(name, "k", k, k.dtype, device, shape)
-    _rows(name, "v", v, k.dtype, device, shape)
-    _call(name, device, stream, _pack_cache(*c), TYPES[k.dtype], _heads(k), _heads(v), at, tokens)
+    dtype = k.dtype if isinstance(k, torch.Tensor) else None
+    if dtype not in _HALVES:
+        _any(name, "k", k, _HALVES, 3, "(tokens, heads, dim)")
+    _rows(name, "k", k, dtype, device, shape)
+    _rows(name, "v", v, dtype, device, shape)
+    k0, k1, _ = k.stride()
+    v0, v1, _ = v.stride()
+    heads = shape[1]
+    _call(name, device, stream, _pack_cache(*c), TYPES[dtype], _pack_heads(k.data_ptr(), heads, k0, k1),
+          _pack_heads(v.data_ptr(), heads, v0, v1), at, tokens)
 
 
 def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None, k_out=None, v_out=None, stream=None):
@@ -253,9 +312,19 @@ def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None,
     if dtype not in _HALVES:
         raise TypeError(f"{name}: dtype must be torch.float16 or torch.bfloat16")
     at, tokens, shape = _slots(name, slots, k_pages, device)
-    k_out = k_pages.new_empty(shape, dtype=dtype) if k_out is None else _rows(name, "k_out", k_out, dtype, device, shape)
-    v_out = k_pages.new_empty(shape, dtype=dtype) if v_out is None else _rows(name, "v_out", v_out, dtype, device, shape)
-    _call(name, device, stream, _pack_cache(*c), TYPES[dtype], _heads(k_out), _heads(v_out), at, tokens)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    else:
+        _rows(name, "k_out", k_out, dtype, device, shape)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    else:
+        _rows(name, "v_out", v_out, dtype, device, shape)
+    k0, k1, _ = k_out.stride()
+    v0, v1, _ = v_out.stride()
+    heads = shape[1]
+    _call(name, device, stream, _pack_cache(*c), TYPES[dtype], _pack_heads(k_out.data_ptr(), heads, k0, k1),
+          _pack_heads(v_out.data_ptr(), heads, v0, v1), at, tokens)
     return k_out, v_out
 
 
@@ -272,23 +341,31 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     (batch, nodes, q heads) float32); rows that see nothing hold 0 and -inf."""
     name = "red_tree_attention"
     device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
-    _any(name, "q", q, _HALVES, 4, "(batch, nodes, q heads, dim)")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.dtype not in _HALVES:
+        _any(name, "q", q, _HALVES, 4, "(batch, nodes, q heads, dim)")
     dtype, shape = q.dtype, q.shape
     batch, nodes, heads, dim = shape
-    if dim != k_pages.shape[3]:
-        raise ValueError(f"{name}: q must be (batch, nodes, q heads, {k_pages.shape[3]})")
-    _rows(name, "q", q, dtype, device, shape)
+    _, _, places, width = k_pages.shape
+    if dim != width:
+        raise ValueError(f"{name}: q must be (batch, nodes, q heads, {width})")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
     cols = table.shape[1]
+    q0, q1, q2, q3 = q.stride()
+    if q.get_device() != device or (q3 != 1 and dim > 1):
+        _rows(name, "q", q, dtype, device, shape)
     _rows(name, "table", table, _INT32, device, (batch, cols))
-    out = q.new_empty(shape) if out is None else _rows(name, "out", out, dtype, device, shape)
-    lse = q.new_empty((batch, nodes, heads), dtype=_FLOAT32)
+    if out is None:
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+    else:
+        _rows(name, "out", out, dtype, device, shape)
+    o0, o1, o2, _ = out.stride()
+    lse = torch.empty((batch, nodes, heads), dtype=_FLOAT32, device=q.device)
     mask = 0 if tree_mask is None else _whole(name, "tree_mask", tree_mask, _INT64, device, (batch, nodes))
     count = 0 if node_count is None else _whole(name, "node_count", node_count, _INT32, device, (batch,))
     _call(name, device, stream, _pack_attention(
-        TYPES[dtype], scale, batch, nodes, heads, cols * k_pages.shape[2] if max_len is None else max_len, q.data_ptr(),
-        out.data_ptr(), lse.data_ptr(), *q.stride()[:3], *out.stride()[:3], *c, table.data_ptr(), cols, table.stride(0),
+        TYPES[dtype], scale, batch, nodes, heads, cols * places if max_len is None else max_len, q.data_ptr(), out.data_ptr(),
+        lse.data_ptr(), q0, q1, q2, o0, o1, o2, *c, table.data_ptr(), cols, table.stride(0),
         _whole(name, "lens", lens, _INT32, device, (batch,)), mask, count))
     return out, lse
 
@@ -303,17 +380,18 @@ def red_verify_drafts(p, q, drafted, u, r, draft_count=None, stream=None):
     ones, the drawn one, then -1)."""
     name = "red_verify_drafts"
     device = _any(name, "p", p, _FLOATS, 3, "(batch, drafts + 1, vocab)")
-    dtype, (batch, steps, vocab) = p.dtype, p.shape
+    dtype, (batch, steps, vocab), (p0, p1, _) = p.dtype, p.shape, p.stride()
     if steps < 1:
         raise ValueError(f"{name}: p must be (batch, drafts + 1, vocab)")
     drafts = steps - 1
     qp = q0 = q1 = 0
     if q is not None:
         qp, (q0, q1, _) = _rows(name, "q", q, dtype, device, (batch, drafts, vocab)).data_ptr(), q.stride()
-    at = _whole(name, "drafted", drafted, _INT64, device, (batch, drafts))
-    up, rp = _whole(name, "u", u, _FLOAT32, device, (batch, drafts)), _whole(name, "r", r, _FLOAT32, device, (batch,))
+    at, up = _whole(name, "drafted", drafted, _INT64, device, (batch, drafts)), _whole(name, "u", u, _FLOAT32, device, (batch, drafts))
+    rp = _whole(name, "r", r, _FLOAT32, device, (batch,))
     count = 0 if draft_count is None else _whole(name, "draft_count", draft_count, _INT32, device, (batch,))
-    accepted, tokens = p.new_empty(batch, dtype=_INT32), p.new_empty((batch, steps), dtype=_INT64)
-    _call(name, device, stream, _pack_verify(TYPES[dtype], batch, drafts, vocab, p.data_ptr(), *p.stride()[:2], qp, q0, q1,
-                                             at, up, rp, count, accepted.data_ptr(), tokens.data_ptr()))
+    accepted = torch.empty(batch, dtype=_INT32, device=p.device)
+    tokens = torch.empty((batch, steps), dtype=_INT64, device=p.device)
+    _call(name, device, stream, _pack_verify(TYPES[dtype], batch, drafts, vocab, p.data_ptr(), p0, p1, qp, q0, q1, at, up, rp,
+                                             count, accepted.data_ptr(), tokens.data_ptr()))
     return accepted, tokens
