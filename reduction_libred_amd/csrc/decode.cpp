@@ -130,9 +130,11 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     k.q_heads = (int)a->q.heads, k.k_heads = (int)a->k.heads, k.dim = (int)D;
     k.rot = (int)a->rot, k.interleaved = a->interleaved != 0, k.eps = a->eps;
     // Waves: a token's heads are shared by several where there are few tokens,
-    // until there are 16 waves a compute unit or a wave has one pass left.
+    // until there are 4 waves a compute unit or a wave has one pass left (1000
+    // tokens x 40 heads, forward / backward: 8.2 / 13.9 us; with 16, where each
+    // works out its token's angles for two passes, 10.0 / 18.0).
     const int passes = rows == 0 ? 1 : (rows + 64 / lanes - 1) / (64 / lanes);
-    const size_t want = (size_t)cus * 16;
+    const size_t want = (size_t)cus * 4;
     size_t parts = T >= want || T == 0 ? 1 : (want + T - 1) / T;
     if (parts > (size_t)passes) parts = passes;
     k.parts = (int)parts;
