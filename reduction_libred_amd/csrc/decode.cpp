@@ -317,15 +317,15 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     while ((size_t)1 << k.places_shift < c.places) ++k.places_shift;
     k.places_factor = (uint32_t)(((uint64_t)1 << (30 + k.places_shift)) / c.places + 1);
     const size_t M = N * G;
-    const libred::AttentionShape shape = libred::attention_shape((int)M);
+    const libred::AttentionShape shape = libred::attention_shape((int)M, (int)D);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());
     // One block a segment where none has more than one tile; else as many as
-    // the card holds at once (two of 4 waves a compute unit), or one a tile.
+    // the card holds at once, or one a tile.
     const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
     const size_t segments = B * c.heads * (size_t)k.row_blocks;
     if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;
     if (tiles > 1) {
-        const size_t hold = (size_t)cus * 2;
+        const size_t hold = (size_t)cus * (size_t)libred::attention_blocks((int)M, (int)D);
         const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
         k.blocks = (int)blocks;
         const size_t rows = (blocks + segments) * (size_t)shape.rows(), plan = (B + 2 + 3) / 4 * 4;

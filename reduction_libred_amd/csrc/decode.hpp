@@ -108,10 +108,18 @@ struct AttentionShape {
     constexpr int tokens() const { return waves_t * step; }
 };
 constexpr AttentionShape kFewestRows = {16, 1, 4, 32}, kFewRows = {32, 1, 4, 32}, kManyRows = {32, 4, 1, 64};
+// Heads of more than 128 elements: 32 rows a wave do not fit the registers.
+constexpr AttentionShape kWideRows = {16, 4, 1, 32};
+constexpr int kNarrowHeads = 128;
 // The shape for `rows` rows of a kv head.
-constexpr AttentionShape attention_shape(int rows) {
-    return rows <= kFewestRows.rows() ? kFewestRows : rows <= kFewRows.rows() ? kFewRows : kManyRows;
+constexpr AttentionShape attention_shape(int rows, int dim) {
+    return rows <= kFewestRows.rows() ? kFewestRows
+           : dim > kNarrowHeads       ? kWideRows
+           : rows <= kFewRows.rows()  ? kFewRows
+                                      : kManyRows;
 }
+// Blocks that a compute unit holds at once.
+constexpr int attention_blocks(int rows, int dim) { return rows <= kFewestRows.rows() && dim > kNarrowHeads ? 1 : 2; }
 // Joins the pieces of every row into the output (rows_a_block: the shape's).
 hipError_t launch_attention_combine(int type, const TreeAttention& a, int rows_a_block, hipStream_t stream);
 hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream);

@@ -178,7 +178,7 @@ struct AttentionTile {
 };
 
 template <class T, class C, int DP, int RW, int WM, int WT, int TS>
-__global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attention_kernel(TreeAttention a) {
+__global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 2 : 1) void tree_attention_kernel(TreeAttention a) {
     using S = AttentionTile<C, DP, RW, WM, WT, TS>;
     constexpr bool kScaled = C::kBytes == 1;
     using VT = std::conditional_t<kScaled, F16, T>;
@@ -297,9 +297,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 ? 2 : 1) void tree_attenti
     // read as zeros, as those from `last` on do.
     const int origin = first + wt * TS;
     const int32_t* pages = A->table + b * A->table_stride;
-    // Up to 64 tokens at once: AT_ONCE tiles, a lane a token, by one wave.
-    constexpr int AT_ONCE = kWave / TS;
-    const int ahead = lane / TS, mine_t = lane % TS;  // this lane's tile of them, and token
+    // AT_ONCE tiles at once, a lane a token, by one wave.
+    constexpr int AT_ONCE = HELD == 2 ? 1 : kWave / TS;
+    const int ahead = AT_ONCE == 1 ? 0 : lane / TS, mine_t = lane % TS;  // this lane's tile of them, and token
     const bool looks = WM == 1 || wm == 0;
     int page = -1, at = 0;
     auto lookup = [&](int i) {
@@ -711,8 +711,9 @@ template <class T, class C, int DP>
 hipError_t launch_attention_dim(const TreeAttention& a, hipStream_t stream) {
     const int rows = a.nodes * a.group;
     if (rows <= kFewestRows.rows()) return launch_attention_shape<T, C, DP, 16, 1, 4, 32>(a, stream);
-    if (rows <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 32, 1, 4, 32>(a, stream);
-    return launch_attention_shape<T, C, DP, 32, 4, 1, 64>(a, stream);
+    if constexpr (DP > kNarrowHeads) return launch_attention_shape<T, C, DP, 16, 4, 1, 32>(a, stream);
+    else if (rows <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 32, 1, 4, 32>(a, stream);
+    else return launch_attention_shape<T, C, DP, 32, 4, 1, 64>(a, stream);
 }
 
 template <class T, class C>
