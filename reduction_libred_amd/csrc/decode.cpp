@@ -317,7 +317,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     while ((size_t)1 << k.places_shift < c.places) ++k.places_shift;
     k.places_factor = (uint32_t)(((uint64_t)1 << (30 + k.places_shift)) / c.places + 1);
     const size_t M = N * G;
-    const libred::AttentionShape shape = libred::attention_shape((int)M, (int)D);
+    const libred::AttentionShape shape = libred::attention_shape((int)M, (int)D, c.type == RED_F16 || c.type == RED_BF16 ? 2 : 1);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());
     // One block a segment where none has more than one tile; else as many as
     // the card holds at once, or one a tile.

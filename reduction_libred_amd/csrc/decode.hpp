@@ -106,17 +106,35 @@ struct AttentionShape {
     int wave_rows, waves_m, waves_t, step;
     constexpr int rows() const { return wave_rows * waves_m; }
     constexpr int tokens() const { return waves_t * step; }
+    constexpr bool is(const AttentionShape& o) const {
+        return wave_rows == o.wave_rows && waves_m == o.waves_m && waves_t == o.waves_t && step == o.step;
+    }
 };
-constexpr AttentionShape kFewestRows = {16, 1, 4, 32}, kFewRows = {32, 1, 4, 32}, kManyRows = {32, 4, 1, 64};
-// Heads of more than 128 elements: 32 rows a wave do not fit the registers.
-constexpr AttentionShape kWideRows = {16, 4, 1, 32};
-constexpr int kNarrowHeads = 128;
-// The shape for `rows` rows of a kv head.
-constexpr AttentionShape attention_shape(int rows, int dim) {
-    return rows <= kFewestRows.rows() ? kFewestRows
-           : dim > kNarrowHeads       ? kWideRows
-           : rows <= kFewRows.rows()  ? kFewRows
-                                      : kManyRows;
+constexpr AttentionShape kFewestRows = {16, 1, 4, 32}, kFewRows = {32, 1, 4, 32}, kHalfRows = {16, 4, 1, 32},
+                         kManyRows = {32, 4, 1, 64};
+constexpr int kNarrowHeads = 128, kNarrowPairs = 96;
+// The shape for `rows` rows of a kv head of `dim` elements, cached in `bytes`
+// each. Few rows share the queries and split the tokens among a block's waves,
+// many rows split the rows and share the tokens; 16 rows a wave read every
+// tile of LDS twice as often, 32 rows need twice the registers: they spill
+// from 97 elements of 16 bits (17 to 32 rows), and do not fit beyond 128.
+// Microseconds of 8 sequences of 3000 to 8000 tokens, 4 kv heads:
+//   rows, heads, cache     kFewRows  kHalfRows  kManyRows
+//   32,    64, bf16          16.3      19.7
+//   32,    96, bf16          20.9      22.8
+//   32,   128, bf16          33.4      23.9       31.5
+//   64,    64, bf16 / e4m3             19.4 / 24.6   22.4 / 25.5
+//   64,   128, bf16 / e4m3             26.0 / 27.3   32.0 / 32.2
+//   128,   64, bf16                    29.5       24.7
+//   128,  128, bf16                    39.5       36.4
+// 32 sequences of 1500 to 16384 tokens, 8 kv heads of 128 in int8, 32 rows:
+// kFewRows 120, kHalfRows 234.
+constexpr AttentionShape attention_shape(int rows, int dim, int bytes) {
+    return rows <= kFewestRows.rows()                                    ? kFewestRows
+           : dim > kNarrowHeads                                          ? kHalfRows
+           : rows <= kFewRows.rows() && (bytes == 1 || dim <= kNarrowPairs) ? kFewRows
+           : rows <= kHalfRows.rows()                                    ? kHalfRows
+                                                                         : kManyRows;
 }
 // Blocks that a compute unit holds at once.
 constexpr int attention_blocks(int rows, int dim) { return rows <= kFewestRows.rows() && dim > kNarrowHeads ? 1 : 2; }

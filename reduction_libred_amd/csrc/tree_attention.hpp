@@ -6,8 +6,8 @@
 // float32. All query heads of a kv head and all nodes are rows of one product,
 // so a tile of keys and values is read once for all of them.
 //
-// Products use the 32x32x16 matrix instruction (16x16x32 for up to 16 rows,
-// with half the registers and exponentials), transposed: S^T = K Q^T puts one
+// Products use the 32x32x16 matrix instruction (16x16x32 where a wave has 16
+// rows, with half the registers and exponentials), transposed: S^T = K Q^T puts one
 // row n in each lane column (lane % 32), 16 of 32 tokens in a lane and the
 // other 16 in lane ^ 32, so maxima and sums are lane-local but for one
 // exchange. The exponentials are then already the operand of O^T = V^T P^T: a
@@ -17,9 +17,10 @@
 // A team of waves walks its tokens in tiles: while one tile is computed, the
 // next is on its way from memory into registers (rows looked up through the
 // page table a tile earlier), and is converted to 16 bits on its way into the
-// LDS, once for all its waves. Up to 32 rows a team is one wave and needs no
-// barrier; the block's waves take tiles in turn and join at the end. 8-bit elements stay whole: the scale of a key
-// multiplies its scores, and the scale of a value joins the exponent,
+// LDS, once for all its waves. With few rows a team is one wave and needs no
+// barrier; the block's waves take tiles in turn and join at the end. 8-bit
+// elements stay whole: the scale of a key multiplies its scores, and the scale
+// of a value joins the exponent,
 //     w_t = 2^(s'_t + log2 c_t - M),  out = sum_t w_t code_t / sum_t w_t / c_t,
 // so that w stays in range whatever the scales are. P is rounded to the type
 // of V in the product (float16 for 8-bit caches, which hold those exactly):
@@ -133,9 +134,6 @@ __device__ __forceinline__ float join_parts(float v, F op) {
 
 // A value that is the same in all lanes, as one the compiler knows to be.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
-}
 
 // The kernel's arguments, as memory that the compiler has not seen yet: what is
 // needed at the two ends of a segment is loaded there and holds no registers in
@@ -710,10 +708,15 @@ hipError_t launch_attention_shape(const TreeAttention& a, hipStream_t stream) {
 template <class T, class C, int DP>
 hipError_t launch_attention_dim(const TreeAttention& a, hipStream_t stream) {
     const int rows = a.nodes * a.group;
-    if (rows <= kFewestRows.rows()) return launch_attention_shape<T, C, DP, 16, 1, 4, 32>(a, stream);
-    if constexpr (DP > kNarrowHeads) return launch_attention_shape<T, C, DP, 16, 4, 1, 32>(a, stream);
-    else if (rows <= kFewRows.rows()) return launch_attention_shape<T, C, DP, 32, 1, 4, 32>(a, stream);
-    else return launch_attention_shape<T, C, DP, 32, 4, 1, 64>(a, stream);
+    const AttentionShape s = attention_shape(rows, DP, C::kBytes);
+    if (s.is(kFewestRows)) return launch_attention_shape<T, C, DP, 16, 1, 4, 32>(a, stream);
+    if (s.is(kHalfRows)) return launch_attention_shape<T, C, DP, 16, 4, 1, 32>(a, stream);
+    if constexpr (DP <= kNarrowHeads) {
+        if constexpr (C::kBytes == 1 || DP <= kNarrowPairs)
+            if (s.is(kFewRows)) return launch_attention_shape<T, C, DP, 32, 1, 4, 32>(a, stream);
+        return launch_attention_shape<T, C, DP, 32, 4, 1, 64>(a, stream);
+    }
+    return hipErrorInvalidValue;  // not reached: the shapes above are all that wide heads take
 }
 
 template <class T, class C>
