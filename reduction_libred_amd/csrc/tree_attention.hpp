@@ -156,6 +156,15 @@ struct AttentionTile {
     static constexpr int kRows = RW * WM;
     static constexpr int kPerLoad = 16 / C::kBytes;  // elements of a 16-byte load
     static constexpr int kRowLoads = DP / kPerLoad;
+    // Place p * kRowLoads + j of a row in the LDS holds the 8 elements that are
+    // part p of load j: the two parts of a load of 8-bit elements, 32 bytes
+    // once widened, are stored apart so that 8 lanes store 128 bytes in a row.
+    // (Side by side they met in the banks, a third of the LDS's cycles: 16
+    // sequences of 2000 to 8000 tokens, 8 kv heads x 4 rows of 128, e4m3, 40.1
+    // us / 37.9.) The order of k's elements is q's too; dim_of() undoes v's.
+    static constexpr int dim_of(int c) {
+        return kPerLoad == 8 ? c : c / 8 % kRowLoads * kPerLoad + c / 8 / kRowLoads * 8 + c % 8;
+    }
     // A team of waves shares a tile of TS tokens: the waves_m waves of
     // different rows, or one wave, which then needs no barriers.
     static constexpr int kTeam = kWave * WM;
@@ -291,8 +300,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
 
     // The team's tiles are numbered from 0 at `origin`, TT tokens apart. A tile
     // goes through three steps: lookup() asks for the page of a lane's token;
-    // settle() notes where the token's rows start; fetch() asks for the rows. A page outside the cache is not followed: its tokens
-    // read as zeros, as those from `last` on do.
+    // settle() notes where the token's rows start; fetch() asks for the rows. A
+    // page outside the cache is not followed: its tokens read as zeros, as
+    // those from `last` on do. (Two tiles on their way, with twice the
+    // registers: 37.9 us / 40.8 in the case above, where nothing spilled.)
     const int origin = first + wt * TS;
     const int32_t* pages = A->table + b * A->table_stride;
     // AT_ONCE tiles at once, a lane a token, by one wave.
@@ -387,15 +398,15 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             __builtin_amdgcn_sched_barrier(0);  // one row's conversion at a time: registers
             if (NL * S::kTeam == TS * S::kRowLoads || e < TS * S::kRowLoads) {
                 if (part && !((in >> t & 1) && c * S::kPerLoad < D)) rk[j] = rv[j] = u32x4{0, 0, 0, 0};
-                u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * (S::kPerLoad * 2));
-                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
+                u32x4* dk = reinterpret_cast<u32x4*>(ldsk + t * S::kPitchK + c * 16);
+                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * 16);
                 if constexpr (kScaled) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const u32x2 k0 = C::template widen4<T>(rk[j][2 * p]), k1 = C::template widen4<T>(rk[j][2 * p + 1]);
                         const u32x2 v0 = C::template widen4<VT>(rv[j][2 * p]), v1 = C::template widen4<VT>(rv[j][2 * p + 1]);
-                        dk[p] = u32x4{k0[0], k0[1], k1[0], k1[1]};
-                        dv[p] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+                        dk[p * S::kRowLoads] = u32x4{k0[0], k0[1], k1[0], k1[1]};
+                        dv[p * S::kRowLoads] = u32x4{v0[0], v0[1], v1[0], v1[1]};
                     }
                 } else {
                     *dk = rk[j];
@@ -408,9 +419,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             for (int j = 0; j < NL; ++j) {
                 const int e = j * S::kTeam + tm, t = e / S::kRowLoads, c = e % S::kRowLoads;
                 if (e >= TS * S::kRowLoads || base + t < len) continue;
-                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * (S::kPerLoad * 2));
+                u32x4* dv = reinterpret_cast<u32x4*>(ldsv + t * S::kPitchV + c * 16);
 #pragma unroll 1
-                for (int p = 0; p < S::kPerLoad / 8; ++p) dv[p] = clean(dv[p]);
+                for (int p = 0; p < S::kPerLoad / 8; ++p) dv[p * S::kRowLoads] = clean(dv[p * S::kRowLoads]);
             }
         }
     };
@@ -435,7 +446,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         if (live) q += b * A->q_batch + node * A->q_node + (h * group + g) * A->q_head;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const int d = s * KD + part * 8;
+            const int d = S::dim_of(s * KD + part * 8);
             qf[s] = *reinterpret_cast<const u32x4*>(q + (d < D ? d : 0));
             qf[s] = (qf[s] ^ A->flip) & (live && d < D ? A->keep : 0u);
         }
@@ -636,7 +647,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int y = 0; y < OX; y += 4) {
-                    const int c = d * RW + PARTS * y + 4 * part;
+                    const int c = S::dim_of(d * RW + PARTS * y + 4 * part);
                     if (c < D) put4(row, c, f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]}, ll);
                 }
         }
@@ -653,7 +664,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int y = 0; y < OX; y += 4)
-                *reinterpret_cast<f32x4*>(ob + d * RW + PARTS * y + 4 * part) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]} * f;
+                *reinterpret_cast<f32x4*>(ob + S::dim_of(d * RW + PARTS * y + 4 * part)) = f32x4{o[d][y], o[d][y + 1], o[d][y + 2], o[d][y + 3]} * f;
         __syncthreads();
         for (int e = tid; e < RW * (DP / 4); e += S::kThreads) {
             const int rn = e / (DP / 4), c = e % (DP / 4) * 4, rw = rb * S::kRows + rn;
