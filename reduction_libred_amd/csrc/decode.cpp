@@ -101,7 +101,9 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     if (empty && !sums) return RED_OK;
 
     // Elements a lane holds: those of a 16-byte load where every row allows
-    // it, 4 elements where 8 bytes (16-bit types) do, else 1.
+    // it, 4 elements where 8 bytes (16-bit types) do, else 1 (16384 tokens x 40
+    // heads of 128 in bf16, forward / backward: 8 elements 60.8 / 96.9 us, 4
+    // elements 65.6 / 114.8, 1 element 164 / 242).
     auto fits = [&](size_t v) {
         const size_t b = v * es;
         if (D % v != 0 || !rows_on(a->q, T, es, b) || !rows_on(a->k, T, es, b) || !rows_on(a->q_out, T, es, b) ||
@@ -149,6 +151,8 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
         const hipError_t e = launch(vec, lanes, k, false, (int)blocks, stream);
         return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
     }
+    // Blocks that go through tokens in turn: 6 a compute unit (16384 tokens x
+    // 40 heads of 128: 97 us; 4 a compute unit 114, 8 a compute unit 100).
     const size_t cap = (size_t)cus * 6;
     if (blocks > cap) blocks = cap;
     void* partials = nullptr;
@@ -228,6 +232,9 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     if (tokens > 0 && (slots == nullptr || !is_aligned(slots, 8))) return RED_ERR_INVALID_ARG;
     if (tokens == 0 || (write && c->pages == 0)) return RED_OK;
     const size_t cb = type_bytes(c->type);
+    // 8 elements a lane, or 1 where rows do not start on 16 bytes (8 in 8 bits;
+    // 32768 tokens x 16 rows of 128, e4m3: write / read 44.8 / 36.1 us, with 1
+    // element 104 / 64).
     const int vec = D % 8 == 0 && rows_on(*k, tokens, 2, 16) && rows_on(*v, tokens, 2, 16) && cache_rows_on(*c, 8 * cb) ? 8 : 1;
     int lanes = 8;
     while ((size_t)(lanes * vec) < D) lanes *= 2;
@@ -249,7 +256,9 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     const size_t groups = (tokens + block_tokens - 1) / block_tokens;
     if (groups > 0x7fffffff) return RED_ERR_INVALID_ARG;
     // A block takes all heads of its tokens; where that makes too few blocks
-    // for 4 a compute unit the heads are shared, down to one row a group.
+    // for 4 a compute unit the heads are shared, down to one row a group (20
+    // tokens x 16 rows, write / read: 3.4 / 3.1 us, not shared 9.1 / 5.1; 32768
+    // tokens: 44.8 / 36.1, shared 69 / 49).
     const size_t want = (size_t)cus * 4, pairs = 2 * c->heads;
     size_t parts = groups >= want ? 1 : (want + groups - 1) / groups;
     if (parts > pairs) parts = pairs;

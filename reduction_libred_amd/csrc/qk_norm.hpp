@@ -15,6 +15,11 @@
 // lane: the product and its reduction to an eighth of a turn in float64 (a
 // position of 2^20 leaves a float32 angle no correct digit behind the point),
 // then the Taylor sums of sine and cosine.
+//
+// Memory bounds both passes. 16384 tokens of 32 + 8 heads of 128 in bf16:
+// forward 336 MB in 60.8 us (5.5 TB/s; a copy of that size reaches 6.15),
+// backward 503 MB in 96.9 us (5.2 TB/s) and 4.8 us for the sum of the weights'
+// partials. 5 tokens take 4.4 us, one trip to memory after another.
 #pragma once
 
 #include "decode_common.hpp"
