@@ -153,8 +153,10 @@ red_status red_cache_read(const red_paged_cache *cache, int type, const red_head
  * boundaries, the rows of out in that order; lse: batch * nodes * q_heads
  * floats. The cache's dim is a multiple of 16 up to 256, its rows start on
  * 16-byte boundaries, those of one head within 64 GiB of each other; the
- * strides of its scales are below 2^32. nodes <= 64, batch and q_heads <= 65535, and batch * kv heads
- * * max_len / 32 below 2^31 (more is RED_ERR_INVALID_ARG). max_len is the
+ * strides of its scales are below 2^32. nodes <= 64, batch and q_heads <=
+ * 65535, max_len <= 2^30, and batch * kv heads * (max_len / 32) * (rows of a kv
+ * head / 64), each rounded up, below 2^31 (where it is not the call may return
+ * RED_ERR_INVALID_ARG). max_len is the
  * largest number of tokens, nodes included, that a sequence may have: it
  * shapes the launch, and tokens from it on (or beyond table_cols pages) are
  * not looked at. A page number outside the cache is not followed: its tokens

@@ -81,7 +81,10 @@ template <class T, class C, int VEC, int G, int NV>
 __global__ __launch_bounds__(kCacheWaves* kWave) void cache_write_kernel(CacheRows a) {
     using V = typename Vec<T, VEC>::type;
     constexpr int R = kWave / G;
-    constexpr int U = NV == 1 ? 4 : 1;  // rows a group has in flight
+    // Rows a group has in flight (8: 46.7 us where 4 take 43.5). Stores stay in
+    // the caches, for the attention that reads them next: past them the write
+    // took 45.8 us and a read after it 39.8 instead of 35.6.
+    constexpr int U = NV == 1 ? 4 : 1;
     const int lane = threadIdx.x % G;
     const int64_t t = (int64_t)blockIdx.x * (kCacheWaves * R) + threadIdx.x / G;
     if (t >= a.tokens) return;  // whole groups leave
