@@ -362,6 +362,20 @@ def test_tree_attention(case):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("kind", [None, I8, E4M3], ids=str)
+@pytest.mark.parametrize("dim", [48, 96, 112, 176])
+@pytest.mark.parametrize("nodes, hq, hk", [(8, 4, 2), (17, 2, 2), (8, 4, 1), (33, 1, 1), (32, 4, 2), (13, 5, 1)])
+def test_tree_attention_rows(nodes, hq, hk, dim, kind):
+    """Numbers of rows (16, 17, 32, 33, 64, 65) and heads on both sides of the
+    borders between the ways to share them among waves."""
+    dt = F16 if (nodes + dim) % 2 else BF16
+    case = ([70, 333], nodes, hq, hk, dim, 16, True, [nodes, max(nodes - 3, 1)], dt, kind or dt, "own")
+    say(case)
+    pg, sc, table, q, mask = attend_inputs(case, 17)
+    out, lse = attend(case, pg, sc, table, q, mask, dim ** -0.5)
+    check_attend(case, pg, sc, table, q, mask, dim ** -0.5, out, lse)
+
+
 @pytest.mark.parametrize("case", [ATTEND[3], ATTEND[5], ATTEND[15]], ids=str)
 @pytest.mark.parametrize("scale_of_v, scale", [(1e-20, 0.3), (1e15, -0.1), (1.0, 0.0)])
 def test_tree_attention_scales(case, scale_of_v, scale):
