@@ -102,8 +102,8 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
 
     // Elements a lane holds: those of a 16-byte load where every row allows
     // it, 4 elements where 8 bytes (16-bit types) do, else 1 (16384 tokens x 40
-    // heads of 128 in bf16, forward / backward: 8 elements 60.8 / 96.9 us, 4
-    // elements 65.6 / 114.8, 1 element 164 / 242).
+    // heads of 128 in bf16, forward / backward: 8 elements 60.8 / 90.9 us, 4
+    // elements 65.6 / 117, 1 element 164 / 249).
     auto fits = [&](size_t v) {
         const size_t b = v * es;
         if (D % v != 0 || !rows_on(a->q, T, es, b) || !rows_on(a->k, T, es, b) || !rows_on(a->q_out, T, es, b) ||
@@ -133,8 +133,8 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     k.rot = (int)a->rot, k.interleaved = a->interleaved != 0, k.eps = a->eps;
     // Waves: a token's heads are shared by several where there are few tokens,
     // until there are 4 waves a compute unit or a wave has one pass left (1000
-    // tokens x 40 heads, forward / backward: 8.2 / 13.9 us; with 16, where each
-    // works out its token's angles for two passes, 10.0 / 18.0).
+    // tokens x 40 heads, forward / backward: 8.2 / 13.7 us; with 16, where each
+    // works out its token's angles for two passes, 10.0 / 17.4; with 2, 9.8 / 15.6).
     const int passes = rows == 0 ? 1 : (rows + 64 / lanes - 1) / (64 / lanes);
     const size_t want = (size_t)cus * 4;
     size_t parts = T >= want || T == 0 ? 1 : (want + T - 1) / T;
@@ -152,7 +152,7 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
         return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
     }
     // Blocks that go through tokens in turn: 6 a compute unit (16384 tokens x
-    // 40 heads of 128: 97 us; 4 a compute unit 114, 8 a compute unit 100).
+    // 40 heads of 128: 91 us; 5 a compute unit 100, 8 a compute unit 95).
     const size_t cap = (size_t)cus * 6;
     if (blocks > cap) blocks = cap;
     void* partials = nullptr;
