@@ -352,6 +352,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     float sk = 0.f, sv = 1.f;
     auto row_at = [&](int j) { return min((j * S::kTeam + tm) / S::kRowLoads, TS - 1); };
     auto column_at = [&](int j) { return (j * S::kTeam + tm) % S::kRowLoads * S::kPerLoad; };
+    // Where a team is a wave its loads do not stay in the caches: all rows that
+    // read the token are in this block. Where it is the block they do, for the
+    // other blocks of rows. (Staying / not: 32 sequences x 32 rows 129 us / 121;
+    // 4 sequences x 512 rows 98.6 / 108.6.)
     auto fetch_one = [&](int j, uint32_t off) {
         const int c = column_at(j);
         const uint64_t at = (uint64_t)off * 16 + (c < D ? c : 0) * C::kBytes;
