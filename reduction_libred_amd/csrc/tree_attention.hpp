@@ -498,11 +498,12 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         // the next turn.
         const bool look = HELD == 2 || i % 2 == 0;
         constexpr int TO_COME = HELD == 2 ? 3 : 2;
-        if (look) lookup(i + TO_COME);
+        if constexpr (HELD == 2) lookup(i + TO_COME);
         if constexpr (HELD == 1) {
             wave_lds_fence();
             store(i);
             wave_lds_fence();
+            if (look) lookup(i + TO_COME);
             if (i + 1 < tiles) fetch(i + 1);
         }
         const char* const ldsk = tiles_lds + i % HELD * S::kTileBytes;
