@@ -495,7 +495,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         // With one tile in the LDS it is written before its products, with
         // two the next is written beside them. The pages of tiles to come are
         // looked up here and settled at the end, before they are fetched in
-        // the next turn.
+        // the next turn; by a team of one wave after it has its rows, since it
+        // would wait for the pages as well (32 sequences x 32 rows, int8: 121
+        // us / 115.5; the block's first wave alone looks, and that costs it
+        // nothing that the order would save).
         const bool look = HELD == 2 || i % 2 == 0;
         constexpr int TO_COME = HELD == 2 ? 3 : 2;
         if constexpr (HELD == 2) lookup(i + TO_COME);
