@@ -328,22 +328,36 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     const size_t M = N * G;
     const libred::AttentionShape shape = libred::attention_shape((int)M, (int)D, c.type == RED_F16 || c.type == RED_BF16 ? 2 : 1);
     k.row_blocks = (int)((M + shape.rows() - 1) / shape.rows());
-    // One block a segment where none has more than one tile; else as many as
-    // the card holds at once, or one a tile.
+    // As many blocks as the card holds at once, or one a tile; or one a segment,
+    // which needs no joining. The cost of the first is the joining: a launch
+    // and latency, and the sums written and read. The cost of the second are
+    // the turns that its blocks take more (of a wave's 32 tokens, or of a
+    // block's 32 or 64), if few: lengths may differ more than the host knows.
+    // 4 segments of 2 / 3 / 4 / 8 tiles (us, kernels alone):
+    //   shared, 32 rows of 128, int8    14.0   12.6   13.0   13.4
+    //   a block a segment               10.8   12.7   14.2   21.2
+    // 64 segments of 4 / 6 / 8 tiles of 128 rows of 128, bf16:
+    //   shared 24.4   26.3   28.0, a block a segment 16.1   19.5   22.6
     const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
     const size_t segments = B * c.heads * (size_t)k.row_blocks;
     if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;
+    const size_t hold = (size_t)cus * (size_t)libred::attention_blocks((int)M, (int)D);
+    const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
     if (tiles > 1) {
-        const size_t hold = (size_t)cus * (size_t)libred::attention_blocks((int)M, (int)D);
-        const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
-        k.blocks = (int)blocks;
+        // The scratch is asked for either way, so that a call of a larger shape
+        // has always provided that of a smaller one, which a capture relies on.
         const size_t rows = (blocks + segments) * (size_t)shape.rows(), plan = (B + 2 + 3) / 4 * 4;
         void* p = nullptr;
         st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)) + plan * sizeof(int), &p);
         if (st != RED_OK) return st;
-        k.part_o = static_cast<float*>(p);
-        k.part_ml = reinterpret_cast<float2*>(k.part_o + rows * D);
-        k.plan = reinterpret_cast<int*>(k.part_ml + rows);
+        const size_t more = tiles * ((segments + hold - 1) / hold) - (segments * tiles + hold - 1) / hold;
+        const size_t turn_ns = 7 * D * (size_t)(shape.waves_t > 1 ? 2 : shape.step / 32);
+        if (tiles > 8 || more * turn_ns > 5500 + rows * D * sizeof(float) / 2500) {
+            k.blocks = (int)blocks;
+            k.part_o = static_cast<float*>(p);
+            k.part_ml = reinterpret_cast<float2*>(k.part_o + rows * D);
+            k.plan = reinterpret_cast<int*>(k.part_ml + rows);
+        }
     }
     hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
     if (e == hipSuccess && k.blocks > 0) e = libred::launch_attention_combine(type, k, shape.rows(), stream);

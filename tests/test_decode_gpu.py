@@ -376,6 +376,20 @@ def test_tree_attention_rows(nodes, hq, hk, dim, kind):
     check_attend(case, pg, sc, table, q, mask, dim ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("kind", [None, I8, E4M3], ids=str)
+@pytest.mark.parametrize("nodes, hq, hk, dim", [(4, 4, 2, 64), (3, 4, 1, 256), (9, 6, 2, 96), (8, 4, 1, 128), (33, 2, 2, 80),
+                                                (24, 4, 1, 128), (33, 4, 2, 64), (33, 2, 1, 192), (8, 3, 1, 208)])
+def test_tree_attention_shared_out(nodes, hq, hk, dim, kind):
+    """Tiles of a few long sequences shared out over all blocks, with pieces to
+    join, for every number of rows, head and cache type."""
+    dt = BF16 if (nodes + dim // 16) % 2 else F16
+    case = ([1500, 2100, 40], nodes, hq, hk, dim, 32, True, [nodes, nodes - 1, nodes], dt, kind or dt, "own")
+    say(case)
+    pg, sc, table, q, mask = attend_inputs(case, 18)
+    out, lse = attend(case, pg, sc, table, q, mask, dim ** -0.5)
+    check_attend(case, pg, sc, table, q, mask, dim ** -0.5, out, lse)
+
+
 @pytest.mark.parametrize("case", [ATTEND[3], ATTEND[5], ATTEND[15]], ids=str)
 @pytest.mark.parametrize("scale_of_v, scale", [(1e-20, 0.3), (1e15, -0.1), (1.0, 0.0)])
 def test_tree_attention_scales(case, scale_of_v, scale):
