@@ -401,6 +401,15 @@ red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
     // rows of 131071: 33 us; 16 and 48 a compute unit 35, a wave a segment 40).
     const size_t waves = ((size_t)cus * 32 + B - 1) / B, all = ((size_t)k.segs + 3) / 4;
     k.blocks = (int)(all < (waves + 3) / 4 ? all : (waves + 3) / 4);
+    // One launch, a block of 16 waves a sequence, where that is one turn of them
+    // or the sequences fill half of the card and it is a few (float32 rows of
+    // 8000 / 32000 / 64000 / 131071; two launches and one, us):
+    //   1 sequence      8.1 / 7.4 / 7.6 / 8.4,      7.7 / 9.8 / 14.4 / 26.2
+    //   192 sequences   10.6 / 15.8 / 22.0 / 34.1,  9.8 / 13.8 / 20.7 / 37.1
+    // Its sums are in the LDS, but the scratch is asked for all the same: a
+    // larger batch's call has then always provided that of a smaller one.
+    // More sequences than the card holds such blocks of would take turns.
+    if (B <= (size_t)cus * 2 && (k.segs <= 16 || (B >= (size_t)cus / 2 && k.segs <= 64))) k.blocks = 0;
     void* sums = nullptr;
     st = host_scratch(dev, stream, B * (size_t)k.segs * sizeof(double), &sums);
     if (st != RED_OK) return st;

@@ -161,7 +161,7 @@ struct Verify {
     double* sums;  // batch * segs
     int64_t vocab, seg;
     int batch, drafts, segs;
-    int blocks;  // a sequence, of 4 waves that take segments in turn
+    int blocks;  // a sequence, of 4 waves that take segments in turn; 0: one launch, a block a sequence
 };
 constexpr int kVerifyMaxSegs = 256;
 hipError_t launch_verify(int type, const Verify& a, hipStream_t stream);

@@ -10,7 +10,8 @@
 // segment of 1024 tokens (each wave finds n for itself, from at most two
 // gathers a draft), and once more in the one segment where the running sum
 // passes its border, by a second launch, a block a sequence with 4 tokens a
-// thread. Sums run in float64: float32 inputs differ exactly there, and a
+// thread; or both by one launch, a block of 16 waves a sequence, where a row is
+// short. Sums run in float64: float32 inputs differ exactly there, and a
 // border is then missed by less than 2^-40 of the sum whatever the order.
 // Memory bounds the first launch, latency the second: 192 rows of p and q of
 // 131071 float32, 201 MB, 32 us (6.3 TB/s) and 4.8 us; one row of 32000 3.8 us
@@ -21,8 +22,8 @@ namespace libred {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
+constexpr int kThreads = 256;     // of a block
+constexpr int kThreadsOne = 1024;  // where one launch does it all
 
 struct AddF64 {
     __device__ double operator()(double a, double b) const { return a + b; }
@@ -76,23 +77,18 @@ __device__ __forceinline__ double weight(float p, float q, int kind, bool token)
     return w < 0.0 ? 0.0 : w;  // a NaN stays one
 }
 
-constexpr int kStep = 1024;  // tokens of a wave at a time in the first launch, of a block in the second
+constexpr int kStep = 1024;  // tokens of a wave at a time in the sums, of a block in the choice
 
+// Sums of the weights of segments seg, seg + stride, ...
 template <class T>
-__global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
+__device__ __forceinline__ void segment_sums(const Verify& a, const Verifier<T>& v, int n, int seg, int stride, double* sums) {
     using V = Verifier<T>;
     constexpr int N = V::kVec, U = kStep / (kWave * N);
-    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));  // one argument of every 64-byte line
-    const V v(a, blockIdx.y);
     const int lane = threadIdx.x % kWave;
-    int seg = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (seg >= a.segs) return;
-    const int n = v.accepted();
-    if (seg == 0 && lane == 0) a.accepted[v.b] = n;
     const int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
     const typename V::B *p = v.row_p(n), *q = kind == kLessRow ? v.row_q(n) : p;
-    for (; seg < a.segs; seg += gridDim.x * kWaves) {
+    for (; seg < a.segs; seg += stride) {
     const int64_t first = (int64_t)seg * a.seg, last = min(first + a.seg, a.vocab);
     double sum = 0.0;
     for (int64_t i0 = first; i0 < last; i0 += kStep) {
@@ -113,12 +109,25 @@ __global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
         }
     }
     sum = group_combine<kWave>(sum, AddF64());
-    if (lane == 0) a.sums[(int64_t)v.b * a.segs + seg] = sum;
+    if (lane == 0) sums[seg] = sum;
     }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void verify_sum_kernel(Verify a) {
+    constexpr int W = kThreads / kWave;
+    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));  // one argument of every 64-byte line
+    const Verifier<T> v(a, blockIdx.y);
+    const int seg = blockIdx.x * W + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (seg >= a.segs) return;
+    const int n = v.accepted();
+    if (seg == 0 && threadIdx.x % kWave == 0) a.accepted[v.b] = n;
+    segment_sums(a, v, n, seg, gridDim.x * W, a.sums + (int64_t)v.b * a.segs);
 }
 
 // Running sum over the threads of the block, this thread's value included; and
 // the whole sum. In a fixed order.
+template <int WAVES>
 __device__ __forceinline__ double block_scan(double v, double* lds, double* total) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     v += dpp_move<0x111, 0xF>(0.0, v);  // shifted by 1, 2, 4 and 8 in rows of 16
@@ -132,7 +141,7 @@ __device__ __forceinline__ double block_scan(double v, double* lds, double* tota
     __syncthreads();
     double before = 0.0, all = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < WAVES; ++w) {
         if (w == wave) before = all;
         all += lds[w];
     }
@@ -141,6 +150,7 @@ __device__ __forceinline__ double block_scan(double v, double* lds, double* tota
 }
 
 // The first (or last) thread for which `is` holds, -1 if none.
+template <int WAVES>
 __device__ __forceinline__ int block_find(bool is, bool last, int* lds) {
     const uint64_t mask = __ballot(is);
     const int wave = threadIdx.x / kWave;
@@ -150,23 +160,21 @@ __device__ __forceinline__ int block_find(bool is, bool last, int* lds) {
     __syncthreads();
     int found = -1;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         if (lds[w] >= 0 && (last || found < 0)) found = lds[w];
     return found;
 }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
+// The token, from the sums of the segments (this thread's: `mine`), and what
+// the sequence's tokens are.
+template <class T, int THREADS>
+__device__ __forceinline__ void choose(const Verify& a, const Verifier<T>& v, int n, double r, double mine) {
     using V = Verifier<T>;
-    constexpr int N = kStep / kThreads;  // tokens of a thread at a time
-    __shared__ double lds[kWaves], start;
-    __shared__ int ids[kWaves];
-    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));
-    const V v(a, blockIdx.x);
+    constexpr int N = kStep / THREADS;  // tokens of a thread at a time
+    constexpr int W = THREADS / kWave;
+    __shared__ double lds[W], start;
+    __shared__ int ids[W];
     const int tid = threadIdx.x;
-    double mine = tid < a.segs ? a.sums[(int64_t)v.b * a.segs + tid] : 0.0;
-    const int n = a.accepted[v.b];
-    const double r = (double)a.r[v.b];
     int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
     const typename V::B *p = v.row_p(n), *q = kind == kLessRow ? v.row_q(n) : p;
@@ -174,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
 
     // The segment in which the running sum passes r times the whole.
     double total, all;
-    double run = block_scan(mine, lds, &total);
+    double run = block_scan<W>(mine, lds, &total);
     if (!(total > 0.0)) {
         // p is nowhere above q: the weights are p itself.
         kind = kAll;
@@ -182,18 +190,18 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
         for (int s = 0; s < a.segs; ++s) {
             const int64_t f = s * a.seg, e = min(f + a.seg, a.vocab);
             double x = 0.0;
-            for (int64_t i = f + tid; i < e; i += kThreads) x += at(i);
-            block_scan(x, lds, &all);
+            for (int64_t i = f + tid; i < e; i += THREADS) x += at(i);
+            block_scan<W>(x, lds, &all);
             if (tid == s) mine = all;
         }
-        run = block_scan(mine, lds, &total);
+        run = block_scan<W>(mine, lds, &total);
     }
     const double border = r * total;
     const bool some = tid < a.segs && mine > 0.0;
-    int seg = block_find(some && run > border, false, ids);
+    int seg = block_find<W>(some && run > border, false, ids);
     // No segment passes the border where r is 1 or more: the last with weight.
     const bool past = seg < 0;
-    if (past) seg = block_find(some, true, ids);
+    if (past) seg = block_find<W>(some, true, ids);
     int64_t pick = -1;
     if (seg >= 0 && total > 0.0) {
         if (tid == seg) start = seg == 0 ? 0.0 : run - mine;
@@ -209,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
                 if (i + j >= e) w[j] = 0.0;
                 own += w[j];
             }
-            double s = before + (block_scan(own, lds, &all) - own);
+            double s = before + (block_scan<W>(own, lds, &all) - own);
             int hit = -1, top = -1;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
@@ -221,8 +229,8 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
             }
             // Of the last element with weight so far in case none passes: the
             // two orders of summation may round the border apart.
-            const int who = past ? -1 : block_find(hit >= 0, false, ids);
-            const int end = who >= 0 ? who : block_find(top >= 0, true, ids);
+            const int who = past ? -1 : block_find<W>(hit >= 0, false, ids);
+            const int end = who >= 0 ? who : block_find<W>(top >= 0, true, ids);
             if (end >= 0) {
                 if (tid == end) ids[0] = who >= 0 ? hit : top;
                 __syncthreads();
@@ -233,12 +241,39 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
             before += all;
         }
     }
-    for (int i = tid; i <= a.drafts; i += kThreads)
+    for (int i = tid; i <= a.drafts; i += THREADS)
         a.tokens[(int64_t)v.b * (a.drafts + 1) + i] = i < n ? v.drafted(i) : i == n ? pick : -1;
 }
 
 template <class T>
+__global__ __launch_bounds__(kThreads) void verify_pick_kernel(Verify a) {
+    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));
+    const Verifier<T> v(a, blockIdx.x);
+    const int tid = threadIdx.x;
+    const double mine = tid < a.segs ? a.sums[(int64_t)v.b * a.segs + tid] : 0.0;
+    choose<T, kThreads>(a, v, a.accepted[v.b], (double)a.r[v.b], mine);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreadsOne) void verify_one_kernel(Verify a) {
+    __shared__ double sums[kVerifyMaxSegs];
+    asm volatile("" ::"s"(a.p), "s"(a.u), "s"(a.vocab));
+    const Verifier<T> v(a, blockIdx.x);
+    const int tid = threadIdx.x;
+    const double r = (double)a.r[v.b];
+    const int n = v.accepted();
+    if (tid == 0) a.accepted[v.b] = n;
+    segment_sums(a, v, n, __builtin_amdgcn_readfirstlane(tid / kWave), kThreadsOne / kWave, sums);
+    __syncthreads();
+    choose<T, kThreadsOne>(a, v, n, r, tid < a.segs ? sums[tid] : 0.0);
+}
+
+template <class T>
 hipError_t verify(const Verify& a, hipStream_t stream) {
+    if (a.blocks == 0) {
+        verify_one_kernel<T><<<(unsigned)a.batch, kThreadsOne, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     verify_sum_kernel<T><<<dim3((unsigned)a.blocks, (unsigned)a.batch), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -558,6 +558,33 @@ def test_verify_drafts_corners():
     check_verify(p, q, drafted, u, r, count.clamp(0, k), got)
 
 
+@pytest.mark.parametrize("case", [(130, 2, 20011, F16, True, 2.0, "own"), (256, 1, 60001, BF16, False, 6.0, "odd"),
+                                  (520, 3, 999, F32, True, 2.0, "own"), (1, 2, 16384, F32, True, 2.0, "own")], ids=str)
+def test_verify_drafts_many(case):
+    """Rows and numbers of sequences at the borders between one launch and two."""
+    test_verify_drafts(case)
+
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16])
+def test_verify_drafts_wide(dt):
+    """A vocabulary that is widened by tokens of no weight (and takes two
+    launches for it) has the same tokens drawn, in the corners too."""
+    b, k, v, wide = 7, 3, 3001, 40003
+    p, q, drafted, u, r, _ = verify_inputs((b, k, v, dt, True, 2.0, "own"), 23)
+    q[0], u[0] = p[0, :k], 1.0                          # refused, and p - q is 0 everywhere
+    p[1] = 0.0                                          # no weight at all
+    p[2, 0, 7] = float("nan")
+    drafted[2, 0], u[2, 0] = 7, 0.5
+    r[3], r[4] = 0.0, 1.0
+    u[5] = 0.0                                          # everything accepted
+    p[5] = p[5] + 1e-4
+    args = [x.to(DEV) for x in (p, q, drafted, u, r)]
+    wider = [torch.nn.functional.pad(x, (0, wide - v)) for x in args[:2]] + args[2:]
+    got, want = rl.red_verify_drafts(*args), rl.red_verify_drafts(*wider)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_verify(p, q, drafted, u, r, None, got)
+
+
 def test_python_refusals():
     q, k = torch.zeros(3, 4, 64, device=DEV), torch.zeros(3, 2, 64, device=DEV)
     pos, freq = torch.zeros(3, dtype=torch.int64, device=DEV), R.frequencies(64).to(DEV)
