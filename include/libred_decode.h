@@ -13,7 +13,7 @@
  * the vocabulary) is always contiguous. Every pointer is aligned to its
  * element. Inputs must not overlap outputs unless a call says otherwise.
  *
- * Scratch: the backward pass of the norms, attention over long caches and the
+ * Scratch: the backward pass of the norms, attention (max_len above 32) and the
  * verification keep partials in the stream's scratch buffer (the one of the
  * column reductions): grown on demand, kept until the process exits. While
  * the stream is being captured into a graph a call whose scratch is missing or

@@ -128,7 +128,7 @@ constexpr int kNarrowHeads = 128, kNarrowPairs = 96;
 //   128,   64, bf16                    29.5       24.7
 //   128,  128, bf16                    39.5       36.4
 // 32 sequences of 1500 to 16384 tokens, 8 kv heads of 128 in int8, 32 rows:
-// kFewRows 120, kHalfRows 234.
+// kFewRows 115.5, kHalfRows 234.
 constexpr AttentionShape attention_shape(int rows, int dim, int bytes) {
     return rows <= kFewestRows.rows()                                    ? kFewestRows
            : dim > kNarrowHeads                                          ? kHalfRows

@@ -35,7 +35,7 @@
 //
 // What it takes, without the joining:
 //   32 sequences of 1500 to 16384 tokens, 8 kv heads x 32 rows of 128, int8:
-//     608 MB in 121 us (5.0 TB/s). Two waves a SIMD, each with its chain of
+//     608 MB in 115.5 us (5.3 TB/s). Two waves a SIMD, each with its chain of
 //     loads, conversion, products and exponentials: vector instructions fill
 //     40 % of the cycles, the LDS is busy for 27 %, the matrix unit for 13 %;
 //     memory alone would need 84 us. More waves do not fit the registers.
