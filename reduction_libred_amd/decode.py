@@ -2,7 +2,9 @@
 
 Like the rest of the binding, each function has the name of the C entry point
 it calls and only marshals arguments. Tensors are taken with the strides they
-have, as long as their last dimension is contiguous.
+have, as long as their last dimension is contiguous. Where a call is given a
+stream, its outputs are allocated there; ordering that stream behind the one
+its inputs come from, and the outputs' readers behind it, is the caller's.
 
 A decoding step makes these calls with little work in each, so the way to the
 C call is kept short: one look at a tensor where it is as it should be (what is
@@ -150,6 +152,16 @@ def _call(name, device, stream, *args):
         raise RedError(name, st, lib().red_last_hip_error())
 
 
+def _on(stream, f, *args):
+    """f(*args) with `stream` (a torch stream or a handle) the current one, so
+    that what it allocates belongs to the stream that writes it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        device = args[0].device if isinstance(args[0], torch.Tensor) and args[0].is_cuda else None
+        stream = torch.cuda.ExternalStream(int(stream), device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return f(*args)
+
+
 def _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out):
     """Raise what is wrong with the arguments, if anything is."""
     device = _any(name, "q", q, _FLOATS, 3, "(tokens, q heads, dim)")
@@ -209,6 +221,8 @@ def red_qk_norm_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps=1e-6, in
     2 * len(freq) elements by pos[t] * freq[i], in one pass. Pairs are halves
     apart, or neighbours if `interleaved`. float32, float16 or bfloat16; pos
     int64, freq float32. q_out and k_out may be q and k. -> (q_out, k_out)."""
+    if stream is not None:
+        return _on(stream, red_qk_norm_rope, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
     name = "red_qk_norm_rope"
     device, q_out, k_out, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
     _call(name, device, stream, args)
@@ -220,6 +234,8 @@ def red_qk_norm_rope_backward(dq, dk, q, k, pos, freq, q_weight=None, k_weight=N
     """Gradients of red_qk_norm_rope: dq and dk are those of its outputs.
     -> (gradient of q, of k, of q_weight, of k_weight), the weights' in float32
     (also where the weight is None, that is ones)."""
+    if stream is not None:
+        return _on(stream, red_qk_norm_rope_backward, dq, dk, q, k, pos, freq, q_weight, k_weight, eps, interleaved)
     name = "red_qk_norm_rope_backward"
     device, q_grad, k_grad, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
     _rows(name, "dq", dq, q.dtype, device, q.shape)
@@ -307,6 +323,8 @@ def red_cache_read(k_pages, v_pages, slots, dtype, k_scales=None, v_scales=None,
     """Read tokens back from a paged cache (see red_cache_write) as float16 or
     bfloat16. A slot outside the cache reads as zeros. -> (k, v), each (tokens,
     heads, dim)."""
+    if stream is not None:
+        return _on(stream, red_cache_read, k_pages, v_pages, slots, dtype, k_scales, v_scales, k_out, v_out)
     name = "red_cache_read"
     device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
     if dtype not in _HALVES:
@@ -339,6 +357,9 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     says how many nodes there are (None: all). max_len: the most tokens, nodes
     included, of a sequence (None: what the table holds). -> (out like q, lse
     (batch, nodes, q heads) float32); rows that see nothing hold 0 and -inf."""
+    if stream is not None:
+        return _on(stream, red_tree_attention, q, k_pages, v_pages, table, lens, scale, max_len, tree_mask, node_count,
+                   k_scales, v_scales, out)
     name = "red_tree_attention"
     device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
     if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.dtype not in _HALVES:
@@ -378,6 +399,8 @@ def red_verify_drafts(p, q, drafted, u, r, draft_count=None, stream=None):
     draft_count (int32): how many drafts a sequence has (None: all).
     -> (accepted (batch) int32, tokens (batch, drafts + 1) int64: the accepted
     ones, the drawn one, then -1)."""
+    if stream is not None:
+        return _on(stream, red_verify_drafts, p, q, drafted, u, r, draft_count)
     name = "red_verify_drafts"
     device = _any(name, "p", p, _FLOATS, 3, "(batch, drafts + 1, vocab)")
     dtype, (batch, steps, vocab), (p0, p1, _) = p.dtype, p.shape, p.stride()

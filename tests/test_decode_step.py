@@ -179,3 +179,25 @@ def test_poisoned_scratch():
                 else:
                     assert same(rl.red_verify_drafts(s["p"], s["draft"], s["drafted"], s["u"], s["r"]), want[10:12])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_outputs_belong_to_the_stream(as_handle):
+    """What a call on a given stream allocates and frees is not handed to
+    another stream's tensors while the call may still write it."""
+    s = step_inputs(11)
+    q = s["q"]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    given = side.cuda_stream if as_handle else side
+    a, b = rl.red_qk_norm_rope(q, s["k"], s["pos"], s["freq"], stream=given)
+    at = a.data_ptr()
+    del a, b
+    others = [torch.empty_like(q) for _ in range(8)]
+    assert all(x.data_ptr() != at for x in others)
+    again, _ = rl.red_qk_norm_rope(q, s["k"], s["pos"], s["freq"], stream=given)
+    side.synchronize()
+    want, _ = rl.red_qk_norm_rope(q, s["k"], s["pos"], s["freq"])
+    torch.cuda.synchronize()
+    assert torch.equal(again, want)
