@@ -173,7 +173,10 @@ __device__ __forceinline__ void choose(const Verify& a, const Verifier<T>& v, in
     constexpr int N = kStep / THREADS;  // tokens of a thread at a time
     constexpr int W = THREADS / kWave;
     __shared__ double lds[W], start;
-    __shared__ int ids[W];
+    // `element`, of the thread that was found, has a word of its own: block_find
+    // ends with reads of all of `ids`, and a wave that is done with them must
+    // not change them under one that is not.
+    __shared__ int ids[W], element;
     const int tid = threadIdx.x;
     int kind = n == v.count ? kAll : a.q ? kLessRow : kLessToken;
     const int64_t token = kind == kLessToken ? v.drafted(n) : -1;
@@ -232,10 +235,9 @@ __device__ __forceinline__ void choose(const Verify& a, const Verifier<T>& v, in
             const int who = past ? -1 : block_find<W>(hit >= 0, false, ids);
             const int end = who >= 0 ? who : block_find<W>(top >= 0, true, ids);
             if (end >= 0) {
-                if (tid == end) ids[0] = who >= 0 ? hit : top;
+                if (tid == end) element = who >= 0 ? hit : top;
                 __syncthreads();
-                pick = i0 + end * N + ids[0];
-                __syncthreads();
+                pick = i0 + end * N + element;  // barriers of the next scan lie before the next write
             }
             if (who >= 0) break;
             before += all;

@@ -1,0 +1,39 @@
+"""The decoding step's operators where they could go wrong without a usual case
+noticing, on the GPU against float64 on the CPU."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():  # pragma: no cover - collected only with a GPU
+    pytest.skip("no GPU visible", allow_module_level=True)
+
+import decode_reference as R  # noqa: E402
+import reduction_libred_amd as rl  # noqa: E402
+
+DEV = torch.device("cuda:0")
+F32, F16, BF16, I8, E4M3 = torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn
+U = 2.0 ** -24
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def integers(n):
+    return torch.zeros(n, dtype=torch.int64, device=DEV)
+
+
+@pytest.mark.parametrize("batch, vocab", [(200, 2999), (130, 60001), (700, 2999), (40, 60001)])
+def test_verify_token_of_every_wave(batch, vocab):
+    """Tokens spread over all waves of a block, by one launch (the first two)
+    and by two: weights of 1, so that r draws token floor(r * vocab)."""
+    r = torch.rand(batch, generator=gen(1))
+    want = torch.floor(r.double() * vocab).long()
+    p = torch.ones(batch, 1, vocab, device=DEV)
+    for _ in range(3):
+        n, tokens = rl.red_verify_drafts(p, None, torch.zeros(batch, 0, dtype=torch.int64, device=DEV),
+                                         torch.zeros(batch, 0, device=DEV), r.to(DEV))
+        assert not n.any() and torch.equal(tokens[:, 0].cpu(), want)
