@@ -247,10 +247,13 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     a.k = to_heads(*k), a.v = to_heads(*v);
     a.slots = slots, a.tokens = (int64_t)tokens;
     if (c->pages == 0) {
-        // A read of nothing: no slot is inside, but the kernel's loads are made
-        // all the same (and dropped), so they get memory to read.
+        // A read of nothing: no slot is inside, but the kernel's loads (of the
+        // first row of every head) are made all the same and dropped, so they
+        // get memory to read: the outputs' first row and the first slot, for
+        // all heads, since the strides of no pages say nothing.
         a.cache.k = k->data, a.cache.v = v->data;
         a.cache.k_scales = a.cache.v_scales = reinterpret_cast<float*>(const_cast<int64_t*>(slots));
+        a.cache.head_stride = a.cache.scale_head_stride = 0;
     }
     const size_t block_tokens = (size_t)(libred::kCacheWaves * 64 / lanes);
     const size_t groups = (tokens + block_tokens - 1) / block_tokens;

@@ -1,0 +1,64 @@
+// The entry points of libred_decode.h (decode.cpp, compiled for the host) over
+// launchers that note what they are asked for and do nothing.
+#include <vector>
+
+#include "decode.cpp"
+
+namespace {
+
+std::vector<size_t> scratch;       // bytes asked for
+std::vector<libred::CacheRows> cache_launches;
+
+}  // namespace
+
+namespace libred {
+
+red_status host_fail(hipError_t, red_status code) { return code; }
+red_status host_compute_units(int* dev, int* cu_count) {
+    *dev = 0, *cu_count = 256;
+    return RED_OK;
+}
+red_status host_scratch(int, hipStream_t, size_t bytes, void** out) {
+    scratch.push_back(bytes);
+    *out = reinterpret_cast<void*>((uintptr_t)1 << 40);
+    return RED_OK;
+}
+
+hipError_t launch_qk_norm_f32(int, int, const QkNorm&, bool, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_qk_norm_f16(int, int, const QkNorm&, bool, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_qk_norm_bf16(int, int, const QkNorm&, bool, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_qk_norm_weights(const float*, int, int, float*, float*, hipStream_t) { return hipSuccess; }
+hipError_t launch_cache_write(int, int, int, int, const CacheRows& a, unsigned int, hipStream_t) {
+    cache_launches.push_back(a);
+    return hipSuccess;
+}
+hipError_t launch_cache_read(int, int, int, int, const CacheRows& a, unsigned int, hipStream_t) {
+    cache_launches.push_back(a);
+    return hipSuccess;
+}
+hipError_t launch_attention_combine(int, const TreeAttention&, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_tree_attention(int, int, const TreeAttention&, hipStream_t) { return hipSuccess; }
+hipError_t launch_verify(int, const Verify&, hipStream_t) { return hipSuccess; }
+
+}  // namespace libred
+
+extern "C" {
+
+void forget() { scratch.clear(), cache_launches.clear(); }
+
+// Bytes from `base` on that the last launch on a cache loads for a token whose
+// slot lies outside the cache: of elements (what 0) or scales (what 1). Such a
+// token's loads are those of the cache's first row of every head.
+int64_t outside_reads(const void* base, int what) {
+    const libred::CacheRows& a = cache_launches.back();
+    const libred::PagedCache& c = a.cache;
+    int64_t end = 0;
+    for (const void* p : {static_cast<const void*>(what ? c.k_scales : c.k), static_cast<const void*>(what ? c.v_scales : c.v)}) {
+        const int64_t last = (c.heads - 1) * (what ? c.scale_head_stride : c.head_stride);
+        const int64_t bytes = what ? 4 * (last + 1) : 2 * (last + c.dim);  // elements of at most 2 bytes
+        const int64_t e = (int64_t)((uintptr_t)p - (uintptr_t)base) + bytes;
+        if (e > end) end = e;
+    }
+    return end;
+}
+}

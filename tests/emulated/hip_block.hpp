@@ -26,6 +26,7 @@
 
 typedef int hipError_t;
 typedef void* hipStream_t;
+constexpr hipError_t hipSuccess = 0;
 struct float2 {
     float x, y;
 };

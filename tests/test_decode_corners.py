@@ -37,3 +37,13 @@ def test_verify_token_of_every_wave(batch, vocab):
         n, tokens = rl.red_verify_drafts(p, None, torch.zeros(batch, 0, dtype=torch.int64, device=DEV),
                                          torch.zeros(batch, 0, device=DEV), r.to(DEV))
         assert not n.any() and torch.equal(tokens[:, 0].cpu(), want)
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3, F16])
+@pytest.mark.parametrize("tokens, heads, places, dim", [(1, 8, 128, 128), (3, 40, 64, 100)])
+def test_read_of_no_pages(kind, tokens, heads, places, dim):
+    pg = torch.empty(0, heads, places, dim, dtype=kind, device=DEV)
+    sc = {n: torch.empty(0, heads, places, device=DEV) for n in ("k_scales", "v_scales")} if kind in R.TOP else {}
+    out = [torch.full((tokens, heads, dim), math.nan, dtype=F16, device=DEV) for _ in range(2)]
+    rl.red_cache_read(pg, pg, integers(tokens), F16, k_out=out[0], v_out=out[1], **sc)
+    assert not out[0].any() and not out[1].any()
