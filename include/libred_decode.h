@@ -18,7 +18,8 @@
  * column reductions): grown on demand, kept until the process exits. While
  * the stream is being captured into a graph a call whose scratch is missing or
  * too small returns RED_ERR_CAPTURE before it touches the stream; an earlier
- * call of the same or a larger shape on the stream provides it.
+ * call on the stream provides it, of the same types, kv heads and dim, and of no
+ * fewer sequences, tokens, nodes, query heads, drafts and vocabulary.
  */
 #ifndef LIBRED_DECODE_H_
 #define LIBRED_DECODE_H_

@@ -346,13 +346,15 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;
     const size_t hold = (size_t)cus * (size_t)libred::attention_blocks((int)M, (int)D);
     const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
-    if (tiles > 1) {
-        // The scratch is asked for either way, so that a call of a larger shape
-        // has always provided that of a smaller one, which a capture relies on.
+    if (k.max_tokens > libred::attention_least_tokens((int)M, (int)D, c.type == RED_F16 || c.type == RED_BF16 ? 2 : 1)) {
+        // The scratch is asked for whichever way is taken, and also for one
+        // tile where fewer rows would have several, so that a call of a larger
+        // shape has always provided that of a smaller one, which a capture
+        // relies on.
         const size_t rows = (blocks + segments) * (size_t)shape.rows(), plan = (B + 2 + 3) / 4 * 4;
         void* p = nullptr;
         st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)) + plan * sizeof(int), &p);
-        if (st != RED_OK) return st;
+        if (st != RED_OK && tiles > 1) return st;  // one tile a segment needs none itself
         const size_t more = tiles * ((segments + hold - 1) / hold) - (segments * tiles + hold - 1) / hold;
         const size_t turn_ns = 7 * D * (size_t)(shape.waves_t > 1 ? 2 : shape.step / 32);
         if (tiles > 8 || more * turn_ns > 5500 + rows * D * sizeof(float) / 2500) {

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "libred_decode.h"
 
 namespace libred {
@@ -135,6 +137,13 @@ constexpr AttentionShape attention_shape(int rows, int dim, int bytes) {
            : rows <= kFewRows.rows() && (bytes == 1 || dim <= kNarrowPairs) ? kFewRows
            : rows <= kHalfRows.rows()                                    ? kHalfRows
                                                                          : kManyRows;
+}
+// The fewest tokens of a tile that so many rows, or fewer, are given.
+constexpr int attention_least_tokens(int rows, int dim, int bytes) {
+    int least = attention_shape(rows, dim, bytes).tokens();
+    for (const int fewer : {kFewestRows.rows(), kFewRows.rows(), kHalfRows.rows()})
+        if (fewer < rows && attention_shape(fewer, dim, bytes).tokens() < least) least = attention_shape(fewer, dim, bytes).tokens();
+    return least;
 }
 // Blocks that a compute unit holds at once.
 constexpr int attention_blocks(int rows, int dim) { return rows <= kFewestRows.rows() && dim > kNarrowHeads ? 1 : 2; }

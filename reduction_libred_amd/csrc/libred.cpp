@@ -188,6 +188,8 @@ hipError_t malloc_outside_capture(void** p, size_t bytes) {
     e = hipMalloc(p, bytes);
     hipStreamCaptureMode back = mode;
     const hipError_t e2 = hipThreadExchangeStreamCaptureMode(&back);
+    // The error is returned, not left for the next launch's check to find.
+    if (e != hipSuccess) (void)hipGetLastError();
     return e != hipSuccess ? e : e2;
 }
 

@@ -62,3 +62,10 @@ int64_t outside_reads(const void* base, int what) {
     return end;
 }
 }
+
+// Bytes of scratch that the calls since forget() asked for, at most.
+extern "C" size_t scratch_asked() {
+    size_t most = 0;
+    for (const size_t s : scratch) most = s > most ? s : most;
+    return most;
+}

@@ -47,3 +47,35 @@ def test_read_of_no_pages(kind, tokens, heads, places, dim):
     out = [torch.full((tokens, heads, dim), math.nan, dtype=F16, device=DEV) for _ in range(2)]
     rl.red_cache_read(pg, pg, integers(tokens), F16, k_out=out[0], v_out=out[1], **sc)
     assert not out[0].any() and not out[1].any()
+
+
+def on_a_new_stream(first, then):
+    """then() captured on a stream on which only first() has run, replayed."""
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        first()
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            got = then()
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, then()):
+            assert torch.equal(x, y)
+        torch.cuda.synchronize()
+
+
+def test_attention_captured_after_more_nodes():
+    """64 nodes of 2 heads (one tile of 64 tokens) before 32 (two of 32)."""
+    g = gen(2)
+    pages = [torch.randn(4, 1, 16, 128, generator=g).to(F16).to(DEV) for _ in range(2)]
+    q = torch.randn(1, 64, 2, 128, generator=g).to(F16).to(DEV)
+    table, lens = torch.arange(4, dtype=torch.int32, device=DEV)[None], torch.tensor([30], dtype=torch.int32, device=DEV)
+
+    def call(nodes):
+        return rl.red_tree_attention(q[:, :nodes], *pages, table, lens, 0.1)
+
+    on_a_new_stream(lambda: call(64), lambda: call(32))

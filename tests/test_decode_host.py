@@ -3,6 +3,7 @@ decode.cpp compiled for it, over launchers that only note what they are asked
 for. No GPU is needed and no kernel runs."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -30,6 +31,7 @@ def calls(tmp_path_factory):
     for name, (res, args) in D.SIGNATURES.items():
         getattr(L, name).restype, getattr(L, name).argtypes = res, args
     L.outside_reads.restype, L.outside_reads.argtypes = I64, [ctypes.c_void_p, ctypes.c_int]
+    L.scratch_asked.restype = ctypes.c_size_t
     L.forget()
     return L
 
@@ -53,3 +55,51 @@ def test_read_of_no_pages_stays_in_its_buffers(calls, kind, tokens, heads, place
     assert calls.outside_reads(A, 0) <= 2 * tokens * heads * dim
     if scaled:
         assert calls.outside_reads(C, 1) <= 8 * tokens
+
+
+def asked(calls, f, *args):
+    """The scratch that a call makes sure of: a buffer has 1 MiB at least."""
+    calls.forget()
+    assert getattr(calls, f)(*args, None) == rl.RED_OK
+    n = calls.scratch_asked()
+    return max(n, 1 << 20) if n else 0
+
+
+def needs(calls, f, *args):
+    calls.forget()
+    assert getattr(calls, f)(*args, None) == rl.RED_OK
+    return calls.scratch_asked()
+
+
+def attention(kind, batch, nodes, group, heads, dim, max_len):
+    scaled = kind >= 3
+    c = D.PagedCache(k=A, v=B, k_scales=C if scaled else None, v_scales=E if scaled else None, type=kind, pages=4, heads=heads,
+                     places=16, dim=dim, page_stride=heads * 16 * dim, head_stride=16 * dim, place_stride=dim,
+                     scale_page_stride=heads * 16, scale_head_stride=16, scale_place_stride=1)
+    h = heads * group
+    cols = -(-max_len // 16)
+    return D.TreeAttentionArgs(type=kind if not scaled else 1, scale=0.25, batch=batch, nodes=nodes, q_heads=h, max_len=max_len,
+                               q=1 << 42, out=1 << 43, lse=F, q_batch_stride=nodes * h * dim, q_node_stride=h * dim,
+                               q_head_stride=dim, out_batch_stride=nodes * h * dim, out_node_stride=h * dim, out_head_stride=dim,
+                               cache=c, table=G, table_cols=cols, table_stride=cols, lens=A)
+
+
+@pytest.mark.parametrize("kind", [1, 3])
+@pytest.mark.parametrize("dim", [64, 96, 128, 144, 256])
+def test_attention_of_a_larger_shape_provides_the_scratch(calls, kind, dim):
+    """Types, kv heads and dim being the same, a call of no fewer sequences,
+    nodes, query heads and tokens asks for no less."""
+    rng = random.Random(dim + kind)
+    lengths = [32, 33, 40, 63, 64, 65, 100, 128, 129, 200, 257, 1000, 5000, 40000]
+    small = [(1, 32, 2, 1, 64), (1, 8, 8, 1, 64), (1, 1, 16, 8, 129)]
+    large = [(1, 64, 2, 1, 64), (1, 9, 8, 1, 64), (1, 2, 16, 8, 129)]
+    for _ in range(400):
+        heads = rng.choice([1, 2, 8])
+        a = [rng.choice([1, 2, 3, 20, 200]), rng.randint(1, 64), rng.choice([1, 2, 4, 8]), heads, rng.choice(lengths)]
+        b = [a[0] + rng.choice([0, 0, 1, 50]), min(64, a[1] + rng.choice([0, 0, 1, 20])), a[2] + rng.choice([0, 0, 1, 8]), heads,
+             a[4] + rng.choice([0, 0, 1, 32, 1000])]
+        small.append(a), large.append(b)
+    for a, b in zip(small, large):
+        x = needs(calls, "red_tree_attention", ref(attention(kind, *a[:4], dim, a[4])))
+        y = asked(calls, "red_tree_attention", ref(attention(kind, *b[:4], dim, b[4])))
+        assert x <= y, (a, b)
