@@ -411,12 +411,15 @@ red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
     // 8000 / 32000 / 64000 / 131071; two launches and one, us):
     //   1 sequence      8.1 / 7.4 / 7.6 / 8.4,      7.7 / 9.8 / 14.4 / 26.2
     //   192 sequences   10.6 / 15.8 / 22.0 / 34.1,  9.8 / 13.8 / 20.7 / 37.1
-    // Its sums are in the LDS, but the scratch is asked for all the same: a
-    // larger batch's call has then always provided that of a smaller one.
     // More sequences than the card holds such blocks of would take turns.
     if (B <= (size_t)cus * 2 && (k.segs <= 16 || (B >= (size_t)cus / 2 && k.segs <= 64))) k.blocks = 0;
+    // The scratch is that of as many segments as a smaller vocabulary may have,
+    // and is asked for where one launch keeps its sums in the LDS as well: a
+    // call of a larger shape has then always provided that of a smaller one,
+    // which a capture relies on.
+    const size_t most = (V + 1023) / 1024 < (size_t)libred::kVerifyMaxSegs ? (V + 1023) / 1024 : (size_t)libred::kVerifyMaxSegs;
     void* sums = nullptr;
-    st = host_scratch(dev, stream, B * (size_t)k.segs * sizeof(double), &sums);
+    st = host_scratch(dev, stream, B * most * sizeof(double), &sums);
     if (st != RED_OK) return st;
     k.sums = static_cast<double*>(sums);
     const hipError_t e = libred::launch_verify(a->type, k, stream);

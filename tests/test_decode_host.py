@@ -103,3 +103,23 @@ def test_attention_of_a_larger_shape_provides_the_scratch(calls, kind, dim):
         x = needs(calls, "red_tree_attention", ref(attention(kind, *a[:4], dim, a[4])))
         y = asked(calls, "red_tree_attention", ref(attention(kind, *b[:4], dim, b[4])))
         assert x <= y, (a, b)
+
+
+def verify(batch, vocab, drafts):
+    return D.VerifyDraftsArgs(type=0, batch=batch, drafts=drafts, vocab=vocab, p=A, p_batch_stride=vocab * (drafts + 1),
+                              p_step_stride=vocab, q=B, q_batch_stride=vocab * drafts, q_step_stride=vocab, drafted=C, u=E, r=F,
+                              draft_count=None, accepted=G, tokens=0x10000000)
+
+
+def test_verification_of_a_larger_shape_provides_the_scratch(calls):
+    """No fewer sequences, drafts and tokens of the vocabulary ask for no less."""
+    rng = random.Random(5)
+    vocabs = [1, 1024, 1025, 32000, 131071, 262144, 262145, 524288, 524289, 1000000, 5000000]
+    pairs = [((2000, 262144), (2000, 262145)), ((600, 524288), (600, 524289)), ((40000, 200000), (40000, 300000))]
+    for _ in range(400):
+        a = (rng.choice([1, 2, 100, 513, 2000, 60000]), rng.choice(vocabs))
+        pairs.append((a, (a[0] + rng.choice([0, 0, 1, 1000]), a[1] + rng.choice([0, 1, 1, 1024, 100000]))))
+    for a, b in pairs:
+        x = needs(calls, "red_verify_drafts", ref(verify(*a, 2)))
+        y = asked(calls, "red_verify_drafts", ref(verify(*b, 2)))
+        assert x <= y, (a, b)
