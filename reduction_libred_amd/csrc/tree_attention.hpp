@@ -216,7 +216,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     __shared__ uint64_t held[WT][4];           // which of them are in the cache
     __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
     __shared__ float red[2][WM * WT][RW];
-    __shared__ int odd;
+    // What is no number among the values: in a node's (odd), which some rows may
+    // not see, or in the scale of a token that all rows see (lost).
+    __shared__ int odd, lost;
 
     // One argument of every 64-byte line, so that all lines are asked for at
     // once: fetched one after the other as they are met, the arguments alone
@@ -400,14 +402,20 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         const bool part = uniform((int)(in != kAllIn)) || DP != D;
         if constexpr (kScaled) {
             if (looks && ahead == i % AT_ONCE) {
-                // A scale of 0 (a row of zeros) is taken as 2^-100.
-                const float c = sv < 0x1p-100f ? 0x1p-100f : sv;
+                // A scale of 0 (a row of zeros) is taken as 2^-100. One that is
+                // no number (a row that held an infinity or a NaN) is left out
+                // of the weights, which it has no part in, and noted: the rows
+                // that see the token get it at the end.
+                const bool number = sv < __builtin_inff();
+                const float c = number ? fmaxf(sv, 0x1p-100f) : 1.f;
                 auto& f = factors[wt][i % HELD];
                 f[0][mine_t] = sk * A->scale;
                 f[1][mine_t] = __builtin_amdgcn_logf(c);
-                // 1 where the scale is no number (the exponent says so), so
-                // that a row that does not see the token adds 0 times it.
-                f[2][mine_t] = c < __builtin_inff() ? 1.f / c : 1.f;
+                f[2][mine_t] = 1.f / c;
+                if (__builtin_expect(!number, false)) {
+                    if (base + mine_t < len) lost = 1;
+                    else odd = 1;
+                }
             }
         }
 #pragma unroll
@@ -471,7 +479,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     }
 
     __syncthreads();  // the segment before is done with the LDS
-    if (tid == 0) odd = 0;
+    if (tid == 0) odd = lost = 0;
     settle(0);
     __syncthreads();
     if (tiles > 0) fetch(0);
@@ -627,16 +635,23 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         }
     };
     // The infinities and NaN in columns c .. c + 3 of the nodes of this chunk
-    // that row rw sees: their weights do not matter.
+    // that row rw sees: their weights do not matter. All columns are NaN where
+    // a scale that it sees is no number.
     auto strange = [&](int rw, int c) {
+        constexpr float kNaN = __builtin_nanf("");
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         const int node = rw / group;
         if (node >= count) return v;
+        if (lost) return f32x4{kNaN, kNaN, kNaN, kNaN};
         const uint64_t word = E->mask ? (uint64_t)E->mask[(int64_t)b * E->nodes + node] : ~0ull >> (63 - node);
 #pragma unroll 1
         for (int t = max(first, len); t < last; ++t) {
             const int page = E->table[b * E->table_stride + t / E->cache.places];
             if (!(word >> (t - len) & 1) || page < 0 || page >= E->cache.pages) continue;
+            if constexpr (kScaled) {
+                const int64_t of = (int64_t)page * E->cache.scale_page_stride + (int64_t)(t % E->cache.places) * E->cache.scale_place_stride + h * E->cache.scale_head_stride;
+                if (!(E->cache.v_scales[of] < __builtin_inff())) return f32x4{kNaN, kNaN, kNaN, kNaN};
+            }
             const int64_t at = (int64_t)page * E->cache.page_stride + (int64_t)(t % E->cache.places) * E->cache.place_stride + h * E->cache.head_stride + c;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -704,7 +719,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         }
     }
     __syncthreads();
-    if (odd) {
+    if (odd | lost) {
         for (int e = tid; e < S::kRows * (DP / 4); e += S::kThreads) {
             const int c = e % (DP / 4) * 4, rw = rb * S::kRows + e / (DP / 4);
             if (c >= D || rw >= M) continue;

@@ -79,3 +79,99 @@ def test_attention_captured_after_more_nodes():
         return rl.red_tree_attention(q[:, :nodes], *pages, table, lens, 0.1)
 
     on_a_new_stream(lambda: call(64), lambda: call(32))
+
+
+def eight_bit_cache(kind, pages, heads, places, dim, seed, scale=1.0):
+    """A cache of random rows with scales around `scale` / 64."""
+    g = gen(seed)
+    codes = [torch.randn(pages, heads, places, dim, generator=g) for _ in range(2)]
+    codes = [(x * 36).clamp(-127, 127).round().to(I8) if kind == I8 else (x * 120).clamp(-448, 448).to(E4M3) for x in codes]
+    scales = [(0.5 + torch.rand(pages, heads, places, generator=g)) / 64 * s for s in (1.0, scale)]
+    return codes, scales
+
+
+def on_device(x):
+    return x.view(I8).to(DEV).view(E4M3) if x.dtype == E4M3 else x.to(DEV)
+
+
+def attention_reference(q, codes, scales, table, lens, mask, scale):
+    """-> out (batch, nodes, heads, dim), lse, and what errors of them are
+    relative to: the sum of the magnitudes of a score's terms, the largest
+    value; in float64. A value row whose scale is no number is NaN."""
+    batch, nodes, hq, dim = q.shape
+    hk, places = codes[0].shape[1], codes[0].shape[2]
+    out, (lse, size, top) = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(3, batch, nodes, hq, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        t = torch.arange(n + nodes)
+        page, at = table[b, t // places].long(), t % places
+        seen = R.visible(n, nodes, mask[b], nodes, n + nodes)
+        for h in range(hk):
+            k, v = (c[page, h, at].double() * s[page, h, at].double()[:, None] for c, s in zip(codes, scales))
+            bad = ~scales[1][page, h, at].isfinite()
+            v = torch.where(bad[:, None], torch.zeros((), dtype=torch.float64), v)
+            group = hq // hk
+            for j in range(group):
+                x, l, _, z = R.tree_attention(q[b, :, h * group + j], k, v, seen, scale)
+                x[(seen & bad).any(1)] = math.nan
+                out[b, :, h * group + j], lse[b, :, h * group + j], size[b, :, h * group + j] = x, l, z
+                top[b, :, h * group + j] = (seen * v.abs().amax(1)).amax(1)
+    return out, lse, size, top
+
+
+def check_attention(got, want, total, dim, log_scales=8):
+    """Scores: dim products and sums in float32, the logarithm of a value's
+    scale (`log_scales` at most) joins them. Sums: `total` terms. The
+    exponentials are rounded to float16 for the product (2^-11, or 2^-25 below
+    its range), the result to bfloat16."""
+    (out, lse), (wout, wlse, size, top) = got, want
+    es = (dim + 8) * U * size + 16 * U * (1 + log_scales)
+    off = (lse - wlse).abs()
+    assert (off <= es + (total + 32) * U + 4 * U * wlse.abs()).all(), off.max()
+    allowed = 2.0 ** -8 * wout.abs() + (top * (2.0 ** -11 + total * 2.0 ** -25 + (total + 32) * U + 2 * es))[..., None]
+    assert torch.equal(out.isnan(), wout.isnan())
+    fine = ~wout.isnan()
+    assert ((out - wout).abs()[fine] <= allowed[fine]).all(), (out - wout).abs()[fine].max()
+
+
+def chains_and_branches(batch, nodes):
+    """Even sequences: a chain; odd ones: every node by itself."""
+    words = [[(1 << (i + 1)) - 1 if b % 2 == 0 else 1 << i for i in range(nodes)] for b in range(batch)]
+    return torch.tensor([[w - 2 ** 64 if w >= 2 ** 63 else w for w in row] for row in words])
+
+
+SHAPES = [  # lens, nodes, q heads, kv heads, dim, places
+    ([70, 33, 0], 4, 4, 2, 64, 16), ([3000, 1700], 3, 4, 1, 128, 32), ([60, 20], 20, 2, 1, 96, 16), ([2500], 24, 4, 1, 128, 16),
+    ([90, 41], 40, 4, 2, 64, 8), ([1800, 2000], 64, 2, 1, 192, 64),
+]
+
+
+def call_attention(q, codes, scales, table, lens, mask, scale):
+    out, lse = rl.red_tree_attention(q.to(DEV), on_device(codes[0]), on_device(codes[1]), table.to(DEV),
+                                     torch.tensor(lens, dtype=torch.int32, device=DEV), scale, tree_mask=mask.to(DEV),
+                                     k_scales=scales[0].to(DEV), v_scales=scales[1].to(DEV))
+    return out.cpu().double(), lse.cpu().double()
+
+
+@pytest.mark.parametrize("where", ["tokens", "nodes"])
+@pytest.mark.parametrize("kind", [I8, E4M3], ids=str)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_value_rows_that_are_no_numbers(shape, kind, where):
+    """A value row stored with an infinity or a NaN reads back as NaN: the rows
+    that see it are NaN, their lse is the scores' alone, and the others are what
+    they are without it."""
+    lens, nodes, hq, hk, dim, places = shape
+    print(shape, kind, where, flush=True)
+    batch, per = len(lens), -(-(max(lens) + nodes) // places)
+    codes, scales = eight_bit_cache(kind, batch * per, hk, places, dim, 3)
+    table = torch.randperm(batch * per, generator=gen(4)).to(torch.int32).view(batch, per)
+    q = torch.randn(batch, nodes, hq, dim, generator=gen(5)).to(BF16)
+    mask = chains_and_branches(batch, nodes)
+    hit = [n + nodes // 2 if where == "nodes" else n // 3 for n in lens]
+    for b, t in enumerate(hit):
+        if where == "nodes" or lens[b] > 0:
+            codes[1].view(I8)[table[b, t // places].long(), :, t % places] = 0
+            scales[1][table[b, t // places].long(), :, t % places] = math.inf if b % 2 else math.nan
+    want = attention_reference(q, codes, scales, table, lens, mask, dim ** -0.5)
+    got = call_attention(q, codes, scales, table, lens, mask, dim ** -0.5)
+    assert want[0].isnan().any() and not (where == "nodes" and want[0].isnan().all())
+    check_attention(got, want, max(lens) + nodes, dim)
