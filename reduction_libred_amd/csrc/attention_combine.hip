@@ -63,9 +63,11 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(TreeAttention a, int 
         load(0);
         if (wl >= here) ml = make_float2(-__builtin_inff(), 0.f);
         const float to = fmaxf(m, group_combine<kWave>(ml.x, MaxOp()));
-        const float f = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - to);
-        const float w = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(ml.x - to);
-        l = l * f + group_combine<kWave>(w * ml.y, AddOp());
+        // Powers of 2 in halves: with 8-bit values a sum may be as far above
+        // its 2^M as their scales are apart.
+        const float hf = m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(0.5f * (m - to)), f = hf * hf;
+        const float hw = ml.x == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(0.5f * (ml.x - to)), w = hw * hw;
+        l = l * hf * hf + group_combine<kWave>(ml.y * hw * hw, AddOp());
         v *= f;
         m = to;
         for (int k1 = 0; k1 < here; k1 += 4 * kSlices) {

@@ -22,7 +22,11 @@
 // elements stay whole: the scale of a key multiplies its scores, and the scale
 // of a value joins the exponent,
 //     w_t = 2^(s'_t + log2 c_t - M),  out = sum_t w_t code_t / sum_t w_t / c_t,
-// so that w stays in range whatever the scales are. P is rounded to the type
+// so that w is at most 1 (2^8 until M follows) whatever the scales are. Where
+// scales are so far apart that some w vanish whose w / c do not, the piece is
+// gone through again without them for the sum, and once more for the output.
+// (Sums that bear any scales in one pass, of squared roots of w / c, cost all
+// others: 32 sequences x 32 rows 130.7 us / 123.5.) P is rounded to the type
 // of V in the product (float16 for 8-bit caches, which hold those exactly):
 // relative 2^-11 or 2^-8 a term, the step of the output's own type.
 //
@@ -160,6 +164,10 @@ __device__ __forceinline__ Arguments arguments_again() {
 }
 
 constexpr float kLazy = 8.f;  // how far (in powers of 2) scores may pass M before M follows
+// Scales of values between these, and a row of zeros taken as kZeroScale (it
+// should not raise M), are never so far apart that a weight vanishes (exp2
+// gives 0 below 2^-126) whose share of the sum, w / c, is above 2^-56.
+constexpr float kLeastScale = 0x1p-50f, kMostScale = 0x1p10f, kZeroScale = 0x1p-60f;
 
 // RW rows a wave (the side of its matrix instruction), WM waves of different
 // rows, WT of different tokens, TS tokens a tile.
@@ -216,9 +224,12 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     __shared__ uint64_t held[WT][4];           // which of them are in the cache
     __shared__ __align__(16) float factors[WT][HELD][3][kScaled ? TS : 4];  // of keys; of values: logarithm, inverse
     __shared__ float red[2][WM * WT][RW];
-    // What is no number among the values: in a node's (odd), which some rows may
-    // not see, or in the scale of a token that all rows see (lost).
-    __shared__ int odd, lost;
+    // Infinities or NaN among a node's values, or for its scale (kOdd), which some
+    // rows may not see; for the scale of a token that all rows see (kLost);
+    // scales beyond kLeastScale and kMostScale (kBeyond).
+    constexpr int kOdd = 1, kLost = 2, kBeyond = 4;
+    __shared__ int notes;
+    __shared__ float unscaled[2][kScaled ? S::kRows : 1];  // maxima and sums of pass 1
 
     // One argument of every 64-byte line, so that all lines are asked for at
     // once: fetched one after the other as they are met, the arguments alone
@@ -301,6 +312,10 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         b = uniform(b), seg = uniform(seg), skip = uniform(skip), now = uniform(now), end = uniform(end);
     }
 
+    // 0: the usual one. 1 and 2, where that has met scales beyond kLeastScale and
+    // kMostScale: without scales of values, for the rows' maxima and sums; with
+    // them, for the output.
+    int pass = 0;
     while (now < end) {
     const Arguments A = arguments_again();
     len = uniform(len), count = uniform(count);
@@ -381,7 +396,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         for (int w = 0; w < 4; ++w) {
             constexpr uint32_t X = Mma<VT>::kExponent;
             const uint32_t keep = ((v[w] & X) == X ? 0u : 0xFFFFu) | ((v[w] >> 16 & X) == X ? 0u : 0xFFFF0000u);
-            if (keep != ~0u) odd = 1;
+            if (keep != ~0u) atomicOr(&notes, kOdd);
             v[w] &= keep;
         }
         return v;
@@ -402,20 +417,19 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         const bool part = uniform((int)(in != kAllIn)) || DP != D;
         if constexpr (kScaled) {
             if (looks && ahead == i % AT_ONCE) {
-                // A scale of 0 (a row of zeros) is taken as 2^-100. One that is
-                // no number (a row that held an infinity or a NaN) is left out
-                // of the weights, which it has no part in, and noted: the rows
-                // that see the token get it at the end.
-                const bool number = sv < __builtin_inff();
-                const float c = number ? fmaxf(sv, 0x1p-100f) : 1.f;
+                // A scale that is no number (of a row that held an infinity or a NaN)
+                // is left out of the weights, which it has no part in, and
+                // noted: the rows that see the token get it at the end.
+                float c = pass == 1 ? 1.f : sv;
+                if (__builtin_expect(!(c >= kLeastScale && c <= kMostScale), false)) {
+                    const bool number = c < __builtin_inff();
+                    if (c != 0.f) atomicOr(&notes, number ? kBeyond : base + mine_t < len ? kLost : kOdd);
+                    c = !number ? 1.f : c != 0.f ? fmaxf(c, 0x1p-100f) : pass ? 0x1p-90f : kZeroScale;
+                }
                 auto& f = factors[wt][i % HELD];
                 f[0][mine_t] = sk * A->scale;
                 f[1][mine_t] = __builtin_amdgcn_logf(c);
                 f[2][mine_t] = 1.f / c;
-                if (__builtin_expect(!number, false)) {
-                    if (base + mine_t < len) lost = 1;
-                    else odd = 1;
-                }
             }
         }
 #pragma unroll
@@ -479,7 +493,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     }
 
     __syncthreads();  // the segment before is done with the LDS
-    if (tid == 0) odd = lost = 0;
+    if (tid == 0) notes = 0;
     settle(0);
     __syncthreads();
     if (tiles > 0) fetch(0);
@@ -642,7 +656,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         const int node = rw / group;
         if (node >= count) return v;
-        if (lost) return f32x4{kNaN, kNaN, kNaN, kNaN};
+        if (notes & kLost) return f32x4{kNaN, kNaN, kNaN, kNaN};
         const uint64_t word = E->mask ? (uint64_t)E->mask[(int64_t)b * E->nodes + node] : ~0ull >> (63 - node);
 #pragma unroll 1
         for (int t = max(first, len); t < last; ++t) {
@@ -675,10 +689,24 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             *reinterpret_cast<f32x4*>(E->part_o + (prow0 + rw) * D + c) = v;
         }
     };
-    const float ll = join_parts<PARTS>(l, [](float x, float y) { return x + y; });
+    // The sum of row r of the block, found with the maximum mm: in pass 2 that of
+    // pass 1, brought to this pass's maximum in two halves (its own may be as far
+    // away as the scales are apart).
+    auto settled = [&](int r, float mm, float ll, bool first) {
+        if constexpr (kScaled) {
+            if (pass == 1 && first) unscaled[0][r] = mm, unscaled[1][r] = ll;
+            if (pass == 2) {
+                const float half = __builtin_amdgcn_exp2f(0.5f * (unscaled[0][r] - mm));
+                ll = unscaled[1][r] == 0.f ? 0.f : unscaled[1][r] * half * half;
+            }
+        }
+        return ll;
+    };
+    float ll = join_parts<PARTS>(l, [](float x, float y) { return x + y; });
     // Columns of an accumulator, in fours: 4 PARTS (y / 4) + 4 part.
     if constexpr (WT == 1) {
         if (row < M) {
+            ll = settled(wm * RW + n, m, ll, part == 0);
             if (part == 0) put_stats(row, m, ll);
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -714,12 +742,13 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
                 lsum += red[1][w][rn];
                 mx = fmaxf(mx, red[0][w][rn]);
             }
+            lsum = settled(rn, mx, lsum, c == 0);
             if (c == 0) put_stats(rw, mx, lsum);
             put4(rw, c, v, lsum);
         }
     }
     __syncthreads();
-    if (odd | lost) {
+    if (notes & (kOdd | kLost)) {
         for (int e = tid; e < S::kRows * (DP / 4); e += S::kThreads) {
             const int c = e % (DP / 4) * 4, rw = rb * S::kRows + e / (DP / 4);
             if (c >= D || rw >= M) continue;
@@ -731,7 +760,12 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             }
         }
     }
+    if (kScaled && (pass ? pass == 1 : (notes & kBeyond) != 0)) {
+        ++pass;
+        continue;
     }
+    }
+    pass = 0;
     now += direct ? 1 : mine;
     skip = 0;
     if (now < end) {  // the next segment that has tiles

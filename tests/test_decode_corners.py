@@ -175,3 +175,32 @@ def test_value_rows_that_are_no_numbers(shape, kind, where):
     got = call_attention(q, codes, scales, table, lens, mask, dim ** -0.5)
     assert want[0].isnan().any() and not (where == "nodes" and want[0].isnan().all())
     check_attention(got, want, max(lens) + nodes, dim)
+
+
+@pytest.mark.parametrize("spread", ["mixed", "zeros first", "zeros last", "far apart"])
+@pytest.mark.parametrize("kind", [I8, E4M3], ids=str)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_value_scales_far_apart(shape, kind, spread):
+    """Rows of zeros among values of 2^50 and more, and scales 2^130 apart: every
+    token has its full weight."""
+    lens, nodes, hq, hk, dim, places = shape
+    print(shape, kind, spread, flush=True)
+    batch, per = len(lens), -(-(max(lens) + nodes) // places)
+    codes, scales = eight_bit_cache(kind, batch * per, hk, places, dim, 6)
+    table = torch.randperm(batch * per, generator=gen(7)).to(torch.int32).view(batch, per)
+    q = (0.5 * torch.randn(batch, nodes, hq, dim, generator=gen(8))).to(BF16)
+    for b, n in enumerate(lens):
+        t = torch.arange(n + nodes)
+        page, at = table[b, t // places].long(), t % places
+        low = {"mixed": t % 2 == 0, "zeros first": t < n * 2 // 3, "zeros last": t >= n // 3, "far apart": t % 3 == 0}[spread]
+        if spread == "far apart":
+            scales[1][page[low], :, at[low]] *= 2.0 ** -60
+            scales[1][page[~low], :, at[~low]] *= 2.0 ** 70
+        else:
+            scales[1][page[low], :, at[low]] = 0.0
+            codes[1].view(I8)[page[low], :, at[low]] = 0
+            scales[1][page[~low], :, at[~low]] *= 2.0 ** (50 + 20 * b)
+    mask = chains_and_branches(batch, nodes)
+    want = attention_reference(q, codes, scales, table, lens, mask, dim ** -0.5)
+    got = call_attention(q, codes, scales, table, lens, mask, dim ** -0.5)
+    check_attention(got, want, max(lens) + nodes, dim, 130)
