@@ -186,7 +186,7 @@ __device__ __forceinline__ void choose(const Verify& a, const Verifier<T>& v, in
     // The segment in which the running sum passes r times the whole.
     double total, all;
     double run = block_scan<W>(mine, lds, &total);
-    if (!(total > 0.0)) {
+    if (total == 0.0) {  // a NaN is no such sum: it draws nothing
         // p is nowhere above q: the weights are p itself.
         kind = kAll;
         mine = 0.0;

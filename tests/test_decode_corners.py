@@ -204,3 +204,27 @@ def test_value_scales_far_apart(shape, kind, spread):
     want = attention_reference(q, codes, scales, table, lens, mask, dim ** -0.5)
     got = call_attention(q, codes, scales, table, lens, mask, dim ** -0.5)
     check_attention(got, want, max(lens) + nodes, dim, 130)
+
+
+@pytest.mark.parametrize("dt", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("vocab", [3001, 40003])
+def test_verify_nan_in_either_row(dt, vocab):
+    """A NaN among the weights of the row that a token is drawn from draws none
+    (-1), whether it is the target's or the draft's; elsewhere it is not looked at."""
+    b, k = 6, 2
+    p = torch.softmax(torch.randn(b, k + 1, vocab, generator=gen(9)), -1).to(dt)
+    q = torch.softmax(torch.randn(b, k, vocab, generator=gen(10)), -1).to(dt)
+    drafted = torch.full((b, k), 5)
+    u, r = torch.full((b, k), 1.0), torch.rand(b, generator=gen(11))
+    q[:, :, 5], p[:, :, 5] = 0.5, 0.25                 # refused by u of 1
+    u[3:, 0] = 0.0                                     # the first is accepted
+    q[0, 0, 9] = q[1, 0, vocab - 1] = p[2, 0, 7] = math.nan
+    q[3, 1, 9], q[4, 0, 9], p[5, 2, 9] = math.nan, math.nan, math.nan
+    n, tokens = rl.red_verify_drafts(*(x.to(DEV) for x in (p, q, drafted, u, r)))
+    assert n.tolist() == [0, 0, 0, 1, 1, 1]
+    assert tokens[:4].tolist() == [[-1, -1, -1]] * 3 + [[5, -1, -1]]
+    for i in (4, 5):
+        w = (p[i, 1].double() - q[i, 1].double()).clamp(min=0)
+        run = torch.cumsum(w, 0)
+        want = int((run > float(r[i]) * run[-1]).nonzero()[0])
+        assert tokens[i].tolist() == [5, want, -1]
