@@ -74,6 +74,16 @@ bool rows_on(const red_heads& h, size_t tokens, size_t esize, size_t bytes) {
            (h.heads == 1 || h.head_stride * (int64_t)esize % (int64_t)bytes == 0);
 }
 
+// A launch has fewer than 2^32 threads: most blocks of 256 that one may have.
+// Calls of more go in several launches, one after the other.
+constexpr size_t kMaxBlocks = ((size_t)1 << 24) - 1;
+static_assert(libred::kQkNormWaves == 4 && libred::kCacheWaves == 4, "blocks of 256 threads");
+
+// Heads from token t on.
+Heads heads_from(const red_heads& h, size_t t, size_t esize) {
+    return Heads{h.data ? static_cast<char*>(h.data) + (int64_t)t * h.token_stride * (int64_t)esize : nullptr, h.token_stride, h.head_stride};
+}
+
 using QkNormLaunch = hipError_t (*)(int, int, const libred::QkNorm&, bool, int, hipStream_t);
 
 red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, const red_heads* dk, float* dqw,
@@ -147,9 +157,18 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
                                 : a->type == RED_F16 ? libred::launch_qk_norm_f16
                                                      : libred::launch_qk_norm_bf16;
     if (!back) {
-        if (blocks > 0x7fffffff) return RED_ERR_INVALID_ARG;
-        const hipError_t e = launch(vec, lanes, k, false, (int)blocks, stream);
-        return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+        // Tokens have one wave each where there are so many.
+        const size_t most = blocks > kMaxBlocks ? kMaxBlocks * libred::kQkNormWaves : T;
+        for (size_t t = 0; t < T; t += most) {
+            const size_t n = T - t < most ? T - t : most;
+            k.q = heads_from(a->q, t, es), k.k = heads_from(a->k, t, es);
+            k.q_out = heads_from(a->q_out, t, es), k.k_out = heads_from(a->k_out, t, es);
+            k.pos = a->pos ? a->pos + t : nullptr, k.tokens = (int64_t)n;
+            const size_t all = (n * parts + libred::kQkNormWaves - 1) / libred::kQkNormWaves;
+            const hipError_t e = launch(vec, lanes, k, false, (int)all, stream);
+            if (e != hipSuccess) return host_fail(e, RED_ERR_HIP);
+        }
+        return RED_OK;
     }
     // Blocks that go through tokens in turn: 6 a compute unit (16384 tokens x
     // 40 heads of 128: 91 us; 5 a compute unit 100, 8 a compute unit 95).
@@ -257,7 +276,6 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     }
     const size_t block_tokens = (size_t)(libred::kCacheWaves * 64 / lanes);
     const size_t groups = (tokens + block_tokens - 1) / block_tokens;
-    if (groups > 0x7fffffff) return RED_ERR_INVALID_ARG;
     // A block takes all heads of its tokens; where that makes too few blocks
     // for 4 a compute unit the heads are shared, down to one row a group (20
     // tokens x 16 rows, write / read: 3.4 / 3.1 us, not shared 9.1 / 5.1; 32768
@@ -267,9 +285,17 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     if (parts > pairs) parts = pairs;
     if (parts > 65535) parts = 65535;
     a.parts = (int)parts;
-    const hipError_t e = write ? libred::launch_cache_write(type, c->type, vec, lanes, a, (unsigned int)groups, stream)
-                               : libred::launch_cache_read(type, c->type, vec, lanes, a, (unsigned int)groups, stream);
-    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+    const size_t most = groups > kMaxBlocks ? kMaxBlocks * block_tokens : tokens;
+    for (size_t t = 0; t < tokens; t += most) {
+        const size_t n = tokens - t < most ? tokens - t : most;
+        a.k = heads_from(*k, t, 2), a.v = heads_from(*v, t, 2);
+        a.slots = slots + t, a.tokens = (int64_t)n;
+        const unsigned int all = (unsigned int)((n + block_tokens - 1) / block_tokens);
+        const hipError_t e = write ? libred::launch_cache_write(type, c->type, vec, lanes, a, all, stream)
+                                   : libred::launch_cache_read(type, c->type, vec, lanes, a, all, stream);
+        if (e != hipSuccess) return host_fail(e, RED_ERR_HIP);
+    }
+    return RED_OK;
 }
 
 red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) {
@@ -364,9 +390,23 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
             k.plan = reinterpret_cast<int*>(k.part_ml + rows);
         }
     }
-    hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
-    if (e == hipSuccess && k.blocks > 0) e = libred::launch_attention_combine(type, k, shape.rows(), stream);
-    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+    if (k.blocks > 0) {
+        hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
+        if (e == hipSuccess) e = libred::launch_attention_combine(type, k, shape.rows(), stream);
+        return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+    }
+    // A block a segment: as many sequences a launch as it may have blocks for.
+    const size_t most = segments > kMaxBlocks ? kMaxBlocks / (segments / B) : B;
+    for (size_t b = 0; b < B; b += most) {
+        k.batch = (int)(B - b < most ? B - b : most);
+        k.q = static_cast<const char*>(a->q) + (int64_t)b * qb * 2, k.out = static_cast<char*>(a->out) + (int64_t)b * bs * 2;
+        k.lse = a->lse + b * N * H;
+        k.table = a->table ? a->table + (int64_t)b * a->table_stride : nullptr, k.lens = a->lens + b;
+        k.mask = a->tree_mask ? a->tree_mask + b * N : nullptr, k.count = a->node_count ? a->node_count + b : nullptr;
+        const hipError_t e = libred::launch_tree_attention(type, c.type, k, stream);
+        if (e != hipSuccess) return host_fail(e, RED_ERR_HIP);
+    }
+    return RED_OK;
 }
 
 // Whether batch x steps rows of `vocab` elements at these strides stay in range.

@@ -228,3 +228,51 @@ def test_verify_nan_in_either_row(dt, vocab):
         run = torch.cumsum(w, 0)
         want = int((run > float(r[i]) * run[-1]).nonzero()[0])
         assert tokens[i].tolist() == [5, want, -1]
+
+
+MANY = (1 << 26) + 5   # a wave or a row each: more than a launch has threads for
+
+
+def test_norms_of_many_tokens():
+    x = torch.randn(MANY, 1, 2, dtype=F16, device=DEV)
+    pos, freq = torch.arange(MANY, device=DEV), torch.tensor([1e-4], device=DEV)
+    got, _ = rl.red_qk_norm_rope(x, x[:, :0], pos, freq)
+    half = MANY // 2
+    for part in (slice(0, half), slice(half, MANY)):
+        want, _ = rl.red_qk_norm_rope(x[part], x[part, :0], pos[part], freq)
+        assert torch.equal(got[part], want)
+
+
+@pytest.mark.parametrize("kind", [F16, I8], ids=str)
+def test_cache_of_many_tokens(kind):
+    x = [torch.randn(MANY, 1, 1, dtype=F16, device=DEV) for _ in range(2)]
+    pages = -(-MANY // 64)
+    pg = [torch.zeros(pages, 1, 64, 1, dtype=kind, device=DEV) for _ in range(2)]
+    sc = dict(k_scales=torch.zeros(pages, 1, 64, device=DEV), v_scales=torch.zeros(pages, 1, 64, device=DEV)) if kind == I8 else {}
+    slots = torch.arange(MANY - 1, -1, -1, device=DEV)
+    rl.red_cache_write(*x, slots, *pg, **sc)
+    for i, s in enumerate(("k_scales", "v_scales")):
+        cached = pg[i].view(-1)[:MANY].flip(0)
+        if kind == I8:      # a row of one element is its own largest: 127 and its sign, or 0
+            assert torch.equal(cached.half() * 1.0, torch.sign(x[i].view(-1)) * 127)
+            top = x[i].view(-1).abs().float()      # by a tensor: torch divides by a number as a product with 1 / 127
+            assert torch.equal(sc[s].view(-1)[:MANY].flip(0), top / torch.full_like(top, 127))
+        else:
+            assert torch.equal(cached, x[i].view(-1))
+    back = rl.red_cache_read(*pg, slots, F16, **sc)
+    for a, b in zip(back, x):
+        assert torch.equal(a, b) if kind == F16 else (a - b).abs().max() <= 2.0 ** -9 * b.abs().max()
+
+
+def test_attention_of_many_segments():
+    """65535 sequences of 257 kv heads, a block each."""
+    batch, heads, dim = 65535, 257, 16
+    pages = [torch.randn(3, heads, 16, dim, generator=gen(12)).to(F16).to(DEV) for _ in range(2)]
+    table = (torch.arange(batch, dtype=torch.int32, device=DEV) % 3)[:, None]
+    lens = torch.arange(batch, dtype=torch.int32, device=DEV) % 16
+    q = torch.randn(batch, 1, heads, dim, dtype=F16, device=DEV)
+    out, lse = rl.red_tree_attention(q, *pages, table, lens, 0.25)
+    half = batch // 2
+    for part in (slice(0, half), slice(half, batch)):
+        want = rl.red_tree_attention(q[part], *pages, table[part], lens[part], 0.25)
+        assert torch.equal(out[part], want[0]) and torch.equal(lse[part], want[1])

@@ -123,3 +123,67 @@ def test_verification_of_a_larger_shape_provides_the_scratch(calls):
         x = needs(calls, "red_verify_drafts", ref(verify(*a, 2)))
         y = asked(calls, "red_verify_drafts", ref(verify(*b, 2)))
         assert x <= y, (a, b)
+
+
+def launched(calls):
+    n = calls.launched(None, 0)
+    to = (I64 * (5 * n))()
+    calls.launched(to, n)
+    return [tuple(to[5 * i:5 * i + 5]) for i in range(n)]
+
+
+def check_launches(calls, items, in_bytes, out_bytes, by_bytes):
+    """Every launch has fewer than 2^32 threads, and together they take all
+    items in their order, from the tensors' starts on."""
+    got = launched(calls)
+    done, (_, _, in0, out0, by0) = 0, got[0]
+    for blocks, n, at_in, at_out, at_by in got:
+        assert 0 < blocks * 256 < 1 << 32 and n > 0
+        assert (at_in - in0, at_out - out0, at_by - by0) == (done * in_bytes, done * out_bytes, done * by_bytes)
+        done += n
+    assert done == items
+    return len(got)
+
+
+BIG = 1 << 44    # fake addresses of large tensors
+
+
+@pytest.mark.parametrize("tokens, many", [(5, False), ((1 << 26) - 4, False), ((1 << 26) + 5, True), (1 << 30, True), (1 << 33, True)])
+@pytest.mark.parametrize("dim", [3, 64])
+def test_norms_of_any_number_of_tokens(calls, tokens, many, dim):
+    def heads(at, n=2):
+        return D.Heads(BIG * at, n, n * dim, dim)
+
+    calls.forget()
+    a = D.QkNormRopeArgs(type=1, interleaved=0, tokens=tokens, dim=dim, rot=2, eps=1e-6, q=heads(1), k=heads(2, 1), q_out=heads(3),
+                         k_out=heads(4, 1), q_weight=None, k_weight=None, pos=BIG * 5, freq=G)
+    assert calls.red_qk_norm_rope(ref(a), None) == rl.RED_OK
+    assert (check_launches(calls, tokens, 4 * dim, 4 * dim, 8) > 1) == many
+    calls.forget()
+    dq, dk = heads(6), heads(7, 1)
+    assert calls.red_qk_norm_rope_backward(ref(a), ref(dq), ref(dk), None, None, None) == rl.RED_OK
+    assert check_launches(calls, tokens, 4 * dim, 4 * dim, 8) == 1
+
+
+@pytest.mark.parametrize("tokens, dim, many", [(5, 64, False), (1 << 26, 64, False), ((1 << 26) - 4, 3, False), ((1 << 26) + 5, 3, True),
+                                               (1 << 32, 64, True), (1 << 30, 7, True)])
+@pytest.mark.parametrize("kind", [1, 3])
+def test_cache_calls_of_any_number_of_tokens(calls, tokens, dim, many, kind):
+    scaled = kind >= 3
+    c = D.PagedCache(k=A, v=B, k_scales=C if scaled else None, v_scales=E if scaled else None, type=kind, pages=1 << 36, heads=1,
+                     places=16, dim=dim, page_stride=0, head_stride=dim * 16, place_stride=dim, scale_page_stride=0,
+                     scale_head_stride=16, scale_place_stride=1)
+    k, v = D.Heads(BIG, 1, dim, dim), D.Heads(BIG * 2, 1, dim, dim)
+    for f in (calls.red_cache_write, calls.red_cache_read):
+        calls.forget()
+        assert f(ref(c), 1, ref(k), ref(v), BIG * 3, tokens, None) == rl.RED_OK
+        assert (check_launches(calls, tokens, 2 * dim, 2 * dim, 8) > 1) == many
+
+
+@pytest.mark.parametrize("batch, heads, many", [(3, 8, False), (65535, 256, False), (65535, 257, True), (65535, 65535, True)])
+def test_attention_of_any_number_of_segments(calls, batch, heads, many):
+    calls.forget()
+    a = attention(1, batch, 1, 1, heads, 16, 16)
+    assert calls.red_tree_attention(ref(a), None) == (rl.RED_OK if batch * heads < 1 << 31 else rl.RED_ERR_INVALID_ARG)
+    if batch * heads < 1 << 31:
+        assert (check_launches(calls, batch, 2 * 16 * heads, 2 * 16 * heads, 4) > 1) == many
