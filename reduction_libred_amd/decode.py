@@ -5,6 +5,8 @@ it calls and only marshals arguments. Tensors are taken with the strides they
 have, as long as their last dimension is contiguous. Where a call is given a
 stream, its outputs are allocated there; ordering that stream behind the one
 its inputs come from, and the outputs' readers behind it, is the caller's.
+red_qk_norm_rope is differentiable; nothing else here is, and its results carry
+no history.
 
 A decoding step makes these calls with little work in each, so the way to the
 C call is kept short: one look at a tensor where it is as it should be (what is
@@ -12,6 +14,7 @@ wrong is found out afterwards), and argument structs packed in one go.
 """
 import ctypes
 import struct
+import warnings
 
 import torch
 
@@ -132,6 +135,7 @@ def _whole(name, what, x, dtype, device, shape):
 
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_grad_enabled = torch.is_grad_enabled
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -220,12 +224,23 @@ def red_qk_norm_rope(q, k, pos, freq, q_weight=None, k_weight=None, eps=1e-6, in
     heads, dim), times the weights, and the rotary rotation of the first
     2 * len(freq) elements by pos[t] * freq[i], in one pass. Pairs are halves
     apart, or neighbours if `interleaved`. float32, float16 or bfloat16; pos
-    int64, freq float32. q_out and k_out may be q and k. -> (q_out, k_out)."""
+    int64, freq float32. q_out and k_out may be q and k. -> (q_out, k_out).
+    Gradients go to q, k and the weights, unless q_out or k_out is given: what
+    is written there carries no history, and a warning says so."""
     if stream is not None:
         return _on(stream, red_qk_norm_rope, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
     name = "red_qk_norm_rope"
+    try:
+        history = _grad_enabled() and (q.requires_grad or k.requires_grad or q_weight is not None and q_weight.requires_grad or
+                                       k_weight is not None and k_weight.requires_grad)
+    except AttributeError:
+        history = False     # no tensors: refused below
+    if history:
+        if q_out is None and k_out is None:
+            return _QkNormRope.apply(q, k, q_weight, k_weight, pos, freq, eps, interleaved)
+        warnings.warn(f"{name}: what is written to q_out and k_out carries no history", stacklevel=2)
     device, q_out, k_out, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out)
-    _call(name, device, stream, args)
+    _call(name, device, None, args)
     return q_out, k_out
 
 
@@ -236,14 +251,43 @@ def red_qk_norm_rope_backward(dq, dk, q, k, pos, freq, q_weight=None, k_weight=N
     (also where the weight is None, that is ones)."""
     if stream is not None:
         return _on(stream, red_qk_norm_rope_backward, dq, dk, q, k, pos, freq, q_weight, k_weight, eps, interleaved)
+    return _qk_norm_backward(dq, dk, q, k, pos, freq, q_weight, k_weight, eps, interleaved, True, True)
+
+
+def _qk_norm_backward(dq, dk, q, k, pos, freq, q_weight, k_weight, eps, interleaved, of_q_weight, of_k_weight):
     name = "red_qk_norm_rope_backward"
     device, q_grad, k_grad, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
     _rows(name, "dq", dq, q.dtype, device, q.shape)
     _rows(name, "dk", dk, q.dtype, device, k.shape)
-    dqw = torch.empty(q.shape[2], dtype=_FLOAT32, device=q.device)
-    dkw = torch.empty_like(dqw)
-    _call(name, device, stream, args, _heads(dq), _heads(dk), dqw.data_ptr(), dkw.data_ptr())
+    dqw = torch.empty(q.shape[2], dtype=_FLOAT32, device=q.device) if of_q_weight else None
+    dkw = torch.empty(q.shape[2], dtype=_FLOAT32, device=q.device) if of_k_weight else None
+    _call(name, device, None, args, _heads(dq), _heads(dk), dqw.data_ptr() if of_q_weight else None,
+          dkw.data_ptr() if of_k_weight else None)
     return q_grad, k_grad, dqw, dkw
+
+
+class _QkNormRope(torch.autograd.Function):
+    """red_qk_norm_rope with red_qk_norm_rope_backward as its gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, pos, freq, eps, interleaved):
+        name = "red_qk_norm_rope"
+        device, q_out, k_out, args = _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, None, None)
+        _call(name, device, None, args)
+        ctx.save_for_backward(q, k, q_weight, k_weight, pos, freq)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return q_out, k_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        q, k, q_weight, k_weight, pos, freq = ctx.saved_tensors
+        # A gradient may be broadcast (that of a sum), also along the rows.
+        dq, dk = (x if x.stride(-1) == 1 or x.shape[-1] <= 1 else x.contiguous() for x in (dq, dk))
+        of_q, of_k, of_qw, of_kw = ctx.needs_input_grad[:4]
+        dq, dk, dqw, dkw = _qk_norm_backward(dq, dk, q, k, pos, freq, q_weight, k_weight, ctx.eps, ctx.interleaved, of_qw, of_kw)
+        return (dq if of_q else None, dk if of_k else None, dqw.to(q.dtype) if of_qw else None,
+                dkw.to(q.dtype) if of_kw else None, None, None, None, None)
 
 
 def _cache_check(name, k_pages, v_pages, k_scales, v_scales):

@@ -276,3 +276,73 @@ def test_attention_of_many_segments():
     for part in (slice(0, half), slice(half, batch)):
         want = rl.red_tree_attention(q[part], *pages, table[part], lens[part], 0.25)
         assert torch.equal(out[part], want[0]) and torch.equal(lse[part], want[1])
+
+
+def norm_tensors(dt, seed):
+    g = gen(seed)
+    x = [torch.randn(37, h, 64, generator=g).to(dt).to(DEV) for h in (6, 2)]
+    w = [(1 + 0.2 * torch.randn(64, generator=g)).to(dt).to(DEV) for _ in range(2)]
+    dy = [torch.randn(37, h, 64, generator=g).to(dt).to(DEV) for h in (6, 2)]
+    return x, w, dy, torch.randint(0, 5000, (37,), generator=g).to(DEV), R.frequencies(48).to(DEV)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dt", [F32, F16, BF16], ids=str)
+def test_norms_have_gradients(dt, interleaved):
+    """The gradients that autograd finds are those of the backward call."""
+    x, w, dy, pos, freq = norm_tensors(dt, 13)
+    leaves = [y.detach().clone().requires_grad_() for y in x + w]
+    out = rl.red_qk_norm_rope(leaves[0], leaves[1], pos, freq, leaves[2], leaves[3], eps=1e-5, interleaved=interleaved)
+    plain = rl.red_qk_norm_rope(x[0], x[1], pos, freq, w[0], w[1], eps=1e-5, interleaved=interleaved)
+    assert torch.equal(out[0], plain[0]) and torch.equal(out[1], plain[1]) and plain[0].grad_fn is None
+    torch.autograd.backward(out, dy)
+    want = rl.red_qk_norm_rope_backward(dy[0], dy[1], x[0], x[1], pos, freq, w[0], w[1], eps=1e-5, interleaved=interleaved)
+    for y, z in zip(leaves, want):
+        assert y.grad.dtype == dt and torch.equal(y.grad, z.to(dt))
+
+
+def test_norms_gradients_of_some_inputs():
+    x, w, dy, pos, freq = norm_tensors(F32, 14)
+    zero = torch.zeros_like(dy[0])
+    want = rl.red_qk_norm_rope_backward(zero, dy[1], x[0], x[1], pos, freq, None, w[1])
+    # only k's output is used, only the weight of k wants a gradient
+    kw = w[1].clone().requires_grad_()
+    _, k = rl.red_qk_norm_rope(x[0], x[1], pos, freq, None, kw)
+    k.backward(dy[1])
+    assert torch.equal(kw.grad, want[3])
+    # q within a larger tensor, no weights; a sum's gradient is broadcast
+    fused = torch.cat(x, 1).requires_grad_()
+    q, k = rl.red_qk_norm_rope(fused[:, :6], fused[:, 6:], pos, freq)
+    (q.sum() + 2 * k.sum()).backward()
+    want = rl.red_qk_norm_rope_backward(torch.ones_like(dy[0]), torch.full_like(dy[1], 2), x[0], x[1], pos, freq)
+    assert torch.equal(fused.grad, torch.cat(want[:2], 1))
+    # on a stream of its own, where the backward pass follows it
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    leaf = x[0].clone().requires_grad_()
+    torch.cuda.synchronize()
+    q, _ = rl.red_qk_norm_rope(leaf, x[1], pos, freq, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    q.sum().backward()
+    torch.cuda.synchronize()
+    assert torch.equal(leaf.grad, rl.red_qk_norm_rope_backward(torch.ones_like(dy[0]), torch.zeros_like(dy[1]), x[0], x[1], pos, freq)[0])
+
+
+def test_norms_without_gradients():
+    x, w, dy, pos, freq = norm_tensors(F16, 15)
+    leaf = x[0].clone().requires_grad_()
+    with torch.no_grad():
+        assert not rl.red_qk_norm_rope(leaf, x[1], pos, freq)[0].requires_grad
+    assert not rl.red_qk_norm_rope(leaf.detach(), x[1], pos, freq)[0].requires_grad
+    to = torch.empty_like(x[0])
+    with pytest.warns(UserWarning, match="no history"):
+        got, _ = rl.red_qk_norm_rope(leaf, x[1], pos, freq, q_out=to)
+    assert got is to and not got.requires_grad
+    with pytest.raises(TypeError):
+        rl.red_qk_norm_rope(leaf, x[1], pos.int(), freq)
+    # an input that is changed before the backward pass is found out
+    y = leaf * 1.0
+    q, _ = rl.red_qk_norm_rope(y, x[1], pos, freq)
+    y.zero_()
+    with pytest.raises(RuntimeError):
+        q.sum().backward()
