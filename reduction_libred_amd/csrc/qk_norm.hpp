@@ -173,7 +173,8 @@ __device__ __forceinline__ void lane_turns(float (&c)[NV][VEC], float (&g)[NV][V
     wave_lds_fence();
 }
 
-// A weight at this lane's columns, or at their partners.
+// A weight at this lane's columns, or at their partners (0 where nothing turns:
+// there the partner has no part in the result, whatever its weight is).
 template <class T, int VEC, int G, int NV>
 __device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const void* p, int dim, int lane) {
 #pragma unroll
@@ -188,24 +189,26 @@ __device__ __forceinline__ void load_weight(float (&w)[NV][VEC], const void* p, 
     }
 }
 template <class T, int VEC, int G, int NV, int MODE>
-__device__ __forceinline__ void load_partner_weight(float (&w)[NV][VEC], const float (&own)[NV][VEC], const void* p, int dim,
-                                                    int rot, int interleaved, int lane) {
+__device__ __forceinline__ void load_partner_weight(float (&w)[NV][VEC], const float (&own)[NV][VEC], const void* p, int rot,
+                                                    int interleaved, int lane) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int d = (lane + v * G) * VEC;
         if constexpr (MODE == kTurnInside) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) w[v][j] = own[v][j ^ 1];
+            for (int j = 0; j < VEC; ++j) w[v][j] = d < rot ? own[v][j ^ 1] : 0.f;
         } else if (p == nullptr) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) w[v][j] = 1.f;
+            for (int j = 0; j < VEC; ++j) w[v][j] = d + j < rot ? 1.f : 0.f;
         } else if constexpr (MODE == kTurnVectors) {
             const int o = d < rot ? (d < rot / 2 ? d + rot / 2 : d - rot / 2) : 0;
             widen_vec<T, VEC>(*reinterpret_cast<const RowVec<T, VEC>*>(static_cast<const typename T::bits*>(p) + o), w[v]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) w[v][j] = d < rot ? w[v][j] : 0.f;
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
-                w[v][j] = T::widen(static_cast<const typename T::bits*>(p)[d + j < dim ? partner_of(d + j, rot, interleaved) : 0]);
+                w[v][j] = d + j < rot ? T::widen(static_cast<const typename T::bits*>(p)[partner_of(d + j, rot, interleaved)]) : 0.f;
         }
     }
 }
@@ -300,8 +303,8 @@ __global__ __launch_bounds__(kQkNormWaves* kWave) void qk_norm_kernel(QkNorm a) 
         float c[NV][VEC], g[NV][VEC];
         load_weight<T, VEC, G, NV>(aq, a.q_weight, a.dim, lane);
         load_weight<T, VEC, G, NV>(ak, a.k_weight, a.dim, lane);
-        load_partner_weight<T, VEC, G, NV, MODE>(bq, aq, a.q_weight, a.dim, a.rot, a.interleaved, lane);
-        load_partner_weight<T, VEC, G, NV, MODE>(bk, ak, a.k_weight, a.dim, a.rot, a.interleaved, lane);
+        load_partner_weight<T, VEC, G, NV, MODE>(bq, aq, a.q_weight, a.rot, a.interleaved, lane);
+        load_partner_weight<T, VEC, G, NV, MODE>(bk, ak, a.k_weight, a.rot, a.interleaved, lane);
         token_angles(a.pos, t, a.freq, a.rot, lds[wave], lds[wave] + kHeadMax / 2);
         lane_turns<VEC, G, NV, MODE, false>(c, g, a.rot, a.interleaved, lane, lds[wave], lds[wave] + kHeadMax / 2);
 #pragma unroll

@@ -346,3 +346,26 @@ def test_norms_without_gradients():
     y.zero_()
     with pytest.raises(RuntimeError):
         q.sum().backward()
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("dt", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("dim, rot, interleaved", [(128, 64, False), (128, 64, True), (128, 128, False), (100, 50, False), (66, 30, True),
+                                                   (96, 0, False), (255, 128, False)])
+def test_norms_weight_that_is_no_number(dim, rot, interleaved, dt, bad):
+    """It reaches its own column and the one that turns with it, no other."""
+    x = [torch.randn(5, h, dim, generator=gen(16)).to(dt).to(DEV) for h in (3, 1)]
+    pos, freq = torch.arange(1, 6, device=DEV), R.frequencies(rot).to(DEV)
+    w = torch.ones(dim, dtype=dt, device=DEV)
+    clean = rl.red_qk_norm_rope(*x, pos, freq, w, w, interleaved=interleaved)
+    for at in {0, dim - 1, rot // 2, max(rot - 1, 0), min(rot, dim - 1)}:
+        v = w.clone()
+        v[at] = bad
+        a, b = R.pairs(rot, interleaved)
+        hit = {at} | {int(q) for p, q in zip(a, b) if p == at} | {int(p) for p, q in zip(a, b) if q == at}
+        rest = [c for c in range(dim) if c not in hit]
+        for got, want in zip(rl.red_qk_norm_rope(*x, pos, freq, v, v, interleaved=interleaved), clean):
+            assert torch.equal(got[..., rest], want[..., rest]), at
+            assert not got[..., sorted(hit)].isfinite().any(), at
+            if at >= rot and bad == math.inf:       # times a number, and nothing else
+                assert got[..., at].isinf().all(), at
