@@ -183,6 +183,13 @@ def _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out):
             _whole(name, what, x, dtype, device, (dim,))
 
 
+def _like(x):
+    """An output for x: laid out as x is, unless that (of rows that overlap)
+    would not have a contiguous last dimension."""
+    y = torch.empty_like(x)
+    return y if y.stride(-1) == 1 or x.shape[-1] <= 1 else x.new_empty(x.shape)
+
+
 def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
     try:
         dtype, device, (tokens, heads, dim) = q.dtype, q.get_device(), q.shape
@@ -202,9 +209,9 @@ def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out,
     if not fine or q_out is not None or k_out is not None:
         _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty_like(q)
+        q_out = _like(q)
     if k_out is None:
-        k_out = torch.empty_like(k)
+        k_out = _like(k)
     a0, a1, _ = q_out.stride()
     b0, b1, _ = k_out.stride()
     return device, q_out, k_out, _pack_qk_norm(

@@ -369,3 +369,22 @@ def test_norms_weight_that_is_no_number(dim, rot, interleaved, dt, bad):
             assert not got[..., sorted(hit)].isfinite().any(), at
             if at >= rot and bad == math.inf:       # times a number, and nothing else
                 assert got[..., at].isinf().all(), at
+
+
+@pytest.mark.parametrize("strides", [(1, 70, 1), (8, 1, 1), (0, 8, 1), (8, 0, 1), (3, 1, 1)])
+def test_norms_of_rows_that_overlap(strides):
+    """Heads that are windows of one another, or broadcast."""
+    x = torch.randn(500, generator=gen(17)).to(DEV)
+    q, k = (x.as_strided((6, h, 8), strides) for h in (3, 2))
+    pos, freq = torch.arange(6, device=DEV), R.frequencies(8).to(DEV)
+    # The roundings of the norms' other tests: 20 of float32 forward, 48 back, and
+    # 200 more in the weights' sums.
+    for got, y in zip(rl.red_qk_norm_rope(q, k, pos, freq), (q, k)):
+        want, size = R.qk_norm_rope(y.cpu(), None, pos.cpu(), freq.cpu(), 1e-6, False)
+        assert ((got.cpu() - want).abs() <= U * (want.abs() + 21 * size)).all()
+    dq, dk = torch.randn(6, 3, 8, generator=gen(18)), torch.randn(6, 2, 8, generator=gen(19))
+    got = rl.red_qk_norm_rope_backward(dq.to(DEV), dk.to(DEV), q, k, pos, freq)
+    for i, (dy, y) in enumerate(((dq, q), (dk, k))):
+        dx, size, dw, dsize = R.qk_norm_rope_backward(dy, y.cpu(), None, pos.cpu(), freq.cpu(), 1e-6, False)
+        assert ((got[i].cpu() - dx).abs() <= U * (dx.abs() + 49 * size)).all()
+        assert ((got[2 + i].cpu() - dw).abs() <= U * (dw.abs() + 249 * dsize)).all()
