@@ -147,6 +147,13 @@ constexpr int attention_least_tokens(int rows, int dim, int bytes) {
 }
 // Blocks that a compute unit holds at once.
 constexpr int attention_blocks(int rows, int dim) { return rows <= kFewestRows.rows() && dim > kNarrowHeads ? 1 : 2; }
+// How many of `all` tiles (below 2^31) each of `blocks` blocks takes, and the
+// first that is block `share`'s.
+__host__ __device__ inline int share_size(int all, int blocks) { return all / blocks + (all % blocks != 0); }
+__host__ __device__ inline int share_begin(int all, int per, int share) {
+    const int64_t at = (int64_t)per * share;
+    return (int)(at < all ? at : all);
+}
 // Joins the pieces of every row into the output (rows_a_block: the shape's).
 hipError_t launch_attention_combine(int type, const TreeAttention& a, int rows_a_block, hipStream_t stream);
 hipError_t launch_tree_attention(int type, int cache_type, const TreeAttention& a, hipStream_t stream);

@@ -285,9 +285,9 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
             all += read_lane(upto, kWave - 1);
         }
         all *= per_seq;
-        const int per = (all + (int)gridDim.x - 1) / (int)gridDim.x;
+        const int per = share_size(all, (int)gridDim.x);
         const bool planner = share == 0 && wave == 0;
-        now = (int)min(share * (int64_t)per, (int64_t)all), end = min(now + per, all);
+        now = share_begin(all, per, share), end = share_begin(all, per, share + 1);
         if (now >= end && !planner) return;
         // The sequence that holds tile `now`.
         const int want = now / per_seq;  // as tiles of one segment of each sequence

@@ -96,3 +96,6 @@ extern "C" size_t scratch_asked() {
     for (const size_t s : scratch) most = s > most ? s : most;
     return most;
 }
+
+extern "C" int share_size(int all, int blocks) { return libred::share_size(all, blocks); }
+extern "C" int share_begin(int all, int per, int share) { return libred::share_begin(all, per, share); }

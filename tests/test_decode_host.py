@@ -187,3 +187,12 @@ def test_attention_of_any_number_of_segments(calls, batch, heads, many):
     assert calls.red_tree_attention(ref(a), None) == (rl.RED_OK if batch * heads < 1 << 31 else rl.RED_ERR_INVALID_ARG)
     if batch * heads < 1 << 31:
         assert (check_launches(calls, batch, 2 * 16 * heads, 2 * 16 * heads, 4) > 1) == many
+
+
+@pytest.mark.parametrize("blocks", [1, 7, 512])
+@pytest.mark.parametrize("tiles", [0, 1, 511, 513, 100000, (1 << 31) - 600, (1 << 31) - 1])
+def test_shares_of_tiles_are_a_partition(calls, tiles, blocks):
+    per = calls.share_size(tiles, blocks)
+    assert per == -(-tiles // blocks)
+    ends = [calls.share_begin(tiles, per, s) for s in range(blocks + 1)]
+    assert ends[0] == 0 and ends[-1] == tiles and all(0 <= b - a <= per for a, b in zip(ends, ends[1:]))
