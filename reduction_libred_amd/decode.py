@@ -423,6 +423,8 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
     cols = table.shape[1]
+    if max_len is not None and max_len < 0:
+        raise ValueError(f"{name}: max_len must not be negative")
     q0, q1, q2, q3 = q.stride()
     if q.get_device() != device or (q3 != 1 and dim > 1):
         _rows(name, "q", q, dtype, device, shape)

@@ -388,3 +388,12 @@ def test_norms_of_rows_that_overlap(strides):
         dx, size, dw, dsize = R.qk_norm_rope_backward(dy, y.cpu(), None, pos.cpu(), freq.cpu(), 1e-6, False)
         assert ((got[i].cpu() - dx).abs() <= U * (dx.abs() + 49 * size)).all()
         assert ((got[2 + i].cpu() - dw).abs() <= U * (dw.abs() + 249 * dsize)).all()
+
+
+def test_attention_refuses_a_negative_length():
+    pages = torch.zeros(2, 1, 16, 64, dtype=F16, device=DEV)
+    q, table, lens = torch.zeros(1, 1, 1, 64, dtype=F16, device=DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        rl.red_tree_attention(q, pages, pages, table, lens, 1.0, max_len=-1)
+    out, lse = rl.red_tree_attention(q, pages, pages, table, lens, 1.0, max_len=0)
+    assert not out.any() and (lse == -math.inf).all()
