@@ -183,13 +183,6 @@ def _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out):
             _whole(name, what, x, dtype, device, (dim,))
 
 
-def _like(x):
-    """An output for x: laid out as x is, unless that (of rows that overlap)
-    would not have a contiguous last dimension."""
-    y = torch.empty_like(x)
-    return y if y.stride(-1) == 1 or x.shape[-1] <= 1 else x.new_empty(x.shape)
-
-
 def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out, k_out):
     try:
         dtype, device, (tokens, heads, dim) = q.dtype, q.get_device(), q.shape
@@ -209,11 +202,18 @@ def _qk_norm(name, q, k, pos, freq, q_weight, k_weight, eps, interleaved, q_out,
     if not fine or q_out is not None or k_out is not None:
         _qk_norm_check(name, q, k, pos, freq, q_weight, k_weight, q_out, k_out)
     if q_out is None:
-        q_out = _like(q)
+        q_out = torch.empty_like(q)
     if k_out is None:
-        k_out = _like(k)
-    a0, a1, _ = q_out.stride()
-    b0, b1, _ = k_out.stride()
+        k_out = torch.empty_like(k)
+    a0, a1, a2 = q_out.stride()
+    b0, b1, b2 = k_out.stride()
+    if dim > 1:     # an output that was laid out like rows that overlap
+        if a2 != 1:
+            q_out = q.new_empty(q.shape)
+            a0, a1, _ = q_out.stride()
+        if b2 != 1:
+            k_out = k.new_empty(k.shape)
+            b0, b1, _ = k_out.stride()
     return device, q_out, k_out, _pack_qk_norm(
         TYPES[dtype], 1 if interleaved else 0, tokens, dim, 2 * half, eps, q.data_ptr(), heads, q0, q1, k.data_ptr(), kh, k0,
         k1, q_out.data_ptr(), heads, a0, a1, k_out.data_ptr(), kh, b0, b1,
