@@ -147,7 +147,8 @@ red_status red_cache_read(const red_paged_cache *cache, int type, const red_head
  * Query head h reads kv head h / (q_heads / cache heads). A row that sees
  * nothing, and every row of a node that does not exist, gets out = 0 and
  * lse = -inf; what lies in the cache behind a mask, infinities and NaN
- * included, does not reach a result.
+ * included, does not reach a result. A value row of an 8-bit cache whose scale
+ * is no number makes the outputs of the rows that see it NaN, not their lse.
  *
  * type: RED_F16 or RED_BF16 of q and out, and of a 16-bit cache. q and out:
  * (batch, nodes, q_heads, dim) with strides of their own, rows on 16-byte
@@ -162,7 +163,8 @@ red_status red_cache_read(const red_paged_cache *cache, int type, const red_head
  * shapes the launch, and tokens from it on (or beyond table_cols pages) are
  * not looked at. A page number outside the cache is not followed: its tokens
  * read as zeros. Scales of an 8-bit cache are not negative; a scale below
- * 2^-100 counts as that for values. Scores and sums are held in float32; in
+ * 2^-100 counts as that for values; calls that meet one outside 2^-50 .. 2^10,
+ * zeros apart, take up to three times as long. Scores and sums are held in float32; in
  * the product with V their exponentials are rounded to `type` (to float16
  * with an 8-bit cache).
  */

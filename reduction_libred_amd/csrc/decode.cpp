@@ -367,6 +367,8 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     //   a block a segment               10.8   12.7   14.2   21.2
     // 64 segments of 4 / 6 / 8 tiles of 128 rows of 128, bf16:
     //   shared 24.4   26.3   28.0, a block a segment 16.1   19.5   22.6
+    // The constants are fitted to these two rows of shapes; heads above 128 were
+    // not among them.
     const size_t tile = (size_t)shape.tokens(), tiles = ((size_t)k.max_tokens + tile - 1) / tile;
     const size_t segments = B * c.heads * (size_t)k.row_blocks;
     if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;

@@ -86,7 +86,7 @@ struct TreeAttention {
     const int64_t* mask;   // null: a chain
     const int32_t* count;  // null: all nodes
     int batch, nodes, group, max_tokens, row_blocks;
-    int blocks;  // 0: one block a segment, of at most one tile, that writes the output
+    int blocks;  // 0: one block a segment, whatever its tiles, that writes the output
     float scale;  // magnitude, times log2(e)
     uint32_t page16, place16;  // strides of the cache's pages and places in units of 16 bytes
     // Token t < 2^30 is in page (4 t factor >> 32) >> shift of its sequence:

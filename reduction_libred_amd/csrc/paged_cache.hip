@@ -4,8 +4,9 @@
 // Write, for a row x: top = max|x|, scale = top / M, element = round(x M / top),
 // M = 127 (int8) or 448 (e4m3). Read: element * scale. Both move each row once;
 // nothing but memory bounds them (32768 tokens x 8 heads of 128, bf16 and e4m3,
-// 204 MB a call: write 44.8 us, 4.6 TB/s; read 36.1 us, 5.7 TB/s; 20 tokens
-// 3.4 and 3.1 us). G lanes hold a row, 8 neighbouring elements
+// 204 MB a call: write 44.7 us, 4.6 TB/s; read 36.0 us, 5.7 TB/s; a cache of
+// bf16, 268 MB a call: 48.4 and 52.6 us, 5.5 and 5.1 TB/s; 20 tokens in int8 3.7
+// and 3.2 us). G lanes hold a row, 8 neighbouring elements
 // each (one 16-byte load), so the maximum takes log2(G) lane moves. A wave
 // takes 64 / G neighbouring tokens and goes through their (key or value, head)
 // pairs: a token's page and place are worked out once, rows of neighbouring

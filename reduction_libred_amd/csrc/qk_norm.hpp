@@ -17,9 +17,9 @@
 // then the Taylor sums of sine and cosine.
 //
 // Memory bounds both passes. 16384 tokens of 32 + 8 heads of 128 in bf16:
-// forward 336 MB in 60.8 us (5.5 TB/s; a copy of that size reaches 6.15),
-// backward 503 MB in 90.9 us (5.5 TB/s) and 4.8 us for the sum of the weights'
-// partials. 5 tokens take 4.4 us, one trip to memory after another.
+// forward 336 MB in 62.1 us (5.4 TB/s; a copy of that size reaches 6.15),
+// backward 503 MB in 91.7 us (5.5 TB/s) and 4.8 us for the sum of the weights'
+// partials. 12 tokens take 4.4 us, one trip to memory after another.
 #pragma once
 
 #include "decode_common.hpp"

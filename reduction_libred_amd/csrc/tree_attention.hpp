@@ -39,17 +39,21 @@
 //
 // What it takes, without the joining:
 //   32 sequences of 1500 to 16384 tokens, 8 kv heads x 32 rows of 128, int8:
-//     608 MB in 115.5 us (5.3 TB/s). Two waves a SIMD, each with its chain of
+//     608 MB in 117.6 us (5.2 TB/s). Two waves a SIMD, each with its chain of
 //     loads, conversion, products and exponentials: vector instructions fill
 //     40 % of the cycles, the LDS is busy for 27 %, the matrix unit for 13 %;
 //     memory alone would need 84 us. More waves do not fit the registers.
 //   4 sequences of 8192 tokens, 8 kv heads x 512 rows of 128, bf16:
-//     64 GFLOP in 99 us (650 TFLOP/s, half of a large product's rate):
+//     64 GFLOP in 100 us (640 TFLOP/s, half of a large product's rate):
 //     the matrix unit is busy for 27 % of the cycles, vector instructions
 //     fill 26 %, the LDS 22 %; exponentials wait for products, products for
 //     exponentials, and the waves for each other's tiles.
 //   1 sequence of 8191 tokens, 8 kv heads x 4 rows of 128, float16: 34 MB in
 //     12 us: latency, of the plan, the page, the rows and the joined sums.
+//   Up to 16 rows a kv head of 128: 32 sequences of 1500 to 16384 tokens, 4 rows,
+//     bf16 1173 MB in 194 us (6.1 TB/s), int8 605 MB in 104.5 us (5.8 TB/s).
+//   Heads of 256, 8 sequences of 3000 to 8000 tokens, bf16: 4 rows 361 MB in
+//     68 us (5.3 TB/s), 64 rows 183 MB in 53.7 us (3.4 TB/s, 215 TFLOP/s).
 #pragma once
 
 #include "decode_common.hpp"
