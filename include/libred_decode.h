@@ -11,7 +11,8 @@
  * Arguments come in structs that the call reads before it returns. Strides
  * count elements of the tensor they belong to; the last dimension (`dim` or
  * the vocabulary) is always contiguous. Every pointer is aligned to its
- * element. Inputs must not overlap outputs unless a call says otherwise.
+ * element. Inputs must not overlap outputs, from their first element to their
+ * last, unless a call says otherwise.
  *
  * Scratch: the backward pass of the norms, attention (max_len above 32) and the
  * verification keep partials in the stream's scratch buffer (the one of the
