@@ -126,8 +126,9 @@ red_status red_cache_write(const red_paged_cache *cache, int type, const red_hea
                            const int64_t *slots, size_t tokens, hipStream_t stream);
 
 /*
- * Read tokens back in 16 bits (8-bit caches: element * scale, rounded once).
- * A slot outside the cache reads as zeros. k and v are written.
+ * Read tokens back in 16 bits (8-bit caches: element * scale in float32, then
+ * rounded to 16 bits). A slot outside the cache reads as zeros. k and v are
+ * written.
  */
 red_status red_cache_read(const red_paged_cache *cache, int type, const red_heads *k, const red_heads *v,
                           const int64_t *slots, size_t tokens, hipStream_t stream);

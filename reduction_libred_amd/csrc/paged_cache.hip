@@ -160,6 +160,15 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_write_kernel(CacheRo
     }
 }
 
+// A product rounded to float32. A float16 conversion right behind it would be
+// made one rounding with it, but not for vectors of 8, and a cache would read
+// differently by how its rows are aligned: the empty asm keeps them apart.
+__device__ __forceinline__ float product(float a, float b) {
+    float p = a * b;
+    asm("" : "+v"(p));
+    return p;
+}
+
 template <class T, class C, int VEC, int G, int NV>
 __global__ __launch_bounds__(kCacheWaves* kWave) void cache_read_kernel(CacheRows a) {
     using V = typename Vec<T, VEC>::type;
@@ -224,7 +233,7 @@ __global__ __launch_bounds__(kCacheWaves* kWave) void cache_read_kernel(CacheRow
                 } else {
                     float f[4];
                     C::unpack4(b[u][v], f);
-                    dst[lane + v * G] = T::narrow(f[0] * s[u]);
+                    dst[lane + v * G] = T::narrow(product(f[0], s[u]));
                 }
             }
         }

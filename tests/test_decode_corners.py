@@ -397,3 +397,21 @@ def test_attention_refuses_a_negative_length():
         rl.red_tree_attention(q, pages, pages, table, lens, 1.0, max_len=-1)
     out, lse = rl.red_tree_attention(q, pages, pages, table, lens, 1.0, max_len=0)
     assert not out.any() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("kind", [I8, E4M3], ids=str)
+@pytest.mark.parametrize("dt", [F16, BF16], ids=str)
+@pytest.mark.parametrize("dim", [61, 64, 100])
+def test_cache_reads_the_same_whatever_the_alignment(dim, dt, kind):
+    """A product in float32 and its rounding, for subnormal results too, where
+    one rounding of the two would differ."""
+    x = (torch.randn(8000, 2, dim, generator=gen(20)) * torch.exp(2 * torch.randn(8000, 2, 1, generator=gen(21)) - 4)).to(dt).to(DEV)
+    raw = [torch.zeros(500 * 2 * 16 * dim + 1, dtype=I8, device=DEV).view(kind) for _ in range(2)]
+    sc = [torch.zeros(500, 2, 16, device=DEV) for _ in range(2)]
+    slots = torch.arange(8000, device=DEV)
+    for first in (0, 1):        # rows on their boundaries, and one byte behind
+        pg = [y[first:first + 500 * 2 * 16 * dim].view(500, 2, 16, dim) for y in raw]
+        rl.red_cache_write(x, -x, slots, *pg, *sc)
+        for got, p, s in zip(rl.red_cache_read(*pg, slots, dt, *sc), pg, sc):
+            want = (p.float() * s[..., None]).to(dt).transpose(1, 2).reshape(8000, 2, dim)
+            assert torch.equal(got, want)
