@@ -1,7 +1,8 @@
 """libred: block-level parallel reductions on AMD Instinct MI355X (gfx950).
 
 A thin ctypes binding over the C ABI of libred.so (include/libred.h,
-include/libred_decode.h, include/libred_ablate.h, include/libred_probe.h). Each function here has the
+include/libred_decode.h, include/libred_serve.h, include/libred_ablate.h,
+include/libred_probe.h). Each function here has the
 name of the C entry point it calls and only marshals arguments: it takes
 PyTorch tensors on a ROCm device (PyTorch supplies device memory and
 streams), passes their data pointers, sizes and a hipStream_t, and raises
@@ -582,4 +583,9 @@ from .decode import (  # noqa: E402,F401
     red_cache_read, red_cache_write, red_qk_norm_rope, red_qk_norm_rope_backward, red_tree_attention,
     red_verify_drafts)
 
+from . import serve  # noqa: E402
+from .serve import (  # noqa: E402,F401
+    red_page_bounds, red_plan_slots, red_sample, red_select_pages, red_sparse_attention)
+
 SIGNATURES.update(decode.SIGNATURES)
+SIGNATURES.update(serve.SIGNATURES)

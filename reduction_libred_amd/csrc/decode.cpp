@@ -4,44 +4,12 @@
 
 #include <initializer_list>
 
-#include "host.hpp"
+#include "decode_host.hpp"
+#include "libred_serve.h"
 
-using libred::Heads;
-using libred::host_compute_units;
-using libred::host_fail;
-using libred::host_scratch;
-using libred::is_aligned;
+using namespace libred;
 
 namespace {
-
-size_t type_bytes(int type) { return type == RED_F32 ? 4 : type == RED_F16 || type == RED_BF16 ? 2 : 1; }
-
-// Largest element offset a strided tensor may reach (the byte offset of an
-// 8-byte element still fits 63 bits).
-constexpr int64_t kMaxSpan = (int64_t)1 << 59;
-
-// Elements spanned by tokens x heads x dim at these strides; -1 if a stride
-// is negative or the span is out of range.
-int64_t span_of(const red_heads& h, size_t tokens, size_t dim) {
-    if (h.heads < 0 || h.token_stride < 0 || h.head_stride < 0) return -1;
-    if (h.heads == 0 || tokens == 0) return 0;
-    int64_t a, b, s;
-    if (__builtin_mul_overflow((int64_t)(tokens - 1), h.token_stride, &a) ||
-        __builtin_mul_overflow(h.heads - 1, h.head_stride, &b) || __builtin_add_overflow(a, b, &s) ||
-        __builtin_add_overflow(s, (int64_t)dim, &s) || s > kMaxSpan)
-        return -1;
-    return s;
-}
-
-// Rows of an output must lie apart from each other.
-bool rows_apart(const red_heads& h, size_t tokens, size_t dim) {
-    const int64_t d = (int64_t)dim, t = (int64_t)tokens;
-    if (h.heads == 0 || t == 0) return true;
-    if (h.heads > 1 && h.head_stride < d) return false;
-    if (t > 1 && h.token_stride < d) return false;
-    if (h.heads == 1 || t == 1) return true;
-    return h.token_stride >= (h.heads - 1) * h.head_stride + d || h.head_stride >= (t - 1) * h.token_stride + d;
-}
 
 bool heads_valid(const red_heads& h, size_t tokens, size_t dim, size_t esize) {
     const int64_t s = span_of(h, tokens, dim);
@@ -74,9 +42,6 @@ bool rows_on(const red_heads& h, size_t tokens, size_t esize, size_t bytes) {
            (h.heads == 1 || h.head_stride * (int64_t)esize % (int64_t)bytes == 0);
 }
 
-// A launch has fewer than 2^32 threads: most blocks of 256 that one may have.
-// Calls of more go in several launches, one after the other.
-constexpr size_t kMaxBlocks = ((size_t)1 << 24) - 1;
 static_assert(libred::kQkNormWaves == 4 && libred::kCacheWaves == 4, "blocks of 256 threads");
 
 // Heads from token t on.
@@ -183,60 +148,6 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
 }
 
-// Elements (or scales) spanned by a paged tensor of these strides, -1 if
-// negative or out of range.
-int64_t paged_span(const red_paged_cache& c, int64_t page, int64_t head, int64_t place, size_t dim) {
-    if (page < 0 || head < 0 || place < 0) return -1;
-    int64_t a, b, d, s;
-    if (__builtin_mul_overflow((int64_t)c.pages - 1, page, &a) || __builtin_mul_overflow((int64_t)c.heads - 1, head, &b) ||
-        __builtin_mul_overflow((int64_t)c.places - 1, place, &d) || __builtin_add_overflow(a, b, &s) ||
-        __builtin_add_overflow(s, d, &s) || __builtin_add_overflow(s, (int64_t)dim, &s) || s > kMaxSpan)
-        return -1;
-    return s;
-}
-
-// A cache with at least one page, or one that holds nothing (pages 0).
-bool cache_valid(const red_paged_cache* c) {
-    if (c == nullptr) return false;
-    if (c->type != RED_F16 && c->type != RED_BF16 && c->type != RED_I8 && c->type != RED_E4M3) return false;
-    if (c->heads < 1 || c->heads > 1 << 20 || c->places < 1 || c->places > 1 << 20 || c->dim < 1 ||
-        c->dim > RED_HEAD_MAX_DIM || c->pages > (size_t)1 << 40)
-        return false;
-    if (c->pages == 0) return true;
-    const bool scaled = c->type == RED_I8 || c->type == RED_E4M3;
-    const size_t es = type_bytes(c->type);
-    if (c->k == nullptr || c->v == nullptr || !is_aligned(c->k, es) || !is_aligned(c->v, es)) return false;
-    if (paged_span(*c, c->page_stride, c->head_stride, c->place_stride, c->dim) < 0) return false;
-    if (!scaled) return c->k_scales == nullptr && c->v_scales == nullptr;
-    if (c->k_scales == nullptr || c->v_scales == nullptr || !is_aligned(c->k_scales, 4) || !is_aligned(c->v_scales, 4))
-        return false;
-    return paged_span(*c, c->scale_page_stride, c->scale_head_stride, c->scale_place_stride, 1) >= 0;
-}
-
-libred::PagedCache to_cache(const red_paged_cache& c) {
-    return libred::PagedCache{c.k,
-                              c.v,
-                              c.k_scales,
-                              c.v_scales,
-                              c.page_stride,
-                              c.head_stride,
-                              c.place_stride,
-                              c.scale_page_stride,
-                              c.scale_head_stride,
-                              c.scale_place_stride,
-                              (int64_t)c.pages,
-                              (int)c.heads,
-                              (int)c.places,
-                              (int)c.dim};
-}
-
-// Whether the cache's rows start on `bytes` boundaries.
-bool cache_rows_on(const red_paged_cache& c, size_t bytes) {
-    const int64_t es = (int64_t)type_bytes(c.type), b = (int64_t)bytes;
-    return is_aligned(c.k, bytes) && is_aligned(c.v, bytes) && (c.pages <= 1 || c.page_stride * es % b == 0) &&
-           (c.heads == 1 || c.head_stride * es % b == 0) && (c.places == 1 || c.place_stride * es % b == 0);
-}
-
 red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, const red_heads* v, const int64_t* slots,
                       size_t tokens, bool write, hipStream_t stream) {
     if (!cache_valid(c) || k == nullptr || v == nullptr) return RED_ERR_INVALID_ARG;
@@ -298,7 +209,8 @@ red_status cache_call(const red_paged_cache* c, int type, const red_heads* k, co
     return RED_OK;
 }
 
-red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) {
+// table_head: from one kv head's table to the next.
+red_status attention_call(const red_tree_attention_args* a, int64_t table_head, hipStream_t stream) {
     if (a == nullptr || !cache_valid(&a->cache)) return RED_ERR_INVALID_ARG;
     const red_paged_cache& c = a->cache;
     const int type = a->type;
@@ -308,6 +220,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     if (D % 16 != 0 || !cache_rows_on(c, 16)) return RED_ERR_INVALID_ARG;
     if (N > RED_TREE_MAX_NODES || H % c.heads != 0 || H > 65535 || B > 65535) return RED_ERR_INVALID_ARG;
     if (a->max_len > (size_t)1 << 30 || a->table_cols > (size_t)1 << 30 || a->table_stride < 0) return RED_ERR_INVALID_ARG;
+    if (table_head < 0 || table_head > (int64_t)1 << 40) return RED_ERR_INVALID_ARG;
     if (a->table_stride > (int64_t)1 << 40 || !(a->scale - a->scale == 0.f)) return RED_ERR_INVALID_ARG;
     if (B == 0 || N == 0 || H == 0) return RED_OK;
     if (a->q == nullptr || a->out == nullptr || a->lse == nullptr || a->lens == nullptr) return RED_ERR_INVALID_ARG;
@@ -345,7 +258,7 @@ red_status attention_call(const red_tree_attention_args* a, hipStream_t stream) 
     k.q_batch = qb, k.q_node = qn, k.q_head = qh;
     k.out_batch = bs, k.out_node = ns, k.out_head = hs;
     k.cache = to_cache(c);
-    k.table = a->table, k.table_stride = a->table_stride;
+    k.table = a->table, k.table_stride = a->table_stride, k.table_head = table_head;
     k.lens = a->lens, k.mask = a->tree_mask, k.count = a->node_count;
     k.batch = (int)B, k.nodes = (int)N, k.group = (int)G, k.max_tokens = c.pages == 0 ? 0 : (int)tokens;
     k.keep = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
@@ -492,7 +405,11 @@ red_status red_cache_read(const red_paged_cache* cache, int type, const red_head
 }
 
 red_status red_tree_attention(const red_tree_attention_args* a, hipStream_t stream) {
-    return attention_call(a, stream);
+    return attention_call(a, 0, stream);
+}
+
+red_status red_sparse_attention(const red_tree_attention_args* a, int64_t table_head_stride, hipStream_t stream) {
+    return attention_call(a, table_head_stride, stream);
 }
 
 red_status red_verify_drafts(const red_verify_drafts_args* a, hipStream_t stream) { return verify_call(a, stream); }

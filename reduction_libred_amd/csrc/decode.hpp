@@ -100,6 +100,7 @@ struct TreeAttention {
     float* part_o;
     float2* part_ml;
     int* plan;  // batch + 2: tiles of a segment before sequence b (block 0 writes it), tiles a block
+    int64_t table_head;  // from one kv head's table to the next; 0: one for all
 };
 
 // How waves share a block: `waves_m` groups of `wave_rows` rows times

@@ -1,0 +1,149 @@
+// The least and the largest elements of the keys of pages:
+//
+//     lo[d] = min over the page's tokens of k[d],  hi[d] = max.
+//
+// A wave has a (page, head): G lanes hold a row, 8 neighbouring elements each
+// (one 16-byte load, or 8 bytes of an 8-bit cache), so 64 / G rows are read at
+// once and joined by lane moves at the end. Minima and maxima are of float32
+// values, and rounding them to 16 bits is the same as rounding the elements,
+// since rounding keeps the order.
+#include "decode_common.hpp"
+#include "serve.hpp"
+
+namespace libred {
+
+namespace {
+
+struct Plain {  // 16-bit cache
+    using bits = uint16_t;
+    static constexpr bool kScaled = false;
+};
+struct CodeI8 {
+    using bits = uint8_t;
+    static constexpr bool kScaled = true;
+    static __device__ __forceinline__ void widen4(uint32_t w, float* f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(w >> (8 * j));
+    }
+};
+struct CodeE4M3 {
+    using bits = uint8_t;
+    static constexpr bool kScaled = true;
+    static __device__ __forceinline__ void widen4(uint32_t w, float* f) {
+        f[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0);
+        f[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1);
+        f[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2);
+        f[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3);
+    }
+};
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// VEC 8: G lanes a row; VEC 1 (any alignment): 64 lanes, up to 4 elements each,
+// 64 apart.
+template <class T, class C, int VEC, int G>
+__global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBounds a) {
+    constexpr int N = VEC == 8 ? 8 : 4, R = kWave / G;
+    const PagedCache& c = a.cache;
+    const int b = blockIdx.y, lane = threadIdx.x % kWave, in = lane % G, row = lane / G;
+    const int64_t item = (int64_t)blockIdx.x * kBoundsWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t nth = item / c.heads;
+    const int h = (int)(item - nth * c.heads);
+    const int len = max(a.lens[b], 0), from = a.first ? max(a.first[b], 0) : 0;
+    const int64_t j = from / c.places + nth;  // page of the sequence
+    if (nth >= a.most || j >= a.cols || from >= len || j * c.places >= len) return;
+    const int page = a.table[b * a.table_stride + j];
+    if (page < 0 || page >= c.pages) return;
+    const int tokens = (int)min((int64_t)c.places, len - j * c.places);
+    const typename C::bits* k = static_cast<const typename C::bits*>(c.k) + page * c.page_stride + h * c.head_stride;
+    const float* scales = C::kScaled ? c.k_scales + page * c.scale_page_stride + h * c.scale_head_stride : nullptr;
+    float lo[N], hi[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) lo[i] = __builtin_inff(), hi[i] = -__builtin_inff();
+    const bool there = VEC == 1 || in * 8 < c.dim;
+    for (int t = row; t < tokens; t += R) {
+        const typename C::bits* r = k + t * c.place_stride;
+        float f[N];
+        if constexpr (VEC == 8) {
+            const int at = there ? in : 0;
+            if constexpr (C::kScaled) {
+                const u32x2 w = reinterpret_cast<const u32x2*>(r)[at];
+                C::widen4(w[0], f);
+                C::widen4(w[1], f + 4);
+            } else {
+                widen_vec<T, 8>(reinterpret_cast<const typename Vec<T, 8>::type*>(r)[at], f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int d = in + i * kWave < c.dim ? in + i * kWave : 0;
+                if constexpr (C::kScaled) {
+                    float w[4];
+                    C::widen4(r[d], w);
+                    f[i] = w[0];
+                } else {
+                    f[i] = T::widen(r[d]);
+                }
+            }
+        }
+        const float s = C::kScaled ? scales[t * c.scale_place_stride] : 1.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v = f[i];
+            if constexpr (C::kScaled) v *= s;
+            // fmin and fmax pass over a NaN.
+            lo[i] = fminf(lo[i], v);
+            hi[i] = fmaxf(hi[i], v);
+        }
+    }
+#pragma unroll
+    for (int o = G; o < kWave; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            lo[i] = fminf(lo[i], __shfl_xor(lo[i], o));
+            hi[i] = fmaxf(hi[i], __shfl_xor(hi[i], o));
+        }
+    const int64_t at = page * a.bound_page + h * a.bound_head;
+    typename T::bits *to_lo = static_cast<typename T::bits*>(a.lo) + at, *to_hi = static_cast<typename T::bits*>(a.hi) + at;
+    if constexpr (VEC == 8) {
+        if (row == 0 && there) {
+            reinterpret_cast<typename Vec<T, 8>::type*>(to_lo)[in] = narrow_vec<T, 8>(lo);
+            reinterpret_cast<typename Vec<T, 8>::type*>(to_hi)[in] = narrow_vec<T, 8>(hi);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (in + i * kWave < c.dim) {
+                to_lo[in + i * kWave] = T::narrow(lo[i]);
+                to_hi[in + i * kWave] = T::narrow(hi[i]);
+            }
+    }
+}
+
+template <class T, class C>
+hipError_t launch_types(int vec, int lanes, const PageBounds& a, dim3 grid, hipStream_t stream) {
+    constexpr int threads = kBoundsWaves * kWave;
+    if (vec == 1) page_bounds_kernel<T, C, 1, 64><<<grid, threads, 0, stream>>>(a);
+    else if (lanes == 8) page_bounds_kernel<T, C, 8, 8><<<grid, threads, 0, stream>>>(a);
+    else if (lanes == 16) page_bounds_kernel<T, C, 8, 16><<<grid, threads, 0, stream>>>(a);
+    else page_bounds_kernel<T, C, 8, 32><<<grid, threads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_cache(int cache_type, int vec, int lanes, const PageBounds& a, dim3 grid, hipStream_t stream) {
+    if (cache_type == RED_I8) return launch_types<T, CodeI8>(vec, lanes, a, grid, stream);
+    if (cache_type == RED_E4M3) return launch_types<T, CodeE4M3>(vec, lanes, a, grid, stream);
+    return launch_types<T, Plain>(vec, lanes, a, grid, stream);
+}
+
+}  // namespace
+
+hipError_t launch_page_bounds(int type, int cache_type, int vec, int lanes, const PageBounds& a, unsigned int blocks,
+                              unsigned int batch, hipStream_t stream) {
+    const dim3 grid(blocks, batch);
+    return type == RED_F16 ? launch_cache<F16>(cache_type, vec, lanes, a, grid, stream)
+                           : launch_cache<BF16>(cache_type, vec, lanes, a, grid, stream);
+}
+
+}  // namespace libred

@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
     // those from `last` on do. (Two tiles on their way, with twice the
     // registers: 37.9 us / 40.8 in the case above, where nothing spilled.)
     const int origin = first + wt * TS;
-    const int32_t* pages = A->table + b * A->table_stride;
+    const int32_t* pages = A->table + b * A->table_stride + h * A->table_head;
     // AT_ONCE tiles at once, a lane a token, by one wave.
     constexpr int AT_ONCE = HELD == 2 ? 1 : kWave / TS;
     const int ahead = AT_ONCE == 1 ? 0 : lane / TS, mine_t = lane % TS;  // this lane's tile of them, and token
@@ -664,7 +664,7 @@ __global__ __launch_bounds__(kWave* WM* WT, DP <= 128 || (RW == 16 && WM > 1) ? 
         const uint64_t word = E->mask ? (uint64_t)E->mask[(int64_t)b * E->nodes + node] : ~0ull >> (63 - node);
 #pragma unroll 1
         for (int t = max(first, len); t < last; ++t) {
-            const int page = E->table[b * E->table_stride + t / E->cache.places];
+            const int page = E->table[b * E->table_stride + h * E->table_head + t / E->cache.places];
             if (!(word >> (t - len) & 1) || page < 0 || page >= E->cache.pages) continue;
             if constexpr (kScaled) {
                 const int64_t of = (int64_t)page * E->cache.scale_page_stride + (int64_t)(t % E->cache.places) * E->cache.scale_place_stride + h * E->cache.scale_head_stride;

@@ -411,7 +411,12 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     if stream is not None:
         return _on(stream, red_tree_attention, q, k_pages, v_pages, table, lens, scale, max_len, tree_mask, node_count,
                    k_scales, v_scales, out)
-    name = "red_tree_attention"
+    return _attend("red_tree_attention", q, k_pages, v_pages, table, lens, scale, max_len, tree_mask, node_count, k_scales,
+                   v_scales, out)
+
+
+def _attend(name, q, k_pages, v_pages, table, lens, scale, max_len, tree_mask, node_count, k_scales, v_scales, out):
+    """red_tree_attention, or red_sparse_attention with a table for each kv head."""
     device, c = _cache(name, k_pages, v_pages, k_scales, v_scales)
     if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.dtype not in _HALVES:
         _any(name, "q", q, _HALVES, 4, "(batch, nodes, q heads, dim)")
@@ -420,15 +425,16 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     _, _, places, width = k_pages.shape
     if dim != width:
         raise ValueError(f"{name}: q must be (batch, nodes, q heads, {width})")
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
-    cols = table.shape[1]
+    per_head = name == "red_sparse_attention"
+    if not isinstance(table, torch.Tensor) or table.dim() != (3 if per_head else 2):
+        raise ValueError(f"{name}: table must be ({batch}, {'kv heads, ' if per_head else ''}pages of a sequence)")
+    cols = table.shape[-1]
     if max_len is not None and max_len < 0:
         raise ValueError(f"{name}: max_len must not be negative")
     q0, q1, q2, q3 = q.stride()
     if q.get_device() != device or (q3 != 1 and dim > 1):
         _rows(name, "q", q, dtype, device, shape)
-    _rows(name, "table", table, _INT32, device, (batch, cols))
+    _rows(name, "table", table, _INT32, device, (batch, k_pages.shape[1], cols) if per_head else (batch, cols))
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
     else:
@@ -437,10 +443,14 @@ def red_tree_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tr
     lse = torch.empty((batch, nodes, heads), dtype=_FLOAT32, device=q.device)
     mask = 0 if tree_mask is None else _whole(name, "tree_mask", tree_mask, _INT64, device, (batch, nodes))
     count = 0 if node_count is None else _whole(name, "node_count", node_count, _INT32, device, (batch,))
-    _call(name, device, stream, _pack_attention(
+    args = _pack_attention(
         TYPES[dtype], scale, batch, nodes, heads, cols * places if max_len is None else max_len, q.data_ptr(), out.data_ptr(),
         lse.data_ptr(), q0, q1, q2, o0, o1, o2, *c, table.data_ptr(), cols, table.stride(0),
-        _whole(name, "lens", lens, _INT32, device, (batch,)), mask, count))
+        _whole(name, "lens", lens, _INT32, device, (batch,)), mask, count)
+    if per_head:
+        _call(name, device, None, args, table.stride(1))
+    else:
+        _call(name, device, None, args)
     return out, lse
 
 
