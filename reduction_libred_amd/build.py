@@ -34,7 +34,7 @@ SOURCES = ["libred.cpp", "flat_sum_f32.hip", "flat_ops.hip", "flat_fused.hip", "
            "decode.cpp", "qk_norm_f32.hip", "qk_norm_f16.hip", "qk_norm_bf16.hip", "paged_cache.hip",
            "attention_f16_16.hip", "attention_f16_i8.hip", "attention_f16_e4m3.hip", "attention_bf16_16.hip",
            "attention_bf16_i8.hip", "attention_bf16_e4m3.hip", "attention_combine.hip", "verify_drafts.hip",
-           "serve.cpp", "plan_slots.hip", "page_bounds.hip", "select_pages.hip", "sample.hip"]
+           "serve.cpp", "plan_slots.hip", "page_bounds.hip", "select_pages.hip", "sample.hip", "sample_split.hip"]
 ARCH = "gfx950"
 
 

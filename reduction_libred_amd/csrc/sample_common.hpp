@@ -1,0 +1,428 @@
+// sample_common.hpp -- sampling from a row of logits with temperature, top-k,
+// top-p and min-p: what the kernels share, and the way that takes a row by one
+// block alone.
+//
+// The tokens' order (falling logits, ties by number) is that of one whole
+// number a token, its code: the logit's bits, turned so that they order, above
+// the number's complement. What top-k, top-p and min-p keep are the codes from
+// a border on. For top-k and top-p it is the first code at which a running sum
+// along the order, of ones or of weights, reaches a target, and it is found by
+// sums over bins, not by sorting: first bins of equal ratios of the weight,
+// down from the largest; then, for what is in the border's bin, bins of the
+// codes' digits, 8 bits at a time.
+//
+// Weights exp((x - max) / T) are float64. Their sums are held in whole numbers
+// of 2^-shift (45 bits for 131072 tokens), so they come out the same in any
+// order, and atomics do no harm.
+#pragma once
+
+#include "decode_common.hpp"
+#include "serve.hpp"
+
+namespace libred {
+
+constexpr int kThreads = 1024, kWaves = kThreads / kWave;
+constexpr int kBins = 256;
+constexpr int kHeld = 2048;        // codes that are gathered in the LDS
+constexpr int kCodeBits = 52;      // 32 of the logit, 20 of the number
+constexpr int kMaxVocab = 1 << 20;
+
+struct AddU64 {
+    __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a + b; }
+};
+struct MaxU64 {
+    __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+};
+
+__device__ __forceinline__ uint64_t code_of(float x, int i) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const uint32_t k = u >> 31 ? ~u : u | 0x80000000u;
+    return (uint64_t)k << 20 | (uint32_t)(kMaxVocab - 1 - i);
+}
+__device__ __forceinline__ float logit_of_key(uint32_t k) { return __builtin_bit_cast(float, k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+__device__ __forceinline__ float logit_of(uint64_t code) {
+    return logit_of_key((uint32_t)(code >> 20));
+}
+__device__ __forceinline__ int token_of(uint64_t code) { return kMaxVocab - 1 - (int)(code & (kMaxVocab - 1)); }
+
+constexpr float kNone = -__builtin_inff();
+constexpr uint32_t kLeastKey = 0x00800000u;  // of the least finite logit
+
+// The first of the keys from kLeastKey to `top` for which `is` holds; it holds
+// for `top` and for all above one for which it does. By one wave.
+template <class F>
+__device__ __forceinline__ uint32_t first_key(uint32_t top, F is) {
+    const uint32_t lane = threadIdx.x % kWave;
+    uint32_t low = kLeastKey, high = top;
+    while (low < high) {
+        const uint32_t step = (high - low) / kWave + 1, probe = min(low + lane * step, high);
+        const uint64_t yes = __ballot(is(logit_of_key(probe)));
+        if (!yes) {
+            low = min(low + (kWave - 1) * step, high - 1) + 1;
+        } else {
+            const uint32_t at = (uint32_t)__ffsll((unsigned long long)yes) - 1;
+            const uint32_t found = min(low + at * step, high);
+            if (at > 0) low = low + (at - 1) * step + 1;
+            high = found;
+        }
+    }
+    return high;
+}
+
+// What the block shares.
+struct Shared {
+    unsigned long long mass[kBins];
+    unsigned int count[kBins];
+    unsigned long long code[kHeld];  // what is in the border's bin
+    unsigned long long own[kHeld];   // the weights of those
+    unsigned long long part[kWaves], found, rest;
+    unsigned int held, bin, cut;
+};
+
+template <class Op>
+__device__ __forceinline__ uint64_t block_combine(uint64_t v, Shared& s, Op op) {
+    v = group_combine<kWave>(v, op);
+    __syncthreads();
+    if (threadIdx.x % kWave == 0) s.part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = s.part[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v = op(v, s.part[w]);
+    return v;
+}
+
+// Running sum over the wave's lanes, this one's value included.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+    const uint64_t none = 0;
+    v += dpp_move<0x111, 0xF>(none, v);  // shifted by 1, 2, 4 and 8 in rows of 16
+    v += dpp_move<0x112, 0xF>(none, v);
+    v += dpp_move<0x114, 0xF>(none, v);
+    v += dpp_move<0x118, 0xF>(none, v);
+    v += dpp_move<0x142, 0xA>(none, v);  // rows 0 and 2 into 1 and 3
+    v += dpp_move<0x143, 0xC>(none, v);  // the first half into the second
+    return v;
+}
+// The sum of the threads before this one.
+__device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& s) {
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const uint64_t upto = wave_scan(v);
+    __syncthreads();
+    if (lane == kWave - 1) s.part[wave] = upto;
+    __syncthreads();
+    uint64_t before = upto - v;
+    for (int w = 0; w < wave; ++w) before += s.part[w];
+    return before;
+}
+
+template <class T>
+struct Row {
+    using B = typename T::bits;
+    static constexpr int kVec = 16 / sizeof(B), kTile = kThreads * kVec;
+    static constexpr int kRun = kWave * kVec;  // tokens that a wave reads at a time
+    // Rows start on element boundaries only (a vocabulary may be odd).
+    typedef B Vector __attribute__((ext_vector_type(16 / sizeof(B)), aligned(sizeof(B))));
+
+    const B* p;
+    int vocab;
+    bool infinite = false;  // the largest logit is +inf: those count as 0, all others as -inf
+    float top_logit = 0.f;
+    double top = 0.0, scale = 0.0, unit = 0.0;
+
+    __device__ __forceinline__ Row(const Sample& a, int b, int step)
+        : p(static_cast<const B*>(a.x) + b * a.batch_stride + step * a.step_stride), vocab(a.vocab) {}
+    // By the first code of the order; -> it, as the row then counts.
+    __device__ __forceinline__ uint64_t settle(uint64_t first, double row_scale, int shift) {
+        top_logit = logit_of(first);
+        infinite = top_logit == __builtin_inff();
+        if (infinite) top_logit = 0.f, first = code_of(0.f, token_of(first));
+        top = top_logit, scale = row_scale, unit = __builtin_ldexp(1.0, shift);
+        return first;
+    }
+
+    __device__ __forceinline__ float seen(B bits) const {
+        const float x = T::widen(bits) + 0.f;  // -0 is 0
+        if (infinite) return x == __builtin_inff() ? 0.f : kNone;
+        return x == x ? x : kNone;
+    }
+    // f(number of the first, logits) of this thread's kVec neighbours in every
+    // tile of the block; kNone behind the last.
+    template <class F>
+    __device__ __forceinline__ void tiles(F f) const {
+        for (int i0 = 0; i0 < vocab; i0 += kTile) {
+            const int i = i0 + threadIdx.x * kVec;
+            float x[kVec];
+            if (i0 + kTile <= vocab) {
+                const Vector v = *reinterpret_cast<const Vector*>(p + i);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) x[j] = seen(v[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) x[j] = i + j < vocab ? seen(p[i + j]) : kNone;
+            }
+            f(i, x);
+        }
+    }
+    // f(number, logit) of every token of this thread.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        tiles([&](int i, const float(&x)[kVec]) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (i + j < vocab) f(i + j, x[j]);
+        });
+    }
+    __device__ __forceinline__ double weight(float x) const {
+        return x == kNone ? 0.0 : exp2(((double)x - top) * scale);
+    }
+    // In units: 2^52 more than a number below it has that number as its last bits.
+    __device__ __forceinline__ uint64_t units(double w) const {
+        return __builtin_bit_cast(uint64_t, w * unit + 0x1p52) & 0xFFFFFFFFFFFFFull;
+    }
+    __device__ __forceinline__ uint64_t kept_units(int i, float x, uint64_t border) const {
+        return x == kNone || code_of(x, i) < border ? 0 : units(weight(x));
+    }
+    // Bins of an eighth of a power of two, from the largest weight down. The
+    // order of the logits holds after each rounding.
+    __device__ __forceinline__ int bin(float x) const {
+        const double d = (top - (double)x) * scale * 8.0;
+        return d < (double)(kBins - 1) ? (int)d : kBins - 1;
+    }
+};
+
+// The bin in which the running sum of `own` (bin tid) reaches `target`, what is
+// missing of the target there, or bin kBins. By the block's first waves.
+__device__ __forceinline__ void find_bin(Shared& s, uint64_t target, bool codes) {
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        const int lane = threadIdx.x;
+        uint64_t own[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // Bins of weights go down from bin 0, digits of codes from the last.
+            own[i] = s.mass[codes ? kBins - 1 - 4 * lane - i : 4 * lane + i];
+            sum += own[i];
+        }
+        const uint64_t upto = wave_scan(sum);
+        if (lane == 0) s.bin = kBins;
+        uint64_t before = upto - sum;
+        wave_lds_fence();
+        if (before < target && upto >= target) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (before < target && before + own[i] >= target) {
+                    s.bin = codes ? kBins - 1 - 4 * lane - i : 4 * lane + i;
+                    s.rest = target - before;
+                }
+                before += own[i];
+            }
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void clear_bins(Shared& s) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) s.mass[i] = 0, s.count[i] = 0;
+    __syncthreads();
+}
+
+// What a running sum of weights must reach for top-p.
+__device__ __forceinline__ uint64_t top_p_target(double p, uint64_t all) {
+    const uint64_t want = (uint64_t)__builtin_ceil(p * (double)all);
+    return want > 0 ? want : 1;
+}
+
+// The first code of the order, among those from `from` on, at which the running
+// sum of value(number, logit) reaches target(whole sum); 0 if it does not.
+// Codes of value 0 are passed over.
+template <class T, class V, class G>
+__device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, uint64_t from, V value, G target) {
+    clear_bins(s);
+    uint64_t last = 0;  // of the last bin, which may hold most tokens: not by atomics
+    unsigned int lasts = 0;
+    row.each([&](int i, float x) {
+        if (x == kNone || code_of(x, i) < from) return;
+        const uint64_t v = value(x);
+        if (v == 0) return;
+        const int j = row.bin(x);
+        if (j == kBins - 1) {
+            last += v, ++lasts;
+        } else {
+            atomicAdd(&s.mass[j], (unsigned long long)v);
+            atomicAdd(&s.count[j], 1u);
+        }
+    });
+    last = group_combine<kWave>(last, AddU64());
+    lasts = group_combine<kWave>(lasts, [](unsigned a, unsigned b) { return a + b; });
+    if (threadIdx.x % kWave == 0 && lasts) {
+        atomicAdd(&s.mass[kBins - 1], (unsigned long long)last);
+        atomicAdd(&s.count[kBins - 1], lasts);
+    }
+    __syncthreads();
+    const uint64_t all = block_combine(threadIdx.x < kBins ? s.mass[threadIdx.x] : 0, s, AddU64());
+    uint64_t want = target(all);
+    if (want > all || want == 0) return 0;
+    find_bin(s, want, false);
+    const int bin = s.bin;
+    want = s.rest;
+    unsigned int in = s.count[bin];
+    // Too many to gather: digits of the codes in that bin, over the whole row.
+    int shift = kCodeBits;
+    uint64_t prefix = 0;
+    auto inside = [&](uint64_t code, float x) { return x != kNone && code >= from && row.bin(x) == bin && code >> shift == prefix; };
+    while (in > kHeld && shift > 0) {
+        const int width = min(shift, 8), down = shift - width;
+        clear_bins(s);
+        row.each([&](int i, float x) {
+            const uint64_t code = code_of(x, i);
+            if (!inside(code, x)) return;
+            const uint64_t v = value(x);
+            if (v == 0) return;
+            const int d = (int)(code >> down) & (255 >> (8 - width));
+            atomicAdd(&s.mass[d], (unsigned long long)v);
+            atomicAdd(&s.count[d], 1u);
+        });
+        find_bin(s, want, true);
+        prefix = prefix << width | s.bin;
+        want = s.rest;
+        in = s.count[s.bin];
+        shift = down;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.held = 0, s.found = 0;
+    __syncthreads();
+    row.each([&](int i, float x) {
+        const uint64_t code = code_of(x, i);
+        if (!inside(code, x)) return;
+        const uint64_t v = value(x);
+        if (v == 0) return;
+        const unsigned int at = atomicAdd(&s.held, 1u);
+        if (at < kHeld) s.code[at] = code, s.own[at] = v;
+    });
+    __syncthreads();
+    const int held = (int)min(s.held, (unsigned)kHeld);
+    // From the first digit in which they differ on.
+    const uint64_t one = s.code[0];
+    for (int i = threadIdx.x; i < held; i += kThreads)
+        if (const uint64_t x = s.code[i] ^ one) atomicOr(&s.found, (unsigned long long)x);
+    __syncthreads();
+    int down = bytes_of(s.found) * 8;
+    prefix = one >> down;
+    while (down > 0) {
+        const int width = min(down, 8), to = down - width;
+        clear_bins(s);
+        for (int i = threadIdx.x; i < held; i += kThreads)
+            if (s.code[i] >> down == prefix) atomicAdd(&s.mass[(s.code[i] >> to) & (255 >> (8 - width))], s.own[i]);
+        find_bin(s, want, true);
+        prefix = prefix << width | s.bin;
+        want = s.rest;
+        down = to;
+    }
+    return prefix;
+}
+
+struct Settings {
+    double p, m, scale;  // p 2: no top-p
+    int64_t k;
+    __device__ Settings(const Sample& a, int b) {
+        const float t = a.temperature ? a.temperature[b] : 1.f;
+        const bool greedy = !(t > 0.f);
+        k = a.top_k ? a.top_k[b] : 0;
+        if (k < 1 || k > a.vocab) k = a.vocab;
+        if (greedy) k = 1;
+        const float tp = a.top_p ? a.top_p[b] : 1.f, mp = a.min_p ? a.min_p[b] : 0.f;
+        p = tp < 1.f && k > 1 ? fmax((double)tp, 0.0) : 2.0;
+        m = mp > 0.f ? fmin((double)mp, 1.0) : 0.0;
+        scale = 1.4426950408889634 / (greedy ? 1.0 : (double)t);
+    }
+};
+
+
+// The border of what a row keeps, `first` being the first code of the order.
+template <class T>
+__device__ __forceinline__ uint64_t row_border(const Row<T>& row, Shared& s, const Settings& set, uint64_t first) {
+    if (set.k == 1) return first;
+    uint64_t border = 0;
+    if (set.k < row.vocab) border = find_border(row, s, 0, [](float) -> uint64_t { return 1; }, [&](uint64_t) { return (uint64_t)set.k; });
+    if (set.p < 2.0) {
+        const uint64_t found = find_border(row, s, border, [&](float x) { return row.units(row.weight(x)); },
+                                           [&](uint64_t all) { return top_p_target(set.p, all); });
+        border = found > border ? found : border;
+    }
+    if (set.m > 0.0) {
+        __syncthreads();
+        if (threadIdx.x < kWave) {
+            const uint32_t cut = first_key((uint32_t)(first >> 20), [&](float x) { return row.weight(x) >= set.m; });
+            if (threadIdx.x == 0) s.cut = cut;
+        }
+        __syncthreads();
+        const uint64_t cut = (uint64_t)s.cut << 20;
+        border = cut > border ? cut : border;
+    }
+    return border;
+}
+
+// The sum of the kept weights, and that of the tokens a wave reads at a time in
+// `runs`.
+template <class T>
+__device__ __forceinline__ uint64_t row_total(const Row<T>& row, Shared& s, unsigned long long* runs, uint64_t border) {
+    using R = Row<T>;
+    const int lane = threadIdx.x % kWave;
+    uint64_t total = 0;
+    __syncthreads();
+    row.tiles([&](int i, const float(&x)[R::kVec]) {
+        uint64_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < R::kVec; ++j) sum += row.kept_units(i + j, x[j], border);
+        sum = group_combine<kWave>(sum, AddU64());
+        if (lane == 0 && i < row.vocab) runs[i / R::kRun] = sum;
+        total += sum;
+    });
+    return block_combine(lane == 0 ? total : 0, s, AddU64());
+}
+
+// What the running sum of the kept weights must reach for the token.
+__device__ __forceinline__ uint64_t draw_target(float r, uint64_t total) {
+    return r < 1.f ? (uint64_t)(fmax((double)r, 0.0) * (double)total) + 1 : total;
+}
+
+// The token at which it does, by the sums of the runs.
+template <class T>
+__device__ __forceinline__ void row_draw(const Row<T>& row, Shared& s, const unsigned long long* runs, uint64_t border, uint64_t want,
+                                         int64_t* token) {
+    using R = Row<T>;
+    constexpr int kOwn = kMaxVocab / R::kRun / kThreads;
+    const int tid = threadIdx.x, count = (row.vocab + R::kRun - 1) / R::kRun;
+    uint64_t own[kOwn], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        own[j] = tid * kOwn + j < count ? runs[tid * kOwn + j] : 0;
+        sum += own[j];
+    }
+    uint64_t before = block_before(sum, s);
+    if (before < want && before + sum >= want)
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            if (before < want && before + own[j] >= want) s.bin = tid * kOwn + j, s.rest = want - before;
+            before += own[j];
+        }
+    __syncthreads();
+    if (tid < kWave) {
+        const int i = (int)s.bin * R::kRun + tid * R::kVec;
+        uint64_t w[R::kVec], mine = 0;
+#pragma unroll
+        for (int j = 0; j < R::kVec; ++j) {
+            w[j] = i + j < row.vocab ? row.kept_units(i + j, row.seen(row.p[i + j]), border) : 0;
+            mine += w[j];
+        }
+        uint64_t upto = wave_scan(mine) - mine;
+        const uint64_t rest = s.rest;
+#pragma unroll
+        for (int j = 0; j < R::kVec; ++j) {
+            if (upto < rest && upto + w[j] >= rest) *token = i + j;
+            upto += w[j];
+        }
+    }
+}
+
+}  // namespace libred

@@ -221,7 +221,7 @@ red_status sample_call(const red_sample_args* a, hipStream_t stream) {
     }
     if (a->tokens == nullptr && a->probs == nullptr) return RED_OK;
     int dev, cus;
-    const red_status st = host_compute_units(&dev, &cus);
+    red_status st = host_compute_units(&dev, &cus);
     if (st != RED_OK) return st;
     Sample k = {};
     k.x = a->logits, k.batch_stride = a->batch_stride, k.step_stride = a->step_stride;
@@ -232,8 +232,32 @@ red_status sample_call(const red_sample_args* a, hipStream_t stream) {
     int log2 = 0;
     while ((size_t)1 << log2 < V) ++log2;
     k.shift = 62 - log2 < 51 ? 62 - log2 : 51;
-    const hipError_t e = launch_sample(a->type, a->probs != nullptr ? a->probs_type : RED_F32, k, (unsigned)(B * S), stream);
-    return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
+    k.filtered = a->top_k != nullptr || a->top_p != nullptr || a->min_p != nullptr;
+    const int probs_type = a->probs != nullptr ? a->probs_type : RED_F32;
+    const size_t rows = B * S;
+    size_t each = rows;
+    if (V > kSampleChunk) {
+        // Rows cut into chunks, as many at a time as 256 MiB hold the bins and
+        // lists of.
+        const size_t chunks = (V + kSampleChunk - 1) / kSampleChunk;
+        const size_t row = chunks * (sizeof(SampleHead) + kSampleGrid * 8) + kSampleList * 8 + sizeof(SamplePlan);
+        constexpr size_t most = (size_t)256 << 20;
+        void* p = nullptr;
+        st = host_scratch(dev, stream, rows < most / row ? rows * row : most, &p);
+        if (st != RED_OK) return st;
+        if (each > most / row) each = most / row;
+        k.chunks = (int)chunks;
+        k.bins = static_cast<unsigned long long*>(p);
+        k.list = k.bins + each * chunks * kSampleGrid;
+        k.heads = reinterpret_cast<SampleHead*>(k.list + each * kSampleList);
+        k.plans = reinterpret_cast<SamplePlan*>(k.heads + each * chunks);
+    }
+    for (size_t at = 0; at < rows; at += each) {
+        k.first_row = (int)at;
+        const hipError_t e = launch_sample(a->type, probs_type, k, (unsigned)(rows - at < each ? rows - at : each), stream);
+        if (e != hipSuccess) return host_fail(e, RED_ERR_HIP);
+    }
+    return RED_OK;
 }
 
 }  // namespace

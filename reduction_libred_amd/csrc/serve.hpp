@@ -67,7 +67,23 @@ struct SelectPages {
 constexpr int kSelectPages = 64;  // pages of a block that scores them
 hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& a, hipStream_t stream);
 
-// Sampling.
+// Sampling. A row goes through one block, or is cut into chunks.
+constexpr int kSampleChunk = 8192, kSampleGrid = 512, kSampleList = 16384;
+struct SampleHead {  // of a chunk
+    uint64_t first;  // the first code of the order
+    int count;       // logits above -inf
+};
+enum { kRowNone = 0, kRowOne = 1, kRowWhole = 2, kRowCut = 3 };  // empty, one token kept, by a block alone, by its chunks
+struct SamplePlan {  // of a row
+    uint64_t first, cut, k_rest, k_before, p_before, all;
+    double norm;  // of a bin's relative sum to units, at bin 0
+    float from[2], upto[2];  // logits that are gathered
+    int state, ranges, low, high;
+    int use_k, use_p;
+    unsigned int held;  // how many are
+    uint64_t border;  // the last code that is kept
+    double share;     // of a weight in the probabilities
+};
 struct Sample {
     const void* x;
     int64_t batch_stride, step_stride;
@@ -79,7 +95,15 @@ struct Sample {
     int64_t probs_batch, probs_step;
     int steps, vocab;
     int shift;  // weights are counted in units of 2^-shift
+    int first_row;
+    int chunks;    // of a row; 0: none
+    int filtered;  // top-k, top-p or min-p may leave something out
+    SampleHead* heads;         // rows * chunks
+    unsigned long long* bins;  // rows * chunks * kSampleGrid
+    unsigned long long* list;  // rows * kSampleList
+    SamplePlan* plans;         // rows
 };
+hipError_t launch_sample_split(int type, int probs_type, const Sample& a, unsigned int rows, hipStream_t stream);
 hipError_t launch_sample(int type, int probs_type, const Sample& a, unsigned int rows, hipStream_t stream);
 
 }  // namespace libred
