@@ -69,6 +69,37 @@ __device__ __forceinline__ uint32_t first_key(uint32_t top, F is) {
     return high;
 }
 
+// 2^t for t <= 0: a polynomial over half a power to either side, that is 1 at 0;
+// N terms leave out 2^-55 (11) or 2^-38 (8) of it. They interpolate (2^f - 1) / f
+// at the Chebyshev points.
+template <int N>
+__device__ __forceinline__ double power2(double t) {
+    static_assert(N == 11 || N == 8, "terms");
+    const double n = __builtin_rint(t), f = t - n;
+    double p;
+    if constexpr (N == 11) {
+        p = __builtin_fma(4.4549605981865186e-10, f, 7.072585949269223e-09);
+        p = __builtin_fma(p, f, 1.0178062445845774e-07);
+        p = __builtin_fma(p, f, 1.321544258792169e-06);
+        p = __builtin_fma(p, f, 1.525273382983612e-05);
+        p = __builtin_fma(p, f, 0.0001540353044173605);
+        p = __builtin_fma(p, f, 0.0013333558146416936);
+        p = __builtin_fma(p, f, 0.009618129107606888);
+        p = __builtin_fma(p, f, 0.0555041086648216);
+        p = __builtin_fma(p, f, 0.24022650695910097);
+        p = __builtin_fma(p, f, 0.6931471805599453);
+    } else {
+        p = __builtin_fma(1.325080551750225e-06, f, 1.5303700711365693e-05);
+        p = __builtin_fma(p, f, 0.00015403475186530786);
+        p = __builtin_fma(p, f, 0.0013333478473685416);
+        p = __builtin_fma(p, f, 0.00961812913523614);
+        p = __builtin_fma(p, f, 0.055504109063258665);
+        p = __builtin_fma(p, f, 0.24022650695888503);
+        p = __builtin_fma(p, f, 0.6931471805568324);
+    }
+    return __builtin_amdgcn_ldexp(__builtin_fma(p, f, 1.0), (int)n);
+}
+
 // What the block shares.
 struct Shared {
     unsigned long long mass[kBins];
@@ -76,6 +107,7 @@ struct Shared {
     unsigned long long code[kHeld];  // what is in the border's bin
     unsigned long long own[kHeld];   // the weights of those
     unsigned long long part[kWaves], found, rest;
+    unsigned long long few[kWave], few_own[kWave];  // what a wave takes
     unsigned int held, bin, cut;
 };
 
@@ -151,7 +183,7 @@ struct Row {
         for (int i0 = 0; i0 < vocab; i0 += kTile) {
             const int i = i0 + threadIdx.x * kVec;
             float x[kVec];
-            if (i0 + kTile <= vocab) {
+            if (i + kVec <= vocab) {
                 const Vector v = *reinterpret_cast<const Vector*>(p + i);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) x[j] = seen(v[j]);
@@ -172,7 +204,7 @@ struct Row {
         });
     }
     __device__ __forceinline__ double weight(float x) const {
-        return x == kNone ? 0.0 : exp2(((double)x - top) * scale);
+        return x == kNone ? 0.0 : power2<11>(((double)x - top) * scale);
     }
     // In units: 2^52 more than a number below it has that number as its last bits.
     __device__ __forceinline__ uint64_t units(double w) const {
@@ -189,8 +221,9 @@ struct Row {
     }
 };
 
-// The bin in which the running sum of `own` (bin tid) reaches `target`, what is
-// missing of the target there, or bin kBins. By the block's first waves.
+// The bin in which the running sum of the bins' reaches `target`, the last that
+// is not empty where it does not, kBins if all are; and what is missing of the
+// target there.
 __device__ __forceinline__ void find_bin(Shared& s, uint64_t target, bool codes) {
     __syncthreads();
     if (threadIdx.x < kWave) {
@@ -205,6 +238,8 @@ __device__ __forceinline__ void find_bin(Shared& s, uint64_t target, bool codes)
         const uint64_t upto = wave_scan(sum);
         if (lane == 0) s.bin = kBins;
         uint64_t before = upto - sum;
+        const uint64_t whole = read_lane(upto, kWave - 1);
+        target = target < whole ? target : whole;
         wave_lds_fence();
         if (before < target && upto >= target) {
 #pragma unroll

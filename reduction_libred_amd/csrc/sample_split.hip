@@ -30,32 +30,48 @@ constexpr int kChunk = kSampleChunk, kChunkThreads = 256, kOwn = kChunk / kChunk
 constexpr int kGrid = kSampleGrid;       // bins: 64 powers of two
 constexpr double kPerPower = 8.0;        // bins a power of two
 constexpr int kList = kSampleList;
-constexpr int kCountAt = 50;             // a bin's number is above this bit, its sum below, in units of 2^-36
-constexpr uint64_t kSumMask = (1ull << kCountAt) - 1;
-static_assert(kChunk <= 1 << (64 - kCountAt - 1) && kChunk <= 1 << (kCountAt - 37), "a chunk's sums have room");
+// A bin adds up doubles 2^52 + v by their bits: v, the relative weight in units
+// of 2^-36, in the low 52, and in the others 0x433 for each, modulo 2^12.
+constexpr uint64_t kSumMask = ((uint64_t)1 << 52) - 1;
+constexpr unsigned int kInverse = 1787;  // of 0x433, modulo 2^12
+static_assert(0x433 * kInverse % 4096 == 1 && kChunk <= 8192, "a bin's number can be told");
+
+// How many were added: known modulo 2^12, and at most 2^(1/8) times the sum.
+__device__ __forceinline__ unsigned int count_of(uint64_t bin) {
+    const uint64_t sum = bin & kSumMask;
+    unsigned int n = (unsigned int)(bin >> 52) * kInverse & 4095u;
+    n += ((uint64_t)n << 36) < sum ? 4096u : 0u;
+    n += ((uint64_t)n << 36) < sum ? 4096u : 0u;
+    return n;
+}
 
 // What a logit is on the grid of a row.
 struct Place {
     double scale;  // 8 log2(e) / T
-    __device__ __forceinline__ double y(float x) const { return (double)x * scale; }
-    __device__ __forceinline__ double floor_of(float x) const { return __builtin_floor(y(x)); }
+    __device__ __forceinline__ double floor_of(float x) const { return __builtin_floor((double)x * scale); }
+    // From the bin's lower edge, by the product before it is rounded.
+    __device__ __forceinline__ double in_bin(float x, double floor) const { return __builtin_fma((double)x, scale, -floor); }
+    // Whether the bins' numbers are small enough for all that is done with them.
+    __device__ __forceinline__ bool fits(float top) const { return __builtin_fabs((double)top * scale) < 0x1p27; }
 };
 
-// 2^36 2^((f - 1) / 8) for the place f in its bin, as the low bits of 2^52 more.
-// Coefficients: (log(2) / 8)^n / n! times 2^36 2^(-1/16), around f = 1/2; what
-// is left out is below 2^-44 of the whole.
-__device__ __forceinline__ uint64_t relative_units(double f) {
-    constexpr double l = 0.69314718055994530942 / 8.0, c = 0x1p36 * 0.95760328069857364694;  // 2^(-1/16)
-    const double t = f - 0.5;
-    double r = c * l * l * l * l * l * l / 720.0;
-    r = __builtin_fma(r, t, c * l * l * l * l * l / 120.0);
-    r = __builtin_fma(r, t, c * l * l * l * l / 24.0);
-    r = __builtin_fma(r, t, c * l * l * l / 6.0);
-    r = __builtin_fma(r, t, c * l * l / 2.0);
-    r = __builtin_fma(r, t, c * l);
-    r = __builtin_fma(r, t, c + 0x1p52);
-    return __builtin_bit_cast(uint64_t, r) & 0xFFFFFFFFFFFFFull;
-}
+// 2^52 + 2^36 2^((f - 1) / 8) for the place f in its bin, rounded to a whole
+// number. The polynomial interpolates at the Chebyshev points of the bin and is
+// off by 2^-41 of the weight. Its coefficients are kept in scalar registers: as
+// constants the compiler moves each into vector registers for each logit, as
+// many instructions as the rest.
+struct Relative {
+    double c0 = 0x1p36 * 0.9170040432043982 + 0x1p52, c1 = 0x1p36 * 0.07945234590833129, c2 = 0x1p36 * 0.003442010367212629,
+           c3 = 0x1p36 * 9.941014004467738e-05, c4 = 0x1p36 * 2.1514114906866102e-06, c5 = 0x1p36 * 3.896824607481367e-08;
+    __device__ __forceinline__ Relative() { asm("" : "+s"(c0), "+s"(c1), "+s"(c2), "+s"(c3), "+s"(c4), "+v"(c5)); }
+    __device__ __forceinline__ uint64_t units(double f) const {
+        double r = __builtin_fma(c5, f, c4);
+        r = __builtin_fma(r, f, c3);
+        r = __builtin_fma(r, f, c2);
+        r = __builtin_fma(r, f, c1);
+        return __builtin_bit_cast(uint64_t, __builtin_fma(r, f, c0));
+    }
+};
 
 template <class T>
 struct Loads {
@@ -65,21 +81,21 @@ struct Loads {
     Vector v[kCount];
 
     // The chunk's logits from number `first` on, those of thread tid: kVec
-    // neighbours every kChunkThreads * kVec. Behind the last: -inf.
+    // neighbours every kChunkThreads * kVec. Behind the last: -inf. (A chunk
+    // that the row ends in is read by vectors too, but for the one that the end
+    // is in: element by element it took as long as all others, 26 us / 16 of 192
+    // rows of 131071.)
     __device__ __forceinline__ Loads(const B* p, int first, int vocab) {
         const int tid = threadIdx.x;
-        if (first + kChunk <= vocab) {
+        auto place = [&](int u) { return first + (u * kChunkThreads + tid) * kVec; };
 #pragma unroll
-            for (int u = 0; u < kCount; ++u) v[u] = *reinterpret_cast<const Vector*>(p + first + (u * kChunkThreads + tid) * kVec);
-        } else {
+        for (int u = 0; u < kCount; ++u) v[u] = *reinterpret_cast<const Vector*>(p + (place(u) + kVec <= vocab ? place(u) : 0));
+        if (first + kChunk > vocab)
 #pragma unroll
             for (int u = 0; u < kCount; ++u)
+                if (place(u) + kVec > vocab)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    const int i = first + (u * kChunkThreads + tid) * kVec + j;
-                    v[u][j] = i < vocab ? p[i] : T::narrow(kNone);
-                }
-        }
+                    for (int j = 0; j < kVec; ++j) v[u][j] = place(u) + j < vocab ? p[place(u) + j] : T::narrow(kNone);
     }
     __device__ __forceinline__ float at(int n) const { return T::widen(v[n / kVec][n % kVec]); }
     __device__ __forceinline__ static int number(int n) { return (n / kVec * kChunkThreads + threadIdx.x) * kVec + n % kVec; }
@@ -88,7 +104,7 @@ struct Loads {
 template <class T>
 __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     constexpr int W = kChunkThreads / kWave;
-    __shared__ __align__(16) unsigned long long bins[kGrid];
+    __shared__ __align__(16) unsigned long long bins[kGrid + kWave];
     __shared__ float tops[W];
     __shared__ int numbers[W], counts[W];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -96,7 +112,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
     const Loads<T> x(p, first, a.vocab);
     const Settings set(a, b);
-    for (int i = tid; i < kGrid; i += kChunkThreads) bins[i] = 0;
+    for (int i = tid; i < kGrid; i += kChunkThreads) bins[i] = 0;  // those behind are not read
     // The largest logit; a NaN is none.
     float top = kNone;
 #pragma unroll
@@ -107,21 +123,32 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     top = tops[0];
 #pragma unroll
     for (int w = 1; w < W; ++w) top = fmaxf(top, tops[w]);
-    // Its first number, how many logits there are above -inf, and the bins.
+    // The bins. Vector instructions bound this kernel, most of them in float64: a
+    // logit below the grid goes to a place of its lane's behind it, without a
+    // branch.
     const Place place{set.scale * kPerPower};
-    const double peak = place.floor_of(top);
-    const bool binned = set.k != 1 && top < __builtin_inff();
-    int number = kChunk, count = 0;
+    const bool binned = set.k != 1 && place.fits(top);
+    int number = kOwn, count = 0;
+    if (binned) {
+        // Bins by their negative numbers, that rise from the first bin down.
+        const Relative relative;
+        const double peak = place.floor_of(top), up = -place.scale, end = kGrid - peak;
+        const int aside = (kGrid + lane) * 8, base = (int)peak * 8;
 #pragma unroll
-    for (int n = 0; n < kOwn; ++n) {
-        const float v = x.at(n);
-        if (v == top) number = min(number, Loads<T>::number(n));
-        if (binned && v > kNone) {
-            ++count;
-            const double y = place.y(v), g = __builtin_floor(y), d = peak - g;
-            if (d < (double)kGrid) atomicAdd(&bins[(int)d], (unsigned long long)(relative_units(y - g) + (1ull << kCountAt)));
+        for (int n = 0; n < kOwn; ++n) {
+            const double v = (double)x.at(n), g = __builtin_ceil(v * up);
+            const int to = g < end ? ((int)g << 3) + base : aside;
+            atomicAdd(reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(bins) + to),
+                      (unsigned long long)relative.units(__builtin_fma(v, place.scale, g)));
         }
+        if (set.k < a.vocab)
+#pragma unroll
+            for (int n = 0; n < kOwn; ++n) count += x.at(n) > kNone ? 1 : 0;
     }
+    // The largest logit's first number.
+#pragma unroll
+    for (int n = kOwn - 1; n >= 0; --n) number = x.at(n) == top ? n : number;
+    number = number < kOwn ? Loads<T>::number(number) : kChunk;
     number = group_combine<kWave>(number, [](int m, int n) { return min(m, n); });
     count = group_combine<kWave>(count, [](int m, int n) { return m + n; });
     if (lane == 0) numbers[wave] = number, counts[wave] = count;
@@ -172,6 +199,15 @@ __device__ __forceinline__ SampleHead row_head(const SampleHead* heads, int chun
     return SampleHead{first, count};
 }
 
+// A bin's sum in units of the largest weight, whose own relative units are
+// `largest`. In the first bin whole multiples of that are exact, so that a row
+// of equal logits has exact sums.
+__device__ __forceinline__ uint64_t scaled(uint64_t sum, int bin, uint64_t largest, double norm, uint64_t unit, double factor) {
+    if (bin > 0) return (uint64_t)((double)sum * (norm * factor));
+    const uint64_t whole = sum / largest;
+    return whole * unit + (uint64_t)((double)(sum - whole * largest) * norm);
+}
+
 // How far the bins of a chunk whose largest logit has this code are below the
 // row's; kGrid and more: none of them counts.
 __device__ __forceinline__ int chunk_shift(const Place& place, double peak, uint64_t code) {
@@ -191,7 +227,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     SamplePlan& plan = a.plans[blockIdx.x];
     const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
     const float top = logit_of(head.first);
-    int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : top == __builtin_inff() ? kRowWhole : kRowCut;
+    int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
     if (tid < 4) s.first[tid] = kGrid;
     if (tid == 0) plan.first = head.first, plan.held = 0, plan.state = state, plan.ranges = 0;
     if (state != kRowCut) return;
@@ -206,16 +242,20 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     uint64_t sum = 0;
     unsigned int count = 0;
     const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
-    for (int c = 0; c < a.chunks; ++c) {
-        const int j = tid - shifts[c];
-        if (j >= 0) {
-            const uint64_t v = bins[(int64_t)c * kGrid + j];
-            sum += v & kSumMask, count += (unsigned int)(v >> kCountAt);
+    for (int c0 = 0; c0 < a.chunks; c0 += 8) {
+        uint64_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int c = min(c0 + u, a.chunks - 1), j = tid - shifts[c];
+            v[u] = bins[(int64_t)c * kGrid + max(j, 0)];
+            if (j < 0 || c0 + u >= a.chunks) v[u] = 0;
         }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u] & kSumMask, count += count_of(v[u]);
     }
-    // In units of the largest weight: bin 0's upper edge is 2^((peak + 1 - y) / 8) of it.
-    const double norm = row.unit * 0x1p-36 * exp2((peak + 1.0 - place.y(top)) / kPerPower);
-    uint64_t mass = (uint64_t)((double)sum * (norm * exp2(-(double)tid / kPerPower)));
+    const uint64_t largest = Relative().units(place.in_bin(top, peak)) & kSumMask, unit = (uint64_t)row.unit;
+    const double norm = row.unit / (double)largest;
+    uint64_t mass = scaled(sum, tid, largest, norm, unit, power2<11>(-(double)tid / kPerPower));
     const unsigned int own_count = count;
     mass = wave_scan(mass);
     count += dpp_move<0x111, 0xF>(0u, count);
@@ -296,7 +336,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
         plan.k_before = before_k;
         plan.p_before = low > 0 && low < kGrid ? s.mass[low - 1] : 0;
         plan.all = all;
-        plan.norm = norm;
+        plan.norm = norm, plan.largest = largest;
     }
 }
 
@@ -305,20 +345,22 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
     constexpr int W = kChunkThreads / kWave;
     __shared__ unsigned int counts[W], start;
     SamplePlan& plan = a.plans[blockIdx.y];
-    if (plan.ranges == 0) return;
-    const float from0 = plan.from[0], upto0 = plan.upto[0];
-    const bool two = plan.ranges == 2;
-    const float from1 = two ? plan.from[1] : 1.f, upto1 = two ? plan.upto[1] : 0.f;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
     const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
-    const Loads<T> x(p, first, a.vocab);
+    const Loads<T> x(p, first, a.vocab);  // before the plan is known: one trip
+    const int ranges = plan.ranges;
+    if (ranges == 0) return;
     uint32_t in = 0;
     static_assert(kOwn <= 32, "a bit a logit");
+    const float from0 = plan.from[0], upto0 = plan.upto[0], from1 = plan.from[1], upto1 = plan.upto[1];
+    for (int r = 0; r < ranges; ++r) {
+        const float from = r ? from1 : from0, upto = r ? upto1 : upto0;
 #pragma unroll
-    for (int n = 0; n < kOwn; ++n) {
-        const float v = x.at(n);
-        if ((v >= from0 && v < upto0) || (v >= from1 && v < upto1)) in |= 1u << n;
+        for (int n = 0; n < kOwn; ++n) {
+            const float v = x.at(n);
+            in |= v >= from && v < upto ? 1u << n : 0u;
+        }
     }
     // Places in the list: this thread's behind those of the threads before.
     unsigned int own = (unsigned)__popc(in), upto = own;
@@ -341,52 +383,69 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
     __syncthreads();
     unsigned int to = start + before + upto - own;
     unsigned long long* list = a.list + (int64_t)blockIdx.y * kList;
-#pragma unroll
-    for (int n = 0; n < kOwn; ++n)
-        if (in >> n & 1) {
-            if (to < kList) list[to] = code_of(x.at(n) + 0.f, first + Loads<T>::number(n));
-            ++to;
-        }
+    // Few have any: read again rather than chosen among registers.
+    while (in) {
+        const int n = __ffs(in) - 1, i = first + Loads<T>::number(n);
+        if (to < kList) list[to] = code_of(T::widen(p[i]) + 0.f, i);
+        ++to, in &= in - 1;
+    }
 }
 
-// The code at which the running sum of value(code), in the order of the codes
-// of the list, among those from `from` to below `upto`, reaches `want`; the last of
-// them where it does not, ~0 where there are none.
-template <class V>
-__device__ __forceinline__ uint64_t list_border(Shared& s, const unsigned long long* list, int n, uint64_t from, uint64_t upto,
-                                                uint64_t want, V value) {
-    __syncthreads();
-    if (threadIdx.x == 0) s.found = 0, s.held = 0, s.rest = ~0ull;
-    __syncthreads();
-    uint64_t least = ~0ull, most = 0, sum = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint64_t c = list[i];
-        if (c >= from && c < upto) {
-            least = c < least ? c : least, most = c > most ? c : most;
-            sum += value(c);
-        }
-    }
-    sum = block_combine(sum, s, AddU64());
-    most = block_combine(most, s, MaxU64());
-    least = ~block_combine(~least, s, MaxU64());
-    if (most == 0) return ~0ull;
-    if (want >= sum) return least;  // also where roundings leave the sum short
-    if (want == 0) want = 1;
-    int down = bytes_of(least ^ most) * 8;
-    uint64_t prefix = most >> down;
-    while (down > 0) {
-        const int to = down - 8;
+// The code at which the running sum of value(i), in the order of the codes
+// code(i), i < n, that lie from `from` to below `upto`, reaches `want`, the last
+// of them where it does not; ~0 where there are none. Digits of 8 bits from the
+// first that `from` and `upto` do not share, until a wave can take the rest.
+template <class C, class V>
+__device__ __forceinline__ uint64_t list_border(Shared& s, int n, uint64_t from, uint64_t upto, uint64_t want, C code, V value) {
+    if (from >= upto) return ~0ull;
+    const int tid = threadIdx.x, lane = tid % kWave;
+    int down = 64 - __builtin_clzll((from ^ (upto - 1)) | 1);
+    uint64_t prefix = from >> down;
+    unsigned int in = n;
+    auto inside = [&](uint64_t c) { return c >= from && c < upto && c >> down == prefix; };
+    want = want > 0 ? want : 1;
+    while (in > kWave && down > 0) {
+        const int width = min(down, 8), to = down - width;
         clear_bins(s);
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint64_t c = list[i];
-            if (c >= from && c < upto && c >> down == prefix) atomicAdd(&s.mass[c >> to & 255], (unsigned long long)value(c));
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t c = code(i);
+            if (!inside(c)) continue;
+            const int d = (int)(c >> to) & ((1 << width) - 1);
+            atomicAdd(&s.mass[d], (unsigned long long)value(i));
+            atomicAdd(&s.count[d], 1u);
         }
         find_bin(s, want, true);
-        prefix = prefix << 8 | s.bin;
-        want = s.rest;
+        if (s.bin >= kBins) return ~0ull;
+        prefix = prefix << width | s.bin;
+        want = s.rest, in = s.count[s.bin];
         down = to;
     }
-    return prefix;
+    if (down == 0) return prefix;
+    __syncthreads();
+    if (tid == 0) s.held = 0, s.found = ~0ull;
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const uint64_t c = code(i);
+        if (inside(c)) {
+            const unsigned int at = atomicAdd(&s.held, 1u);
+            if (at < kWave) s.few[at] = c, s.few_own[at] = value(i);
+        }
+    }
+    __syncthreads();
+    if (tid < kWave) {
+        const int held = min((int)s.held, kWave);
+        const uint64_t c = lane < held ? s.few[lane] : 0, own = lane < held ? s.few_own[lane] : 0;
+        uint64_t before = 0, all = 0;
+        for (int i = 0; i < held; ++i) {
+            const uint64_t other = s.few_own[i];
+            all += other;
+            if (s.few[i] > c) before += other;
+        }
+        const uint64_t goal = want < all ? want : all;
+        if (lane < held && before < goal && before + own >= goal) s.found = c;
+    }
+    __syncthreads();
+    return s.found;
 }
 
 template <class T>
@@ -394,17 +453,20 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     using R = Row<T>;
     __shared__ Shared s;
     __shared__ unsigned long long runs[kMaxVocab / R::kRun];
+    __shared__ double factors[kGrid];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps;
-    SamplePlan& plan = a.plans[blockIdx.x];
+    const SamplePlan plan = a.plans[blockIdx.x];
+    SamplePlan& to = a.plans[blockIdx.x];
+    const float r = a.r ? a.r[at] : 0.f;
     const int state = plan.state;
     const Settings set(a, b);
     R row(a, b, step);
     const uint64_t first = row.settle(plan.first, set.scale, a.shift);
     if (state == kRowNone || state == kRowOne) {
         if (tid == 0) {
-            plan.border = state == kRowOne ? first : ~0ull;
-            plan.share = 1.0;
+            to.border = state == kRowOne ? first : ~0ull;
+            to.share = 1.0;
             if (a.tokens) a.tokens[at] = state == kRowOne ? token_of(first) : -1;
         }
         return;
@@ -412,73 +474,82 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     if (state == kRowWhole) {
         const uint64_t border = row_border(row, s, set, first);
         const uint64_t total = row_total(row, s, runs, border);
-        if (tid == 0) plan.border = border, plan.share = row.unit / (double)total;
-        if (a.tokens) row_draw(row, s, runs, border, draw_target(a.r[at], total), a.tokens + at);
+        if (tid == 0) to.border = border, to.share = row.unit / (double)total;
+        if (a.tokens) row_draw(row, s, runs, border, draw_target(r, total), a.tokens + at);
         return;
     }
-    // The border among the gathered codes.
+    // The chunks' sums in the bins above those gathered, which are kept whole.
+    const Place place{set.scale * kPerPower};
+    const double peak = place.floor_of(row.top_logit), norm = plan.norm;
+    const int bin = plan.ranges > 0 ? plan.low : kGrid;
+    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
+    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
+    for (int i = tid; i < kGrid; i += kThreads) factors[i] = power2<11>(-(double)i / kPerPower);
+    __syncthreads();
+    for (int c = wave; c < a.chunks; c += kWaves) {
+        uint64_t v[kGrid / kWave], sum = 0;
+#pragma unroll
+        for (int u = 0; u < kGrid / kWave; ++u) v[u] = bins[(int64_t)c * kGrid + u * kWave + lane];
+        const int shift = chunk_shift(place, peak, heads[c].first);
+#pragma unroll
+        for (int u = 0; u < kGrid / kWave; ++u) {
+            const int j = u * kWave + lane + shift;
+            if (j < bin) sum += scaled(v[u] & kSumMask, j, plan.largest, norm, (uint64_t)row.unit, factors[min(j, kGrid - 1)]);
+        }
+        sum = group_combine<kWave>(sum, AddU64());
+        if (lane == 0) runs[c] = sum;
+    }
+    // The border among the gathered codes: in the LDS, with their weights, as far
+    // as there is room.
     const unsigned long long* list = a.list + (int64_t)blockIdx.x * kList;
     const int held = (int)min(plan.held, (unsigned)kList), ranges = plan.ranges;
-    auto key = [](float x) { return code_of(x, kMaxVocab - 1); };  // the last code of a logit
-    uint64_t border = 0;
     auto units = [&](uint64_t c) { return row.units(row.weight(logit_of(c))); };
+    for (int i = tid; i < min(held, kHeld); i += kThreads) {
+        const uint64_t c = list[i];
+        s.code[i] = c, s.own[i] = units(c);
+    }
+    auto code = [&](int i) -> uint64_t { return i < kHeld ? s.code[i] : list[i]; };
+    auto weight = [&](int i) -> uint64_t { return i < kHeld ? s.own[i] : units(list[i]); };
+    auto key = [](float x) { return code_of(x, kMaxVocab - 1); };  // the last code of a logit
+    __syncthreads();
+    uint64_t border = 0;
     if (plan.use_k) {
-        const int r = ranges - 1;
-        border = list_border(s, list, held, key(plan.from[r]), key(plan.upto[r]), plan.k_rest, [](uint64_t) -> uint64_t { return 1; });
+        border = list_border(s, held, key(ranges == 2 ? plan.from[1] : plan.from[0]), key(ranges == 2 ? plan.upto[1] : plan.upto[0]), plan.k_rest, code, [](int) -> uint64_t { return 1; });
     }
     if (plan.use_p) {
         uint64_t all = plan.all;
         if (plan.use_k) {
-            // Those of the bin of top-k's border that are kept.
-            const uint64_t from = border, upto = key(plan.upto[ranges - 1]);
+            // What top-k keeps: bins above the last range, and of that what is above
+            // the border.
+            const uint64_t upto = key(ranges == 2 ? plan.upto[1] : plan.upto[0]);
             uint64_t sum = 0;
-            for (int i = tid; i < held; i += kThreads)
-                if (list[i] >= from && list[i] < upto) sum += units(list[i]);
-            sum = block_combine(sum, s, AddU64());
-            // of the last range's first bin on: with one range what lies between is counted with it
-            all = (ranges == 2 ? plan.k_before : plan.p_before) + sum;
+            for (int i = tid; i < held; i += kThreads) {
+                const uint64_t c = code(i);
+                if (c >= border && c < upto) sum += weight(i);
+            }
+            all = (ranges == 2 ? plan.k_before : plan.p_before) + block_combine(sum, s, AddU64());
         }
-        const uint64_t want = top_p_target(set.p, all);
+        const uint64_t want = top_p_target(set.p, all), upto = key(plan.upto[0]);
         uint64_t from = key(plan.from[0]);
         from = from > border ? from : border;
-        const uint64_t upto = key(plan.upto[0]);
-        const uint64_t found = want > plan.p_before ? list_border(s, list, held, from, upto, want - plan.p_before, units) : upto;
-        border = found > border ? found : border;
-        if (found == ~0ull) border = upto;
+        const uint64_t found = want > plan.p_before ? list_border(s, held, from, upto, want - plan.p_before, code, weight) : upto;
+        border = found == ~0ull ? upto : found > border ? found : border;
     }
     border = plan.cut > border ? plan.cut : border;
-    // The sums of the chunks: bins above the list's by what the chunks have of
-    // them, and what is kept of the list.
-    const Place place{set.scale * kPerPower};
-    const double peak = place.floor_of(row.top_logit);
-    const int bin = ranges > 0 ? plan.low : kGrid;                    // bins before this one are kept whole
-    const uint64_t above = ranges > 0 ? key(plan.upto[0]) : 0;  // their codes, from here on
-    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
-    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
-    __syncthreads();
-    for (int c = wave; c < a.chunks; c += kWaves) {
-        const int shift = chunk_shift(place, peak, heads[c].first);
-        uint64_t sum = 0;
-        for (int j = lane; j < kGrid; j += kWave)
-            if (j + shift < bin) {
-                const uint64_t v = bins[(int64_t)c * kGrid + j] & kSumMask;
-                sum += (uint64_t)((double)v * (plan.norm * exp2(-(double)(j + shift) / kPerPower)));
-            }
-        sum = group_combine<kWave>(sum, AddU64());
-        if (lane == 0) runs[c] = sum;
-    }
+    // The sums of the chunks: bins above the list's, and what is kept of the list.
+    const uint64_t above = ranges > 0 ? key(plan.upto[0]) : 0;
     __syncthreads();
     if (ranges > 0)
         for (int i = tid; i < held; i += kThreads) {
-            const uint64_t c = list[i];
-            if (c >= border && c < above) atomicAdd(&runs[token_of(c) / kChunk], (unsigned long long)units(c));
+            const uint64_t c = code(i);
+            if (c >= border && c < above) atomicAdd(&runs[token_of(c) / kChunk], (unsigned long long)weight(i));
         }
     __syncthreads();
     uint64_t own = tid < a.chunks ? runs[tid] : 0;
     const uint64_t total = block_combine(own, s, AddU64());
-    if (tid == 0) plan.border = border, plan.share = row.unit / (double)total;
+    if (tid == 0) to.border = border, to.share = row.unit / (double)total;
     if (!a.tokens) return;
-    const uint64_t want = draw_target(a.r[at], total);
+    const uint64_t want = draw_target(r, total);
     uint64_t before = block_before(own, s);
     if (own > 0 && before < want && before + own >= want) s.bin = tid, s.rest = want - before;
     __syncthreads();
@@ -525,7 +596,9 @@ __global__ __launch_bounds__(kChunkThreads) void sample_probs_kernel(Sample a) {
             const float f = row.seen(x.v[u][j]);
             const bool kept = f != kNone && code_of(f, i0 + j) >= border;
             // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
-            v[j] = P::narrow(kept ? (float)(row.weight(f) * share) : 0.f);
+            float w = 0.f;
+            if (__any(kept) && kept) w = (float)(power2<8>(((double)f - row.top) * row.scale) * share);
+            v[j] = P::narrow(w);
         }
         if (i0 + L::kVec <= a.vocab) {
             *reinterpret_cast<Out*>(probs + i0) = v;

@@ -71,11 +71,12 @@ hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& 
 constexpr int kSampleChunk = 8192, kSampleGrid = 512, kSampleList = 16384;
 struct SampleHead {  // of a chunk
     uint64_t first;  // the first code of the order
-    int count;       // logits above -inf
+    int count;       // logits above -inf, where top-k asks for it
 };
 enum { kRowNone = 0, kRowOne = 1, kRowWhole = 2, kRowCut = 3 };  // empty, one token kept, by a block alone, by its chunks
 struct SamplePlan {  // of a row
     uint64_t first, cut, k_rest, k_before, p_before, all;
+    uint64_t largest;  // relative units of the largest weight
     double norm;  // of a bin's relative sum to units, at bin 0
     float from[2], upto[2];  // logits that are gathered
     int state, ranges, low, high;

@@ -404,7 +404,9 @@ def check_sample(x, r, t=None, k=None, p=None, m=None, probs=F32, exact=False):
             kept, near = S.sample(wide[b, s], of["temperature"], None if k is None else k[b], of["top_p"], of["min_p"])
             sure = exact or near > certain(vocab)
             assert sure, "a border closer to its target than sums of 64 bits tell"
-            token, close = S.token_of(kept, float(r[b, s]))
+            # weights below half a unit count as 0 where they are summed
+            unit = 2.0 ** -min(51, 62 - math.ceil(math.log2(vocab)))
+            token, close = S.token_of(np.where(kept < unit / 2, 0, kept), float(r[b, s]))
             assert exact or close > certain(vocab)
             assert tokens[b][s] == token, (b, s, tokens[b][s], token)
             want = (kept / kept.sum() if kept.sum() > 0 else kept).astype(np.float64)
@@ -445,7 +447,7 @@ def test_sample(case):
                  probs=probs)
 
 
-@pytest.mark.parametrize("vocab", [5, 2049, 40000, 131071])
+@pytest.mark.parametrize("vocab", [5, 2049, 9001, 16001, 40000, 131071])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_sample_of_equal_logits(vocab, dtype):
     """Whole rows of ties: weights are whole, sums exact, and the lower numbers are kept."""
@@ -457,6 +459,33 @@ def test_sample_of_equal_logits(vocab, dtype):
     # halves and quarters of the sum are met exactly
     check_sample(x[:5], r[:5], p=[0.5, 0.25, 0.0, 0.75, 1.0], exact=True)
     check_sample(x[:5], r[:5], k=[4, 4, 0, vocab, 2], p=[0.5, 0.25, 0.5, 0.75, 0.5], m=[1.0, 5.0, 0.5, 0.0, -1.0], exact=True)
+
+
+@pytest.mark.parametrize("vocab", [100, 9000, 131071])
+def test_sample_of_a_few_equal_logits_among_masked_ones(vocab):
+    """What a grammar leaves: borders and draws at whole multiples of one weight."""
+    x = torch.full((8, 1, vocab), -math.inf)
+    x[:, 0, [3, 50, vocab // 2, vocab - 1]] = 7.3
+    r = torch.tensor([0.0, 0.25, 0.5, 0.75, 0.2499, 0.99, 1.0, 0.5])[:, None]
+    check_sample(x, r, exact=True)
+    check_sample(x, r, p=[0.25, 0.5, 0.75, 0.5, 0.5001, 0.9, 0.0, 0.24], exact=True)
+    check_sample(x, r, k=[1, 2, 3, 4, 5, 2, 3, 0], p=[0.5] * 8, m=[1.0] * 8, exact=True)
+    x[:, 0, [5, 60]] = 7.3 - 60 * math.log(2)        # 2^-60 of the others: more than nothing, less than a unit
+    check_sample(x, r[:6].repeat(2, 1)[:8], k=[5] * 8, exact=True)
+
+
+@pytest.mark.parametrize("case", [(0.7, 900, 0.93, None), (1.3, 40, 0.2, 0.3), (1.0, 3000, 0.999, 0.001), (0.4, 20000, 0.95, None), (1.0, 5, 0.9999, 0.9),
+                                  (2.0, 30000, None, None), (2.0, None, 0.5, 0.0001), (1.0, None, None, 0.02), (8.0, 15000, 0.5, 0.7),
+                                  (30.0, 25000, 0.97, None), (0.01, None, 0.999999, 1e-30), (1e-4, 20, 0.9, None)], ids=str)
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_sample_filters_together(case, dtype):
+    """Borders of one filter above, within and below those of the others, in bins of few and of most tokens."""
+    t, k, p, m = case
+    g = gen(77)
+    x = torch.randn(3, 1, 32768, generator=g) * torch.tensor([1.0, 2.0, 4.0])[:, None, None] + torch.tensor([0.0, 30.0, -100.0])[:, None, None]
+    x = x.to(dtype)
+    check_sample(x, torch.rand(3, 1, generator=g), t=[t] * 3, k=None if k is None else [k] * 3, p=None if p is None else [p] * 3,
+                 m=None if m is None else [m] * 3)
 
 
 def test_sample_of_few_values_over_many_tokens():
