@@ -9,19 +9,18 @@ template <class T, class P>
 __global__ __launch_bounds__(kThreads) void sample_row_kernel(Sample a) {
     using R = Row<T>;
     __shared__ Shared s;
-    __shared__ unsigned long long runs[kMaxVocab / R::kRun];
     const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps, tid = threadIdx.x;
     const Settings set(a, b);
     R row(a, b, step);
     typename P::bits* probs = a.probs ? static_cast<typename P::bits*>(a.probs) + b * a.probs_batch + step * a.probs_step : nullptr;
 
     uint64_t first = 0;
-    row.each([&](int i, float x) {
-        const uint64_t c = code_of(x, i);
+    row.each([&](int i, float x) __attribute__((always_inline)) {
+        const uint64_t c = R::C::of(x, i);
         first = c > first ? c : first;
     });
     first = block_combine(first, s, MaxU64());
-    if (logit_of(first) == kNone) {
+    if (R::C::logit(first) == kNone) {
         if (a.tokens && tid == 0) a.tokens[at] = -1;
         if (probs)
             for (int i = tid; i < a.vocab; i += kThreads) probs[i] = P::narrow(0.f);
@@ -29,16 +28,16 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(Sample a) {
     }
     first = row.settle(first, set.scale, a.shift);
     const uint64_t border = row_border(row, s, set, first);
-    const uint64_t total = row_total(row, s, runs, border);
-    if (a.tokens) row_draw(row, s, runs, border, draw_target(a.r[at], total), a.tokens + at);
+    const uint64_t total = row_total(row, s, border);
+    if (a.tokens) row_draw(row, s, border, draw_target(a.r[at], total), a.tokens + at);
     if (probs) {
         const double share = row.unit / (double)total;
-        row.tiles([&](int i, const float(&x)[R::kVec]) {
+        row.tiles([&](int i, const float(&x)[R::kVec]) __attribute__((always_inline)) {
             typename P::bits v[R::kVec];
             // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
 #pragma unroll
             for (int j = 0; j < R::kVec; ++j)
-                v[j] = P::narrow(x[j] == kNone || code_of(x[j], i + j) < border ? 0.f : (float)(row.weight(x[j]) * share));
+                v[j] = P::narrow(x[j] == kNone || R::C::of(x[j], i + j) < border ? 0.f : (float)(row.weight(x[j]) * share));
             for (int j = 0; j < R::kVec; ++j)
                 if (i + j < a.vocab) probs[i + j] = v[j];
         });

@@ -24,8 +24,8 @@ namespace libred {
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
 constexpr int kBins = 256;
 constexpr int kHeld = 2048;        // codes that are gathered in the LDS
-constexpr int kCodeBits = 52;      // 32 of the logit, 20 of the number
 constexpr int kMaxVocab = 1 << 20;
+static_assert(2 * kHeld >= kMaxVocab / (kWave * 4), "a run is what a wave reads at a time");
 
 struct AddU64 {
     __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a + b; }
@@ -34,40 +34,48 @@ struct MaxU64 {
     __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
 };
 
-__device__ __forceinline__ uint64_t code_of(float x, int i) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    const uint32_t k = u >> 31 ? ~u : u | 0x80000000u;
-    return (uint64_t)k << 20 | (uint32_t)(kMaxVocab - 1 - i);
-}
-__device__ __forceinline__ float logit_of_key(uint32_t k) { return __builtin_bit_cast(float, k >> 31 ? k & 0x7FFFFFFFu : ~k); }
-__device__ __forceinline__ float logit_of(uint64_t code) {
-    return logit_of_key((uint32_t)(code >> 20));
-}
-__device__ __forceinline__ int token_of(uint64_t code) { return kMaxVocab - 1 - (int)(code & (kMaxVocab - 1)); }
+// Codes of logits of type T: the bits that order as they do (the key) above 20 of
+// the number's complement.
+template <class T>
+struct Code {
+    static constexpr int kKeyBits = 8 * sizeof(typename T::bits), kBits = kKeyBits + 20;
+    static constexpr uint32_t kSign = 1u << (kKeyBits - 1), kMask = kSign - 1 + kSign;
+    // Of the least finite logit: one above that of -inf.
+    static constexpr uint32_t kLeast = sizeof(typename T::bits) == 4 ? 0x00800000u : std::is_same_v<T, F16> ? 0x0400u : 0x0080u;
+
+    static __device__ __forceinline__ uint64_t of(float x, int i) {
+        const uint32_t u = T::narrow(x);  // exact: x was of this type
+        return (uint64_t)(u & kSign ? ~u & kMask : u | kSign) << 20 | (uint32_t)(kMaxVocab - 1 - i);
+    }
+    static __device__ __forceinline__ float logit_of_key(uint32_t k) {
+        return T::widen((typename T::bits)(k & kSign ? k & ~kSign : ~k & kMask));
+    }
+    static __device__ __forceinline__ float logit(uint64_t code) { return logit_of_key((uint32_t)(code >> 20)); }
+    static __device__ __forceinline__ int token(uint64_t code) { return kMaxVocab - 1 - (int)(code & (kMaxVocab - 1)); }
+
+    // The first of the keys from kLeast to `top` for which `is` holds; it holds
+    // for `top` and for all above one for which it does. By one wave.
+    template <class F>
+    static __device__ __forceinline__ uint32_t first_key(uint32_t top, F is) {
+        const uint32_t lane = threadIdx.x % kWave;
+        uint32_t low = kLeast, high = top;
+        while (low < high) {
+            const uint32_t step = (high - low) / kWave + 1, probe = min(low + lane * step, high);
+            const uint64_t yes = __ballot(is(logit_of_key(probe)));
+            if (!yes) {
+                low = min(low + (kWave - 1) * step, high - 1) + 1;
+            } else {
+                const uint32_t at = (uint32_t)__ffsll((unsigned long long)yes) - 1;
+                const uint32_t found = min(low + at * step, high);
+                if (at > 0) low = low + (at - 1) * step + 1;
+                high = found;
+            }
+        }
+        return high;
+    }
+};
 
 constexpr float kNone = -__builtin_inff();
-constexpr uint32_t kLeastKey = 0x00800000u;  // of the least finite logit
-
-// The first of the keys from kLeastKey to `top` for which `is` holds; it holds
-// for `top` and for all above one for which it does. By one wave.
-template <class F>
-__device__ __forceinline__ uint32_t first_key(uint32_t top, F is) {
-    const uint32_t lane = threadIdx.x % kWave;
-    uint32_t low = kLeastKey, high = top;
-    while (low < high) {
-        const uint32_t step = (high - low) / kWave + 1, probe = min(low + lane * step, high);
-        const uint64_t yes = __ballot(is(logit_of_key(probe)));
-        if (!yes) {
-            low = min(low + (kWave - 1) * step, high - 1) + 1;
-        } else {
-            const uint32_t at = (uint32_t)__ffsll((unsigned long long)yes) - 1;
-            const uint32_t found = min(low + at * step, high);
-            if (at > 0) low = low + (at - 1) * step + 1;
-            high = found;
-        }
-    }
-    return high;
-}
 
 // 2^t for t <= 0: a polynomial over half a power to either side, that is 1 at 0;
 // N terms leave out 2^-55 (11) or 2^-38 (8) of it. They interpolate (2^f - 1) / f
@@ -104,8 +112,16 @@ __device__ __forceinline__ double power2(double t) {
 struct Shared {
     unsigned long long mass[kBins];
     unsigned int count[kBins];
-    unsigned long long code[kHeld];  // what is in the border's bin
-    unsigned long long own[kHeld];   // the weights of those
+    union {
+        struct {
+            unsigned long long code[kHeld];  // what is in the border's bin
+            unsigned long long own[kHeld];   // the weights of those
+            unsigned long long runs[2 * kHeld];  // a row's kept weights, in runs
+        };
+        struct {  // where no runs are needed
+            unsigned long long list[2 * kHeld], list_own[2 * kHeld];
+        };
+    };
     unsigned long long part[kWaves], found, rest;
     unsigned long long few[kWave], few_own[kWave];  // what a wave takes
     unsigned int held, bin, cut;
@@ -134,25 +150,31 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
     v += dpp_move<0x143, 0xC>(none, v);  // the first half into the second
     return v;
 }
-// The sum of the threads before this one.
-__device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& s) {
+// The sum of the threads before this one, and of all.
+__device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& s, uint64_t* all) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const uint64_t upto = wave_scan(v);
     __syncthreads();
     if (lane == kWave - 1) s.part[wave] = upto;
     __syncthreads();
-    uint64_t before = upto - v;
-    for (int w = 0; w < wave; ++w) before += s.part[w];
-    return before;
+    uint64_t before = 0, whole = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) before = whole;
+        whole += s.part[w];
+    }
+    *all = whole;
+    return before + upto - v;
 }
 
 template <class T>
 struct Row {
     using B = typename T::bits;
-    static constexpr int kVec = 16 / sizeof(B), kTile = kThreads * kVec;
+    using C = Code<T>;
+    static constexpr int kVec = 4, kTile = kThreads * kVec;
     static constexpr int kRun = kWave * kVec;  // tokens that a wave reads at a time
     // Rows start on element boundaries only (a vocabulary may be odd).
-    typedef B Vector __attribute__((ext_vector_type(16 / sizeof(B)), aligned(sizeof(B))));
+    typedef B Vector __attribute__((ext_vector_type(4), aligned(sizeof(B))));
 
     const B* p;
     int vocab;
@@ -164,9 +186,9 @@ struct Row {
         : p(static_cast<const B*>(a.x) + b * a.batch_stride + step * a.step_stride), vocab(a.vocab) {}
     // By the first code of the order; -> it, as the row then counts.
     __device__ __forceinline__ uint64_t settle(uint64_t first, double row_scale, int shift) {
-        top_logit = logit_of(first);
+        top_logit = C::logit(first);
         infinite = top_logit == __builtin_inff();
-        if (infinite) top_logit = 0.f, first = code_of(0.f, token_of(first));
+        if (infinite) top_logit = 0.f, first = C::of(0.f, C::token(first));
         top = top_logit, scale = row_scale, unit = __builtin_ldexp(1.0, shift);
         return first;
     }
@@ -176,6 +198,21 @@ struct Row {
         if (infinite) return x == __builtin_inff() ? 0.f : kNone;
         return x == x ? x : kNone;
     }
+    // N logits from number i on, kNone behind the last.
+    template <int N>
+    __device__ __forceinline__ void neighbours(int i, float (&x)[N]) const {
+        static_assert(N % kVec == 0, "whole vectors");
+        if (i + N <= vocab) {
+            Vector v[N / kVec];
+#pragma unroll
+            for (int u = 0; u < N / kVec; ++u) v[u] = *reinterpret_cast<const Vector*>(p + i + u * kVec);
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = seen(v[j / kVec][j % kVec]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] = i + j < vocab ? seen(p[i + j]) : kNone;
+        }
+    }
     // f(number of the first, logits) of this thread's kVec neighbours in every
     // tile of the block; kNone behind the last.
     template <class F>
@@ -183,21 +220,14 @@ struct Row {
         for (int i0 = 0; i0 < vocab; i0 += kTile) {
             const int i = i0 + threadIdx.x * kVec;
             float x[kVec];
-            if (i + kVec <= vocab) {
-                const Vector v = *reinterpret_cast<const Vector*>(p + i);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) x[j] = seen(v[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) x[j] = i + j < vocab ? seen(p[i + j]) : kNone;
-            }
+            neighbours<kVec>(i, x);
             f(i, x);
         }
     }
     // f(number, logit) of every token of this thread.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        tiles([&](int i, const float(&x)[kVec]) {
+        tiles([&](int i, const float(&x)[kVec]) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
                 if (i + j < vocab) f(i + j, x[j]);
@@ -211,7 +241,7 @@ struct Row {
         return __builtin_bit_cast(uint64_t, w * unit + 0x1p52) & 0xFFFFFFFFFFFFFull;
     }
     __device__ __forceinline__ uint64_t kept_units(int i, float x, uint64_t border) const {
-        return x == kNone || code_of(x, i) < border ? 0 : units(weight(x));
+        return x == kNone || C::of(x, i) < border ? 0 : units(weight(x));
     }
     // Bins of an eighth of a power of two, from the largest weight down. The
     // order of the logits holds after each rounding.
@@ -275,8 +305,8 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     clear_bins(s);
     uint64_t last = 0;  // of the last bin, which may hold most tokens: not by atomics
     unsigned int lasts = 0;
-    row.each([&](int i, float x) {
-        if (x == kNone || code_of(x, i) < from) return;
+    row.each([&](int i, float x) __attribute__((always_inline)) {
+        if (x == kNone || Code<T>::of(x, i) < from) return;
         const uint64_t v = value(x);
         if (v == 0) return;
         const int j = row.bin(x);
@@ -302,14 +332,14 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     want = s.rest;
     unsigned int in = s.count[bin];
     // Too many to gather: digits of the codes in that bin, over the whole row.
-    int shift = kCodeBits;
+    int shift = Code<T>::kBits;
     uint64_t prefix = 0;
-    auto inside = [&](uint64_t code, float x) { return x != kNone && code >= from && row.bin(x) == bin && code >> shift == prefix; };
+    auto inside = [&](uint64_t code, float x) __attribute__((always_inline)) { return x != kNone && code >= from && row.bin(x) == bin && code >> shift == prefix; };
     while (in > kHeld && shift > 0) {
         const int width = min(shift, 8), down = shift - width;
         clear_bins(s);
-        row.each([&](int i, float x) {
-            const uint64_t code = code_of(x, i);
+        row.each([&](int i, float x) __attribute__((always_inline)) {
+            const uint64_t code = Code<T>::of(x, i);
             if (!inside(code, x)) return;
             const uint64_t v = value(x);
             if (v == 0) return;
@@ -326,8 +356,8 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     __syncthreads();
     if (threadIdx.x == 0) s.held = 0, s.found = 0;
     __syncthreads();
-    row.each([&](int i, float x) {
-        const uint64_t code = code_of(x, i);
+    row.each([&](int i, float x) __attribute__((always_inline)) {
+        const uint64_t code = Code<T>::of(x, i);
         if (!inside(code, x)) return;
         const uint64_t v = value(x);
         if (v == 0) return;
@@ -380,14 +410,14 @@ __device__ __forceinline__ uint64_t row_border(const Row<T>& row, Shared& s, con
     uint64_t border = 0;
     if (set.k < row.vocab) border = find_border(row, s, 0, [](float) -> uint64_t { return 1; }, [&](uint64_t) { return (uint64_t)set.k; });
     if (set.p < 2.0) {
-        const uint64_t found = find_border(row, s, border, [&](float x) { return row.units(row.weight(x)); },
+        const uint64_t found = find_border(row, s, border, [&](float x) __attribute__((always_inline)) { return row.units(row.weight(x)); },
                                            [&](uint64_t all) { return top_p_target(set.p, all); });
         border = found > border ? found : border;
     }
     if (set.m > 0.0) {
         __syncthreads();
         if (threadIdx.x < kWave) {
-            const uint32_t cut = first_key((uint32_t)(first >> 20), [&](float x) { return row.weight(x) >= set.m; });
+            const uint32_t cut = Code<T>::first_key((uint32_t)(first >> 20), [&](float x) { return row.weight(x) >= set.m; });
             if (threadIdx.x == 0) s.cut = cut;
         }
         __syncthreads();
@@ -397,20 +427,20 @@ __device__ __forceinline__ uint64_t row_border(const Row<T>& row, Shared& s, con
     return border;
 }
 
-// The sum of the kept weights, and that of the tokens a wave reads at a time in
-// `runs`.
+// The sum of the kept weights, and in s.runs those of the tokens a wave reads at
+// a time.
 template <class T>
-__device__ __forceinline__ uint64_t row_total(const Row<T>& row, Shared& s, unsigned long long* runs, uint64_t border) {
+__device__ __forceinline__ uint64_t row_total(const Row<T>& row, Shared& s, uint64_t border) {
     using R = Row<T>;
     const int lane = threadIdx.x % kWave;
     uint64_t total = 0;
     __syncthreads();
-    row.tiles([&](int i, const float(&x)[R::kVec]) {
+    row.tiles([&](int i, const float(&x)[R::kVec]) __attribute__((always_inline)) {
         uint64_t sum = 0;
 #pragma unroll
         for (int j = 0; j < R::kVec; ++j) sum += row.kept_units(i + j, x[j], border);
         sum = group_combine<kWave>(sum, AddU64());
-        if (lane == 0 && i < row.vocab) runs[i / R::kRun] = sum;
+        if (lane == 0 && i < row.vocab) s.runs[i / R::kRun] = sum;
         total += sum;
     });
     return block_combine(lane == 0 ? total : 0, s, AddU64());
@@ -423,18 +453,18 @@ __device__ __forceinline__ uint64_t draw_target(float r, uint64_t total) {
 
 // The token at which it does, by the sums of the runs.
 template <class T>
-__device__ __forceinline__ void row_draw(const Row<T>& row, Shared& s, const unsigned long long* runs, uint64_t border, uint64_t want,
-                                         int64_t* token) {
+__device__ __forceinline__ void row_draw(const Row<T>& row, Shared& s, uint64_t border, uint64_t want, int64_t* token) {
     using R = Row<T>;
     constexpr int kOwn = kMaxVocab / R::kRun / kThreads;
     const int tid = threadIdx.x, count = (row.vocab + R::kRun - 1) / R::kRun;
     uint64_t own[kOwn], sum = 0;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-        own[j] = tid * kOwn + j < count ? runs[tid * kOwn + j] : 0;
+        own[j] = tid * kOwn + j < count ? s.runs[tid * kOwn + j] : 0;
         sum += own[j];
     }
-    uint64_t before = block_before(sum, s);
+    uint64_t all;
+    uint64_t before = block_before(sum, s, &all);
     if (before < want && before + sum >= want)
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) {
@@ -444,10 +474,12 @@ __device__ __forceinline__ void row_draw(const Row<T>& row, Shared& s, const uns
     __syncthreads();
     if (tid < kWave) {
         const int i = (int)s.bin * R::kRun + tid * R::kVec;
+        float x[R::kVec];
+        row.template neighbours<R::kVec>(i, x);
         uint64_t w[R::kVec], mine = 0;
 #pragma unroll
         for (int j = 0; j < R::kVec; ++j) {
-            w[j] = i + j < row.vocab ? row.kept_units(i + j, row.seen(row.p[i + j]), border) : 0;
+            w[j] = row.kept_units(i + j, x[j], border);
             mine += w[j];
         }
         uint64_t upto = wave_scan(mine) - mine;

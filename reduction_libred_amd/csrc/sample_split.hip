@@ -156,7 +156,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     const int64_t chunk = (int64_t)blockIdx.y * a.chunks + blockIdx.x;
     if (tid == 0) {
         for (int w = 1; w < W; ++w) number = min(number, numbers[w]), count += counts[w];
-        a.heads[chunk] = SampleHead{code_of(top + 0.f, first + (number < kChunk ? number : 0)), count};
+        a.heads[chunk] = SampleHead{Code<T>::of(top + 0.f, first + (number < kChunk ? number : 0)), count};
     }
     if (binned)
         for (int i = tid; i < kGrid / 2; i += kChunkThreads)
@@ -200,18 +200,23 @@ __device__ __forceinline__ SampleHead row_head(const SampleHead* heads, int chun
 }
 
 // A bin's sum in units of the largest weight, whose own relative units are
-// `largest`. In the first bin whole multiples of that are exact, so that a row
-// of equal logits has exact sums.
-__device__ __forceinline__ uint64_t scaled(uint64_t sum, int bin, uint64_t largest, double norm, uint64_t unit, double factor) {
-    if (bin > 0) return (uint64_t)((double)sum * (norm * factor));
-    const uint64_t whole = sum / largest;
-    return whole * unit + (uint64_t)((double)(sum - whole * largest) * norm);
+// `largest`; norm: unit / largest; factor: 2^(-bin / 8). Where all of it are of
+// that weight it is exact, so that a row of equal logits has exact sums.
+__device__ __forceinline__ uint64_t scaled(uint64_t v, double norm, double factor, uint64_t largest, uint64_t unit, bool first) {
+    const uint64_t sum = v & kSumMask;
+    uint64_t of = (uint64_t)((double)sum * (norm * factor));
+    if (first) {
+        const unsigned int n = count_of(v);
+        if (n * largest == sum) of = n * unit;
+    }
+    return of;
 }
 
 // How far the bins of a chunk whose largest logit has this code are below the
 // row's; kGrid and more: none of them counts.
+template <class T>
 __device__ __forceinline__ int chunk_shift(const Place& place, double peak, uint64_t code) {
-    const float x = logit_of(code);
+    const float x = Code<T>::logit(code);
     const double d = x > kNone ? peak - place.floor_of(x) : (double)kGrid;
     return d < (double)kGrid ? (int)d : kGrid;
 }
@@ -226,7 +231,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
     SamplePlan& plan = a.plans[blockIdx.x];
     const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
-    const float top = logit_of(head.first);
+    const float top = Code<T>::logit(head.first);
     int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
     if (tid < 4) s.first[tid] = kGrid;
     if (tid == 0) plan.first = head.first, plan.held = 0, plan.state = state, plan.ranges = 0;
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     row.settle(head.first, set.scale, a.shift);
     const Place place{set.scale * kPerPower};
     const double peak = place.floor_of(top);
-    for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift(place, peak, heads[c].first);
+    for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift<T>(place, peak, heads[c].first);
     __syncthreads();
     // Bin tid of the row.
     uint64_t sum = 0;
@@ -255,7 +260,8 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     }
     const uint64_t largest = Relative().units(place.in_bin(top, peak)) & kSumMask, unit = (uint64_t)row.unit;
     const double norm = row.unit / (double)largest;
-    uint64_t mass = scaled(sum, tid, largest, norm, unit, power2<11>(-(double)tid / kPerPower));
+    uint64_t mass = (uint64_t)((double)sum * (norm * power2<11>(-(double)tid / kPerPower)));
+    if (tid == 0 && count * largest == sum) mass = count * unit;  // all of the largest weight: exact
     const unsigned int own_count = count;
     mass = wave_scan(mass);
     count += dpp_move<0x111, 0xF>(0u, count);
@@ -271,7 +277,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     s.mass[tid] = mass, s.count[tid] = count;
     // The least logit that min-p keeps.
     if (wave == 0 && set.m > 0.0) {
-        const uint32_t cut = first_key((uint32_t)(head.first >> 20), [&](float x) { return row.weight(x) >= set.m; });
+        const uint32_t cut = Code<T>::first_key((uint32_t)(head.first >> 20), [&](float x) { return row.weight(x) >= set.m; });
         if (lane == 0) s.cut = cut;
     }
     __syncthreads();
@@ -300,7 +306,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     uint64_t cut = 0;
     if (state == kRowCut && set.m > 0.0) {
         cut = (uint64_t)s.cut << 20;
-        const double d = peak - place.floor_of(logit_of(cut));
+        const double d = peak - place.floor_of(Code<T>::logit(cut));
         const int mbin = d < (double)kGrid ? (int)d : kGrid;
         if (mbin < low || high < 0) {
             // min-p keeps fewer than the others, or is alone.
@@ -321,7 +327,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     if (wave < 2 * ranges) {
         const int bin = wave == 0 ? high : wave == 1 ? low - 1 : wave == 2 ? kbin : kbin - 1;
         const uint32_t key = (uint32_t)(head.first >> 20);
-        const uint32_t edge = bin < 0 ? key + 1 : first_key(key, [&](float x) { return peak - place.floor_of(x) <= (double)bin; });
+        const uint32_t edge = bin < 0 ? key + 1 : Code<T>::first_key(key, [&](float x) { return peak - place.floor_of(x) <= (double)bin; });
         if (lane == 0) s.edge[wave] = edge;
     }
     __syncthreads();
@@ -329,7 +335,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
         plan.state = state, plan.ranges = ranges;
         plan.use_k = use_k && ranges > 0, plan.use_p = use_p && ranges > 0;
         plan.cut = cut;
-        for (int r = 0; r < ranges; ++r) plan.from[r] = logit_of_key(s.edge[2 * r]), plan.upto[r] = logit_of_key(s.edge[2 * r + 1]);
+        for (int r = 0; r < ranges; ++r) plan.from[r] = Code<T>::logit_of_key(s.edge[2 * r]), plan.upto[r] = Code<T>::logit_of_key(s.edge[2 * r + 1]);
         plan.low = low, plan.high = high;
         const int before = second ? kbin : low;  // bins before the range that has top-k's border
         plan.k_rest = use_k && ranges > 0 ? (uint64_t)set.k - (before > 0 ? s.count[before - 1] : 0) : 0;
@@ -386,34 +392,60 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
     // Few have any: read again rather than chosen among registers.
     while (in) {
         const int n = __ffs(in) - 1, i = first + Loads<T>::number(n);
-        if (to < kList) list[to] = code_of(T::widen(p[i]) + 0.f, i);
+        if (to < kList) list[to] = Code<T>::of(T::widen(p[i]) + 0.f, i);
         ++to, in &= in - 1;
     }
 }
 
-// The code at which the running sum of value(i), in the order of the codes
-// code(i), i < n, that lie from `from` to below `upto`, reaches `want`, the last
-// of them where it does not; ~0 where there are none. Digits of 8 bits from the
-// first that `from` and `upto` do not share, until a wave can take the rest.
-template <class C, class V>
-__device__ __forceinline__ uint64_t list_border(Shared& s, int n, uint64_t from, uint64_t upto, uint64_t want, C code, V value) {
+// The codes of a list: the first kFast of them with their weights in the LDS, the
+// others in memory.
+constexpr int kFast = 2 * kHeld;
+template <class T>
+struct List {
+    const Row<T>& row;
+    Shared& s;
+    const unsigned long long* rest;
+    int n;
+    __device__ __forceinline__ uint64_t units(uint64_t c) const { return row.units(row.weight(Code<T>::logit(c))); }
+    // f(code, weight) of all, weight() what it weighs.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        for (int i = threadIdx.x; i < min(n, kFast); i += kThreads) f(s.list[i], [&]() __attribute__((always_inline)) -> uint64_t { return s.list_own[i]; });
+        if (n <= kFast) return;
+        uint64_t next = rest[min(kFast + (int)threadIdx.x, n - 1)];
+#pragma unroll 1
+        for (int i = kFast + threadIdx.x; i < n; i += kThreads) {
+            const uint64_t c = next;
+            next = rest[min(i + kThreads, n - 1)];
+            f(c, [&]() __attribute__((always_inline)) -> uint64_t { return units(c); });
+        }
+    }
+};
+
+// The code at which the running sum of the list's weights (`ones`: of ones), in
+// the order of the codes, among those from `from` to below `upto`, reaches `want`,
+// the last of them where it does not; ~0 where there are none. Digits of 8 bits
+// from the first that `from` and `upto` do not share, until a wave can take the
+// rest.
+template <class T>
+__device__ __forceinline__ uint64_t list_border(const List<T>& list, uint64_t from, uint64_t upto, uint64_t want, bool ones) {
     if (from >= upto) return ~0ull;
+    Shared& s = list.s;
     const int tid = threadIdx.x, lane = tid % kWave;
     int down = 64 - __builtin_clzll((from ^ (upto - 1)) | 1);
     uint64_t prefix = from >> down;
-    unsigned int in = n;
-    auto inside = [&](uint64_t c) { return c >= from && c < upto && c >> down == prefix; };
+    unsigned int in = list.n;
+    auto inside = [&](uint64_t c) __attribute__((always_inline)) { return c >= from && c < upto && c >> down == prefix; };
     want = want > 0 ? want : 1;
     while (in > kWave && down > 0) {
         const int width = min(down, 8), to = down - width;
         clear_bins(s);
-        for (int i = tid; i < n; i += kThreads) {
-            const uint64_t c = code(i);
-            if (!inside(c)) continue;
+        list.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
+            if (!inside(c)) return;
             const int d = (int)(c >> to) & ((1 << width) - 1);
-            atomicAdd(&s.mass[d], (unsigned long long)value(i));
+            atomicAdd(&s.mass[d], (unsigned long long)(ones ? 1 : weight()));
             atomicAdd(&s.count[d], 1u);
-        }
+        });
         find_bin(s, want, true);
         if (s.bin >= kBins) return ~0ull;
         prefix = prefix << width | s.bin;
@@ -424,22 +456,21 @@ __device__ __forceinline__ uint64_t list_border(Shared& s, int n, uint64_t from,
     __syncthreads();
     if (tid == 0) s.held = 0, s.found = ~0ull;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-        const uint64_t c = code(i);
-        if (inside(c)) {
-            const unsigned int at = atomicAdd(&s.held, 1u);
-            if (at < kWave) s.few[at] = c, s.few_own[at] = value(i);
-        }
-    }
+    list.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
+        if (!inside(c)) return;
+        const unsigned int at = atomicAdd(&s.held, 1u);
+        if (at < kWave) s.few[at] = c, s.few_own[at] = ones ? 1 : weight();
+    });
     __syncthreads();
     if (tid < kWave) {
         const int held = min((int)s.held, kWave);
         const uint64_t c = lane < held ? s.few[lane] : 0, own = lane < held ? s.few_own[lane] : 0;
         uint64_t before = 0, all = 0;
+#pragma unroll 8
         for (int i = 0; i < held; ++i) {
             const uint64_t other = s.few_own[i];
             all += other;
-            if (s.few[i] > c) before += other;
+            before += s.few[i] > c ? other : 0;
         }
         const uint64_t goal = want < all ? want : all;
         if (lane < held && before < goal && before + own >= goal) s.found = c;
@@ -448,125 +479,148 @@ __device__ __forceinline__ uint64_t list_border(Shared& s, int n, uint64_t from,
     return s.found;
 }
 
+// A chunk's sum over the bins before `bin` of the row, from its own, of which
+// this lane of a wave has those kWave apart. -> in lane 0.
+__device__ __forceinline__ uint64_t chunk_sum(const uint64_t (&v)[kGrid / kWave], int shift, int bin, const SamplePlan& plan, uint64_t unit,
+                                              const double* factors) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int u = 0; u < kGrid / kWave; ++u) {
+        const int j = u * kWave + threadIdx.x % kWave + shift;
+        if (j < bin) sum += scaled(v[u], plan.norm, factors[min(j, kGrid - 1)], plan.largest, unit, u == 0 && j == 0);
+    }
+    return group_combine<kWave>(sum, AddU64());
+}
+
 template <class T>
 __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     using R = Row<T>;
+    constexpr int kPer = kGrid / kWave, kFirst = kFast / kThreads;
     __shared__ Shared s;
-    __shared__ unsigned long long runs[kMaxVocab / R::kRun];
+    __shared__ unsigned long long runs[kMaxVocab / kChunk];
     __shared__ double factors[kGrid];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps;
+    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
+    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
+    const unsigned long long* list = a.list + (int64_t)blockIdx.x * kList;
+    // All that does not wait for anything else is asked for at once: the list's
+    // first codes whether there are so many or not, the bins of a chunk a wave.
+    uint64_t codes[kFirst], v[kPer];
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u) codes[u] = list[u * kThreads + tid];
+    const int own_chunk = min(wave, a.chunks - 1);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) v[u] = bins[(int64_t)own_chunk * kGrid + u * kWave + lane];
+    const uint64_t head = heads[own_chunk].first;
     const SamplePlan plan = a.plans[blockIdx.x];
     SamplePlan& to = a.plans[blockIdx.x];
     const float r = a.r ? a.r[at] : 0.f;
     const int state = plan.state;
     const Settings set(a, b);
+    for (int i = tid; i < kGrid; i += kThreads) factors[i] = power2<11>(-(double)i / kPerPower);
     R row(a, b, step);
     const uint64_t first = row.settle(plan.first, set.scale, a.shift);
     if (state == kRowNone || state == kRowOne) {
         if (tid == 0) {
             to.border = state == kRowOne ? first : ~0ull;
             to.share = 1.0;
-            if (a.tokens) a.tokens[at] = state == kRowOne ? token_of(first) : -1;
+            if (a.tokens) a.tokens[at] = state == kRowOne ? R::C::token(first) : -1;
         }
         return;
     }
     if (state == kRowWhole) {
         const uint64_t border = row_border(row, s, set, first);
-        const uint64_t total = row_total(row, s, runs, border);
+        const uint64_t total = row_total(row, s, border);
         if (tid == 0) to.border = border, to.share = row.unit / (double)total;
-        if (a.tokens) row_draw(row, s, runs, border, draw_target(r, total), a.tokens + at);
+        if (a.tokens) row_draw(row, s, border, draw_target(r, total), a.tokens + at);
         return;
     }
+    // The gathered codes: in the LDS, with their weights, as far as there is room.
+    const int held = (int)min(plan.held, (unsigned)kList), ranges = plan.ranges;
+    const List<T> of{row, s, list, held};
+#pragma unroll
+    for (int u = 0; u < kFirst; ++u) {
+        const int i = u * kThreads + tid;
+        if (i < held) s.list[i] = codes[u], s.list_own[i] = of.units(codes[u]);
+    }
+    __syncthreads();
     // The chunks' sums in the bins above those gathered, which are kept whole.
     const Place place{set.scale * kPerPower};
-    const double peak = place.floor_of(row.top_logit), norm = plan.norm;
-    const int bin = plan.ranges > 0 ? plan.low : kGrid;
-    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
-    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
-    for (int i = tid; i < kGrid; i += kThreads) factors[i] = power2<11>(-(double)i / kPerPower);
-    __syncthreads();
-    for (int c = wave; c < a.chunks; c += kWaves) {
-        uint64_t v[kGrid / kWave], sum = 0;
+    const double peak = place.floor_of(row.top_logit);
+    const int bin = ranges > 0 ? plan.low : kGrid;
+    const uint64_t unit = (uint64_t)row.unit;
+    if (wave < a.chunks) {
+        const uint64_t sum = chunk_sum(v, chunk_shift<T>(place, peak, head), bin, plan, unit, factors);
+        if (lane == 0) runs[wave] = sum;
+    }
+    for (int c = wave + kWaves; c < a.chunks; c += kWaves) {
 #pragma unroll
-        for (int u = 0; u < kGrid / kWave; ++u) v[u] = bins[(int64_t)c * kGrid + u * kWave + lane];
-        const int shift = chunk_shift(place, peak, heads[c].first);
-#pragma unroll
-        for (int u = 0; u < kGrid / kWave; ++u) {
-            const int j = u * kWave + lane + shift;
-            if (j < bin) sum += scaled(v[u] & kSumMask, j, plan.largest, norm, (uint64_t)row.unit, factors[min(j, kGrid - 1)]);
-        }
-        sum = group_combine<kWave>(sum, AddU64());
+        for (int u = 0; u < kPer; ++u) v[u] = bins[(int64_t)c * kGrid + u * kWave + lane];
+        const uint64_t sum = chunk_sum(v, chunk_shift<T>(place, peak, heads[c].first), bin, plan, unit, factors);
         if (lane == 0) runs[c] = sum;
     }
-    // The border among the gathered codes: in the LDS, with their weights, as far
-    // as there is room.
-    const unsigned long long* list = a.list + (int64_t)blockIdx.x * kList;
-    const int held = (int)min(plan.held, (unsigned)kList), ranges = plan.ranges;
-    auto units = [&](uint64_t c) { return row.units(row.weight(logit_of(c))); };
-    for (int i = tid; i < min(held, kHeld); i += kThreads) {
-        const uint64_t c = list[i];
-        s.code[i] = c, s.own[i] = units(c);
-    }
-    auto code = [&](int i) -> uint64_t { return i < kHeld ? s.code[i] : list[i]; };
-    auto weight = [&](int i) -> uint64_t { return i < kHeld ? s.own[i] : units(list[i]); };
-    auto key = [](float x) { return code_of(x, kMaxVocab - 1); };  // the last code of a logit
-    __syncthreads();
+    // The border among the gathered codes.
+    auto key = [](float x) { return R::C::of(x, kMaxVocab - 1); };  // the last code of a logit
     uint64_t border = 0;
-    if (plan.use_k) {
-        border = list_border(s, held, key(ranges == 2 ? plan.from[1] : plan.from[0]), key(ranges == 2 ? plan.upto[1] : plan.upto[0]), plan.k_rest, code, [](int) -> uint64_t { return 1; });
-    }
+    const uint64_t from0 = key(plan.from[0]), above = ranges > 0 ? key(plan.upto[0]) : 0;
+    const uint64_t k_from = ranges == 2 ? key(plan.from[1]) : from0, k_upto = ranges == 2 ? key(plan.upto[1]) : above;
+    if (plan.use_k) border = list_border(of, k_from, k_upto, plan.k_rest, true);
     if (plan.use_p) {
         uint64_t all = plan.all;
         if (plan.use_k) {
             // What top-k keeps: bins above the last range, and of that what is above
             // the border.
-            const uint64_t upto = key(ranges == 2 ? plan.upto[1] : plan.upto[0]);
             uint64_t sum = 0;
-            for (int i = tid; i < held; i += kThreads) {
-                const uint64_t c = code(i);
-                if (c >= border && c < upto) sum += weight(i);
-            }
+            of.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
+                if (c >= border && c < k_upto) sum += weight();
+            });
             all = (ranges == 2 ? plan.k_before : plan.p_before) + block_combine(sum, s, AddU64());
         }
-        const uint64_t want = top_p_target(set.p, all), upto = key(plan.upto[0]);
-        uint64_t from = key(plan.from[0]);
-        from = from > border ? from : border;
-        const uint64_t found = want > plan.p_before ? list_border(s, held, from, upto, want - plan.p_before, code, weight) : upto;
-        border = found == ~0ull ? upto : found > border ? found : border;
+        const uint64_t want = top_p_target(set.p, all), from = from0 > border ? from0 : border;
+        const uint64_t found = want > plan.p_before ? list_border(of, from, above, want - plan.p_before, false) : above;
+        border = found == ~0ull ? above : found > border ? found : border;
     }
     border = plan.cut > border ? plan.cut : border;
-    // The sums of the chunks: bins above the list's, and what is kept of the list.
-    const uint64_t above = ranges > 0 ? key(plan.upto[0]) : 0;
+    // What is kept of the list joins its chunks.
     __syncthreads();
     if (ranges > 0)
-        for (int i = tid; i < held; i += kThreads) {
-            const uint64_t c = code(i);
-            if (c >= border && c < above) atomicAdd(&runs[token_of(c) / kChunk], (unsigned long long)weight(i));
-        }
+        of.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
+            // The gathering left a chunk's codes side by side: a wave has mostly those of
+            // one, and adds them up first.
+            const int chunk = R::C::token(c) / kChunk, one = __builtin_amdgcn_readfirstlane(chunk);
+            uint64_t w = c >= border && c < above ? weight() : 0;
+            if (__ballot(true) == ~0ull && __all(chunk == one)) {
+                w = group_combine<kWave>(w, AddU64());
+                if (lane == 0 && w) atomicAdd(&runs[one], (unsigned long long)w);
+            } else if (w) {
+                atomicAdd(&runs[chunk], (unsigned long long)w);
+            }
+        });
     __syncthreads();
-    uint64_t own = tid < a.chunks ? runs[tid] : 0;
-    const uint64_t total = block_combine(own, s, AddU64());
+    const uint64_t own = tid < a.chunks ? runs[tid] : 0;
+    uint64_t total;
+    uint64_t before = block_before(own, s, &total);
     if (tid == 0) to.border = border, to.share = row.unit / (double)total;
     if (!a.tokens) return;
     const uint64_t want = draw_target(r, total);
-    uint64_t before = block_before(own, s);
     if (own > 0 && before < want && before + own >= want) s.bin = tid, s.rest = want - before;
     __syncthreads();
     // The chunk, in which sums by weights may fall short of those by bins.
     constexpr int kEach = kChunk / kThreads;
     const int i0 = (int)s.bin * kChunk + tid * kEach;
     const uint64_t rest = s.rest;
-    uint64_t w[kEach], mine = 0;
+    float x[kEach];
+    row.template neighbours<kEach>(i0, x);
+    uint64_t w[kEach], mine = 0, whole;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        w[j] = i0 + j < a.vocab ? row.kept_units(i0 + j, row.seen(row.p[i0 + j]), border) : 0;
+        w[j] = row.kept_units(i0 + j, x[j], border);
         mine += w[j];
     }
-    before = block_before(mine, s);
-    const uint64_t whole = block_combine(mine, s, AddU64());
+    before = block_before(mine, s, &whole);
     const uint64_t goal = rest < whole ? rest : whole;
-    if (whole == 0 && tid == 0) a.tokens[at] = token_of(first);  // weights that are less than a unit each
+    if (whole == 0 && tid == 0) a.tokens[at] = R::C::token(first);  // weights that are less than a unit each
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         if (before < goal && before + w[j] >= goal) a.tokens[at] = i0 + j;
@@ -594,7 +648,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_probs_kernel(Sample a) {
 #pragma unroll
         for (int j = 0; j < L::kVec; ++j) {
             const float f = row.seen(x.v[u][j]);
-            const bool kept = f != kNone && code_of(f, i0 + j) >= border;
+            const bool kept = f != kNone && Code<T>::of(f, i0 + j) >= border;
             // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
             float w = 0.f;
             if (__any(kept) && kept) w = (float)(power2<8>(((double)f - row.top) * row.scale) * share);
