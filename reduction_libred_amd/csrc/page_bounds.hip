@@ -2,9 +2,8 @@
 //
 //     lo[d] = min over the page's tokens of k[d],  hi[d] = max.
 //
-// A wave has a (page, head): G lanes hold a row, 8 neighbouring elements each
-// (one 16-byte load, or 8 bytes of an 8-bit cache), so 64 / G rows are read at
-// once and joined by lane moves at the end. Minima and maxima are of float32
+// A wave has a (page, head): G lanes hold a row, one 16-byte load each, so 64 / G
+// rows are read at once, four times over, and joined by lane moves at the end. Minima and maxima are of float32
 // values, and rounding them to 16 bits is the same as rounding the elements,
 // since rounding keeps the order.
 #include "decode_common.hpp"
@@ -37,13 +36,13 @@ struct CodeE4M3 {
     }
 };
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// VEC 8: G lanes a row; VEC 1 (any alignment): 64 lanes, up to 4 elements each,
-// 64 apart.
+// VEC elements a lane: those of a 16-byte load, G lanes a row; VEC 1 (any
+// alignment): 64 lanes, up to 4 elements each, 64 apart.
 template <class T, class C, int VEC, int G>
 __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBounds a) {
-    constexpr int N = VEC == 8 ? 8 : 4, R = kWave / G;
+    constexpr int N = VEC == 1 ? 4 : VEC, R = kWave / G;
+    // Groups of R rows on their way at once.
+    constexpr int U = VEC == 1 ? 1 : 4;
     const PagedCache& c = a.cache;
     const int b = blockIdx.y, lane = threadIdx.x % kWave, in = lane % G, row = lane / G;
     const int64_t item = (int64_t)blockIdx.x * kBoundsWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -60,40 +59,47 @@ __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBo
     float lo[N], hi[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) lo[i] = __builtin_inff(), hi[i] = -__builtin_inff();
-    const bool there = VEC == 1 || in * 8 < c.dim;
-    for (int t = row; t < tokens; t += R) {
-        const typename C::bits* r = k + t * c.place_stride;
-        float f[N];
-        if constexpr (VEC == 8) {
-            const int at = there ? in : 0;
-            if constexpr (C::kScaled) {
-                const u32x2 w = reinterpret_cast<const u32x2*>(r)[at];
-                C::widen4(w[0], f);
-                C::widen4(w[1], f + 4);
+    const bool there = VEC == 1 || in * VEC < c.dim;
+    for (int t0 = 0; t0 < tokens; t0 += R * U) {
+        u32x4 x[U];
+        float s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            // Rows behind the last are the last again.
+            const int t = min(t0 + u * R + row, tokens - 1);
+            if constexpr (VEC > 1) x[u] = reinterpret_cast<const u32x4*>(k + t * c.place_stride)[there ? in : 0];
+            s[u] = C::kScaled ? scales[t * c.scale_place_stride] : 1.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[N];
+            if constexpr (VEC == 1) {
+                const typename C::bits* r = k + min(t0 + row, tokens - 1) * c.place_stride;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int d = in + i * kWave < c.dim ? in + i * kWave : 0;
+                    if constexpr (C::kScaled) {
+                        float w[4];
+                        C::widen4(r[d], w);
+                        f[i] = w[0];
+                    } else {
+                        f[i] = T::widen(r[d]);
+                    }
+                }
+            } else if constexpr (C::kScaled) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) C::widen4(x[u][w], f + 4 * w);
             } else {
-                widen_vec<T, 8>(reinterpret_cast<const typename Vec<T, 8>::type*>(r)[at], f);
+                widen_vec<T, 8>(__builtin_bit_cast(typename Vec<T, 8>::type, x[u]), f);
             }
-        } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int d = in + i * kWave < c.dim ? in + i * kWave : 0;
-                if constexpr (C::kScaled) {
-                    float w[4];
-                    C::widen4(r[d], w);
-                    f[i] = w[0];
-                } else {
-                    f[i] = T::widen(r[d]);
-                }
+                float v = f[i];
+                if constexpr (C::kScaled) v *= s[u];
+                // fmin and fmax pass over a NaN.
+                lo[i] = fminf(lo[i], v);
+                hi[i] = fmaxf(hi[i], v);
             }
-        }
-        const float s = C::kScaled ? scales[t * c.scale_place_stride] : 1.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float v = f[i];
-            if constexpr (C::kScaled) v *= s;
-            // fmin and fmax pass over a NaN.
-            lo[i] = fminf(lo[i], v);
-            hi[i] = fmaxf(hi[i], v);
         }
     }
 #pragma unroll
@@ -105,10 +111,11 @@ __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBo
         }
     const int64_t at = page * a.bound_page + h * a.bound_head;
     typename T::bits *to_lo = static_cast<typename T::bits*>(a.lo) + at, *to_hi = static_cast<typename T::bits*>(a.hi) + at;
-    if constexpr (VEC == 8) {
+    if constexpr (VEC > 1) {
+        using V = typename Vec<T, VEC>::type;
         if (row == 0 && there) {
-            reinterpret_cast<typename Vec<T, 8>::type*>(to_lo)[in] = narrow_vec<T, 8>(lo);
-            reinterpret_cast<typename Vec<T, 8>::type*>(to_hi)[in] = narrow_vec<T, 8>(hi);
+            reinterpret_cast<V*>(to_lo)[in] = narrow_vec<T, VEC>(lo);
+            reinterpret_cast<V*>(to_hi)[in] = narrow_vec<T, VEC>(hi);
         }
     } else {
 #pragma unroll
@@ -122,11 +129,11 @@ __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBo
 
 template <class T, class C>
 hipError_t launch_types(int vec, int lanes, const PageBounds& a, dim3 grid, hipStream_t stream) {
-    constexpr int threads = kBoundsWaves * kWave;
+    constexpr int threads = kBoundsWaves * kWave, V = C::kScaled ? 16 : 8;
     if (vec == 1) page_bounds_kernel<T, C, 1, 64><<<grid, threads, 0, stream>>>(a);
-    else if (lanes == 8) page_bounds_kernel<T, C, 8, 8><<<grid, threads, 0, stream>>>(a);
-    else if (lanes == 16) page_bounds_kernel<T, C, 8, 16><<<grid, threads, 0, stream>>>(a);
-    else page_bounds_kernel<T, C, 8, 32><<<grid, threads, 0, stream>>>(a);
+    else if (lanes == 8) page_bounds_kernel<T, C, V, 8><<<grid, threads, 0, stream>>>(a);
+    else if (lanes == 16) page_bounds_kernel<T, C, V, 16><<<grid, threads, 0, stream>>>(a);
+    else if (!C::kScaled) page_bounds_kernel<T, C, V, 32><<<grid, threads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -56,17 +56,27 @@ __device__ __forceinline__ int last_upto(const int* x, int n, int v) {
     return low;
 }
 
-// The sums (a block).
+// The sums (a block). What a sequence brings is asked for at once; with more than
+// kThreads of them it is asked for again for the second sums.
 __device__ __forceinline__ void plan_sums(const PlanSlots& a) {
     __shared__ int64_t lds[kWaves];
     __shared__ int lds32[kWaves], taken;
+    struct Sequence {
+        int count, len, held, done;
+    };
     const int tid = threadIdx.x;
+    auto sequence = [&](int b) {
+        Sequence q = {0, 0, 0, 0};
+        if (b < a.batch) q = Sequence{a.counts[b], a.lens[b], a.held[b], a.done ? a.done[b] : 0};
+        return Sequence{max(q.count, 0), max(q.len, 0), clamped(q.held, a.cols), q.done};
+    };
+    Sequence q = sequence(tid);
     const int height = clamped(a.height[0], a.pages);
     int given = 0;
     if (a.done) {
         for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-            const int b = b0 + tid;
-            const int own = b < a.batch && a.done[b] ? clamped(a.held[b], a.cols) : 0;
+            if (b0 > 0) q = sequence(b0 + tid);
+            const int b = b0 + tid, own = q.done ? q.held : 0;
             int all;
             const int upto = given + block_scan(own, lds32, &all);
             if (b < a.batch) a.back[b] = upto - own;
@@ -78,15 +88,11 @@ __device__ __forceinline__ void plan_sums(const PlanSlots& a) {
     int64_t tokens = 0;
     int wants = 0;
     for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        int n = 0, len = 0, have = 0;
-        if (b < a.batch) {
-            n = max(a.counts[b], 0), len = max(a.lens[b], 0);
-            have = a.done && a.done[b] ? 0 : clamped(a.held[b], a.cols);
-        }
+        if (a.batch > kThreads) q = sequence(b0 + tid);
+        const int b = b0 + tid, n = q.count, have = q.done ? 0 : q.held;
         int64_t all;
         const int64_t upto = tokens + block_scan((int64_t)n, lds, &all);
-        const int64_t need = ((int64_t)len + n + a.places - 1) / a.places;
+        const int64_t need = ((int64_t)q.len + n + a.places - 1) / a.places;
         const bool fits = n > 0 && upto <= a.tokens && need <= a.cols;
         const int want = fits ? max((int)need - have, 0) : 0;
         int all32;
@@ -162,7 +168,12 @@ __global__ __launch_bounds__(kThreads) void plan_one_kernel(PlanSlots a) {
     plan_tokens(a, threadIdx.x, kThreads);
 }
 
-__global__ __launch_bounds__(kThreads) void plan_sums_kernel(PlanSlots a) { plan_sums(a); }
+__global__ __launch_bounds__(kThreads) void plan_sums_kernel(PlanSlots a, int few) {
+    plan_sums(a);
+    if (!few) return;
+    __syncthreads();
+    plan_pages(a, threadIdx.x, kThreads);
+}
 
 constexpr int kWide = 256;
 __global__ __launch_bounds__(kWide) void plan_pages_kernel(PlanSlots a) {
@@ -174,15 +185,14 @@ __global__ __launch_bounds__(kWide) void plan_tokens_kernel(PlanSlots a) {
 
 }  // namespace
 
-// blocks 0: one launch of one block.
-hipError_t launch_plan_slots(const PlanSlots& a, int blocks, hipStream_t stream) {
+hipError_t launch_plan_slots(const PlanSlots& a, int blocks, bool few, hipStream_t stream) {
     if (blocks == 0) {
         plan_one_kernel<<<1, kThreads, 0, stream>>>(a);
         return hipGetLastError();
     }
-    plan_sums_kernel<<<1, kThreads, 0, stream>>>(a);
+    plan_sums_kernel<<<1, kThreads, 0, stream>>>(a, few);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess) plan_pages_kernel<<<blocks, kWide, 0, stream>>>(a), e = hipGetLastError();
+    if (e == hipSuccess && !few) plan_pages_kernel<<<blocks, kWide, 0, stream>>>(a), e = hipGetLastError();
     if (e == hipSuccess) plan_tokens_kernel<<<blocks, kWide, 0, stream>>>(a), e = hipGetLastError();
     return e;
 }

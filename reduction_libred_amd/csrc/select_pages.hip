@@ -8,11 +8,11 @@
 // pages that float32 would leave in doubt are told apart, and the order of the
 // sum does not matter to the choice.
 //
-// First launch: scores. A block has 64 pages of one kv head; G lanes take a
+// First launch: scores. A block has some pages of one kv head; G lanes take a
 // page, 8 neighbouring elements each of both bounds. Second launch: a block a
-// (sequence, kv head) finds the budget-th largest score digit by digit (8 bits
-// at a time, from the first byte in which the scores differ) and lists the pages
-// above it, and of those equal to it the lowest, in order.
+// (sequence, kv head) finds the border among the scores by digits of 8 bits from
+// the first bit in which they differ, until a wave can rank the rest, and lists
+// the pages above it, and of those equal to it the lowest, in order.
 #include "decode_common.hpp"
 #include "serve.hpp"
 
@@ -52,9 +52,9 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     constexpr int N = VEC == 8 ? 8 : 4, R = kWave / G, W = kScoreThreads / kWave;
     __shared__ double up[RED_HEAD_MAX_DIM], down[RED_HEAD_MAX_DIM];
     __shared__ double parts[2][kScoreThreads];
-    const int b = blockIdx.z, h = blockIdx.y, first = blockIdx.x * kSelectPages;
+    const int b = blockIdx.z, h = blockIdx.x, first = blockIdx.y * a.share;  // the heads of the same pages side by side
     const Pages p(a, b);
-    const int last = min(first + kSelectPages, min(p.all, p.tail));
+    const int last = min(first + a.share, min(p.all, p.tail));
     if (p.all <= a.budget || first >= last) return;  // all are selected, or none of these is scored
 
     // U and D: `dims` threads side by side, the rows shared among the rest.
@@ -94,38 +94,68 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     const typename T::bits* lo = static_cast<const typename T::bits*>(a.lo) + h * a.bound_head;
     const typename T::bits* hi = static_cast<const typename T::bits*>(a.hi) + h * a.bound_head;
     uint64_t* keys = a.keys + ((int64_t)b * a.heads + h) * a.most;
-    for (int j0 = first + wave * R; j0 < last; j0 += W * R) {
-        const int j = j0 + lane / G;
-        const int page = j < last ? table[j] : -1;
-        const bool good = page >= 0 && page < a.pages;
-        const int64_t at = good ? page * a.bound_page : 0;
-        double s = 0.0;
-        if (good) {
-            if constexpr (VEC == 8) {
-                float fl[8], fh[8];
-                const int c = there[0] ? in : 0;
-                widen_vec<T, 8>(reinterpret_cast<const typename Vec<T, 8>::type*>(lo + at)[c], fl);
-                widen_vec<T, 8>(reinterpret_cast<const typename Vec<T, 8>::type*>(hi + at)[c], fh);
-                if (there[0])
+    // U pages of each group of lanes are on their way at once.
+    constexpr int U = VEC == 8 ? 4 : 1;
+    using V = typename Vec<T, VEC>::type;
+    for (int j0 = first + wave * (R * U); j0 < last; j0 += W * R * U) {
+        int page[U];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s += pu[i] * (double)fh[i] + pd[i] * (double)fl[i];
+        for (int k = 0; k < U; ++k) page[k] = table[min(j0 + k * R + lane / G, last - 1)];
+        V l[U][VEC == 8 ? 1 : N], m[U][VEC == 8 ? 1 : N];
+        bool good[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            good[k] = page[k] >= 0 && page[k] < a.pages;
+            const int64_t at = good[k] ? page[k] * a.bound_page : 0;
+            if constexpr (VEC == 8) {
+                const int c = there[0] ? in : 0;
+                l[k][0] = reinterpret_cast<const V*>(lo + at)[c];
+                m[k][0] = reinterpret_cast<const V*>(hi + at)[c];
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (there[i]) s += pu[i] * (double)T::widen(hi[at + in + i * kWave]) + pd[i] * (double)T::widen(lo[at + in + i * kWave]);
+                for (int i = 0; i < N; ++i) {
+                    const int e = there[i] ? in + i * kWave : 0;
+                    l[k][i] = lo[at + e], m[k][i] = hi[at + e];
+                }
             }
         }
-        s = group_combine<G>(s, AddF64());
-        if (in == 0 && j < last) keys[j] = good ? ordered(s) : 0;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            float fl[N], fh[N];
+            if constexpr (VEC == 8) {
+                widen_vec<T, 8>(l[k][0], fl);
+                widen_vec<T, 8>(m[k][0], fh);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) fl[i] = T::widen(l[k][i]), fh[i] = T::widen(m[k][i]);
+            }
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (there[i]) s += pu[i] * (double)fh[i] + pd[i] * (double)fl[i];
+            s = group_combine<G>(s, AddF64());
+            const int j = j0 + k * R + lane / G;
+            if (in == 0 && j < last) keys[j] = good[k] ? ordered(s) : 0;
+        }
     }
 }
 
-constexpr int kThreads = 1024, kBits = 8, kBins = 1 << kBits;
+constexpr int kThreads = 512, kOwn = 8, kTile = kThreads * kOwn, kBits = 8, kBins = 1 << kBits;
+
+__device__ __forceinline__ int wave_scan(int v) {
+    v += dpp_move<0x111, 0xF>(0, v);  // shifted by 1, 2, 4 and 8 in rows of 16
+    v += dpp_move<0x112, 0xF>(0, v);
+    v += dpp_move<0x114, 0xF>(0, v);
+    v += dpp_move<0x118, 0xF>(0, v);
+    v += dpp_move<0x142, 0xA>(0, v);  // rows 0 and 2 into 1 and 3
+    v += dpp_move<0x143, 0xC>(0, v);  // the first half into the second
+    return v;
+}
 
 __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
     constexpr int W = kThreads / kWave;
-    __shared__ int bins[kBins], lds[W], digit, rest, held;
-    __shared__ unsigned long long differ;
+    __shared__ int bins[kBins], lds[W], digit, rest, held, few_pages[kWave];
+    __shared__ unsigned long long differ, few[kWave], border;
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const Pages p(a, b);
     int32_t* out = a.selected + ((int64_t)b * a.heads + h) * a.budget;
@@ -135,85 +165,136 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
         for (int i = tid; i < a.budget; i += kThreads) out[i] = i < p.all ? table[i] : -1;
         return;
     }
+    // Pages from `begin` to `end` have scores, all others are selected.
     const uint64_t* keys = a.keys + ((int64_t)b * a.heads + h) * a.most;
-    auto key = [&](int j) { return j < a.first || j >= p.tail ? ~0ull : keys[j]; };
-    // The budget-th largest key: `prefix` above bit `shift`, zeros below; of the
-    // keys that begin like it the largest `need` are selected.
-    const uint64_t one = key(0);
-    if (tid == 0) differ = 0;
+    const int begin = min(a.first, p.all), end = max(min(p.tail, p.all), begin);
+    int need = a.budget - (p.all - (end - begin));
+    // A thread has kOwn pages side by side of every kTile; those of the first
+    // kTile stay in registers, most sequences have no more.
+    uint64_t own[kOwn];
+    int32_t pages[kOwn];
+    auto load = [&](int j0, int i) -> uint64_t {
+        const int j = j0 + tid * kOwn + i;
+        return keys[min(max(j, begin), max(end - 1, begin))];
+    };
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) own[i] = load(0, i), pages[i] = table[min(tid * kOwn + i, p.all - 1)];
+    auto each = [&](auto f) __attribute__((always_inline)) {
+        for (int j0 = 0; j0 < end; j0 += kTile)
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const int j = j0 + tid * kOwn + i;
+                if (j >= begin && j < end) f(j0 == 0 ? own[i] : load(j0, i), j);
+            }
+    };
+    // The need-th largest key: bits from `shift` on are `prefix`.
+    if (tid == 0) differ = 0, held = 0;
+    const uint64_t one = keys[begin];  // of some page: also where none has a score, it is then not used
     __syncthreads();
     uint64_t x = 0;
-    for (int j = tid; j < p.all; j += kThreads) x |= key(j) ^ one;
-    if (x) atomicOr(&differ, x);
+    each([&](uint64_t k, int) { x |= k ^ one; });
+    x = group_combine<kWave>(x, [](uint64_t m, uint64_t n) { return m | n; });
+    if (lane == 0 && x) atomicOr(&differ, (unsigned long long)x);
     __syncthreads();
-    int shift = bytes_of(differ) * 8;                 // bits below this one differ
-    uint64_t prefix = shift < 64 ? one >> shift : 0;  // the keys' bits from `shift` on
-    int need = a.budget;
-    while (shift > 0) {
-        const int down = shift - kBits;
+    int shift = 64 - __builtin_clzll(differ | 1);  // bits below this one differ
+    auto above = [&](uint64_t k) { return shift < 64 ? k >> shift : 0; };
+    uint64_t prefix = above(one);
+    int in = end - begin;
+    while (in > kWave && in > need && shift > 0) {
+        const int width = min(shift, kBits), down = shift - width;
         for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
         __syncthreads();
-        for (int j = tid; j < p.all; j += kThreads) {
-            const uint64_t k = key(j);
-            if (shift == 64 || k >> shift == prefix) atomicAdd(&bins[k >> down & (kBins - 1)], 1);
-        }
+        each([&](uint64_t k, int) {
+            if (above(k) == prefix) atomicAdd(&bins[(int)(k >> down) & ((1 << width) - 1)], 1);
+        });
         __syncthreads();
         if (wave == 0) {
-            // Lane l has bins 255 - 4 l and the 3 below; `upto` counts from the top.
-            int own[4], sum = 0;
+            // Lane l has bins 255 - 4 l and the 3 below; counted from the top.
+            int of[4], sum = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) own[i] = bins[kBins - 1 - 4 * lane - i], sum += own[i];
-            int upto = sum;
-            upto += dpp_move<0x111, 0xF>(0, upto);
-            upto += dpp_move<0x112, 0xF>(0, upto);
-            upto += dpp_move<0x114, 0xF>(0, upto);
-            upto += dpp_move<0x118, 0xF>(0, upto);
-            upto += dpp_move<0x142, 0xA>(0, upto);
-            upto += dpp_move<0x143, 0xC>(0, upto);
+            for (int i = 0; i < 4; ++i) of[i] = bins[kBins - 1 - 4 * lane - i], sum += of[i];
+            const int upto = wave_scan(sum);
             int before = upto - sum;
             if (before < need && upto >= need) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (before < need && before + own[i] >= need) digit = kBins - 1 - 4 * lane - i, rest = need - before, held = own[i];
-                    before += own[i];
+                    if (before < need && before + of[i] >= need) digit = kBins - 1 - 4 * lane - i, rest = need - before, in = of[i];
+                    before += of[i];
                 }
+                held = in;
             }
         }
         __syncthreads();
-        prefix = (shift == 64 ? 0 : prefix << kBits) | (uint64_t)digit;
-        need = rest;
+        prefix = (shift < 64 ? prefix << width : 0) | (uint64_t)digit;
+        need = rest, in = held;
         shift = down;
-        if (held == need) break;  // all that begin like this
     }
-    // Pages above, and the lowest `need` of those that begin like the border.
-    int above = 0, equal = 0;
-    for (int j0 = 0; j0 < p.all; j0 += kThreads) {
-        const int j = j0 + tid;
-        int more = 0, same = 0;
-        if (j < p.all) {
-            const uint64_t k = key(j) >> shift;
-            more = k > prefix, same = k == prefix;
+    // Of the `in` that begin like this all are selected, or one of a wave's worth
+    // is the border, or all are equal: then the lowest `need`.
+    if (in > need && in <= kWave && shift > 0) {
+        __syncthreads();
+        if (tid == 0) held = 0;
+        __syncthreads();
+        each([&](uint64_t k, int j) {
+            if (above(k) != prefix) return;
+            const int at = atomicAdd(&held, 1);
+            if (at < kWave) few[at] = k, few_pages[at] = j;
+        });
+        __syncthreads();
+        if (wave == 0) {
+            const int n = min(held, kWave);
+            const uint64_t mine = lane < n ? few[lane] : 0;
+            const int page = lane < n ? few_pages[lane] : 0;
+            int ahead = 0, larger = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint64_t k = few[i];
+                larger += k > mine, ahead += k > mine || (k == mine && few_pages[i] < page);
+            }
+            if (lane < n && ahead == need - 1) border = mine, rest = need - larger;
         }
-        const uint64_t ms = __ballot(more), ss = __ballot(same), below = (1ull << lane) - 1;
-        const int m = __popcll(ms & below), s = __popcll(ss & below);
         __syncthreads();
-        if (lane == 0) lds[wave] = __popcll(ms) << 16 | __popcll(ss);
+        prefix = border, need = rest, shift = 0;
+    }
+    // The selected ones in order: those without a score, those above the border, and
+    // of those that begin like it the lowest `need`.
+    int more_before = 0, same_before = 0;
+    for (int j0 = 0; j0 < p.all; j0 += kTile) {
+        uint64_t k[kOwn];
+        int more = 0, same = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int j = j0 + tid * kOwn + i;
+            k[i] = j0 == 0 ? own[i] : load(j0, i);
+            const bool scored = j >= begin && j < end;
+            more += j < p.all && (!scored || above(k[i]) > prefix);
+            same += scored && above(k[i]) == prefix;
+        }
+        const int v = more << 16 | same, upto = wave_scan(v);  // at most kTile each
         __syncthreads();
-        int before = 0, all = 0;
+        if (lane == kWave - 1) lds[wave] = upto;
+        __syncthreads();
+        int before = upto - v, all = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            if (w == wave) before = all;
+            if (w == wave) before += all;
             all += lds[w];
         }
-        const int mb = above + (before >> 16) + m, sb = equal + (before & 0xFFFF) + s;
-        if (more || (same && sb < need)) out[mb + min(sb, need)] = table[j];
-        above += all >> 16, equal += all & 0xFFFF;
+        int m = more_before + (before >> 16), s = same_before + (before & 0xFFFF);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int j = j0 + tid * kOwn + i;
+            if (j >= p.all) continue;
+            const bool scored = j >= begin && j < end, is_more = !scored || above(k[i]) > prefix, is_same = scored && above(k[i]) == prefix;
+            if (is_more || (is_same && s < need)) out[m + min(s, need)] = j0 == 0 ? pages[i] : table[j];
+            m += is_more, s += is_same;
+        }
+        more_before += all >> 16, same_before += all & 0xFFFF;
     }
 }
 
 template <class T>
 hipError_t select_pages(int vec, int lanes, const SelectPages& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.most + kSelectPages - 1) / kSelectPages), (unsigned)a.heads, (unsigned)a.batch);
+    const dim3 grid((unsigned)a.heads, (unsigned)((a.most + a.share - 1) / a.share), (unsigned)a.batch);
     if (a.most > a.budget) {
         if (vec == 1) score_kernel<T, 1, 64><<<grid, kScoreThreads, 0, stream>>>(a);
         else if (lanes == 8) score_kernel<T, 8, 8><<<grid, kScoreThreads, 0, stream>>>(a);

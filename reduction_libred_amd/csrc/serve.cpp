@@ -65,8 +65,11 @@ red_status plan_call(const red_plan_slots_args* a, hipStream_t stream) {
     k.batch = (int)B, k.tokens = (int)T, k.cols = (int)C, k.places = (int)a->places, k.pages = (int)a->pages;
     k.have = static_cast<int32_t*>(p);
     k.before = k.have + B + 1, k.back = k.before + B + 1, k.sums = k.back + B + 1, k.fresh = k.sums + 4;
-    const size_t blocks = T <= 8192 ? 0 : (T + 255) / 256 < (size_t)cus * 8 ? (T + 255) / 256 : (size_t)cus * 8;
-    const hipError_t e = launch_plan_slots(k, (int)blocks, stream);
+    const size_t wide = (T + 255) / 256 < (size_t)cus * 8 ? (T + 255) / 256 : (size_t)cus * 8;
+    const int blocks = T <= 4096 ? 0 : (int)wide;
+    // The block of the sums moves the pages too, if they may be few.
+    const bool few = T / a->places + B <= 16384;
+    const hipError_t e = launch_plan_slots(k, blocks, few, stream);
     return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
 }
 
@@ -119,7 +122,8 @@ red_status bounds_call(const red_page_bounds_args* a, hipStream_t stream) {
     const red_status st = host_compute_units(&dev, &cus);
     if (st != RED_OK) return st;
     const size_t cb = type_bytes(c.type);
-    const int vec = D % 8 == 0 && cache_rows_on(c, 8 * cb) && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, c.pages, H) ? 8 : 1;
+    const int load = (int)(16 / cb);  // elements
+    const int vec = D % load == 0 && cache_rows_on(c, 16) && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, c.pages, H) ? load : 1;
     const size_t each = kMaxBlocks / blocks < B ? kMaxBlocks / blocks : B;  // sequences a launch
     for (size_t b = 0; b < B; b += each) {
         k.table = a->table + (int64_t)b * a->table_stride, k.lens = a->lens + b, k.first = a->first ? a->first + b : nullptr;
@@ -164,26 +168,29 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
             return RED_ERR_INVALID_ARG;
     }
     if (meet(a->selected, out, a->selected_lens, B * 4)) return RED_ERR_INVALID_ARG;
-    const size_t blocks = H * ((most + kSelectPages - 1) / kSelectPages);  // a sequence
-    if (blocks > kMaxBlocks) return RED_ERR_INVALID_ARG;
     int dev, cus;
     red_status st = host_compute_units(&dev, &cus);
     if (st != RED_OK) return st;
+    // A block that scores pages first adds up the queries: 64 pages of it, or as
+    // many times that as leave 4 blocks a compute unit.
+    const size_t parts = B * H * ((most + kSelectPages - 1) / kSelectPages) / ((size_t)cus * 4);
+    const size_t share = kSelectPages * (parts < 1 ? 1 : parts);
+    const size_t blocks = H * ((most + share - 1) / share);  // a sequence; few thousand a kv head at most
     SelectPages k = {};
     k.q = a->q, k.q_batch = a->q_batch_stride, k.q_node = a->q_node_stride, k.q_head = a->q_head_stride;
     k.lo = a->lo, k.hi = a->hi, k.bound_page = a->bound_page_stride, k.bound_head = a->bound_head_stride;
     k.table_stride = a->table_stride, k.pages = (int64_t)a->pages;
     k.nodes = (int)N, k.heads = (int)H, k.group = (int)(a->q_heads / H), k.dim = (int)D, k.places = (int)a->places;
     k.budget = (int)a->budget, k.first = (int)a->first, k.last = (int)a->last;
-    k.most = (int)most, k.max_len = (int)tokens;
+    k.most = (int)most, k.share = (int)share, k.max_len = (int)tokens;
     void* p = nullptr;
     if (most > a->budget) {
         st = host_scratch(dev, stream, B * H * most * sizeof(uint64_t), &p);
         if (st != RED_OK) return st;
     }
     const int vec = D % 8 == 0 && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, a->pages, H) ? 8 : 1;
-    // A launch has fewer than 2^32 threads; those that choose come in 1024.
-    const size_t most_blocks = blocks > H * 4 ? kMaxBlocks / blocks : kMaxBlocks / (4 * H);
+    // A launch has fewer than 2^32 threads; those that choose come in 512.
+    const size_t most_blocks = blocks > H * 2 ? kMaxBlocks / blocks : kMaxBlocks / (2 * H);
     const size_t each = most_blocks < B ? most_blocks : B;
     for (size_t b = 0; b < B; b += each) {
         k.batch = (int)(B - b < each ? B - b : each);

@@ -32,7 +32,8 @@ struct PlanSlots {
     int32_t* sums;   // 4: stack's height before, with the pages given back, and behind the step
     int32_t* fresh;  // the pages taken
 };
-hipError_t launch_plan_slots(const PlanSlots& a, int blocks, hipStream_t stream);
+// blocks 0: one launch of one block; else two, or three unless `few` pages are moved.
+hipError_t launch_plan_slots(const PlanSlots& a, int blocks, bool few, hipStream_t stream);
 
 // Bounds of the keys of pages.
 struct PageBounds {
@@ -61,10 +62,11 @@ struct SelectPages {
     uint64_t* keys;  // batch * heads * most: of pages, larger for those that are rather selected
     int64_t pages;
     int batch, nodes, heads, group, dim, places, budget, first, last;
-    int most;  // pages of a sequence
+    int most;   // pages of a sequence
+    int share;  // of them that a block scores
     int max_len;
 };
-constexpr int kSelectPages = 64;  // pages of a block that scores them
+constexpr int kSelectPages = 64;  // a multiple of this many pages has a block that scores them
 hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& a, hipStream_t stream);
 
 // Sampling. A row goes through one block, or is cut into chunks.
