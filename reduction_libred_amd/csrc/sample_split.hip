@@ -466,11 +466,10 @@ __device__ __forceinline__ uint64_t list_border(const List<T>& list, uint64_t fr
         const int held = min((int)s.held, kWave);
         const uint64_t c = lane < held ? s.few[lane] : 0, own = lane < held ? s.few_own[lane] : 0;
         uint64_t before = 0, all = 0;
-#pragma unroll 8
         for (int i = 0; i < held; ++i) {
-            const uint64_t other = s.few_own[i];
+            const uint64_t other = read_lane(own, i);
             all += other;
-            before += s.few[i] > c ? other : 0;
+            before += read_lane(c, i) > c ? other : 0;
         }
         const uint64_t goal = want < all ? want : all;
         if (lane < held && before < goal && before + own >= goal) s.found = c;

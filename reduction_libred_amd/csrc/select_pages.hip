@@ -10,9 +10,10 @@
 //
 // First launch: scores. A block has some pages of one kv head; G lanes take a
 // page, 8 neighbouring elements each of both bounds. Second launch: a block a
-// (sequence, kv head) finds the border among the scores by digits of 8 bits from
-// the first bit in which they differ, until a wave can rank the rest, and lists
-// the pages above it, and of those equal to it the lowest, in order.
+// (sequence, kv head) finds the border among the scores by bins of equal width,
+// in whose one a wave ranks the rest (where many are close or equal, after bins
+// of their bits), and lists the pages above it, and of those equal to it the
+// lowest, in order.
 #include "decode_common.hpp"
 #include "serve.hpp"
 
@@ -47,6 +48,8 @@ __device__ __forceinline__ uint64_t ordered(double s) {
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
+__device__ __forceinline__ double score_of(uint64_t key) { return __builtin_bit_cast(double, key >> 63 ? key & ~(1ull << 63) : ~key); }
+
 template <class T, int VEC, int G>
 __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     constexpr int N = VEC == 8 ? 8 : 4, R = kWave / G, W = kScoreThreads / kWave;
@@ -57,20 +60,65 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     const int last = min(first + a.share, min(p.all, p.tail));
     if (p.all <= a.budget || first >= last) return;  // all are selected, or none of these is scored
 
+    const int tid = threadIdx.x, lane = tid % kWave, in = lane % G, wave = tid / kWave;
+    const int32_t* table = a.table + b * a.table_stride;
+    const typename T::bits* lo = static_cast<const typename T::bits*>(a.lo) + h * a.bound_head;
+    const typename T::bits* hi = static_cast<const typename T::bits*>(a.hi) + h * a.bound_head;
+    uint64_t* keys = a.keys + ((int64_t)b * a.heads + h) * a.most;
+    // U pages of each group of lanes at a time, the next ones on their way: the
+    // first before the queries are added up, page numbers a step earlier still.
+    constexpr int U = VEC == 8 ? 2 : 1, P = VEC == 8 ? 1 : N;
+    constexpr int kStep = W * R * U;
+    using V = typename Vec<T, VEC>::type;
+    struct Bounds {
+        V l[U][P], m[U][P];
+        bool good[U];
+    };
+    int page[U];
+    auto look = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) page[k] = table[min(j0 + (wave * U + k) * R + lane / G, last - 1)];
+    };
+    auto load = [&](Bounds& x) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            x.good[k] = page[k] >= 0 && page[k] < a.pages;
+            const int64_t at = x.good[k] ? page[k] * a.bound_page : 0;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int e = (in + i * kWave) * VEC < a.dim ? in + i * kWave : 0;
+                x.l[k][i] = reinterpret_cast<const V*>(lo + at)[e];
+                x.m[k][i] = reinterpret_cast<const V*>(hi + at)[e];
+            }
+        }
+    };
+    Bounds x;
+    look(first);
+    load(x);
+    look(first + kStep);
+
     // U and D: `dims` threads side by side, the rows shared among the rest.
-    const int tid = threadIdx.x;
     int dims = 1;
     while (dims < a.dim) dims <<= 1;
-    const int d = tid % dims, share = tid / dims, shares = kScoreThreads / dims;
+    const int d = tid % dims, share = tid / dims, shares = kScoreThreads / dims, rows = p.count * a.group;
     double u = 0.0, v = 0.0;
     if (d < a.dim) {
         const typename T::bits* q = static_cast<const typename T::bits*>(a.q) + b * a.q_batch + d;
-        for (int r = share; r < p.count * a.group; r += shares) {
-            const int node = r / a.group, g = r - node * a.group;
-            const double x = (double)T::widen(q[node * a.q_node + (h * a.group + g) * a.q_head]);
-            // A NaN takes part in both.
-            u += x < 0.0 ? 0.0 : x;
-            v += x > 0.0 ? 0.0 : x;
+        for (int r0 = share; r0 < rows; r0 += 8 * shares) {
+            typename T::bits f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = min(r0 + k * shares, rows - 1), node = r / a.group, g = r - node * a.group;
+                f[k] = q[node * a.q_node + (h * a.group + g) * a.q_head];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (r0 + k * shares < rows) {
+                    // A NaN takes part in both.
+                    const double y = (double)T::widen(f[k]);
+                    u += y < 0.0 ? 0.0 : y;
+                    v += y > 0.0 ? 0.0 : y;
+                }
         }
     }
     parts[0][tid] = u, parts[1][tid] = v;
@@ -80,8 +128,6 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
         up[tid] = u, down[tid] = v;
     }
     __syncthreads();
-
-    const int lane = tid % kWave, in = lane % G, wave = tid / kWave;
     double pu[N], pd[N];
     bool there[N];
 #pragma unroll
@@ -90,52 +136,29 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
         there[i] = e < a.dim;
         pu[i] = there[i] ? up[e] : 0.0, pd[i] = there[i] ? down[e] : 0.0;
     }
-    const int32_t* table = a.table + b * a.table_stride;
-    const typename T::bits* lo = static_cast<const typename T::bits*>(a.lo) + h * a.bound_head;
-    const typename T::bits* hi = static_cast<const typename T::bits*>(a.hi) + h * a.bound_head;
-    uint64_t* keys = a.keys + ((int64_t)b * a.heads + h) * a.most;
-    // U pages of each group of lanes are on their way at once.
-    constexpr int U = VEC == 8 ? 4 : 1;
-    using V = typename Vec<T, VEC>::type;
-    for (int j0 = first + wave * (R * U); j0 < last; j0 += W * R * U) {
-        int page[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) page[k] = table[min(j0 + k * R + lane / G, last - 1)];
-        V l[U][VEC == 8 ? 1 : N], m[U][VEC == 8 ? 1 : N];
-        bool good[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            good[k] = page[k] >= 0 && page[k] < a.pages;
-            const int64_t at = good[k] ? page[k] * a.bound_page : 0;
-            if constexpr (VEC == 8) {
-                const int c = there[0] ? in : 0;
-                l[k][0] = reinterpret_cast<const V*>(lo + at)[c];
-                m[k][0] = reinterpret_cast<const V*>(hi + at)[c];
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int e = there[i] ? in + i * kWave : 0;
-                    l[k][i] = lo[at + e], m[k][i] = hi[at + e];
-                }
-            }
+    for (int j0 = first; j0 < last; j0 += kStep) {
+        const Bounds now = x;
+        if (j0 + kStep < last) {
+            load(x);
+            look(j0 + 2 * kStep);
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             float fl[N], fh[N];
             if constexpr (VEC == 8) {
-                widen_vec<T, 8>(l[k][0], fl);
-                widen_vec<T, 8>(m[k][0], fh);
+                widen_vec<T, 8>(now.l[k][0], fl);
+                widen_vec<T, 8>(now.m[k][0], fh);
             } else {
 #pragma unroll
-                for (int i = 0; i < N; ++i) fl[i] = T::widen(l[k][i]), fh[i] = T::widen(m[k][i]);
+                for (int i = 0; i < N; ++i) fl[i] = T::widen(now.l[k][i]), fh[i] = T::widen(now.m[k][i]);
             }
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (there[i]) s += pu[i] * (double)fh[i] + pd[i] * (double)fl[i];
             s = group_combine<G>(s, AddF64());
-            const int j = j0 + k * R + lane / G;
-            if (in == 0 && j < last) keys[j] = good[k] ? ordered(s) : 0;
+            const int j = j0 + (wave * U + k) * R + lane / G;
+            if (in == 0 && j < last) keys[j] = now.good[k] ? ordered(s) : 0;
         }
     }
 }
@@ -155,7 +178,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
     constexpr int W = kThreads / kWave;
     __shared__ int bins[kBins], lds[W], digit, rest, held, few_pages[kWave];
-    __shared__ unsigned long long differ, few[kWave], border;
+    __shared__ unsigned long long least, most, few[kWave], border;
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const Pages p(a, b);
     int32_t* out = a.selected + ((int64_t)b * a.heads + h) * a.budget;
@@ -187,29 +210,27 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
                 if (j >= begin && j < end) f(j0 == 0 ? own[i] : load(j0, i), j);
             }
     };
-    // The need-th largest key: bits from `shift` on are `prefix`.
-    if (tid == 0) differ = 0, held = 0;
-    const uint64_t one = keys[begin];  // of some page: also where none has a score, it is then not used
+    // The need-th largest. First by bins of equal width between the least and the
+    // largest score that are finite, which leaves few in the border's bin.
+    if (tid == 0) least = ~0ull, most = 0, held = 0;
+    for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
     __syncthreads();
-    uint64_t x = 0;
-    each([&](uint64_t k, int) { x |= k ^ one; });
-    x = group_combine<kWave>(x, [](uint64_t m, uint64_t n) { return m | n; });
-    if (lane == 0 && x) atomicOr(&differ, (unsigned long long)x);
+    constexpr uint64_t kLow = 0x0010000000000000ull, kHigh = 0xFFEFFFFFFFFFFFFFull;  // of the finite scores
+    uint64_t low = ~0ull, high = 0;
+    each([&](uint64_t k, int) {
+        if (k >= kLow && k <= kHigh) low = k < low ? k : low, high = k > high ? k : high;
+    });
+    low = group_combine<kWave>(low, [](uint64_t m, uint64_t n) { return m < n ? m : n; });
+    high = group_combine<kWave>(high, [](uint64_t m, uint64_t n) { return m > n ? m : n; });
+    if (lane == 0 && low <= high) atomicMin(&least, (unsigned long long)low), atomicMax(&most, (unsigned long long)high);
     __syncthreads();
-    int shift = 64 - __builtin_clzll(differ | 1);  // bits below this one differ
-    auto above = [&](uint64_t k) { return shift < 64 ? k >> shift : 0; };
-    uint64_t prefix = above(one);
-    int in = end - begin;
-    while (in > kWave && in > need && shift > 0) {
-        const int width = min(shift, kBits), down = shift - width;
-        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
-        __syncthreads();
-        each([&](uint64_t k, int) {
-            if (above(k) == prefix) atomicAdd(&bins[(int)(k >> down) & ((1 << width) - 1)], 1);
-        });
+    const double from = score_of(least), width = score_of(most) - from, per = width > 0.0 && width < __builtin_inf() ? kBins / width : 0.0;
+    auto bin = [&](uint64_t k) { return k < kLow ? 0 : k > kHigh ? kBins - 1 : min(max((int)((score_of(k) - from) * per), 0), kBins - 1); };
+    // The bin (from the last down) in which the need-th is, of those counted.
+    auto find = [&]() {
         __syncthreads();
         if (wave == 0) {
-            // Lane l has bins 255 - 4 l and the 3 below; counted from the top.
+            // Lane l has bins 255 - 4 l and the 3 below.
             int of[4], sum = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) of[i] = bins[kBins - 1 - 4 * lane - i], sum += of[i];
@@ -218,42 +239,62 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
             if (before < need && upto >= need) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (before < need && before + of[i] >= need) digit = kBins - 1 - 4 * lane - i, rest = need - before, in = of[i];
+                    if (before < need && before + of[i] >= need) digit = kBins - 1 - 4 * lane - i, rest = need - before, held = of[i];
                     before += of[i];
                 }
-                held = in;
             }
         }
         __syncthreads();
-        prefix = (shift < 64 ? prefix << width : 0) | (uint64_t)digit;
-        need = rest, in = held;
-        shift = down;
-    }
-    // Of the `in` that begin like this all are selected, or one of a wave's worth
-    // is the border, or all are equal: then the lowest `need`.
-    if (in > need && in <= kWave && shift > 0) {
-        __syncthreads();
-        if (tid == 0) held = 0;
-        __syncthreads();
-        each([&](uint64_t k, int j) {
-            if (above(k) != prefix) return;
-            const int at = atomicAdd(&held, 1);
-            if (at < kWave) few[at] = k, few_pages[at] = j;
-        });
-        __syncthreads();
-        if (wave == 0) {
-            const int n = min(held, kWave);
-            const uint64_t mine = lane < n ? few[lane] : 0;
-            const int page = lane < n ? few_pages[lane] : 0;
-            int ahead = 0, larger = 0;
-            for (int i = 0; i < n; ++i) {
-                const uint64_t k = few[i];
-                larger += k > mine, ahead += k > mine || (k == mine && few_pages[i] < page);
-            }
-            if (lane < n && ahead == need - 1) border = mine, rest = need - larger;
+    };
+    // The border is a key: `prefix`, of which the lowest `need` pages are selected.
+    uint64_t prefix = ~0ull;
+    if (need > 0) {
+        each([&](uint64_t k, int) { atomicAdd(&bins[bin(k)], 1); });
+        find();
+        const int where = digit;
+        need = rest;
+        int in = held, shift = 64;
+        prefix = 0;
+        auto inside = [&](uint64_t k) { return bin(k) == where && (shift == 64 || k >> shift == prefix); };
+        // Then, where many scores are close or equal, by digits of their bits.
+        while (in > kWave && shift > 0) {
+            const int down = shift - kBits;
+            __syncthreads();
+            for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+            __syncthreads();
+            each([&](uint64_t k, int) {
+                if (inside(k)) atomicAdd(&bins[k >> down & (kBins - 1)], 1);
+            });
+            find();
+            prefix = (shift == 64 ? 0 : prefix << kBits) | (uint64_t)digit;
+            need = rest, in = held;
+            shift = down;
         }
-        __syncthreads();
-        prefix = border, need = rest, shift = 0;
+        // A wave ranks what is left.
+        if (shift > 0) {
+            __syncthreads();
+            if (tid == 0) held = 0;
+            __syncthreads();
+            each([&](uint64_t k, int j) {
+                if (!inside(k)) return;
+                const int at = atomicAdd(&held, 1);
+                if (at < kWave) few[at] = k, few_pages[at] = j;
+            });
+            __syncthreads();
+            if (wave == 0) {
+                const int n = min(held, kWave);
+                const uint64_t mine = lane < n ? few[lane] : 0;
+                const int page = lane < n ? few_pages[lane] : 0;
+                int ahead = 0, larger = 0;
+                for (int i = 0; i < n; ++i) {
+                    const uint64_t k = read_lane(mine, i);
+                    larger += k > mine, ahead += k > mine || (k == mine && read_lane(page, i) < page);
+                }
+                if (lane < n && ahead == need - 1) border = mine, rest = need - larger;
+            }
+            __syncthreads();
+            prefix = border, need = rest;
+        }
     }
     // The selected ones in order: those without a score, those above the border, and
     // of those that begin like it the lowest `need`.
@@ -266,8 +307,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
             const int j = j0 + tid * kOwn + i;
             k[i] = j0 == 0 ? own[i] : load(j0, i);
             const bool scored = j >= begin && j < end;
-            more += j < p.all && (!scored || above(k[i]) > prefix);
-            same += scored && above(k[i]) == prefix;
+            more += j < p.all && (!scored || k[i] > prefix);
+            same += scored && k[i] == prefix;
         }
         const int v = more << 16 | same, upto = wave_scan(v);  // at most kTile each
         __syncthreads();
@@ -284,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
         for (int i = 0; i < kOwn; ++i) {
             const int j = j0 + tid * kOwn + i;
             if (j >= p.all) continue;
-            const bool scored = j >= begin && j < end, is_more = !scored || above(k[i]) > prefix, is_same = scored && above(k[i]) == prefix;
+            const bool scored = j >= begin && j < end, is_more = !scored || k[i] > prefix, is_same = scored && k[i] == prefix;
             if (is_more || (is_same && s < need)) out[m + min(s, need)] = j0 == 0 ? pages[i] : table[j];
             m += is_more, s += is_same;
         }
