@@ -15,7 +15,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(Sample a) {
     typename P::bits* probs = a.probs ? static_cast<typename P::bits*>(a.probs) + b * a.probs_batch + step * a.probs_step : nullptr;
 
     uint64_t first = 0;
-    row.each([&](int i, float x) __attribute__((always_inline)) {
+    row.each([&](int i, float x) {
         const uint64_t c = R::C::of(x, i);
         first = c > first ? c : first;
     });
@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void sample_row_kernel(Sample a) {
     if (a.tokens) row_draw(row, s, border, draw_target(a.r[at], total), a.tokens + at);
     if (probs) {
         const double share = row.unit / (double)total;
-        row.tiles([&](int i, const float(&x)[R::kVec]) __attribute__((always_inline)) {
+        row.tiles([&](int i, const float(&x)[R::kVec]) {
             typename P::bits v[R::kVec];
             // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
 #pragma unroll

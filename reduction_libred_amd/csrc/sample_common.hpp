@@ -22,16 +22,17 @@
 namespace libred {
 
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
+static_assert(kWaves == 16, "the waves' sums are joined by the lanes of a row of 16");
 constexpr int kBins = 256;
 constexpr int kHeld = 2048;        // codes that are gathered in the LDS
 constexpr int kMaxVocab = 1 << 20;
 static_assert(2 * kHeld >= kMaxVocab / (kWave * 4), "a run is what a wave reads at a time");
 
 struct AddU64 {
-    __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a + b; }
+    __device__ __forceinline__ uint64_t operator()(uint64_t a, uint64_t b) const { return a + b; }
 };
 struct MaxU64 {
-    __device__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
+    __device__ __forceinline__ uint64_t operator()(uint64_t a, uint64_t b) const { return a > b ? a : b; }
 };
 
 // Codes of logits of type T: the bits that order as they do (the key) above 20 of
@@ -133,10 +134,7 @@ __device__ __forceinline__ uint64_t block_combine(uint64_t v, Shared& s, Op op) 
     __syncthreads();
     if (threadIdx.x % kWave == 0) s.part[threadIdx.x / kWave] = v;
     __syncthreads();
-    v = s.part[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) v = op(v, s.part[w]);
-    return v;
+    return group_combine<kWaves>((uint64_t)s.part[threadIdx.x % kWaves], op);  // in every 16 lanes
 }
 
 // Running sum over the wave's lanes, this one's value included.
@@ -157,12 +155,15 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& s, uint64_t
     __syncthreads();
     if (lane == kWave - 1) s.part[wave] = upto;
     __syncthreads();
-    uint64_t before = 0, whole = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = whole;
-        whole += s.part[w];
-    }
+    // The waves' sums, in each 16 lanes.
+    const uint64_t part = s.part[lane % kWaves];
+    uint64_t sums = part;
+    sums += dpp_move<0x111, 0xF>((uint64_t)0, sums);
+    sums += dpp_move<0x112, 0xF>((uint64_t)0, sums);
+    sums += dpp_move<0x114, 0xF>((uint64_t)0, sums);
+    sums += dpp_move<0x118, 0xF>((uint64_t)0, sums);
+    const int own = __builtin_amdgcn_readfirstlane(wave);
+    const uint64_t before = read_lane(sums, own) - read_lane(part, own), whole = read_lane(sums, kWaves - 1);
     *all = whole;
     return before + upto - v;
 }
@@ -227,7 +228,7 @@ struct Row {
     // f(number, logit) of every token of this thread.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        tiles([&](int i, const float(&x)[kVec]) __attribute__((always_inline)) {
+        tiles([&](int i, const float(&x)[kVec]) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
                 if (i + j < vocab) f(i + j, x[j]);
@@ -305,7 +306,7 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     clear_bins(s);
     uint64_t last = 0;  // of the last bin, which may hold most tokens: not by atomics
     unsigned int lasts = 0;
-    row.each([&](int i, float x) __attribute__((always_inline)) {
+    row.each([&](int i, float x) {
         if (x == kNone || Code<T>::of(x, i) < from) return;
         const uint64_t v = value(x);
         if (v == 0) return;
@@ -334,11 +335,11 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     // Too many to gather: digits of the codes in that bin, over the whole row.
     int shift = Code<T>::kBits;
     uint64_t prefix = 0;
-    auto inside = [&](uint64_t code, float x) __attribute__((always_inline)) { return x != kNone && code >= from && row.bin(x) == bin && code >> shift == prefix; };
+    auto inside = [&](uint64_t code, float x) { return x != kNone && code >= from && row.bin(x) == bin && code >> shift == prefix; };
     while (in > kHeld && shift > 0) {
         const int width = min(shift, 8), down = shift - width;
         clear_bins(s);
-        row.each([&](int i, float x) __attribute__((always_inline)) {
+        row.each([&](int i, float x) {
             const uint64_t code = Code<T>::of(x, i);
             if (!inside(code, x)) return;
             const uint64_t v = value(x);
@@ -356,7 +357,7 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
     __syncthreads();
     if (threadIdx.x == 0) s.held = 0, s.found = 0;
     __syncthreads();
-    row.each([&](int i, float x) __attribute__((always_inline)) {
+    row.each([&](int i, float x) {
         const uint64_t code = Code<T>::of(x, i);
         if (!inside(code, x)) return;
         const uint64_t v = value(x);
@@ -389,7 +390,7 @@ __device__ __forceinline__ uint64_t find_border(const Row<T>& row, Shared& s, ui
 struct Settings {
     double p, m, scale;  // p 2: no top-p
     int64_t k;
-    __device__ Settings(const Sample& a, int b) {
+    __device__ __forceinline__ Settings(const Sample& a, int b) {
         const float t = a.temperature ? a.temperature[b] : 1.f;
         const bool greedy = !(t > 0.f);
         k = a.top_k ? a.top_k[b] : 0;
@@ -410,7 +411,7 @@ __device__ __forceinline__ uint64_t row_border(const Row<T>& row, Shared& s, con
     uint64_t border = 0;
     if (set.k < row.vocab) border = find_border(row, s, 0, [](float) -> uint64_t { return 1; }, [&](uint64_t) { return (uint64_t)set.k; });
     if (set.p < 2.0) {
-        const uint64_t found = find_border(row, s, border, [&](float x) __attribute__((always_inline)) { return row.units(row.weight(x)); },
+        const uint64_t found = find_border(row, s, border, [&](float x) { return row.units(row.weight(x)); },
                                            [&](uint64_t all) { return top_p_target(set.p, all); });
         border = found > border ? found : border;
     }
@@ -435,7 +436,7 @@ __device__ __forceinline__ uint64_t row_total(const Row<T>& row, Shared& s, uint
     const int lane = threadIdx.x % kWave;
     uint64_t total = 0;
     __syncthreads();
-    row.tiles([&](int i, const float(&x)[R::kVec]) __attribute__((always_inline)) {
+    row.tiles([&](int i, const float(&x)[R::kVec]) {
         uint64_t sum = 0;
 #pragma unroll
         for (int j = 0; j < R::kVec; ++j) sum += row.kept_units(i + j, x[j], border);

@@ -26,23 +26,21 @@ namespace libred {
 
 namespace {
 
-constexpr int kChunk = kSampleChunk, kChunkThreads = 256, kOwn = kChunk / kChunkThreads;
+constexpr int kOwn = 32;                  // logits of a thread that holds a part of a row
 constexpr int kGrid = kSampleGrid;       // bins: 64 powers of two
 constexpr double kPerPower = 8.0;        // bins a power of two
-constexpr int kList = kSampleList;
 // A bin adds up doubles 2^52 + v by their bits: v, the relative weight in units
 // of 2^-36, in the low 52, and in the others 0x433 for each, modulo 2^12.
 constexpr uint64_t kSumMask = ((uint64_t)1 << 52) - 1;
 constexpr unsigned int kInverse = 1787;  // of 0x433, modulo 2^12
-static_assert(0x433 * kInverse % 4096 == 1 && kChunk <= 8192, "a bin's number can be told");
+static_assert(0x433 * kInverse % 4096 == 1 && kSampleChunk <= 32768, "a bin's number can be told");
 
-// How many were added: known modulo 2^12, and at most 2^(1/8) times the sum.
+// How many were added: known modulo 2^12, at least the sum and at most 2^(1/8)
+// times it, which leaves one number up to 32768.
 __device__ __forceinline__ unsigned int count_of(uint64_t bin) {
     const uint64_t sum = bin & kSumMask;
-    unsigned int n = (unsigned int)(bin >> 52) * kInverse & 4095u;
-    n += ((uint64_t)n << 36) < sum ? 4096u : 0u;
-    n += ((uint64_t)n << 36) < sum ? 4096u : 0u;
-    return n;
+    const unsigned int least = (unsigned int)((sum + ((1ull << 36) - 1)) >> 36), n = (unsigned int)(bin >> 52) * kInverse & 4095u;
+    return least + ((n - least) & 4095u);
 }
 
 // What a logit is on the grid of a row.
@@ -73,24 +71,24 @@ struct Relative {
     }
 };
 
-template <class T>
+template <class T, int THREADS>
 struct Loads {
     using B = typename T::bits;
-    static constexpr int kVec = 16 / sizeof(B), kCount = kOwn / kVec;
+    static constexpr int kVec = 16 / sizeof(B), kCount = kOwn / kVec, kAll = THREADS * kOwn;
     typedef B Vector __attribute__((ext_vector_type(16 / sizeof(B)), aligned(sizeof(B))));
     Vector v[kCount];
 
-    // The chunk's logits from number `first` on, those of thread tid: kVec
-    // neighbours every kChunkThreads * kVec. Behind the last: -inf. (A chunk
+    // kAll logits from number `first` on, those of thread tid: kVec neighbours
+    // every THREADS * kVec. Behind the last: -inf. (A chunk
     // that the row ends in is read by vectors too, but for the one that the end
     // is in: element by element it took as long as all others, 26 us / 16 of 192
     // rows of 131071.)
     __device__ __forceinline__ Loads(const B* p, int first, int vocab) {
         const int tid = threadIdx.x;
-        auto place = [&](int u) { return first + (u * kChunkThreads + tid) * kVec; };
+        auto place = [&](int u) { return first + (u * THREADS + tid) * kVec; };
 #pragma unroll
         for (int u = 0; u < kCount; ++u) v[u] = *reinterpret_cast<const Vector*>(p + (place(u) + kVec <= vocab ? place(u) : 0));
-        if (first + kChunk > vocab)
+        if (first + kAll > vocab)
 #pragma unroll
             for (int u = 0; u < kCount; ++u)
                 if (place(u) + kVec > vocab)
@@ -98,69 +96,54 @@ struct Loads {
                     for (int j = 0; j < kVec; ++j) v[u][j] = place(u) + j < vocab ? p[place(u) + j] : T::narrow(kNone);
     }
     __device__ __forceinline__ float at(int n) const { return T::widen(v[n / kVec][n % kVec]); }
-    __device__ __forceinline__ static int number(int n) { return (n / kVec * kChunkThreads + threadIdx.x) * kVec + n % kVec; }
+    __device__ __forceinline__ static int number(int n) { return (n / kVec * THREADS + threadIdx.x) * kVec + n % kVec; }
 };
 
-template <class T>
-__global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
-    constexpr int W = kChunkThreads / kWave;
-    __shared__ __align__(16) unsigned long long bins[kGrid + kWave];
-    __shared__ float tops[W];
-    __shared__ int numbers[W], counts[W];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
-    const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
-    const Loads<T> x(p, first, a.vocab);
-    const Settings set(a, b);
-    for (int i = tid; i < kGrid; i += kChunkThreads) bins[i] = 0;  // those behind are not read
-    // The largest logit; a NaN is none.
-    float top = kNone;
+// Every logit of `x` into its bin. Vector instructions bound this, most of them in
+// float64: a logit below the grid goes to a place of its lane's behind it, without
+// a branch. Bins go by their negative numbers, that rise from the first bin down.
+template <class L>
+__device__ __forceinline__ void fill_bins(const L& x, const Place& place, double peak, unsigned long long* bins) {
+    const Relative relative;
+    const double up = -place.scale, end = kGrid - peak;
+    const int aside = (kGrid + (int)threadIdx.x % kWave) * 8, base = (int)peak * 8;
 #pragma unroll
-    for (int n = 0; n < kOwn; ++n) top = fmaxf(top, x.at(n));
-    top = group_combine<kWave>(top, [](float m, float n) { return fmaxf(m, n); });
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    top = tops[0];
+    for (int n = 0; n < kOwn; ++n) {
+        const double v = (double)x.at(n), g = __builtin_ceil(v * up);
+        const int to = g < end ? ((int)g << 3) + base : aside;
+        atomicAdd(reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(bins) + to),
+                  (unsigned long long)relative.units(__builtin_fma(v, place.scale, g)));
+    }
+}
+
+// The probabilities of the logits that a thread holds, which begin at number
+// `first` of the row.
+template <class P, class T, int THREADS>
+__device__ __forceinline__ void write_probs(const Row<T>& row, const Loads<T, THREADS>& x, int first, uint64_t border, double share,
+                                            typename P::bits* probs) {
+    using L = Loads<T, THREADS>;
+    typedef typename P::bits Out __attribute__((ext_vector_type(L::kVec), aligned(sizeof(typename P::bits))));
 #pragma unroll
-    for (int w = 1; w < W; ++w) top = fmaxf(top, tops[w]);
-    // The bins. Vector instructions bound this kernel, most of them in float64: a
-    // logit below the grid goes to a place of its lane's behind it, without a
-    // branch.
-    const Place place{set.scale * kPerPower};
-    const bool binned = set.k != 1 && place.fits(top);
-    int number = kOwn, count = 0;
-    if (binned) {
-        // Bins by their negative numbers, that rise from the first bin down.
-        const Relative relative;
-        const double peak = place.floor_of(top), up = -place.scale, end = kGrid - peak;
-        const int aside = (kGrid + lane) * 8, base = (int)peak * 8;
+    for (int u = 0; u < L::kCount; ++u) {
+        const int i0 = first + L::number(u * L::kVec);
+        Out v;
 #pragma unroll
-        for (int n = 0; n < kOwn; ++n) {
-            const double v = (double)x.at(n), g = __builtin_ceil(v * up);
-            const int to = g < end ? ((int)g << 3) + base : aside;
-            atomicAdd(reinterpret_cast<unsigned long long*>(reinterpret_cast<char*>(bins) + to),
-                      (unsigned long long)relative.units(__builtin_fma(v, place.scale, g)));
+        for (int j = 0; j < L::kVec; ++j) {
+            const float f = row.seen(x.v[u][j]);
+            const bool kept = f != kNone && Code<T>::of(f, i0 + j) >= border;
+            // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
+            float w = 0.f;
+            if (__any(kept) && kept) w = (float)(power2<8>(((double)f - row.top) * row.scale) * share);
+            v[j] = P::narrow(w);
         }
-        if (set.k < a.vocab)
+        if (i0 + L::kVec <= row.vocab) {
+            *reinterpret_cast<Out*>(probs + i0) = v;
+        } else {
 #pragma unroll
-            for (int n = 0; n < kOwn; ++n) count += x.at(n) > kNone ? 1 : 0;
+            for (int j = 0; j < L::kVec; ++j)
+                if (i0 + j < row.vocab) probs[i0 + j] = v[j];
+        }
     }
-    // The largest logit's first number.
-#pragma unroll
-    for (int n = kOwn - 1; n >= 0; --n) number = x.at(n) == top ? n : number;
-    number = number < kOwn ? Loads<T>::number(number) : kChunk;
-    number = group_combine<kWave>(number, [](int m, int n) { return min(m, n); });
-    count = group_combine<kWave>(count, [](int m, int n) { return m + n; });
-    if (lane == 0) numbers[wave] = number, counts[wave] = count;
-    __syncthreads();
-    const int64_t chunk = (int64_t)blockIdx.y * a.chunks + blockIdx.x;
-    if (tid == 0) {
-        for (int w = 1; w < W; ++w) number = min(number, numbers[w]), count += counts[w];
-        a.heads[chunk] = SampleHead{Code<T>::of(top + 0.f, first + (number < kChunk ? number : 0)), count};
-    }
-    if (binned)
-        for (int i = tid; i < kGrid / 2; i += kChunkThreads)
-            reinterpret_cast<u32x4*>(a.bins + chunk * kGrid)[i] = reinterpret_cast<const u32x4*>(bins)[i];
 }
 
 // What the block that finds shares.
@@ -181,24 +164,6 @@ __device__ __forceinline__ int first_bin(Found& s, int at, bool is) {
     return s.first[at];
 }
 
-__device__ __forceinline__ SampleHead row_head(const SampleHead* heads, int chunks, unsigned long long* lds, unsigned int* lds32) {
-    const int waves = blockDim.x / kWave;
-    uint64_t first = 0;
-    int count = 0;
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-        const SampleHead h = heads[c];
-        first = h.first > first ? h.first : first;
-        count += h.count;
-    }
-    first = group_combine<kWave>(first, MaxU64());
-    count = group_combine<kWave>(count, [](int m, int n) { return m + n; });
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = first, lds32[threadIdx.x / kWave] = (unsigned)count;
-    __syncthreads();
-    count = 0, first = 0;
-    for (int w = 0; w < waves; ++w) first = lds[w] > first ? lds[w] : first, count += (int)lds32[w];
-    return SampleHead{first, count};
-}
-
 // A bin's sum in units of the largest weight, whose own relative units are
 // `largest`; norm: unit / largest; factor: 2^(-bin / 8). Where all of it are of
 // that weight it is exact, so that a row of equal logits has exact sums.
@@ -212,52 +177,16 @@ __device__ __forceinline__ uint64_t scaled(uint64_t v, double norm, double facto
     return of;
 }
 
-// How far the bins of a chunk whose largest logit has this code are below the
-// row's; kGrid and more: none of them counts.
+// Where the borders of a row are: its ranges of logits to be gathered, `most_held`
+// of them at most, and what the draw needs to know of the bins, in `plan`. `sum`
+// and `count` are those of bin tid.
 template <class T>
-__device__ __forceinline__ int chunk_shift(const Place& place, double peak, uint64_t code) {
-    const float x = Code<T>::logit(code);
-    const double d = x > kNone ? peak - place.floor_of(x) : (double)kGrid;
-    return d < (double)kGrid ? (int)d : kGrid;
-}
-
-template <class T>
-__global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
-    __shared__ Found s;
-    __shared__ int shifts[kMaxVocab / kChunk];
+__device__ __forceinline__ void find_ranges(const Row<T>& row, const Settings& set, const SampleHead& head, uint64_t sum, unsigned int count,
+                                            unsigned int most_held, Found& s, SamplePlan& plan) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps;
-    const Settings set(a, b);
-    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
-    SamplePlan& plan = a.plans[blockIdx.x];
-    const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
-    const float top = Code<T>::logit(head.first);
-    int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
-    if (tid < 4) s.first[tid] = kGrid;
-    if (tid == 0) plan.first = head.first, plan.held = 0, plan.state = state, plan.ranges = 0;
-    if (state != kRowCut) return;
-
-    Row<T> row(a, b, step);
-    row.settle(head.first, set.scale, a.shift);
     const Place place{set.scale * kPerPower};
+    const float top = row.top_logit;
     const double peak = place.floor_of(top);
-    for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift<T>(place, peak, heads[c].first);
-    __syncthreads();
-    // Bin tid of the row.
-    uint64_t sum = 0;
-    unsigned int count = 0;
-    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
-    for (int c0 = 0; c0 < a.chunks; c0 += 8) {
-        uint64_t v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int c = min(c0 + u, a.chunks - 1), j = tid - shifts[c];
-            v[u] = bins[(int64_t)c * kGrid + max(j, 0)];
-            if (j < 0 || c0 + u >= a.chunks) v[u] = 0;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) sum += v[u] & kSumMask, count += count_of(v[u]);
-    }
     const uint64_t largest = Relative().units(place.in_bin(top, peak)) & kSumMask, unit = (uint64_t)row.unit;
     const double norm = row.unit / (double)largest;
     uint64_t mass = (uint64_t)((double)sum * (norm * power2<11>(-(double)tid / kPerPower)));
@@ -282,6 +211,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     }
     __syncthreads();
     const uint64_t all = s.mass[kGrid - 1];
+    int state = kRowCut;
     const bool has_k = set.k < head.count, has_p = set.p < 2.0;
     // Bins in which the borders lie: top-k's; from `low` to `high` those in which
     // top-p's may (its target is known to 2^-30, or as far as the bin of top-k's
@@ -320,7 +250,7 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     if (ranges > 0) {
         unsigned int n = s.count[high] - (low > 0 ? s.count[low - 1] : 0);
         if (second) n += s.count[kbin] - s.count[kbin - 1];
-        if (n > kList) state = kRowWhole, ranges = 0;
+        if (n > most_held) state = kRowWhole, ranges = 0;
     }
     // Their logits: from the first of the last bin to below the first of the bin
     // before the first.
@@ -346,6 +276,276 @@ __global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
     }
 }
 
+// The least code of a logit.
+template <class T>
+__device__ __forceinline__ uint64_t first_code(float x) {
+    return Code<T>::of(x, kMaxVocab - 1);
+}
+
+// The codes of a list: the first kFast of them with their weights in the LDS, the
+// others in memory.
+constexpr int kFast = 2 * kHeld;
+template <class T>
+struct List {
+    const Row<T>& row;
+    Shared& s;
+    const unsigned long long* rest;
+    int n;
+    __device__ __forceinline__ uint64_t units(uint64_t c) const { return row.units(row.weight(Code<T>::logit(c))); }
+    // f(code, weight) of all, weight() what it weighs.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+        for (int i = threadIdx.x; i < min(n, kFast); i += kThreads) f(s.list[i], [&]() -> uint64_t { return s.list_own[i]; });
+        if (n <= kFast) return;
+        uint64_t next = rest[min(kFast + (int)threadIdx.x, n - 1)];
+#pragma unroll 1
+        for (int i = kFast + threadIdx.x; i < n; i += kThreads) {
+            const uint64_t c = next;
+            next = rest[min(i + kThreads, n - 1)];
+            f(c, [&]() -> uint64_t { return units(c); });
+        }
+    }
+};
+
+// Of up to kWave codes and their weights, one a lane (0: none): the code at which
+// the sum of the weights, in the order of the codes, reaches `want`, the last where
+// it does not; ~0 for none. By a wave; -> in all lanes.
+__device__ __forceinline__ uint64_t rank_border(uint64_t c, uint64_t own, int n, uint64_t want) {
+    uint64_t before = 0, all = 0;
+    for (int i = 0; i < n; ++i) {
+        const uint64_t other = read_lane(own, i);
+        all += other;
+        before += read_lane(c, i) > c ? other : 0;
+    }
+    want = want > 0 ? want : 1;
+    const uint64_t goal = want < all ? want : all, is = __ballot(own > 0 && before < goal && before + own >= goal);
+    return is ? read_lane(c, __ffsll((unsigned long long)is) - 1) : ~0ull;
+}
+
+// The code at which the running sum of the list's weights (`ones`: of ones), in
+// the order of the codes, among those from `from` to below `upto`, reaches `want`,
+// the last of them where it does not; ~0 where there are none. Digits of 8 bits
+// from the first that `from` and `upto` do not share, until a wave can take the
+// rest. By the block.
+template <class T>
+__device__ __forceinline__ uint64_t list_border(const List<T>& list, uint64_t from, uint64_t upto, uint64_t want, bool ones) {
+    if (from >= upto) return ~0ull;
+    Shared& s = list.s;
+    const int tid = threadIdx.x, lane = tid % kWave;
+    int down = 64 - __builtin_clzll((from ^ (upto - 1)) | 1);
+    uint64_t prefix = from >> down;
+    unsigned int in = list.n;
+    auto inside = [&](uint64_t c) { return c >= from && c < upto && c >> down == prefix; };
+    want = want > 0 ? want : 1;
+    while (in > kWave && down > 0) {
+        const int width = min(down, 8), to = down - width;
+        clear_bins(s);
+        list.each([&](uint64_t c, auto weight) {
+            if (!inside(c)) return;
+            const int d = (int)(c >> to) & ((1 << width) - 1);
+            atomicAdd(&s.mass[d], (unsigned long long)(ones ? 1 : weight()));
+            atomicAdd(&s.count[d], 1u);
+        });
+        find_bin(s, want, true);
+        if (s.bin >= kBins) return ~0ull;
+        prefix = prefix << width | s.bin;
+        want = s.rest, in = s.count[s.bin];
+        down = to;
+    }
+    if (down == 0) return prefix;
+    __syncthreads();
+    if (tid == 0) s.held = 0;
+    __syncthreads();
+    list.each([&](uint64_t c, auto weight) {
+        if (!inside(c)) return;
+        const unsigned int at = atomicAdd(&s.held, 1u);
+        if (at < kWave) s.few[at] = c, s.few_own[at] = ones ? 1 : weight();
+    });
+    __syncthreads();
+    if (tid < kWave) {
+        const int held = min((int)s.held, kWave);
+        const uint64_t found = rank_border(lane < held ? s.few[lane] : 0, lane < held ? s.few_own[lane] : 0, held, want);
+        if (lane == 0) s.found = found;
+    }
+    __syncthreads();
+    return s.found;
+}
+
+// The border of a row from its plan: search(from, upto, want, ones) is the code at
+// which a sum is reached, kept_sum(from, upto) the weights of the list's codes from
+// `from` to below `upto`. above: the first code above those gathered for it.
+template <class T, class F, class G>
+__device__ __forceinline__ uint64_t border_of(const Settings& set, const SamplePlan& plan, uint64_t above, F search, G kept_sum) {
+    const uint64_t from0 = first_code<T>(plan.from[0]);
+    const bool two = plan.ranges == 2;
+    const uint64_t k_from = two ? first_code<T>(plan.from[1]) : from0, k_upto = two ? first_code<T>(plan.upto[1]) : above;
+    uint64_t border = 0;
+    if (plan.use_k) border = search(k_from, k_upto, plan.k_rest, true);
+    if (plan.use_p) {
+        // What top-k keeps: bins above the last range, and of that what is above the
+        // border.
+        const uint64_t all = plan.use_k ? (two ? plan.k_before : plan.p_before) + kept_sum(border, k_upto) : plan.all;
+        const uint64_t want = top_p_target(set.p, all), from = from0 > border ? from0 : border;
+        const uint64_t found = want > plan.p_before ? search(from, above, want - plan.p_before, false) : above;
+        border = found == ~0ull ? above : found > border ? found : border;
+    }
+    return plan.cut > border ? plan.cut : border;
+}
+
+// That border; what a wave can rank, one wave does for the block: with 16 at it each
+// instruction takes four times as long.
+template <class T>
+__device__ __forceinline__ uint64_t cut_border(const List<T>& of, const Settings& set, const SamplePlan& plan, uint64_t above) {
+    Shared& s = of.s;
+    const int lane = threadIdx.x % kWave;
+    if (of.n <= kWave) {
+        if (threadIdx.x < kWave) {
+            const uint64_t c = lane < of.n ? s.list[lane] : 0, w = lane < of.n ? s.list_own[lane] : 0;
+            auto is = [&](uint64_t from, uint64_t upto) { return lane < of.n && c >= from && c < upto; };
+            const uint64_t border = border_of<T>(
+                set, plan, above,
+                [&](uint64_t from, uint64_t upto, uint64_t want, bool ones) {
+                    return rank_border(is(from, upto) ? c : 0, is(from, upto) ? ones ? 1 : w : 0, of.n, want);
+                },
+                [&](uint64_t from, uint64_t upto) { return group_combine<kWave>(is(from, upto) ? w : 0, AddU64()); });
+            if (lane == 0) s.found = border;
+        }
+        __syncthreads();
+        return s.found;
+    }
+    return border_of<T>(
+        set, plan, above, [&](uint64_t from, uint64_t upto, uint64_t want, bool ones) { return list_border(of, from, upto, want, ones); },
+        [&](uint64_t from, uint64_t upto) {
+            uint64_t sum = 0;
+            of.each([&](uint64_t c, auto weight) {
+                if (c >= from && c < upto) sum += weight();
+            });
+            return block_combine(sum, s, AddU64());
+        });
+}
+
+constexpr int kChunk = kSampleChunk, kChunkThreads = kChunk / kOwn;
+static_assert(kChunkThreads == 256, "a block of four waves");
+constexpr int kList = kSampleList;
+template <class T>
+using Chunk = Loads<T, kChunkThreads>;
+
+template <class T>
+__global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
+    constexpr int W = kChunkThreads / kWave;
+    __shared__ __align__(16) unsigned long long bins[kGrid + kWave];
+    __shared__ float tops[W];
+    __shared__ int numbers[W], counts[W];
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
+    const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
+    const Chunk<T> x(p, first, a.vocab);
+    const Settings set(a, b);
+    for (int i = tid; i < kGrid; i += kChunkThreads) bins[i] = 0;  // those behind are not read
+    // The largest logit; a NaN is none.
+    float top = kNone;
+#pragma unroll
+    for (int n = 0; n < kOwn; ++n) top = fmaxf(top, x.at(n));
+    top = group_combine<kWave>(top, [](float m, float n) { return fmaxf(m, n); });
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = tops[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = fmaxf(top, tops[w]);
+    const Place place{set.scale * kPerPower};
+    const bool binned = set.k != 1 && place.fits(top);
+    int number = kOwn, count = 0;
+    if (binned) {
+        fill_bins(x, place, place.floor_of(top), bins);
+        if (set.k < a.vocab)
+#pragma unroll
+            for (int n = 0; n < kOwn; ++n) count += x.at(n) > kNone ? 1 : 0;
+    }
+    // The largest logit's first number.
+#pragma unroll
+    for (int n = kOwn - 1; n >= 0; --n) number = x.at(n) == top ? n : number;
+    number = number < kOwn ? Chunk<T>::number(number) : kChunk;
+    number = group_combine<kWave>(number, [](int m, int n) { return min(m, n); });
+    count = group_combine<kWave>(count, [](int m, int n) { return m + n; });
+    if (lane == 0) numbers[wave] = number, counts[wave] = count;
+    __syncthreads();
+    const int64_t chunk = (int64_t)blockIdx.y * a.chunks + blockIdx.x;
+    if (tid == 0) {
+        for (int w = 1; w < W; ++w) number = min(number, numbers[w]), count += counts[w];
+        a.heads[chunk] = SampleHead{Code<T>::of(top + 0.f, first + (number < kChunk ? number : 0)), count};
+    }
+    if (binned)
+        for (int i = tid; i < kGrid / 2; i += kChunkThreads)
+            reinterpret_cast<u32x4*>(a.bins + chunk * kGrid)[i] = reinterpret_cast<const u32x4*>(bins)[i];
+}
+
+__device__ __forceinline__ SampleHead row_head(const SampleHead* heads, int chunks, unsigned long long* lds, unsigned int* lds32) {
+    const int waves = blockDim.x / kWave;
+    uint64_t first = 0;
+    int count = 0;
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+        const SampleHead h = heads[c];
+        first = h.first > first ? h.first : first;
+        count += h.count;
+    }
+    first = group_combine<kWave>(first, MaxU64());
+    count = group_combine<kWave>(count, [](int m, int n) { return m + n; });
+    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = first, lds32[threadIdx.x / kWave] = (unsigned)count;
+    __syncthreads();
+    count = 0, first = 0;
+    for (int w = 0; w < waves; ++w) first = lds[w] > first ? lds[w] : first, count += (int)lds32[w];
+    return SampleHead{first, count};
+}
+
+// How far the bins of a chunk whose largest logit has this code are below the
+// row's; kGrid and more: none of them counts.
+template <class T>
+__device__ __forceinline__ int chunk_shift(const Place& place, double peak, uint64_t code) {
+    const float x = Code<T>::logit(code);
+    const double d = x > kNone ? peak - place.floor_of(x) : (double)kGrid;
+    return d < (double)kGrid ? (int)d : kGrid;
+}
+
+template <class T>
+__global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
+    __shared__ Found s;
+    __shared__ int shifts[kMaxVocab / kChunk];
+    const int tid = threadIdx.x;
+    const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps;
+    const Settings set(a, b);
+    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
+    SamplePlan& plan = a.plans[blockIdx.x];
+    const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
+    const float top = Code<T>::logit(head.first);
+    int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
+    if (tid < 4) s.first[tid] = kGrid;
+    if (tid == 0) plan.first = head.first, plan.held = 0, plan.state = state, plan.ranges = 0;
+    if (state != kRowCut) return;
+
+    Row<T> row(a, b, step);
+    row.settle(head.first, set.scale, a.shift);
+    const Place place{set.scale * kPerPower};
+    const double peak = place.floor_of(top);
+    for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift<T>(place, peak, heads[c].first);
+    __syncthreads();
+    // Bin tid of the row.
+    uint64_t sum = 0;
+    unsigned int count = 0;
+    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
+    for (int c0 = 0; c0 < a.chunks; c0 += 8) {
+        uint64_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int c = min(c0 + u, a.chunks - 1), j = tid - shifts[c];
+            v[u] = bins[(int64_t)c * kGrid + max(j, 0)];
+            if (j < 0 || c0 + u >= a.chunks) v[u] = 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += v[u] & kSumMask, count += count_of(v[u]);
+    }
+    find_ranges(row, set, head, sum, count, kList, s, plan);
+}
+
 template <class T>
 __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) {
     constexpr int W = kChunkThreads / kWave;
@@ -354,7 +554,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
     const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
-    const Loads<T> x(p, first, a.vocab);  // before the plan is known: one trip
+    const Chunk<T> x(p, first, a.vocab);  // before the plan is known: one trip
     const int ranges = plan.ranges;
     if (ranges == 0) return;
     uint32_t in = 0;
@@ -391,91 +591,10 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
     unsigned long long* list = a.list + (int64_t)blockIdx.y * kList;
     // Few have any: read again rather than chosen among registers.
     while (in) {
-        const int n = __ffs(in) - 1, i = first + Loads<T>::number(n);
+        const int n = __ffs(in) - 1, i = first + Chunk<T>::number(n);
         if (to < kList) list[to] = Code<T>::of(T::widen(p[i]) + 0.f, i);
         ++to, in &= in - 1;
     }
-}
-
-// The codes of a list: the first kFast of them with their weights in the LDS, the
-// others in memory.
-constexpr int kFast = 2 * kHeld;
-template <class T>
-struct List {
-    const Row<T>& row;
-    Shared& s;
-    const unsigned long long* rest;
-    int n;
-    __device__ __forceinline__ uint64_t units(uint64_t c) const { return row.units(row.weight(Code<T>::logit(c))); }
-    // f(code, weight) of all, weight() what it weighs.
-    template <class F>
-    __device__ __forceinline__ void each(F f) const {
-        for (int i = threadIdx.x; i < min(n, kFast); i += kThreads) f(s.list[i], [&]() __attribute__((always_inline)) -> uint64_t { return s.list_own[i]; });
-        if (n <= kFast) return;
-        uint64_t next = rest[min(kFast + (int)threadIdx.x, n - 1)];
-#pragma unroll 1
-        for (int i = kFast + threadIdx.x; i < n; i += kThreads) {
-            const uint64_t c = next;
-            next = rest[min(i + kThreads, n - 1)];
-            f(c, [&]() __attribute__((always_inline)) -> uint64_t { return units(c); });
-        }
-    }
-};
-
-// The code at which the running sum of the list's weights (`ones`: of ones), in
-// the order of the codes, among those from `from` to below `upto`, reaches `want`,
-// the last of them where it does not; ~0 where there are none. Digits of 8 bits
-// from the first that `from` and `upto` do not share, until a wave can take the
-// rest.
-template <class T>
-__device__ __forceinline__ uint64_t list_border(const List<T>& list, uint64_t from, uint64_t upto, uint64_t want, bool ones) {
-    if (from >= upto) return ~0ull;
-    Shared& s = list.s;
-    const int tid = threadIdx.x, lane = tid % kWave;
-    int down = 64 - __builtin_clzll((from ^ (upto - 1)) | 1);
-    uint64_t prefix = from >> down;
-    unsigned int in = list.n;
-    auto inside = [&](uint64_t c) __attribute__((always_inline)) { return c >= from && c < upto && c >> down == prefix; };
-    want = want > 0 ? want : 1;
-    while (in > kWave && down > 0) {
-        const int width = min(down, 8), to = down - width;
-        clear_bins(s);
-        list.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
-            if (!inside(c)) return;
-            const int d = (int)(c >> to) & ((1 << width) - 1);
-            atomicAdd(&s.mass[d], (unsigned long long)(ones ? 1 : weight()));
-            atomicAdd(&s.count[d], 1u);
-        });
-        find_bin(s, want, true);
-        if (s.bin >= kBins) return ~0ull;
-        prefix = prefix << width | s.bin;
-        want = s.rest, in = s.count[s.bin];
-        down = to;
-    }
-    if (down == 0) return prefix;
-    __syncthreads();
-    if (tid == 0) s.held = 0, s.found = ~0ull;
-    __syncthreads();
-    list.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
-        if (!inside(c)) return;
-        const unsigned int at = atomicAdd(&s.held, 1u);
-        if (at < kWave) s.few[at] = c, s.few_own[at] = ones ? 1 : weight();
-    });
-    __syncthreads();
-    if (tid < kWave) {
-        const int held = min((int)s.held, kWave);
-        const uint64_t c = lane < held ? s.few[lane] : 0, own = lane < held ? s.few_own[lane] : 0;
-        uint64_t before = 0, all = 0;
-        for (int i = 0; i < held; ++i) {
-            const uint64_t other = read_lane(own, i);
-            all += other;
-            before += read_lane(c, i) > c ? other : 0;
-        }
-        const uint64_t goal = want < all ? want : all;
-        if (lane < held && before < goal && before + own >= goal) s.found = c;
-    }
-    __syncthreads();
-    return s.found;
 }
 
 // A chunk's sum over the bins before `bin` of the row, from its own, of which
@@ -560,31 +679,12 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
         if (lane == 0) runs[c] = sum;
     }
     // The border among the gathered codes.
-    auto key = [](float x) { return R::C::of(x, kMaxVocab - 1); };  // the last code of a logit
-    uint64_t border = 0;
-    const uint64_t from0 = key(plan.from[0]), above = ranges > 0 ? key(plan.upto[0]) : 0;
-    const uint64_t k_from = ranges == 2 ? key(plan.from[1]) : from0, k_upto = ranges == 2 ? key(plan.upto[1]) : above;
-    if (plan.use_k) border = list_border(of, k_from, k_upto, plan.k_rest, true);
-    if (plan.use_p) {
-        uint64_t all = plan.all;
-        if (plan.use_k) {
-            // What top-k keeps: bins above the last range, and of that what is above
-            // the border.
-            uint64_t sum = 0;
-            of.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
-                if (c >= border && c < k_upto) sum += weight();
-            });
-            all = (ranges == 2 ? plan.k_before : plan.p_before) + block_combine(sum, s, AddU64());
-        }
-        const uint64_t want = top_p_target(set.p, all), from = from0 > border ? from0 : border;
-        const uint64_t found = want > plan.p_before ? list_border(of, from, above, want - plan.p_before, false) : above;
-        border = found == ~0ull ? above : found > border ? found : border;
-    }
-    border = plan.cut > border ? plan.cut : border;
+    const uint64_t above = ranges > 0 ? first_code<T>(plan.upto[0]) : 0;
+    const uint64_t border = cut_border(of, set, plan, above);
     // What is kept of the list joins its chunks.
     __syncthreads();
     if (ranges > 0)
-        of.each([&](uint64_t c, auto weight) __attribute__((always_inline)) {
+        of.each([&](uint64_t c, auto weight) {
             // The gathering left a chunk's codes side by side: a wave has mostly those of
             // one, and adds them up first.
             const int chunk = R::C::token(c) / kChunk, one = __builtin_amdgcn_readfirstlane(chunk);
@@ -629,7 +729,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
 
 template <class T, class P>
 __global__ __launch_bounds__(kChunkThreads) void sample_probs_kernel(Sample a) {
-    using L = Loads<T>;
+    using L = Chunk<T>;
     const SamplePlan& plan = a.plans[blockIdx.y];
     const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
     const Settings set(a, b);
@@ -639,28 +739,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_probs_kernel(Sample a) {
     const uint64_t border = plan.border;
     const double share = plan.share;
     row.settle(plan.first, set.scale, a.shift);
-    typedef typename P::bits Out __attribute__((ext_vector_type(L::kVec), aligned(sizeof(typename P::bits))));
-#pragma unroll
-    for (int u = 0; u < L::kCount; ++u) {
-        const int i0 = first + L::number(u * L::kVec);
-        Out v;
-#pragma unroll
-        for (int j = 0; j < L::kVec; ++j) {
-            const float f = row.seen(x.v[u][j]);
-            const bool kept = f != kNone && Code<T>::of(f, i0 + j) >= border;
-            // A second rounding, from float32, moves a 16-bit one by 2^-16 of its step at most.
-            float w = 0.f;
-            if (__any(kept) && kept) w = (float)(power2<8>(((double)f - row.top) * row.scale) * share);
-            v[j] = P::narrow(w);
-        }
-        if (i0 + L::kVec <= a.vocab) {
-            *reinterpret_cast<Out*>(probs + i0) = v;
-        } else {
-#pragma unroll
-            for (int j = 0; j < L::kVec; ++j)
-                if (i0 + j < a.vocab) probs[i0 + j] = v[j];
-        }
-    }
+    write_probs<P>(row, x, first, border, share, probs);
 }
 
 template <class T>

@@ -104,15 +104,16 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     double u = 0.0, v = 0.0;
     if (d < a.dim) {
         const typename T::bits* q = static_cast<const typename T::bits*>(a.q) + b * a.q_batch + d;
-        for (int r0 = share; r0 < rows; r0 += 8 * shares) {
-            typename T::bits f[8];
+        constexpr int K = 4;
+        for (int r0 = share; r0 < rows; r0 += K * shares) {
+            typename T::bits f[K];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = min(r0 + k * shares, rows - 1), node = r / a.group, g = r - node * a.group;
-                f[k] = q[node * a.q_node + (h * a.group + g) * a.q_head];
+            for (int k = 0; k < K; ++k) {
+                const int r = min(r0 + k * shares, rows - 1), node = (int)((uint64_t)r * a.group_factor >> 40);
+                f[k] = q[node * a.q_node + (h * a.group + r - node * a.group) * a.q_head];
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < K; ++k)
                 if (r0 + k * shares < rows) {
                     // A NaN takes part in both.
                     const double y = (double)T::widen(f[k]);

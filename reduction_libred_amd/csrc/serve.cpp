@@ -182,6 +182,7 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     k.table_stride = a->table_stride, k.pages = (int64_t)a->pages;
     k.nodes = (int)N, k.heads = (int)H, k.group = (int)(a->q_heads / H), k.dim = (int)D, k.places = (int)a->places;
     k.budget = (int)a->budget, k.first = (int)a->first, k.last = (int)a->last;
+    k.group_factor = k.group > 0 ? (((uint64_t)1 << 40) + k.group - 1) / k.group : 0;
     k.most = (int)most, k.share = (int)share, k.max_len = (int)tokens;
     void* p = nullptr;
     if (most > a->budget) {
@@ -243,7 +244,7 @@ red_status sample_call(const red_sample_args* a, hipStream_t stream) {
     const int probs_type = a->probs != nullptr ? a->probs_type : RED_F32;
     const size_t rows = B * S;
     size_t each = rows;
-    if (V > kSampleChunk) {
+    if (V > kSampleRow) {
         // Rows cut into chunks, as many at a time as 256 MiB hold the bins and
         // lists of.
         const size_t chunks = (V + kSampleChunk - 1) / kSampleChunk;

@@ -64,6 +64,7 @@ struct SelectPages {
     int batch, nodes, heads, group, dim, places, budget, first, last;
     int most;   // pages of a sequence
     int share;  // of them that a block scores
+    uint64_t group_factor;  // row r < 2^22 is of node r * group_factor >> 40: 2^40 / group, rounded up
     int max_len;
 };
 constexpr int kSelectPages = 64;  // a multiple of this many pages has a block that scores them
@@ -71,6 +72,12 @@ hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& 
 
 // Sampling. A row goes through one block, or is cut into chunks.
 constexpr int kSampleChunk = 8192, kSampleGrid = 512, kSampleList = 16384;
+// Rows of up to so many logits go through one block. (Microseconds of 1 / 192 /
+// 2000 float32 rows, top-p: 4000 logits 16.5 / 18.4 / 124 by a block, 21.6 / 24.4 /
+// 129 by chunks; 8000 logits 21.6 / 24.2 / 171 and 23.1 / 25.7 / 148; 32000 logits
+// 52 / 58 / 451 and 24 / 33 / 229. With top-k as well: 4000 logits 19 / 24 / 170 and
+// 24 / 27 / 141, 8000 logits 26 / 29 / 211 and 24 / 27 / 147.)
+constexpr int kSampleRow = 4096;
 struct SampleHead {  // of a chunk
     uint64_t first;  // the first code of the order
     int count;       // logits above -inf, where top-k asks for it
