@@ -8,10 +8,11 @@
  * that the call reads before it returns, strides in elements with a contiguous
  * last dimension, inputs that do not overlap outputs, refusals before any HIP
  * call, deterministic results. Scratch: every call here but the bounds of pages
- * keeps intermediate results in the stream's scratch buffer, under the rule of
- * libred_decode.h: while a stream is captured, an earlier call on it of the
- * same types, kv heads, dim and places, and no less of the rest, must have
- * provided it, else the call returns RED_ERR_CAPTURE.
+ * and the sampling of up to 4096 tokens keeps intermediate results in the
+ * stream's scratch buffer, under the rule of libred_decode.h: while a stream is
+ * captured, an earlier call on it of the same types, kv heads, dim and places,
+ * and no less of the rest, must have provided it, else the call returns
+ * RED_ERR_CAPTURE.
  */
 #ifndef LIBRED_SERVE_H_
 #define LIBRED_SERVE_H_
@@ -187,7 +188,11 @@ red_status red_sparse_attention(const red_tree_attention_args *a, int64_t table_
  * more, or NaN, the token is the last of positive w.
  *
  * Weights are float64; their sums are whole multiples of 2^(ceil(log2 vocab) -
- * 62), so they do not depend on any order.
+ * 62), so they do not depend on any order. Rows of more than 4096 tokens are
+ * added up by bins of equal ratios of the weight, in which a weight counts to
+ * within 2^-35 of itself; where all kept tokens have the largest logit the sums
+ * are exact. A border or token whose target lies closer to a running sum than
+ * that may be the neighbouring one, the same one every time.
  *
  * type: RED_F32, RED_F16 or RED_BF16 of the logits; probs_type the same of
  * probs. tokens (with r) or probs may be NULL: not wanted. tokens and r are

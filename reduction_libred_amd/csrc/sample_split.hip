@@ -49,8 +49,11 @@ struct Place {
     __device__ __forceinline__ double floor_of(float x) const { return __builtin_floor((double)x * scale); }
     // From the bin's lower edge, by the product before it is rounded.
     __device__ __forceinline__ double in_bin(float x, double floor) const { return __builtin_fma((double)x, scale, -floor); }
-    // Whether the bins' numbers are small enough for all that is done with them.
-    __device__ __forceinline__ bool fits(float top) const { return __builtin_fabs((double)top * scale) < 0x1p27; }
+    // Whether the bins' numbers are small enough for all that is done with them: of
+    // a row by its largest logit, and of a chunk, with room for any that is on the
+    // grid of a row for which they are.
+    __device__ __forceinline__ bool fits(float top) const { return __builtin_fabs((double)top * scale) < 0x1p26; }
+    __device__ __forceinline__ bool chunk_fits(float top) const { return __builtin_fabs((double)top * scale) < 0x1p27; }
 };
 
 // 2^52 + 2^36 2^((f - 1) / 8) for the place f in its bin, rounded to a whole
@@ -453,7 +456,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
 #pragma unroll
     for (int w = 1; w < W; ++w) top = fmaxf(top, tops[w]);
     const Place place{set.scale * kPerPower};
-    const bool binned = set.k != 1 && place.fits(top);
+    const bool binned = set.k != 1 && place.chunk_fits(top);
     int number = kOwn, count = 0;
     if (binned) {
         fill_bins(x, place, place.floor_of(top), bins);

@@ -4,9 +4,16 @@ Whole numbers are equal: slots, pages, tokens. Where a token or a kept set hangs
 on a sum of weights, the reference says how close a border came to its target,
 relative to the largest weight; the library's sums are whole multiples of
 2^(ceil(log2 vocab) - 62) of that, each weight off by half of one and by the
-2^-50 of a float64 exponential, so a border further away than vocab * 2^-45 +
-2^-40 is certain. Cases that come closer by chance are not (none is known to);
-those that meet a border exactly do so with whole weights, which are exact."""
+2^-50 of a float64 exponential. In rows that are cut into chunks of 8192, sums
+are those of bins: a weight counts in them as a whole number of 2^-36 of its
+bin's upper edge, which is at most 2^(1/8) of it, so it is off by 1.1 * 2^-37,
+by 2^-41 of the polynomial, and by as much again by the largest weight's own
+number, which all are divided by: less than 2^-35 of itself in all. The sum of a
+bin of a chunk is cut off to a whole unit: 512 bins of vocab / 8192 chunks and of
+at most 2 vocab 2^-62 each are off by vocab^2 2^-65, which is at most vocab *
+2^-45. So a border further away than sum * 2^-35 + vocab * 2^-45 + 2^-40 is
+certain. Cases that come closer by chance are not (none is known to); those that
+meet a border exactly do so with whole weights, which are exact."""
 import math
 import random
 import sys
@@ -383,8 +390,9 @@ def test_sparse_attention_pages_outside_and_masked_nan():
 # ---------------------------------------------------------------------------
 # Sampling
 # ---------------------------------------------------------------------------
-def certain(vocab):
-    return vocab * 2.0 ** -45 + 2.0 ** -40
+def certain(weights):
+    """weights: those of the whole row, the largest 1."""
+    return float(np.sum(weights)) * 2.0 ** -35 + len(weights) * 2.0 ** -45 + 2.0 ** -40
 
 
 def check_sample(x, r, t=None, k=None, p=None, m=None, probs=F32, exact=False):
@@ -402,12 +410,13 @@ def check_sample(x, r, t=None, k=None, p=None, m=None, probs=F32, exact=False):
         of = {n: None if y is None else float(y[b]) for n, y in settings.items()}
         for s in range(steps):
             kept, near = S.sample(wide[b, s], of["temperature"], None if k is None else k[b], of["top_p"], of["min_p"])
-            sure = exact or near > certain(vocab)
+            every, _ = S.sample(wide[b, s], of["temperature"])
+            sure = exact or near > certain(every)
             assert sure, "a border closer to its target than sums of 64 bits tell"
             # weights below half a unit count as 0 where they are summed
             unit = 2.0 ** -min(51, 62 - math.ceil(math.log2(vocab)))
             token, close = S.token_of(np.where(kept < unit / 2, 0, kept), float(r[b, s]))
-            assert exact or close > certain(vocab)
+            assert exact or close > certain(every)
             assert tokens[b][s] == token, (b, s, tokens[b][s], token)
             want = (kept / kept.sum() if kept.sum() > 0 else kept).astype(np.float64)
             # one rounding to the type, one to float32, and the weights' own
@@ -524,6 +533,24 @@ def test_sample_far_tails():
     x = (-torch.arange(3000.0) / 4)[None, None].repeat(3, 1, 1)
     check_sample(x, torch.tensor([[0.5], [0.999999], [1.0]]), k=[2999, 500, 100], exact=True)
     check_sample(x.flip(-1).contiguous(), torch.tensor([[0.5], [0.999999], [0.1]]), p=[0.9, 0.99, 0.5])
+
+
+@pytest.mark.parametrize("power", [26, 27])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_sample_of_large_logits(power, sign):
+    """Eighths of powers of two of the weights whose numbers pass 2^26 and 2^27
+    within the row, in other chunks than the largest logit's."""
+    border = sign * round(2.0 ** power / (8 * math.log2(math.e)))
+    x = torch.full((4, 1, 40000), float(border - 30))
+    x[:, 0, ::9] = border - 4
+    x[:, 0, 9000:9100] = border + 4
+    x[:, 0, 20000:20007] = border - 1
+    x[1, 0, :16384], x[2, 0, :24576] = border - 9, -torch.finfo(F32).max
+    x[3, 0, 9000:9100], x[3, 0, 30000] = border - 6, border + 2
+    r = torch.tensor([0.3, 0.999, 0.7, 0.05])[:, None]
+    check_sample(x, r)
+    check_sample(x, r, p=[0.99, 0.9995, 0.7, 0.6], k=[2000, 39000, 40000, 300])
+    check_sample(x, r, t=[3.0] * 4, p=[0.99, 0.9995, 0.7, 0.6], m=[0.0, 0.001, 0.02, 0.3])
 
 
 def test_sample_layouts():
