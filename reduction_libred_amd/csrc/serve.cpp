@@ -184,8 +184,10 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     k.budget = (int)a->budget, k.first = (int)a->first, k.last = (int)a->last;
     k.group_factor = k.group > 0 ? (((uint64_t)1 << 40) + k.group - 1) / k.group : 0;
     k.most = (int)most, k.share = (int)share, k.max_len = (int)tokens;
+    // Asked for where the budget takes all pages as well, so that a call provides
+    // it for those of a smaller budget.
     void* p = nullptr;
-    if (most > a->budget) {
+    if (most > 0) {
         st = host_scratch(dev, stream, B * H * most * sizeof(uint64_t), &p);
         if (st != RED_OK) return st;
     }
