@@ -36,6 +36,35 @@ struct CodeE4M3 {
     }
 };
 
+// Joins the N elements that each lane has of the 64 / G rows that a wave read. At
+// every step two lanes hand each other half of what they have left, so each ends
+// with N * G / 64 elements of all rows, those from (bit 5 of the lane) * N / 2 +
+// (bit 4) * N / 4 + (bit 3) * N / 8 on, and all lanes write.
+template <int N, int G, class F>
+__device__ __forceinline__ void join_rows(float (&v)[N], F op) {
+    auto bits = [](float x) { return __builtin_bit_cast(uint32_t, x); };
+    auto number = [](uint32_t x) { return __builtin_bit_cast(float, x); };
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const auto s = __builtin_amdgcn_permlane32_swap(bits(v[i]), bits(v[i + N / 2]), false, false);
+        v[i] = op(number(s[0]), number(s[1]));
+    }
+    if constexpr (G <= 16)
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const auto s = __builtin_amdgcn_permlane16_swap(bits(v[i]), bits(v[i + N / 4]), false, false);
+            v[i] = op(number(s[0]), number(s[1]));
+        }
+    if constexpr (G <= 8) {
+        const bool upper = threadIdx.x >> 3 & 1;
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            const float own = upper ? v[i + N / 8] : v[i], other = upper ? v[i] : v[i + N / 8];
+            v[i] = op(own, dpp_move<0x128, 0xF>(other, other));  // 8 lanes on, in rows of 16
+        }
+    }
+}
+
 // VEC elements a lane: those of a 16-byte load, G lanes a row; VEC 1 (any
 // alignment): 64 lanes, up to 4 elements each, 64 apart.
 template <class T, class C, int VEC, int G>
@@ -102,20 +131,20 @@ __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBo
             }
         }
     }
-#pragma unroll
-    for (int o = G; o < kWave; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            lo[i] = fminf(lo[i], __shfl_xor(lo[i], o));
-            hi[i] = fmaxf(hi[i], __shfl_xor(hi[i], o));
-        }
     const int64_t at = page * a.bound_page + h * a.bound_head;
     typename T::bits *to_lo = static_cast<typename T::bits*>(a.lo) + at, *to_hi = static_cast<typename T::bits*>(a.hi) + at;
     if constexpr (VEC > 1) {
-        using V = typename Vec<T, VEC>::type;
-        if (row == 0 && there) {
-            reinterpret_cast<V*>(to_lo)[in] = narrow_vec<T, VEC>(lo);
-            reinterpret_cast<V*>(to_hi)[in] = narrow_vec<T, VEC>(hi);
+        constexpr int L = N / R;
+        typedef typename T::bits Out __attribute__((ext_vector_type(L)));
+        join_rows<N, G>(lo, [](float m, float n) { return fminf(m, n); });
+        join_rows<N, G>(hi, [](float m, float n) { return fmaxf(m, n); });
+        if (there) {
+            Out l, m;
+#pragma unroll
+            for (int i = 0; i < L; ++i) l[i] = T::narrow(lo[i]), m[i] = T::narrow(hi[i]);
+            const int e = in * N + (lane >> 5 & 1) * (N / 2) + (G <= 16 ? (lane >> 4 & 1) * (N / 4) : 0) + (G <= 8 ? (lane >> 3 & 1) * (N / 8) : 0);
+            *reinterpret_cast<Out*>(to_lo + e) = l;
+            *reinterpret_cast<Out*>(to_hi + e) = m;
         }
     } else {
 #pragma unroll
@@ -133,7 +162,7 @@ hipError_t launch_types(int vec, int lanes, const PageBounds& a, dim3 grid, hipS
     if (vec == 1) page_bounds_kernel<T, C, 1, 64><<<grid, threads, 0, stream>>>(a);
     else if (lanes == 8) page_bounds_kernel<T, C, V, 8><<<grid, threads, 0, stream>>>(a);
     else if (lanes == 16) page_bounds_kernel<T, C, V, 16><<<grid, threads, 0, stream>>>(a);
-    else if (!C::kScaled) page_bounds_kernel<T, C, V, 32><<<grid, threads, 0, stream>>>(a);
+    else if constexpr (!C::kScaled) page_bounds_kernel<T, C, V, 32><<<grid, threads, 0, stream>>>(a);
     return hipGetLastError();
 }
 

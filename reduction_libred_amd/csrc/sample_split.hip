@@ -327,35 +327,33 @@ __device__ __forceinline__ uint64_t rank_border(uint64_t c, uint64_t own, int n,
 
 // The code at which the running sum of the list's weights (`ones`: of ones), in
 // the order of the codes, among those from `from` to below `upto`, reaches `want`,
-// the last of them where it does not; ~0 where there are none. Digits of 8 bits
-// from the first that `from` and `upto` do not share, until a wave can take the
-// rest. By the block.
+// the last of them where it does not; ~0 where there are none. By bins of equal
+// numbers of codes, 129 to 256 of them, and again in the border's bin, until a wave
+// can take the rest. (Digits of 8 bits fell into few bins, one even, where the codes
+// pass a power of two.) By the block.
 template <class T>
 __device__ __forceinline__ uint64_t list_border(const List<T>& list, uint64_t from, uint64_t upto, uint64_t want, bool ones) {
     if (from >= upto) return ~0ull;
     Shared& s = list.s;
     const int tid = threadIdx.x, lane = tid % kWave;
-    int down = 64 - __builtin_clzll((from ^ (upto - 1)) | 1);
-    uint64_t prefix = from >> down;
     unsigned int in = list.n;
-    auto inside = [&](uint64_t c) { return c >= from && c < upto && c >> down == prefix; };
+    auto inside = [&](uint64_t c) { return c >= from && c < upto; };
     want = want > 0 ? want : 1;
-    while (in > kWave && down > 0) {
-        const int width = min(down, 8), to = down - width;
+    while (in > kWave) {
+        const int bits = 64 - __builtin_clzll((upto - from - 1) | 1), to = bits > 8 ? bits - 8 : 0;
         clear_bins(s);
         list.each([&](uint64_t c, auto weight) {
             if (!inside(c)) return;
-            const int d = (int)(c >> to) & ((1 << width) - 1);
+            const int d = (int)((c - from) >> to);
             atomicAdd(&s.mass[d], (unsigned long long)(ones ? 1 : weight()));
             atomicAdd(&s.count[d], 1u);
         });
         find_bin(s, want, true);
         if (s.bin >= kBins) return ~0ull;
-        prefix = prefix << width | s.bin;
+        from += (uint64_t)s.bin << to;
+        upto = upto - from < (1ull << to) ? upto : from + (1ull << to);
         want = s.rest, in = s.count[s.bin];
-        down = to;
     }
-    if (down == 0) return prefix;
     __syncthreads();
     if (tid == 0) s.held = 0;
     __syncthreads();

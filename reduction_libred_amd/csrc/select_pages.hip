@@ -97,24 +97,35 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     load(x);
     look(first + kStep);
 
-    // U and D: `dims` threads side by side, the rows shared among the rest.
-    int dims = 1;
-    while (dims < a.dim) dims <<= 1;
-    const int d = tid % dims, share = tid / dims, shares = kScoreThreads / dims, rows = p.count * a.group;
+    // U and D: `dims` threads side by side, the rows shared among the rest. A row's
+    // place follows from the last one's: the division by the group for each took as
+    // long as the pages.
+    int log2 = 0;
+    while (1 << log2 < a.dim) ++log2;
+    const int dims = 1 << log2, d = tid & (dims - 1), share = tid >> log2, shares = kScoreThreads >> log2, rows = p.count * a.group;
     double u = 0.0, v = 0.0;
-    if (d < a.dim) {
-        const typename T::bits* q = static_cast<const typename T::bits*>(a.q) + b * a.q_batch + d;
+    if (d < a.dim && share < rows) {
+        const int node = share / a.group, skip = shares / a.group, over = shares - skip * a.group;
+        int member = share - node * a.group, r = share;
+        const typename T::bits* q = static_cast<const typename T::bits*>(a.q) + b * a.q_batch + node * a.q_node + (h * a.group + member) * a.q_head + d;
+        const int64_t step = skip * a.q_node + over * a.q_head, wrap = a.q_node - a.group * a.q_head;
         constexpr int K = 4;
-        for (int r0 = share; r0 < rows; r0 += K * shares) {
+        while (r < rows) {
             typename T::bits f[K];
+            bool good[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int r = min(r0 + k * shares, rows - 1), node = (int)((uint64_t)r * a.group_factor >> 40);
-                f[k] = q[node * a.q_node + (h * a.group + r - node * a.group) * a.q_head];
+                good[k] = r < rows;
+                f[k] = *q;
+                r += shares;
+                if (r < rows) {  // else the last row again
+                    q += step, member += over;
+                    if (member >= a.group) q += wrap, member -= a.group;
+                }
             }
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (r0 + k * shares < rows) {
+                if (good[k]) {
                     // A NaN takes part in both.
                     const double y = (double)T::widen(f[k]);
                     u += y < 0.0 ? 0.0 : y;
@@ -125,7 +136,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     parts[0][tid] = u, parts[1][tid] = v;
     __syncthreads();
     if (tid < a.dim) {
-        for (int s = 1; s < shares; ++s) u += parts[0][s * dims + tid], v += parts[1][s * dims + tid];
+        for (int s = 1; s < min(shares, rows); ++s) u += parts[0][s * dims + tid], v += parts[1][s * dims + tid];
         up[tid] = u, down[tid] = v;
     }
     __syncthreads();
@@ -156,7 +167,8 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
             double s = 0.0;
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (there[i]) s += pu[i] * (double)fh[i] + pd[i] * (double)fl[i];
+                if (VEC == 8 || there[i]) s = __builtin_fma(pd[i], (double)fl[i], __builtin_fma(pu[i], (double)fh[i], s));
+            if (VEC == 8 && !there[0]) s = 0.0;  // a lane's elements are all there, or none
             s = group_combine<G>(s, AddF64());
             const int j = j0 + (wave * U + k) * R + lane / G;
             if (in == 0 && j < last) keys[j] = now.good[k] ? ordered(s) : 0;

@@ -182,7 +182,6 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     k.table_stride = a->table_stride, k.pages = (int64_t)a->pages;
     k.nodes = (int)N, k.heads = (int)H, k.group = (int)(a->q_heads / H), k.dim = (int)D, k.places = (int)a->places;
     k.budget = (int)a->budget, k.first = (int)a->first, k.last = (int)a->last;
-    k.group_factor = k.group > 0 ? (((uint64_t)1 << 40) + k.group - 1) / k.group : 0;
     k.most = (int)most, k.share = (int)share, k.max_len = (int)tokens;
     // Asked for where the budget takes all pages as well, so that a call provides
     // it for those of a smaller budget.

@@ -64,7 +64,6 @@ struct SelectPages {
     int batch, nodes, heads, group, dim, places, budget, first, last;
     int most;   // pages of a sequence
     int share;  // of them that a block scores
-    uint64_t group_factor;  // row r < 2^22 is of node r * group_factor >> 40: 2^40 / group, rounded up
     int max_len;
 };
 constexpr int kSelectPages = 64;  // a multiple of this many pages has a block that scores them
