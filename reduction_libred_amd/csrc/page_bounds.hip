@@ -3,9 +3,15 @@
 //     lo[d] = min over the page's tokens of k[d],  hi[d] = max.
 //
 // A wave has a (page, head): G lanes hold a row, one 16-byte load each, so 64 / G
-// rows are read at once, four times over, and joined by lane moves at the end. Minima and maxima are of float32
-// values, and rounding them to 16 bits is the same as rounding the elements,
-// since rounding keeps the order.
+// rows are read at once, four times over, and joined by lane moves at the end.
+// Minima and maxima are of float32 values, and rounding them to 16 bits is the same
+// as rounding the elements, since rounding keeps the order.
+//
+// 8 sequences of 7001 to 16384 tokens, 8 heads of 128 in pages of 64, int8 (101 MB):
+// 21.4 us, 4.7 TB/s of the 7.2 that a read reaches; a decoding step's page or two of
+// 32 sequences 3.3 us, a launch. What is left is the chain of each wave (length, page
+// number, keys) at 4 waves a SIMD: 2 or 8 loads in flight, or 6 waves, take 21 to 23.
+// Joined by 96 moves through the LDS instead of 28 lane swaps: 25.4.
 #include "decode_common.hpp"
 #include "serve.hpp"
 

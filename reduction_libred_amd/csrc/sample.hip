@@ -1,4 +1,7 @@
 // Sampling: a block a row, in one launch, and the choice of the kernel by types.
+// A row goes through the block once for its largest logit, once or twice more for
+// each border and twice for the token. It is for short rows, where latency is all
+// there is: 4000 logits, top-p, 16.5 us for 1 row, 18.4 for 192 (see kSampleRow).
 #include "sample_common.hpp"
 
 namespace libred {

@@ -66,9 +66,14 @@ red_status plan_call(const red_plan_slots_args* a, hipStream_t stream) {
     k.have = static_cast<int32_t*>(p);
     k.before = k.have + B + 1, k.back = k.before + B + 1, k.sums = k.back + B + 1, k.fresh = k.sums + 4;
     const size_t wide = (T + 255) / 256 < (size_t)cus * 8 ? (T + 255) / 256 : (size_t)cus * 8;
-    const int blocks = T <= 4096 ? 0 : (int)wide;
-    // The block of the sums moves the pages too, if they may be few.
-    const bool few = T / a->places + B <= 16384;
+    // One block, or the tokens in a launch of their own. (Microseconds, replayed:
+    // 1024 tokens 7.4 / 8.8, 4096 tokens 12.6 / 10.2, 16384 tokens 34 / 12.)
+    const int blocks = T <= 2048 ? 0 : (int)wide;
+    // The block of the sums moves the pages too, if few are taken, else a launch of
+    // its own does. (Replayed: 256 pages 10.2 / 11.5, 1024 pages 11.6 / 12.9, 2048
+    // pages 14.4 / 14.3, 16384 pages 43 / 14; from Python, where a launch more is 2 us
+    // of the host's, 2100 taken and 16000 given back 15.4 / 17.3.)
+    const bool few = T / a->places + B <= 4096;
     const hipError_t e = launch_plan_slots(k, blocks, few, stream);
     return e == hipSuccess ? RED_OK : host_fail(e, RED_ERR_HIP);
 }
