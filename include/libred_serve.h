@@ -132,8 +132,8 @@ red_status red_page_bounds(const red_page_bounds_args *a, hipStream_t stream);
  * most tokens of a sequence, nodes included; it shapes the launch, and tokens
  * from it on, or beyond table_cols pages, do not count. Page numbers outside
  * [0, pages) have score NaN. budget >= first + last + 1 + ceil(nodes /
- * places). nodes <= 64, batch, q_heads and kv heads <= 65535, dim 1 .. 256,
- * max_len <= 2^30, batch * kv heads * ceil(max_len / places) below 2^31.
+ * places). nodes <= 64, batch and q_heads <= 65535, q_heads a multiple of the kv
+ * heads and not 0, dim 1 .. 256, max_len <= 2^30, batch * kv heads * ceil(max_len / places) below 2^31.
  */
 typedef struct red_select_pages_args {
     int type;

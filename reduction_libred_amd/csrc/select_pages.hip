@@ -89,8 +89,10 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     };
     auto load = [&](Bounds& x) {
 #pragma unroll
+        for (int k = 0; k < U; ++k) x.good[k] = page[k] >= 0 && page[k] < a.pages;
+        if (a.pages == 0) return;  // nothing may be read
+#pragma unroll
         for (int k = 0; k < U; ++k) {
-            x.good[k] = page[k] >= 0 && page[k] < a.pages;
             const int64_t at = x.good[k] ? page[k] * a.bound_page : 0;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
             }
         }
     };
-    Bounds x;
+    Bounds x = {};
     look(first);
     load(x);
     look(first + kStep);

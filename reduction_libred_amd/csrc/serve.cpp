@@ -142,7 +142,7 @@ red_status bounds_call(const red_page_bounds_args* a, hipStream_t stream) {
 red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     if (a == nullptr || (a->type != RED_F16 && a->type != RED_BF16)) return RED_ERR_INVALID_ARG;
     const size_t B = a->batch, N = a->nodes, H = a->kv_heads, D = a->dim;
-    if (B > 65535 || N > RED_TREE_MAX_NODES || H < 1 || H > 65535 || a->q_heads > 65535 || a->q_heads % H != 0) return RED_ERR_INVALID_ARG;
+    if (B > 65535 || N > RED_TREE_MAX_NODES || H < 1 || a->q_heads < 1 || a->q_heads > 65535 || a->q_heads % H != 0) return RED_ERR_INVALID_ARG;
     if (D < 1 || D > RED_HEAD_MAX_DIM || a->places < 1 || a->places > (size_t)1 << 20 || a->pages > kMost32) return RED_ERR_INVALID_ARG;
     if (a->max_len > (size_t)1 << 30 || a->table_cols > (size_t)1 << 30 || a->table_stride < 0 || a->table_stride > (int64_t)1 << 40)
         return RED_ERR_INVALID_ARG;
@@ -158,7 +158,7 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     const size_t tokens = a->table_cols * a->places < a->max_len ? a->table_cols * a->places : a->max_len;
     const size_t most = (tokens + a->places - 1) / a->places;
     if (most > 0 && a->table == nullptr) return RED_ERR_INVALID_ARG;
-    const bool scored = most > a->budget && N > 0 && a->q_heads > 0;
+    const bool scored = most > a->budget && N > 0;
     if (scored && (a->q == nullptr || (a->pages > 0 && (a->lo == nullptr || a->hi == nullptr)))) return RED_ERR_INVALID_ARG;
     if (!is_aligned(a->q, 2) || !is_aligned(a->lo, 2) || !is_aligned(a->hi, 2)) return RED_ERR_INVALID_ARG;
     for (const void* p : {(const void*)a->table, (const void*)a->lens, (const void*)a->node_count, (const void*)a->selected, (const void*)a->selected_lens})

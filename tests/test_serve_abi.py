@@ -89,7 +89,7 @@ def _select(**kw):
 
 
 SELECT_BAD = [
-    dict(type=0), dict(type=4), dict(batch=65536), dict(nodes=65), dict(q_heads=3), dict(q_heads=65536 * 2), dict(kv_heads=0),
+    dict(type=0), dict(type=4), dict(batch=65536), dict(nodes=65), dict(q_heads=3), dict(q_heads=0), dict(q_heads=65536 * 2), dict(kv_heads=0),
     dict(kv_heads=65536, q_heads=65536), dict(dim=0), dict(dim=257), dict(places=0), dict(places=(1 << 20) + 1), dict(pages=1 << 31),
     dict(max_len=(1 << 30) + 1), dict(table_cols=(1 << 30) + 1), dict(table_stride=-1), dict(budget=0), dict(budget=3), dict(first=4),
     dict(last=4), dict(first=1 << 63), dict(last=(1 << 64) - 2), dict(budget=(1 << 30) + 1), dict(q_batch_stride=-1), dict(q_head_stride=-16),
