@@ -80,10 +80,12 @@ constexpr float kNone = -__builtin_inff();
 
 // 2^t for t <= 0: a polynomial over half a power to either side, that is 1 at 0;
 // N terms leave out 2^-55 (11) or 2^-38 (8) of it. They interpolate (2^f - 1) / f
-// at the Chebyshev points.
+// at the Chebyshev points. Where t is a product, f is of it before it is rounded (the
+// compiler fuses the two), which for t far below the last power is anything: not used.
 template <int N>
 __device__ __forceinline__ double power2(double t) {
     static_assert(N == 11 || N == 8, "terms");
+    if (t < -1100.0) return 0.0;
     const double n = __builtin_rint(t), f = t - n;
     double p;
     if constexpr (N == 11) {
@@ -465,6 +467,7 @@ __device__ __forceinline__ void row_draw(const Row<T>& row, Shared& s, uint64_t 
         sum += own[j];
     }
     uint64_t all;
+    if (tid == 0) s.bin = 0, s.rest = 1;  // a place in the row whatever the sums are
     uint64_t before = block_before(sum, s, &all);
     if (before < want && before + sum >= want)
 #pragma unroll

@@ -694,6 +694,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     const uint64_t border = cut_border(of, set, plan, above);
     // What is kept of the list joins its chunks.
     __syncthreads();
+    if (tid == 0) s.bin = 0, s.rest = 1;  // a place in the row whatever the sums are
     if (ranges > 0)
         of.each([&](uint64_t c, auto weight) {
             // The gathering left a chunk's codes side by side: a wave has mostly those of
