@@ -20,12 +20,14 @@
 // Microseconds of bins / find / gather / draw (/ probabilities): one row of 32000
 // float32, top-k 50 and top-p, 4.5 / 6.2 / 3.8 / 9.6; 192 rows of 131071, top-p, 22.1 /
 // 7.6 / 18.6 / 20.4; 224 rows of bfloat16, top-p and min-p, 24.7 / 8.0 / 13.8 / 16.1 /
-// 33.4. The bins are bound by vector instructions, 11 of a logit in float64 at
-// half rate (a read of the 100 MB would take 14); the gathering and the probabilities
-// by memory (5.4 and 5.3 TB/s); find and draw by their latency, a block a row, the
-// draw by the longest list (6000 codes where 1000 are usual). Finding, gathering and
-// drawing in one launch of a block a row: 55 instead of 47 for the 192 rows, 23
-// instead of 20 for the one.
+// 33.4. The bins take turns at the read (the 100 MB alone 14), 22 vector
+// instructions a logit, half of them float64 (two thirds of the cycles), and an LDS
+// atomic each (two fifths): 17 instructions a logit took 23, blocks that go through
+// several chunks with the next one's logits on their way 24 to 27. The gathering and
+// the probabilities are bound by memory (5.4 and 5.3 TB/s); find and draw by their
+// latency, a block a row, the draw by the longest list (6000 codes where 1000 are
+// usual). Finding, gathering and drawing in one launch of a block a row: 55 instead
+// of 47 for the 192 rows, 23 instead of 20 for the one.
 //
 // Where more logits than kList are near a border (thousands of equal ones), or
 // the border is further than 64 powers of two below the largest weight, the
@@ -112,8 +114,7 @@ struct Loads {
     __device__ __forceinline__ static int number(int n) { return (n / kVec * THREADS + threadIdx.x) * kVec + n % kVec; }
 };
 
-// Every logit of `x` into its bin. Vector instructions bound this, most of them in
-// float64: a logit below the grid goes to a place of its lane's behind it, without
+// Every logit of `x` into its bin: a logit below the grid goes to a place of its lane's behind it, without
 // a branch. Bins go by their negative numbers, that rise from the first bin down.
 template <class L>
 __device__ __forceinline__ void fill_bins(const L& x, const Place& place, double peak, unsigned long long* bins) {
