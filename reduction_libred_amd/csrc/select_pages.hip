@@ -20,8 +20,9 @@
 // nodes (41 MB). Half of that is instructions, most of them float64; the rest waits:
 // lengths, page numbers, bounds, one after another, and then a few steps a wave. 1 or 4
 // pages in flight instead of 2, 64 or 256 pages a block, 6 waves a SIMD, more query
-// rows in flight were slower or even. The choice: 8 to 9 us whatever the
-// sizes, seven steps of the block one after another.
+// rows in flight were slower or even. The choice: 5.3 to 7 us for up to 2048 pages,
+// seven steps of the block one after another, which the pages of a thread lengthen
+// (8 of them: 8 to 9 us).
 #include "decode_common.hpp"
 #include "serve.hpp"
 
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     }
 }
 
-constexpr int kThreads = 512, kOwn = 8, kTile = kThreads * kOwn, kBits = 8, kBins = 1 << kBits;
+constexpr int kBits = 8, kBins = 1 << kBits;
 
 __device__ __forceinline__ int wave_scan(int v) {
     v += dpp_move<0x111, 0xF>(0, v);  // shifted by 1, 2, 4 and 8 in rows of 16
@@ -198,8 +199,10 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-__global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
-    constexpr int W = kThreads / kWave;
+// A thread has OWN pages side by side of every tile.
+template <int THREADS, int OWN>
+__global__ __launch_bounds__(THREADS) void choose_kernel(SelectPages a) {
+    constexpr int W = THREADS / kWave, kTile = THREADS * OWN;
     __shared__ int bins[kBins], lds[W], digit, rest, held, few_pages[kWave];
     __shared__ unsigned long long least, most, few[kWave], border;
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
@@ -208,35 +211,34 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
     const int32_t* table = a.table + b * a.table_stride;
     if (h == 0 && tid == 0) a.selected_lens[b] = p.count > 0 ? (int)(p.len - (int64_t)(p.all - p.chosen) * a.places) : 0;
     if (p.all <= a.budget) {
-        for (int i = tid; i < a.budget; i += kThreads) out[i] = i < p.all ? table[i] : -1;
+        for (int i = tid; i < a.budget; i += THREADS) out[i] = i < p.all ? table[i] : -1;
         return;
     }
     // Pages from `begin` to `end` have scores, all others are selected.
     const uint64_t* keys = a.keys + ((int64_t)b * a.heads + h) * a.most;
     const int begin = min(a.first, p.all), end = max(min(p.tail, p.all), begin);
     int need = a.budget - (p.all - (end - begin));
-    // A thread has kOwn pages side by side of every kTile; those of the first
-    // kTile stay in registers, most sequences have no more.
-    uint64_t own[kOwn];
-    int32_t pages[kOwn];
+    // The pages of the first tile stay in registers, most sequences have no more.
+    uint64_t own[OWN];
+    int32_t pages[OWN];
     auto load = [&](int j0, int i) -> uint64_t {
-        const int j = j0 + tid * kOwn + i;
+        const int j = j0 + tid * OWN + i;
         return keys[min(max(j, begin), max(end - 1, begin))];
     };
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) own[i] = load(0, i), pages[i] = table[min(tid * kOwn + i, p.all - 1)];
+    for (int i = 0; i < OWN; ++i) own[i] = load(0, i), pages[i] = table[min(tid * OWN + i, p.all - 1)];
     auto each = [&](auto f) __attribute__((always_inline)) {
         for (int j0 = 0; j0 < end; j0 += kTile)
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-                const int j = j0 + tid * kOwn + i;
+            for (int i = 0; i < OWN; ++i) {
+                const int j = j0 + tid * OWN + i;
                 if (j >= begin && j < end) f(j0 == 0 ? own[i] : load(j0, i), j);
             }
     };
     // The need-th largest. First by bins of equal width between the least and the
     // largest score that are finite, which leaves few in the border's bin.
     if (tid == 0) least = ~0ull, most = 0, held = 0;
-    for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+    for (int i = tid; i < kBins; i += THREADS) bins[i] = 0;
     __syncthreads();
     constexpr uint64_t kLow = 0x0010000000000000ull, kHigh = 0xFFEFFFFFFFFFFFFFull;  // of the finite scores
     uint64_t low = ~0ull, high = 0;
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
         while (in > kWave && shift > 0) {
             const int down = shift - kBits;
             __syncthreads();
-            for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+            for (int i = tid; i < kBins; i += THREADS) bins[i] = 0;
             __syncthreads();
             each([&](uint64_t k, int) {
                 if (inside(k)) atomicAdd(&bins[k >> down & (kBins - 1)], 1);
@@ -323,11 +325,11 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
     // of those that begin like it the lowest `need`.
     int more_before = 0, same_before = 0;
     for (int j0 = 0; j0 < p.all; j0 += kTile) {
-        uint64_t k[kOwn];
+        uint64_t k[OWN];
         int more = 0, same = 0;
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int j = j0 + tid * kOwn + i;
+        for (int i = 0; i < OWN; ++i) {
+            const int j = j0 + tid * OWN + i;
             k[i] = j0 == 0 ? own[i] : load(j0, i);
             const bool scored = j >= begin && j < end;
             more += j < p.all && (!scored || k[i] > prefix);
@@ -345,8 +347,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(SelectPages a) {
         }
         int m = more_before + (before >> 16), s = same_before + (before & 0xFFFF);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            const int j = j0 + tid * kOwn + i;
+        for (int i = 0; i < OWN; ++i) {
+            const int j = j0 + tid * OWN + i;
             if (j >= p.all) continue;
             const bool scored = j >= begin && j < end, is_more = !scored || k[i] > prefix, is_same = scored && k[i] == prefix;
             if (is_more || (is_same && s < need)) out[m + min(s, need)] = j0 == 0 ? pages[i] : table[j];
@@ -367,7 +369,13 @@ hipError_t select_pages(int vec, int lanes, const SelectPages& a, hipStream_t st
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    choose_kernel<<<dim3((unsigned)a.heads, (unsigned)a.batch), kThreads, 0, stream>>>(a);
+    // (Microseconds of 300 / 1024 / 2048 / 4096 / 32768 pages: 512 threads with 2 pages
+    // each 5.3 / 5.5 / 7.3 / 11.4 / 68, with 4 pages 6.1 / 6.5 / 6.4 / 10.3 / 59, 1024
+    // threads with 4 pages 6.8 / 7.0 / 7.1 / 8.8 / 40.)
+    const dim3 each((unsigned)a.heads, (unsigned)a.batch);
+    if (a.most <= 1024) choose_kernel<512, 2><<<each, 512, 0, stream>>>(a);
+    else if (a.most <= 2048) choose_kernel<512, 4><<<each, 512, 0, stream>>>(a);
+    else choose_kernel<1024, 4><<<each, 1024, 0, stream>>>(a);
     return hipGetLastError();
 }
 

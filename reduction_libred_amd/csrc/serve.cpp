@@ -196,8 +196,8 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
         if (st != RED_OK) return st;
     }
     const int vec = D % 8 == 0 && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, a->pages, H) ? 8 : 1;
-    // A launch has fewer than 2^32 threads; those that choose come in 512.
-    const size_t most_blocks = blocks > H * 2 ? kMaxBlocks / blocks : kMaxBlocks / (2 * H);
+    // A launch has fewer than 2^32 threads; those that choose come in 1024 at most.
+    const size_t most_blocks = blocks > H * 4 ? kMaxBlocks / blocks : kMaxBlocks / (4 * H);
     const size_t each = most_blocks < B ? most_blocks : B;
     for (size_t b = 0; b < B; b += each) {
         k.batch = (int)(B - b < each ? B - b : each);

@@ -41,7 +41,7 @@ hipError_t launch_page_bounds(int, int, int, int, const PageBounds& a, unsigned 
     return hipSuccess;
 }
 hipError_t launch_select_pages(int, int, int, const SelectPages& a, hipStream_t) {
-    const int64_t scores = (int64_t)(a.most + a.share - 1) / a.share * a.heads * a.batch * 256, chooses = (int64_t)a.heads * a.batch * 512;
+    const int64_t scores = (int64_t)(a.most + a.share - 1) / a.share * a.heads * a.batch * 256, chooses = (int64_t)a.heads * a.batch * 1024;
     launches.push_back({scores > chooses ? scores : chooses, 1, a.batch, at(a.lens), at(a.selected)});
     return hipSuccess;
 }
