@@ -16,11 +16,11 @@
 // lowest, in order.
 //
 // Scores (32 query and 8 kv heads of 128): 5.2 us for one sequence of 2048 pages, 10.7
-// for 32 of up to 512 (36 MB of bounds, 3.4 TB/s), 16.4 for 8 of up to 2048 with 8
-// nodes (41 MB). Half of that is instructions, most of them float64; the rest waits:
-// lengths, page numbers, bounds, one after another, and then a few steps a wave. 1 or 4
-// pages in flight instead of 2, 64 or 256 pages a block, 6 waves a SIMD, more query
-// rows in flight were slower or even. The choice: 5.3 to 7 us for up to 2048 pages,
+// for 32 of up to 512 (36 MB of bounds, 3.4 TB/s), 14.8 for 8 of up to 2048 with 8
+// nodes (41 MB). In the last the chain to the first score (lengths, page numbers, bounds,
+// queries) is 8, the queries' sums 2 and the other steps 5. 1 or 4 pages in flight
+// instead of 2, two steps ahead instead of one, 64 or 256 pages a block, 6 waves a SIMD
+// were slower or even; queries added up an element a thread took 16.5. The choice: 5.3 to 7 us for up to 2048 pages,
 // seven steps of the block one after another, which the pages of a thread lengthen
 // (8 of them: 8 to 9 us).
 #include "decode_common.hpp"
@@ -63,7 +63,8 @@ template <class T, int VEC, int G>
 __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     constexpr int N = VEC == 8 ? 8 : 4, R = kWave / G, W = kScoreThreads / kWave;
     __shared__ double up[RED_HEAD_MAX_DIM], down[RED_HEAD_MAX_DIM];
-    __shared__ double parts[2][kScoreThreads];
+    constexpr int Q = VEC == 8 ? 4 : 1;  // elements of a query that a thread adds up
+    __shared__ double parts[2][kScoreThreads * Q];
     const int b = blockIdx.z, h = blockIdx.x, first = blockIdx.y * a.share;  // the heads of the same pages side by side
     const Pages p(a, b);
     const int last = min(first + a.share, min(p.all, p.tail));
@@ -108,26 +109,27 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
     load(x);
     look(first + kStep);
 
-    // U and D: `dims` threads side by side, the rows shared among the rest. A row's
-    // place follows from the last one's: the division by the group for each took as
-    // long as the pages.
+    // U and D: threads side by side take Q elements each of a row, the rows are shared
+    // among the rest. A row's place follows from the last one's: the division by the
+    // group for each took as long as the pages.
     int log2 = 0;
-    while (1 << log2 < a.dim) ++log2;
-    const int dims = 1 << log2, d = tid & (dims - 1), share = tid >> log2, shares = kScoreThreads >> log2, rows = p.count * a.group;
-    double u = 0.0, v = 0.0;
+    while (Q << log2 < a.dim) ++log2;
+    const int d = (tid & ((1 << log2) - 1)) * Q, share = tid >> log2, shares = kScoreThreads >> log2, rows = p.count * a.group;
+    double u[Q] = {}, v[Q] = {};
     if (d < a.dim && share < rows) {
+        typedef typename T::bits QV __attribute__((ext_vector_type(Q)));
         const int node = share / a.group, skip = shares / a.group, over = shares - skip * a.group;
         int member = share - node * a.group, r = share;
         const typename T::bits* q = static_cast<const typename T::bits*>(a.q) + b * a.q_batch + node * a.q_node + (h * a.group + member) * a.q_head + d;
         const int64_t step = skip * a.q_node + over * a.q_head, wrap = a.q_node - a.group * a.q_head;
-        constexpr int K = 4;
+        constexpr int K = 2;
         while (r < rows) {
-            typename T::bits f[K];
+            QV f[K];
             bool good[K];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 good[k] = r < rows;
-                f[k] = *q;
+                f[k] = *reinterpret_cast<const QV*>(q);
                 r += shares;
                 if (r < rows) {  // else the last row again
                     q += step, member += over;
@@ -136,19 +138,23 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
             }
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (good[k]) {
-                    // A NaN takes part in both.
-                    const double y = (double)T::widen(f[k]);
-                    u += y < 0.0 ? 0.0 : y;
-                    v += y > 0.0 ? 0.0 : y;
-                }
+                if (good[k])
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        // A NaN takes part in both.
+                        const double z = (double)T::widen(f[k][i]);
+                        u[i] += z < 0.0 ? 0.0 : z;
+                        v[i] += z > 0.0 ? 0.0 : z;
+                    }
         }
     }
-    parts[0][tid] = u, parts[1][tid] = v;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) parts[0][tid * Q + i] = u[i], parts[1][tid * Q + i] = v[i];
     __syncthreads();
     if (tid < a.dim) {
-        for (int s = 1; s < min(shares, rows); ++s) u += parts[0][s * dims + tid], v += parts[1][s * dims + tid];
-        up[tid] = u, down[tid] = v;
+        double all_u = 0.0, all_v = 0.0;
+        for (int s = 0; s < min(shares, rows); ++s) all_u += parts[0][(s * Q << log2) + tid], all_v += parts[1][(s * Q << log2) + tid];
+        up[tid] = all_u, down[tid] = all_v;
     }
     __syncthreads();
     double pu[N], pd[N];

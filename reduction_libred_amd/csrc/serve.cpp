@@ -195,7 +195,10 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
         st = host_scratch(dev, stream, B * H * most * sizeof(uint64_t), &p);
         if (st != RED_OK) return st;
     }
-    const int vec = D % 8 == 0 && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, a->pages, H) ? 8 : 1;
+    // Bounds 16 bytes at a time, and queries 8.
+    const bool q_on_8 = is_aligned(a->q, 8) && (B == 1 || a->q_batch_stride % 4 == 0) && (N <= 1 || a->q_node_stride % 4 == 0) &&
+                        (a->q_heads == 1 || a->q_head_stride % 4 == 0);
+    const int vec = D % 8 == 0 && q_on_8 && bounds_on_16(a->lo, a->hi, a->bound_page_stride, a->bound_head_stride, a->pages, H) ? 8 : 1;
     // A launch has fewer than 2^32 threads; those that choose come in 1024 at most.
     const size_t most_blocks = blocks > H * 4 ? kMaxBlocks / blocks : kMaxBlocks / (4 * H);
     const size_t each = most_blocks < B ? most_blocks : B;

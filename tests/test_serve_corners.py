@@ -49,6 +49,24 @@ def test_selection_without_nodes_or_tokens():
     assert (sel == -1).all()
 
 
+@pytest.mark.parametrize("shift, pad", [(1, 0), (4, 0), (0, 1), (0, 4)])
+def test_selection_by_queries_at_any_address(shift, pad):
+    """Queries that begin or follow each other off the boundaries that wide loads need."""
+    g = gen(9)
+    lo = torch.randn(60, 2, 128, generator=g).to(BF16)
+    hi = lo + 1
+    q = torch.randn(2, 5, 6, 128, generator=g).to(BF16)
+    table = torch.randperm(60, generator=g).view(2, 30).to(I32)
+    buf = torch.zeros(2 * 5 * 6 * (128 + pad) + shift, dtype=BF16, device=DEV)
+    d = buf[shift:].view(2, 5, 6, 128 + pad)[..., :128]
+    d.copy_(q)
+    sel, _ = rl.red_select_pages(d, lo.to(DEV), hi.to(DEV), table.to(DEV), ints([440, 333]), 16, 9)
+    for b, n in enumerate((440, 333)):
+        chosen, _ = S.select_pages(q[b], lo, hi, table[b], n, 5, 16, 9, 1, 1, 480)
+        for h in range(2):
+            assert sel[b, h].tolist() == [int(table[b, p]) for p in chosen[h]]
+
+
 def test_slots_without_pages_or_sequences():
     say("no pages")
     c = dict(lens=[3, 0], counts=[1, 2], done=[0, 1], table=[[], []], held=[0, 4], stack=[], height=0, places=16, tokens=6)
