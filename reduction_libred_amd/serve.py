@@ -59,12 +59,12 @@ SIGNATURES = {
 }
 
 
+# The arguments are checked in one expression; where that does not hold, they are
+# gone through one by one for what is wrong.
 def _table(name, table, device, batch):
-    """-> (address, columns, stride) of a table (batch, pages of a sequence)."""
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError(f"{name}: table must be ({batch}, pages of a sequence)")
     _rows(name, "table", table, _INT32, device, (batch, table.shape[1]))
-    return table.data_ptr(), table.shape[1], table.stride(0)
 
 
 def _count(name, what, n):
@@ -86,35 +86,52 @@ def red_plan_slots(lens, counts, table, held, free_pages, free_count, places, to
     (batch) int32: counts, or 0 where there was no place)."""
     if stream is not None:
         return _on(stream, red_plan_slots, lens, counts, table, held, free_pages, free_count, places, tokens, done)
-    name = "red_plan_slots"
-    device = _any(name, "lens", lens, (_INT32,), 1, "(batch)")
-    batch, at = lens.shape[0], lens.device
-    tp, cols, t0 = _table(name, table, device, batch)
-    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
-        raise ValueError(f"{name}: free_pages must have one dimension")
-    pages = free_pages.shape[0]
-    _count(name, "tokens", tokens)
-    if places < 1:
-        raise ValueError(f"{name}: places must be positive")
-    slots, pos = (torch.empty(tokens, dtype=_INT64, device=at) for _ in range(2))
+    _count("red_plan_slots", "tokens", tokens)
+    try:
+        one, (batch, cols), pages, device = lens.shape, table.shape, free_pages.shape, lens.get_device()
+        fits = (lens.dtype is _INT32 and counts.dtype is _INT32 and table.dtype is _INT32 and held.dtype is _INT32 and
+                free_pages.dtype is _INT32 and free_count.dtype is _INT32 and device >= 0 and counts.get_device() == device and
+                table.get_device() == device and held.get_device() == device and free_pages.get_device() == device and
+                free_count.get_device() == device and one == (batch,) and counts.shape == one and held.shape == one and
+                len(pages) == 1 and free_count.shape == (1,) and lens.is_contiguous() and counts.is_contiguous() and
+                held.is_contiguous() and free_pages.is_contiguous() and (table.stride(1) == 1 or cols <= 1) and places >= 1 and
+                (done is None or (done.dtype is _INT32 and done.get_device() == device and done.shape == one and done.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _plan_check(lens, counts, table, held, free_pages, free_count, places, done)
+    at = lens.device
+    slots, pos = torch.empty(tokens, dtype=_INT64, device=at), torch.empty(tokens, dtype=_INT64, device=at)
     starts, granted = torch.empty(batch + 1, dtype=_INT32, device=at), torch.empty(batch, dtype=_INT32, device=at)
-    one = (batch,)
-    _call(name, device, None, _pack_plan(
-        batch, tokens, places, pages, _whole(name, "lens", lens, _INT32, device, one),
-        _whole(name, "counts", counts, _INT32, device, one), 0 if done is None else _whole(name, "done", done, _INT32, device, one),
-        tp, cols, t0, _whole(name, "held", held, _INT32, device, one), _whole(name, "free_pages", free_pages, _INT32, device, (pages,)),
-        _whole(name, "free_count", free_count, _INT32, device, (1,)), slots.data_ptr(), pos.data_ptr(), starts.data_ptr(),
-        granted.data_ptr()))
+    _call("red_plan_slots", device, None, _pack_plan(
+        batch, tokens, places, pages[0], lens.data_ptr(), counts.data_ptr(), 0 if done is None else done.data_ptr(), table.data_ptr(), cols,
+        table.stride(0), held.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), slots.data_ptr(), pos.data_ptr(),
+        starts.data_ptr(), granted.data_ptr()))
     return slots, pos, starts, granted
 
 
+def _plan_check(lens, counts, table, held, free_pages, free_count, places, done):
+    """Raise what is wrong with the arguments."""
+    name = "red_plan_slots"
+    device = _any(name, "lens", lens, (_INT32,), 1, "(batch)")
+    batch = lens.shape[0]
+    _table(name, table, device, batch)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError(f"{name}: free_pages must have one dimension")
+    for what, x, shape in (("counts", counts, (batch,)), ("done", done, (batch,)), ("held", held, (batch,)),
+                           ("free_pages", free_pages, free_pages.shape), ("free_count", free_count, (1,))):
+        if what != "done" or x is not None:
+            _whole(name, what, x, _INT32, device, shape)
+    if places < 1:
+        raise ValueError(f"{name}: places must be positive")
+    raise ValueError(f"{name}: lens must be contiguous")
+
+
 def _bounds(name, lo, hi, dtype, device, shape):
-    """-> (address of lo, of hi, stride of pages, of heads)"""
     _rows(name, "lo", lo, dtype, device, shape)
     _rows(name, "hi", hi, dtype, device, shape)
     if lo.stride() != hi.stride():
         raise ValueError(f"{name}: lo and hi must have the same strides")
-    return lo.data_ptr(), hi.data_ptr(), *lo.stride()[:2]
 
 
 def red_page_bounds(k_pages, table, lens, lo, hi, first=None, most=None, k_scales=None, stream=None):
@@ -123,29 +140,50 @@ def red_page_bounds(k_pages, table, lens, lo, hi, first=None, most=None, k_scale
     or bfloat16, the cache's type where that has 16 bits): of the pages of
     sequence b that hold tokens first[b] (int32; None: 0) to lens[b] - 1, at
     most `most` pages of a sequence (None: what the table holds)."""
+    try:
+        (pages, heads, places, dim), (p0, p1, p2, inner), kind, dtype = k_pages.shape, k_pages.stride(), TYPES[k_pages.dtype], lo.dtype
+        (batch, cols), shape, device, (b0, b1, b2) = table.shape, lo.shape, k_pages.get_device(), lo.stride()
+        fits = (0 < kind and dtype in _HALVES and (kind >= 3 or dtype is k_pages.dtype) and hi.dtype is dtype and
+                lens.dtype is _INT32 and table.dtype is _INT32 and device >= 0 and lo.get_device() == device and
+                hi.get_device() == device and lens.get_device() == device and table.get_device() == device and
+                shape == (pages, heads, dim) and hi.shape == shape and hi.stride() == (b0, b1, b2) and
+                ((inner == 1 and b2 == 1) or dim <= 1) and lens.shape == (batch,) and lens.is_contiguous() and
+                (table.stride(1) == 1 or cols <= 1) and (kind >= 3) == (k_scales is not None) and
+                (first is None or (first.dtype is _INT32 and first.get_device() == device and first.shape == lens.shape and
+                                   first.is_contiguous())) and
+                (k_scales is None or (k_scales.dtype is _FLOAT32 and k_scales.get_device() == device and
+                                      k_scales.shape == k_pages.shape[:3])))
+    except (AttributeError, TypeError, ValueError, KeyError):
+        fits = False
+    if not fits:
+        _bounds_check(k_pages, table, lens, lo, hi, first, k_scales)
+    ks, (s0, s1, s2) = (0, (0, 0, 0)) if k_scales is None else (k_scales.data_ptr(), k_scales.stride())
+    _call("red_page_bounds", device, stream, _pack_bounds(
+        TYPES[dtype], batch, cols if most is None else _count("red_page_bounds", "most", most), k_pages.data_ptr(), 0, ks, 0, kind,
+        pages, heads, places, dim, p0, p1, p2, s0, s1, s2, table.data_ptr(), cols, table.stride(0), lens.data_ptr(),
+        0 if first is None else first.data_ptr(), lo.data_ptr(), hi.data_ptr(), b0, b1))
+
+
+def _bounds_check(k_pages, table, lens, lo, hi, first, k_scales):
+    """Raise what is wrong with the arguments."""
     name = "red_page_bounds"
     device = _any(name, "k_pages", k_pages, _CACHES, 4, "(pages, heads, places, dim)")
-    pages, heads, places, dim = k_pages.shape
-    kind = TYPES[k_pages.dtype]
-    dtype = lo.dtype if isinstance(lo, torch.Tensor) else None
-    if dtype not in _HALVES or (kind < 3 and dtype is not k_pages.dtype):
-        _any(name, "lo", lo, _HALVES if kind >= 3 else (k_pages.dtype,), 3, "(pages, heads, dim)")
-    if (kind >= 3) != (k_scales is not None):
+    pages, heads, _, dim = k_pages.shape
+    scaled = TYPES[k_pages.dtype] >= 3
+    _any(name, "lo", lo, _HALVES if scaled else (k_pages.dtype,), 3, "(pages, heads, dim)")
+    if scaled != (k_scales is not None):
         raise ValueError(f"{name}: 8-bit caches take k_scales, 16-bit ones do not")
-    ks, strides = 0, (0, 0, 0)
-    if k_scales is not None:
-        if not isinstance(k_scales, torch.Tensor) or k_scales.dtype is not _FLOAT32 or k_scales.get_device() != device or \
-                k_scales.shape != k_pages.shape[:3]:
-            raise ValueError(f"{name}: k_scales must be float32 {tuple(k_pages.shape[:3])} on cuda:{device}")
-        ks, strides = k_scales.data_ptr(), k_scales.stride()
-    batch = lens.shape[0] if isinstance(lens, torch.Tensor) and lens.dim() == 1 else -1
-    lens_at = _whole(name, "lens", lens, _INT32, device, (batch,))
-    tp, cols, t0 = _table(name, table, device, batch)
-    at = _bounds(name, lo, hi, dtype, device, (pages, heads, dim))
-    _call(name, device, stream, _pack_bounds(
-        TYPES[dtype], batch, cols if most is None else _count(name, "most", most),
-        k_pages.data_ptr(), 0, ks, 0, kind, pages, heads, places, dim, *k_pages.stride()[:3], *strides, tp, cols, t0, lens_at,
-        0 if first is None else _whole(name, "first", first, _INT32, device, (batch,)), *at))
+    if k_scales is not None and not (isinstance(k_scales, torch.Tensor) and k_scales.dtype is _FLOAT32 and
+                                     k_scales.get_device() == device and k_scales.shape == k_pages.shape[:3]):
+        raise ValueError(f"{name}: k_scales must be float32 {tuple(k_pages.shape[:3])} on cuda:{device}")
+    _any(name, "lens", lens, (_INT32,), 1, "(batch)")
+    batch = lens.shape[0]
+    _whole(name, "lens", lens, _INT32, device, (batch,))
+    _table(name, table, device, batch)
+    _bounds(name, lo, hi, lo.dtype, device, (pages, heads, dim))
+    if first is not None:
+        _whole(name, "first", first, _INT32, device, (batch,))
+    raise ValueError(f"{name}: the last dimension of k_pages must be contiguous")
 
 
 def red_select_pages(q, lo, hi, table, lens, places, budget, first=1, last=1, max_len=None, node_count=None, stream=None):
@@ -162,27 +200,48 @@ def red_select_pages(q, lo, hi, table, lens, places, budget, first=1, last=1, ma
     takes."""
     if stream is not None:
         return _on(stream, red_select_pages, q, lo, hi, table, lens, places, budget, first, last, max_len, node_count)
+    try:
+        (batch, nodes, q_heads, dim), (q0, q1, q2, inner), dtype, device = q.shape, q.stride(), q.dtype, q.get_device()
+        (pages, heads, wide), (b0, b1, b2), (rows, cols), one = lo.shape, lo.stride(), table.shape, lens.shape
+        fits = (dtype in _HALVES and lo.dtype is dtype and hi.dtype is dtype and table.dtype is _INT32 and lens.dtype is _INT32 and
+                device >= 0 and lo.get_device() == device and hi.get_device() == device and table.get_device() == device and
+                lens.get_device() == device and wide == dim and hi.shape == lo.shape and hi.stride() == (b0, b1, b2) and
+                ((inner == 1 and b2 == 1) or dim <= 1) and rows == batch and (table.stride(1) == 1 or cols <= 1) and
+                one == (batch,) and lens.is_contiguous() and budget >= 0 and first >= 0 and last >= 0 and places >= 1 and
+                (max_len is None or max_len >= 0) and
+                (node_count is None or (node_count.dtype is _INT32 and node_count.get_device() == device and
+                                        node_count.shape == one and node_count.is_contiguous())))
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _select_check(q, lo, hi, table, lens, places, budget, first, last, max_len, node_count)
+    selected = torch.empty((batch, heads, budget), dtype=_INT32, device=q.device)
+    selected_lens = torch.empty(batch, dtype=_INT32, device=q.device)
+    _call("red_select_pages", device, None, _pack_select(
+        TYPES[dtype], batch, nodes, q_heads, heads, dim, pages, places, budget, first, last,
+        cols * places if max_len is None else max_len, q.data_ptr(), q0, q1, q2, lo.data_ptr(), hi.data_ptr(), b0, b1, table.data_ptr(),
+        cols, table.stride(0), lens.data_ptr(), 0 if node_count is None else node_count.data_ptr(), selected.data_ptr(),
+        selected_lens.data_ptr()))
+    return selected, selected_lens
+
+
+def _select_check(q, lo, hi, table, lens, places, budget, first, last, max_len, node_count):
+    """Raise what is wrong with the arguments."""
     name = "red_select_pages"
     device = _any(name, "q", q, _HALVES, 4, "(batch, nodes, q heads, dim)")
-    batch, nodes, q_heads, dim = q.shape
+    batch, _, _, dim = q.shape
     if not isinstance(lo, torch.Tensor) or lo.dim() != 3:
         raise ValueError(f"{name}: lo must be (pages, kv heads, {dim})")
-    pages, heads, _ = lo.shape
-    at = _bounds(name, lo, hi, q.dtype, device, (pages, heads, dim))
-    tp, cols, t0 = _table(name, table, device, batch)
+    _bounds(name, lo, hi, q.dtype, device, (*lo.shape[:2], dim))
+    _table(name, table, device, batch)
     for what, n in (("budget", budget), ("first", first), ("last", last), ("max_len", max_len or 0)):
         _count(name, what, n)
     if places < 1:
         raise ValueError(f"{name}: places must be positive")
-    selected = torch.empty((batch, heads, budget), dtype=_INT32, device=q.device)
-    selected_lens = torch.empty(batch, dtype=_INT32, device=q.device)
-    _call(name, device, None, _pack_select(
-        TYPES[q.dtype], batch, nodes, q_heads, heads, dim, pages, places, budget, first, last,
-        cols * places if max_len is None else max_len, q.data_ptr(), *q.stride()[:3], *at, tp, cols, t0,
-        _whole(name, "lens", lens, _INT32, device, (batch,)),
-        0 if node_count is None else _whole(name, "node_count", node_count, _INT32, device, (batch,)),
-        selected.data_ptr(), selected_lens.data_ptr()))
-    return selected, selected_lens
+    _whole(name, "lens", lens, _INT32, device, (batch,))
+    if node_count is not None:
+        _whole(name, "node_count", node_count, _INT32, device, (batch,))
+    raise ValueError(f"{name}: arguments do not fit each other")
 
 
 def red_sparse_attention(q, k_pages, v_pages, table, lens, scale, max_len=None, tree_mask=None, node_count=None, k_scales=None,
