@@ -8,7 +8,7 @@
  * that the call reads before it returns, strides in elements with a contiguous
  * last dimension, inputs that do not overlap outputs, refusals before any HIP
  * call, deterministic results. Scratch: every call here but the bounds of pages
- * and the sampling of up to 4096 tokens keeps intermediate results in the
+ * and the sampling of up to 8192 tokens keeps intermediate results in the
  * stream's scratch buffer, under the rule of libred_decode.h: while a stream is
  * captured, an earlier call on it of the same types, kv heads, dim and places,
  * and no less of the rest, must have provided it, else the call returns
@@ -188,7 +188,7 @@ red_status red_sparse_attention(const red_tree_attention_args *a, int64_t table_
  * more, or NaN, the token is the last of positive w.
  *
  * Weights are float64; their sums are whole multiples of 2^(ceil(log2 vocab) -
- * 62), so they do not depend on any order. Rows of more than 4096 tokens are
+ * 62), so they do not depend on any order. Rows of more than 8192 tokens are
  * added up by bins of equal ratios of the weight, in which a weight counts to
  * within 2^-35 of itself; where all kept tokens have the largest logit the sums
  * are exact. A border or token whose target lies closer to a running sum than

@@ -1,6 +1,6 @@
 // sample_common.hpp -- sampling from a row of logits with temperature, top-k,
-// top-p and min-p: what the kernels share, and the way that takes a row by one
-// block alone.
+// top-p and min-p: what the kernels share, and the way that takes a row of any
+// length by one block alone.
 //
 // The tokens' order (falling logits, ties by number) is that of one whole
 // number a token, its code: the logit's bits, turned so that they order, above
@@ -111,10 +111,16 @@ __device__ __forceinline__ double power2(double t) {
     return __builtin_amdgcn_ldexp(__builtin_fma(p, f, 1.0), (int)n);
 }
 
-// What the block shares.
-struct Shared {
+// What the block shares: for sums and borders, and for rows and lists that are not
+// held in registers.
+struct Sums {
     unsigned long long mass[kBins];
     unsigned int count[kBins];
+    unsigned long long part[kWaves], found, rest;
+    unsigned long long few[kWave], few_own[kWave];  // what a wave takes
+    unsigned int held, bin, cut;
+};
+struct Shared : Sums {
     union {
         struct {
             unsigned long long code[kHeld];  // what is in the border's bin
@@ -125,13 +131,10 @@ struct Shared {
             unsigned long long list[2 * kHeld], list_own[2 * kHeld];
         };
     };
-    unsigned long long part[kWaves], found, rest;
-    unsigned long long few[kWave], few_own[kWave];  // what a wave takes
-    unsigned int held, bin, cut;
 };
 
 template <class Op>
-__device__ __forceinline__ uint64_t block_combine(uint64_t v, Shared& s, Op op) {
+__device__ __forceinline__ uint64_t block_combine(uint64_t v, Sums& s, Op op) {
     v = group_combine<kWave>(v, op);
     __syncthreads();
     if (threadIdx.x % kWave == 0) s.part[threadIdx.x / kWave] = v;
@@ -151,7 +154,7 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
     return v;
 }
 // The sum of the threads before this one, and of all.
-__device__ __forceinline__ uint64_t block_before(uint64_t v, Shared& s, uint64_t* all) {
+__device__ __forceinline__ uint64_t block_before(uint64_t v, Sums& s, uint64_t* all) {
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const uint64_t upto = wave_scan(v);
     __syncthreads();
@@ -257,7 +260,7 @@ struct Row {
 // The bin in which the running sum of the bins' reaches `target`, the last that
 // is not empty where it does not, kBins if all are; and what is missing of the
 // target there.
-__device__ __forceinline__ void find_bin(Shared& s, uint64_t target, bool codes) {
+__device__ __forceinline__ void find_bin(Sums& s, uint64_t target, bool codes) {
     __syncthreads();
     if (threadIdx.x < kWave) {
         const int lane = threadIdx.x;
@@ -288,10 +291,25 @@ __device__ __forceinline__ void find_bin(Shared& s, uint64_t target, bool codes)
     __syncthreads();
 }
 
-__device__ __forceinline__ void clear_bins(Shared& s) {
+__device__ __forceinline__ void clear_bins(Sums& s) {
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.mass[i] = 0, s.count[i] = 0;
     __syncthreads();
+}
+
+// Of up to kWave codes and their weights, one a lane (0: none): the code at which
+// the sum of the weights, in the order of the codes, reaches `want`, the last where
+// it does not; ~0 for none. By a wave; -> in all lanes.
+__device__ __forceinline__ uint64_t rank_border(uint64_t c, uint64_t own, int n, uint64_t want) {
+    uint64_t before = 0, all = 0;
+    for (int i = 0; i < n; ++i) {
+        const uint64_t other = read_lane(own, i);
+        all += other;
+        before += read_lane(c, i) > c ? other : 0;
+    }
+    want = want > 0 ? want : 1;
+    const uint64_t goal = want < all ? want : all, is = __ballot(own > 0 && before < goal && before + own >= goal);
+    return is ? read_lane(c, __ffsll((unsigned long long)is) - 1) : ~0ull;
 }
 
 // What a running sum of weights must reach for top-p.

@@ -321,21 +321,6 @@ struct List {
     }
 };
 
-// Of up to kWave codes and their weights, one a lane (0: none): the code at which
-// the sum of the weights, in the order of the codes, reaches `want`, the last where
-// it does not; ~0 for none. By a wave; -> in all lanes.
-__device__ __forceinline__ uint64_t rank_border(uint64_t c, uint64_t own, int n, uint64_t want) {
-    uint64_t before = 0, all = 0;
-    for (int i = 0; i < n; ++i) {
-        const uint64_t other = read_lane(own, i);
-        all += other;
-        before += read_lane(c, i) > c ? other : 0;
-    }
-    want = want > 0 ? want : 1;
-    const uint64_t goal = want < all ? want : all, is = __ballot(own > 0 && before < goal && before + own >= goal);
-    return is ? read_lane(c, __ffsll((unsigned long long)is) - 1) : ~0ull;
-}
-
 // The code at which the running sum of the list's weights (`ones`: of ones), in
 // the order of the codes, among those from `from` to below `upto`, reaches `want`,
 // the last of them where it does not; ~0 where there are none. By bins of equal

@@ -71,12 +71,11 @@ hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& 
 
 // Sampling. A row goes through one block, or is cut into chunks.
 constexpr int kSampleChunk = 8192, kSampleGrid = 512, kSampleList = 16384;
-// Rows of up to so many logits go through one block. (Microseconds of 1 / 192 /
-// 2000 float32 rows, top-p: 4000 logits 16.5 / 18.4 / 124 by a block, 21.6 / 24.4 /
-// 129 by chunks; 8000 logits 21.6 / 24.2 / 171 and 23.1 / 25.7 / 148; 32000 logits
-// 52 / 58 / 451 and 24 / 33 / 229. With top-k as well: 4000 logits 19 / 24 / 170 and
-// 24 / 27 / 141, 8000 logits 26 / 29 / 211 and 24 / 27 / 147.)
-constexpr int kSampleRow = 4096;
+// Rows of up to so many logits are held by one block. (Microseconds of 1 / 192 / 1900
+// float32 rows, top-p, replayed: 4000 logits 10.4 / 11.6 / 74 by a block, 22 / 24 / 120
+// by chunks; 8000 logits 15.0 / 16.7 / 117 and 23 / 26 / 145; 12000 logits, for which a
+// block's registers are too few, 29 / 39 / 286 and 24 / 29 / 139.)
+constexpr int kSampleRow = 8192;
 struct SampleHead {  // of a chunk
     uint64_t first;  // the first code of the order
     int count;       // logits above -inf, where top-k asks for it

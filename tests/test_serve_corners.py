@@ -143,7 +143,7 @@ def test_pages_beyond_32_bit_offsets():
             assert sel[b, h].tolist() == [int(table[b, p]) for p in chosen[h]]
 
 
-@pytest.mark.parametrize("vocab", [1000, 5000])
+@pytest.mark.parametrize("vocab", [1000, 5000, 9000])
 def test_rows_beyond_32_bit_offsets(vocab):
     say("far rows", vocab)
     g = gen(8)
@@ -157,7 +157,7 @@ def test_rows_beyond_32_bit_offsets(vocab):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
-@pytest.mark.parametrize("vocab", [4097, 9000])
+@pytest.mark.parametrize("vocab", [4097, 8193, 9000])
 def test_more_rows_than_a_pass(vocab):
     """Rows go through the scratch some two thousand at a time: the same results as a few at a time."""
     say("many rows", vocab)

@@ -91,7 +91,7 @@ def test_a_larger_shape_provides_the_scratch(calls):
 
 
 def test_where_no_scratch_is_needed(calls):
-    assert call(calls, "red_sample", sample(2000, 4096))[0] == 0
+    assert call(calls, "red_sample", sample(2000, 8192))[0] == 0
     assert call(calls, "red_page_bounds", bounds(200, 3000))[0] == 0
 
 
@@ -117,7 +117,7 @@ def test_selection_of_any_number_of_pages(calls, batch, cols, heads, budget, man
     assert done == batch and (len(got) > 1) == many
 
 
-@pytest.mark.parametrize("batch, steps, vocab, many", [(1, 1, 1, False), (65535, 63, 4096, False), (65535, 8, 4097, True), (192, 1, 131071, False),
+@pytest.mark.parametrize("batch, steps, vocab, many", [(1, 1, 1, False), (65535, 63, 8192, False), (65535, 8, 8193, True), (192, 1, 131071, False),
                                                        (5000, 3, 1 << 20, True)])
 def test_sampling_of_any_number_of_rows(calls, batch, steps, vocab, many):
     """Rows in their order, as many at a time as the scratch holds."""
@@ -126,5 +126,5 @@ def test_sampling_of_any_number_of_rows(calls, batch, steps, vocab, many):
     for _, _, n, first, end in got:
         assert first == done
         done += n
-        assert vocab <= 4096 or end <= calls.scratch_at() + scratch
+        assert vocab <= 8192 or end <= calls.scratch_at() + scratch
     assert done == batch * steps and (len(got) > 1) == many
