@@ -267,29 +267,52 @@ def red_sample(logits, r=None, temperature=None, top_k=None, top_p=None, min_p=N
     None)."""
     if stream is not None:
         return _on(stream, red_sample, logits, r, temperature, top_k, top_p, min_p, probs)
+    try:
+        shape, strides, dtype, device = logits.shape, logits.stride(), logits.dtype, logits.get_device()
+        if len(shape) == 2:
+            (batch, vocab), steps, step_stride, rows = shape, 1, 0, shape[:1]
+        else:
+            (batch, steps, vocab), (_, step_stride, _), rows = shape, strides, shape[:2]
+        one = (batch,)
+        fits = (dtype in _FLOATS and device >= 0 and vocab >= 1 and (strides[-1] == 1 or vocab == 1) and
+                (probs is None or probs in _FLOATS) and
+                (r is None or (r.dtype is _FLOAT32 and r.get_device() == device and r.shape == rows and r.is_contiguous())) and
+                (temperature is None or _setting(temperature, _FLOAT32, device, one)) and
+                (top_k is None or _setting(top_k, _INT32, device, one)) and
+                (top_p is None or _setting(top_p, _FLOAT32, device, one)) and
+                (min_p is None or _setting(min_p, _FLOAT32, device, one)))
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        _sample_check(logits, r, temperature, top_k, top_p, min_p, probs)
+    tokens = None if r is None else torch.empty(rows, dtype=_INT64, device=logits.device)
+    given, p0, p1 = None, 0, 0
+    if probs is not None:
+        given = torch.empty(shape, dtype=probs, device=logits.device)
+        p0, p1 = steps * vocab, vocab
+    _call("red_sample", device, None, _pack_sample(
+        TYPES[dtype], 0 if probs is None else TYPES[probs], batch, steps, vocab, logits.data_ptr(), strides[0], step_stride,
+        0 if temperature is None else temperature.data_ptr(), 0 if top_k is None else top_k.data_ptr(),
+        0 if top_p is None else top_p.data_ptr(), 0 if min_p is None else min_p.data_ptr(), 0 if r is None else r.data_ptr(),
+        0 if tokens is None else tokens.data_ptr(), 0 if given is None else given.data_ptr(), p0, p1))
+    return tokens, given
+
+
+def _setting(x, dtype, device, shape):
+    return x.dtype is dtype and x.get_device() == device and x.shape == shape and x.is_contiguous()
+
+
+def _sample_check(logits, r, temperature, top_k, top_p, min_p, probs):
+    """Raise what is wrong with the arguments."""
     name = "red_sample"
     dims = 2 if isinstance(logits, torch.Tensor) and logits.dim() == 2 else 3
     device = _any(name, "logits", logits, _FLOATS, dims, "(batch, vocab) or (batch, steps, vocab)")
-    shape, strides = logits.shape, logits.stride()
-    batch, vocab = shape[0], shape[-1]
-    steps, step_stride = (1, 0) if dims == 2 else (shape[1], strides[1])
-    if vocab < 1:
+    if logits.shape[-1] < 1:
         raise ValueError(f"{name}: logits must have a vocabulary")
-    one = (batch,)
-    tp, kp, pp, mp = (0 if x is None else _whole(name, what, x, dtype, device, one) for what, x, dtype in (
-        ("temperature", temperature, _FLOAT32), ("top_k", top_k, _INT32), ("top_p", top_p, _FLOAT32), ("min_p", min_p, _FLOAT32)))
+    for what, x, dtype in (("temperature", temperature, _FLOAT32), ("top_k", top_k, _INT32), ("top_p", top_p, _FLOAT32), ("min_p", min_p, _FLOAT32)):
+        if x is not None:
+            _whole(name, what, x, dtype, device, logits.shape[:1])
     if probs is not None and probs not in _FLOATS:
         raise TypeError(f"{name}: probs must be torch.float32, torch.float16 or torch.bfloat16")
-    tokens = given = None
-    rp = 0
-    if r is not None:
-        rp = _whole(name, "r", r, _FLOAT32, device, shape[:-1])
-        tokens = torch.empty(shape[:-1], dtype=_INT64, device=logits.device)
-    p0 = p1 = 0
-    if probs is not None:
-        given = torch.empty(shape, dtype=probs, device=logits.device)
-        p0, p1 = given.stride(0), 0 if dims == 2 else given.stride(1)
-    _call(name, device, None, _pack_sample(
-        TYPES[logits.dtype], 0 if probs is None else TYPES[probs], batch, steps, vocab, logits.data_ptr(), strides[0], step_stride,
-        tp, kp, pp, mp, rp, 0 if tokens is None else tokens.data_ptr(), 0 if given is None else given.data_ptr(), p0, p1))
-    return tokens, given
+    _whole(name, "r", r, _FLOAT32, device, logits.shape[:-1])
+    raise ValueError(f"{name}: arguments do not fit each other")
