@@ -1,4 +1,5 @@
-// Sampling: rows cut into chunks, in four launches (five with probabilities).
+// Sampling: rows cut into chunks, in three or four launches (one more with
+// probabilities).
 //
 //  1. bins: a block a chunk of 8192 logits, held in registers. Every logit
 //     goes into a bin of an eighth of a power of two of its weight: with y = 8
@@ -11,14 +12,15 @@
 //  2. find: a block a row adds up the chunks' bins and finds those in which the
 //     borders of top-k, top-p and min-p lie, as ranges of logits.
 //  3. gather: the codes of the logits in these ranges, a few thousand; a
-//     second read of the row, with two comparisons a logit.
+//     second read of the row, with two comparisons a logit. Few rows, or short
+//     ones: in the launch before.
 //  4. draw: a block a row finds the border among them, the chunk in which the
 //     running sum of the kept weights passes its target, by the chunks' bins,
 //     and the token in that chunk.
 //  5. probabilities.
 //
 // Microseconds of bins / find / gather / draw (/ probabilities): one row of 32000
-// float32, top-k 50 and top-p, 4.5 / 6.2 / 3.8 / 9.6; 192 rows of 131071, top-p, 22.1 /
+// float32, top-k 50 and top-p, 4.5 / 8.7 with the gathering / 9.6; 192 rows of 131071, top-p, 22.1 /
 // 7.6 / 18.6 / 20.4; 224 rows of bfloat16, top-p and min-p, 24.7 / 8.0 / 13.8 / 16.1 /
 // 33.4. The bins take turns at the read (the 100 MB alone 14), 22 vector
 // instructions a logit, half of them float64 (two thirds of the cycles), and an LDS
@@ -98,6 +100,7 @@ struct Loads {
     // that the row ends in is read by vectors too, but for the one that the end
     // is in: element by element it took as long as all others, 26 us / 16 of 192
     // rows of 131071.)
+    Loads() = default;
     __device__ __forceinline__ Loads(const B* p, int first, int vocab) {
         const int tid = threadIdx.x;
         auto place = [&](int u) { return first + (u * THREADS + tid) * kVec; };
@@ -160,6 +163,17 @@ __device__ __forceinline__ void write_probs(const Row<T>& row, const Loads<T, TH
     }
 }
 
+// Running sum over the wave's lanes, this one's value included.
+__device__ __forceinline__ unsigned int count_scan(unsigned int v) {
+    v += dpp_move<0x111, 0xF>(0u, v);
+    v += dpp_move<0x112, 0xF>(0u, v);
+    v += dpp_move<0x114, 0xF>(0u, v);
+    v += dpp_move<0x118, 0xF>(0u, v);
+    v += dpp_move<0x142, 0xA>(0u, v);
+    v += dpp_move<0x143, 0xC>(0u, v);
+    return v;
+}
+
 // What the block that finds shares.
 struct Found {
     unsigned long long mass[kGrid];  // weights of the bins up to one, in units
@@ -207,12 +221,7 @@ __device__ __forceinline__ void find_ranges(const Row<T>& row, const Settings& s
     if (tid == 0 && count * largest == sum) mass = count * unit;  // all of the largest weight: exact
     const unsigned int own_count = count;
     mass = wave_scan(mass);
-    count += dpp_move<0x111, 0xF>(0u, count);
-    count += dpp_move<0x112, 0xF>(0u, count);
-    count += dpp_move<0x114, 0xF>(0u, count);
-    count += dpp_move<0x118, 0xF>(0u, count);
-    count += dpp_move<0x142, 0xA>(0u, count);
-    count += dpp_move<0x143, 0xC>(0u, count);
+    count = count_scan(count);
     __syncthreads();
     if (lane == kWave - 1) s.part[wave] = mass, s.parts[wave] = count;
     __syncthreads();
@@ -470,6 +479,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     if (tid == 0) {
         for (int w = 1; w < W; ++w) number = min(number, numbers[w]), count += counts[w];
         a.heads[chunk] = SampleHead{Code<T>::of(top + 0.f, first + (number < kChunk ? number : 0)), count};
+        if (blockIdx.x == 0) a.plans[blockIdx.y].held = 0;
     }
     if (binned)
         for (int i = tid; i < kGrid / 2; i += kChunkThreads)
@@ -503,59 +513,17 @@ __device__ __forceinline__ int chunk_shift(const Place& place, double peak, uint
     return d < (double)kGrid ? (int)d : kGrid;
 }
 
-template <class T>
-__global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a) {
-    __shared__ Found s;
-    __shared__ int shifts[kMaxVocab / kChunk];
-    const int tid = threadIdx.x;
-    const int at = a.first_row + blockIdx.x, b = at / a.steps, step = at - b * a.steps;
-    const Settings set(a, b);
-    const SampleHead* heads = a.heads + (int64_t)blockIdx.x * a.chunks;
-    SamplePlan& plan = a.plans[blockIdx.x];
-    const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
-    const float top = Code<T>::logit(head.first);
-    int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
-    if (tid < 4) s.first[tid] = kGrid;
-    if (tid == 0) plan.first = head.first, plan.held = 0, plan.state = state, plan.ranges = 0;
-    if (state != kRowCut) return;
-
-    Row<T> row(a, b, step);
-    row.settle(head.first, set.scale, a.shift);
-    const Place place{set.scale * kPerPower};
-    const double peak = place.floor_of(top);
-    for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift<T>(place, peak, heads[c].first);
-    __syncthreads();
-    // Bin tid of the row.
-    uint64_t sum = 0;
-    unsigned int count = 0;
-    const unsigned long long* bins = a.bins + (int64_t)blockIdx.x * a.chunks * kGrid;
-    for (int c0 = 0; c0 < a.chunks; c0 += 8) {
-        uint64_t v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int c = min(c0 + u, a.chunks - 1), j = tid - shifts[c];
-            v[u] = bins[(int64_t)c * kGrid + max(j, 0)];
-            if (j < 0 || c0 + u >= a.chunks) v[u] = 0;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) sum += v[u] & kSumMask, count += count_of(v[u]);
-    }
-    find_ranges(row, set, head, sum, count, kList, s, plan);
-}
-
-template <class T>
-__global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) {
-    constexpr int W = kChunkThreads / kWave;
+// The codes of the logits that a thread holds, which begin at number `first` of the
+// row, and lie in the ranges of `plan`, go into the row's list.
+template <class T, int THREADS>
+__device__ __forceinline__ void gather(const Loads<T, THREADS>& x, int first, const SamplePlan& plan, const typename T::bits* p,
+                                       unsigned int* held, unsigned long long* list) {
+    constexpr int W = THREADS / kWave;
     __shared__ unsigned int counts[W], start;
-    SamplePlan& plan = a.plans[blockIdx.y];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
-    const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
-    const Chunk<T> x(p, first, a.vocab);  // before the plan is known: one trip
-    const int ranges = plan.ranges;
-    if (ranges == 0) return;
     uint32_t in = 0;
     static_assert(kOwn <= 32, "a bit a logit");
+    const int ranges = plan.ranges;
     const float from0 = plan.from[0], upto0 = plan.upto[0], from1 = plan.from[1], upto1 = plan.upto[1];
     for (int r = 0; r < ranges; ++r) {
         const float from = r ? from1 : from0, upto = r ? upto1 : upto0;
@@ -566,13 +534,7 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
         }
     }
     // Places in the list: this thread's behind those of the threads before.
-    unsigned int own = (unsigned)__popc(in), upto = own;
-    upto += dpp_move<0x111, 0xF>(0u, upto);
-    upto += dpp_move<0x112, 0xF>(0u, upto);
-    upto += dpp_move<0x114, 0xF>(0u, upto);
-    upto += dpp_move<0x118, 0xF>(0u, upto);
-    upto += dpp_move<0x142, 0xA>(0u, upto);
-    upto += dpp_move<0x143, 0xC>(0u, upto);
+    const unsigned int own = (unsigned)__popc(in), upto = count_scan(own);
     if (lane == kWave - 1) counts[wave] = upto;
     __syncthreads();
     unsigned int before = 0, all = 0;
@@ -582,16 +544,78 @@ __global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) 
         all += counts[w];
     }
     if (all == 0) return;
-    if (tid == 0) start = atomicAdd(&plan.held, all);
+    if (tid == 0) start = atomicAdd(held, all);
     __syncthreads();
     unsigned int to = start + before + upto - own;
-    unsigned long long* list = a.list + (int64_t)blockIdx.y * kList;
     // Few have any: read again rather than chosen among registers.
     while (in) {
-        const int n = __ffs(in) - 1, i = first + Chunk<T>::number(n);
+        const int n = __ffs(in) - 1, i = first + Loads<T, THREADS>::number(n);
         if (to < kList) list[to] = Code<T>::of(T::widen(p[i]) + 0.f, i);
         ++to, in &= in - 1;
     }
+}
+
+// The plan of a row, by one block; or by one for each 16384 logits, which then
+// gathers from these.
+template <class T>
+__global__ __launch_bounds__(kGrid) void sample_find_kernel(Sample a, bool gathers) {
+    using L = Loads<T, kGrid>;
+    __shared__ Found s;
+    __shared__ SamplePlan plan;
+    __shared__ int shifts[kMaxVocab / kChunk];
+    const int tid = threadIdx.x, first = blockIdx.x * L::kAll;
+    const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps;
+    Row<T> row(a, b, step);
+    L x;
+    if (gathers) x = L(row.p, first, a.vocab);  // before the plan is known: one trip
+    const Settings set(a, b);
+    const SampleHead* heads = a.heads + (int64_t)blockIdx.y * a.chunks;
+    const SampleHead head = row_head(heads, a.chunks, s.part, s.parts);
+    const float top = Code<T>::logit(head.first);
+    const int state = top == kNone ? kRowNone : set.k == 1 ? kRowOne : !Place{set.scale * kPerPower}.fits(top) ? kRowWhole : kRowCut;
+    if (tid < 4) s.first[tid] = kGrid;
+    if (tid == 0) plan.first = head.first, plan.state = state, plan.ranges = 0;
+    if (state == kRowCut) {
+        row.settle(head.first, set.scale, a.shift);
+        const Place place{set.scale * kPerPower};
+        const double peak = place.floor_of(top);
+        for (int c = tid; c < a.chunks; c += kGrid) shifts[c] = chunk_shift<T>(place, peak, heads[c].first);
+        __syncthreads();
+        // Bin tid of the row.
+        uint64_t sum = 0;
+        unsigned int count = 0;
+        const unsigned long long* bins = a.bins + (int64_t)blockIdx.y * a.chunks * kGrid;
+        for (int c0 = 0; c0 < a.chunks; c0 += 8) {
+            uint64_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int c = min(c0 + u, a.chunks - 1), j = tid - shifts[c];
+                v[u] = bins[(int64_t)c * kGrid + max(j, 0)];
+                if (j < 0 || c0 + u >= a.chunks) v[u] = 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum += v[u] & kSumMask, count += count_of(v[u]);
+        }
+        find_ranges(row, set, head, sum, count, kList, s, plan);
+    }
+    __syncthreads();
+    SamplePlan& to = a.plans[blockIdx.y];
+    if (blockIdx.x == 0 && tid == 0) {
+        to.first = plan.first, to.state = plan.state, to.ranges = plan.ranges, to.use_k = plan.use_k, to.use_p = plan.use_p, to.cut = plan.cut;
+        for (int r = 0; r < 2; ++r) to.from[r] = plan.from[r], to.upto[r] = plan.upto[r];
+        to.low = plan.low, to.high = plan.high, to.k_rest = plan.k_rest, to.k_before = plan.k_before, to.p_before = plan.p_before;
+        to.all = plan.all, to.norm = plan.norm, to.largest = plan.largest;
+    }
+    if (gathers && plan.ranges > 0) gather<T, kGrid>(x, first, plan, row.p, &to.held, a.list + (int64_t)blockIdx.y * kList);
+}
+
+template <class T>
+__global__ __launch_bounds__(kChunkThreads) void sample_gather_kernel(Sample a) {
+    SamplePlan& plan = a.plans[blockIdx.y];
+    const int at = a.first_row + blockIdx.y, b = at / a.steps, step = at - b * a.steps, first = blockIdx.x * kChunk;
+    const typename T::bits* p = static_cast<const typename T::bits*>(a.x) + b * a.batch_stride + step * a.step_stride;
+    const Chunk<T> x(p, first, a.vocab);  // before the plan is known: one trip
+    if (plan.ranges > 0) gather<T, kChunkThreads>(x, first, plan, p, &plan.held, a.list + (int64_t)blockIdx.y * kList);
 }
 
 // A chunk's sum over the bins before `bin` of the row, from its own, of which
@@ -745,8 +769,15 @@ hipError_t split(int probs_type, const Sample& a, unsigned int rows, hipStream_t
     const dim3 grid((unsigned)a.chunks, rows);
     sample_bins_kernel<T><<<grid, kChunkThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess) sample_find_kernel<T><<<rows, kGrid, 0, stream>>>(a), e = hipGetLastError();
-    if (e == hipSuccess && a.filtered) sample_gather_kernel<T><<<grid, kChunkThreads, 0, stream>>>(a), e = hipGetLastError();
+    // Where few blocks would gather, each makes the row's plan itself, which saves a
+    // launch. (Microseconds of the whole call, top-p, gathering apart / by the blocks
+    // that find: 1 row of 32000 float32 25.1 / 24.1, 16 rows of 131071 (128 blocks) 27.9 /
+    // 27.8, 64 rows of 65536 (256 blocks) 28.0 / 30.2, 192 rows of 131071 61 / 75. With
+    // one block a row it saves 1 to 3 whatever the rows: 1900 rows of 16000 153 / 149.)
+    const unsigned int blocks = (a.vocab + Loads<T, kGrid>::kAll - 1) / Loads<T, kGrid>::kAll;
+    const bool few = a.filtered && (blocks == 1 || blocks * rows <= 128);
+    if (e == hipSuccess) sample_find_kernel<T><<<dim3(few ? blocks : 1, rows), kGrid, 0, stream>>>(a, few), e = hipGetLastError();
+    if (e == hipSuccess && a.filtered && !few) sample_gather_kernel<T><<<grid, kChunkThreads, 0, stream>>>(a), e = hipGetLastError();
     if (e == hipSuccess) sample_draw_kernel<T><<<rows, kThreads, 0, stream>>>(a), e = hipGetLastError();
     if (e != hipSuccess || !a.probs) return e;
     if (probs_type == RED_F16) sample_probs_kernel<T, F16><<<grid, kChunkThreads, 0, stream>>>(a);

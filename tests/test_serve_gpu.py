@@ -435,6 +435,7 @@ SAMPLES = [  # batch, steps, vocab, dtype, spread, k, p, m, masked, probs
     (1, 1, (1 << 20) - 5, BF16, 2.5, 1000, True, False, 0.0, F32), (300, 1, 513, F32, 2.0, 20, True, True, 0.1, F32),
     (3, 1, 20000, F32, 2.0, None, False, False, 0.1, F32), (3, 1, 8191, BF16, 1.0, 3000, True, True, 0.2, BF16),
     (3, 1, 8192, F32, 0.2, 5000, True, False, 0.0, F16), (3, 2, 8193, F16, 2.0, 4000, True, True, 0.1, F32), (9, 1, 6001, F32, 2.5, 70, True, False, 0.5, F32),
+    (70, 1, 33000, F32, 2.0, None, True, False, 0.1, F32), (30, 2, 50001, BF16, 2.5, 400, True, True, 0.3, F16),
 ]
 
 
