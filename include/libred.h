@@ -28,7 +28,9 @@
  *    (block partials plus a completion counter), allocated on the first call
  *    per (device, stream) and kept until the process exits. Calls on one
  *    stream are ordered, so they can share it; eager calls on different
- *    streams use different workspaces and may run concurrently. The column
+ *    streams use different workspaces and may run concurrently. Host threads
+ *    may call on the same stream: the launches of a call are enqueued with no
+ *    others of the library on that stream between them. The column
  *    entry points keep their partials in a per-stream scratch buffer under
  *    the same rule. The library allocates with the calling thread in relaxed
  *    capture mode, so a first call on a stream that is not being captured

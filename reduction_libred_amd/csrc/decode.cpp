@@ -3,6 +3,7 @@
 #include "decode.hpp"
 
 #include <initializer_list>
+#include <optional>
 
 #include "decode_host.hpp"
 #include "libred_serve.h"
@@ -139,6 +140,7 @@ red_status qk_norm_call(const red_qk_norm_rope_args* a, const red_heads* dq, con
     // 40 heads of 128: 91 us; 5 a compute unit 100, 8 a compute unit 95).
     const size_t cap = (size_t)cus * 6;
     if (blocks > cap) blocks = cap;
+    const StreamTurn turn(dev, stream);
     void* partials = nullptr;
     st = host_scratch(dev, stream, blocks * 2 * D * sizeof(float), &partials);
     if (st != RED_OK) return st;
@@ -287,12 +289,14 @@ red_status attention_call(const red_tree_attention_args* a, int64_t table_head, 
     if (segments * (tiles > 0 ? tiles : 1) > 0x7fffffff) return RED_ERR_INVALID_ARG;
     const size_t hold = (size_t)cus * (size_t)libred::attention_blocks((int)M, (int)D);
     const size_t blocks = segments * tiles < hold ? segments * tiles : hold;
+    std::optional<StreamTurn> turn;  // where there is scratch
     if (k.max_tokens > libred::attention_least_tokens((int)M, (int)D, c.type == RED_F16 || c.type == RED_BF16 ? 2 : 1)) {
         // The scratch is asked for whichever way is taken, and also for one
         // tile where fewer rows would have several, so that a call of a larger
         // shape has always provided that of a smaller one, which a capture
         // relies on.
         const size_t rows = (blocks + segments) * (size_t)shape.rows(), plan = (B + 2 + 3) / 4 * 4;
+        turn.emplace(dev, stream);
         void* p = nullptr;
         st = host_scratch(dev, stream, rows * (D * sizeof(float) + sizeof(float2)) + plan * sizeof(int), &p);
         if (st != RED_OK && tiles > 1) return st;  // one tile a segment needs none itself
@@ -368,6 +372,7 @@ red_status verify_call(const red_verify_drafts_args* a, hipStream_t stream) {
     //   192 sequences   10.6 / 15.8 / 22.0 / 34.1,  9.8 / 13.8 / 20.7 / 37.1
     // More sequences than the card holds such blocks of would take turns.
     if (B <= (size_t)cus * 2 && (k.segs <= 16 || (B >= (size_t)cus / 2 && k.segs <= 64))) k.blocks = 0;
+    const StreamTurn turn(dev, stream);
     // The scratch is that of as many segments as a smaller vocabulary may have,
     // and is asked for where one launch keeps its sums in the LDS as well: a
     // call of a larger shape has then always provided that of a smaller one,

@@ -8,6 +8,7 @@
 #include <map>
 #include <mutex>
 #include <numeric>
+#include <optional>
 #include <utility>
 #include <vector>
 
@@ -20,6 +21,7 @@
 
 using libred::FlatPolicy;
 using libred::RowsPolicy;
+using libred::StreamTurn;
 using libred::Workspace;
 
 // The block partials of red_sum_f32_noalloc, which allocates nothing: a
@@ -375,6 +377,7 @@ red_status flat_call(const In* x, size_t n, Out* out, const red_flat_policy* pol
     DeviceInfo info;
     red_status st = current_device(&dev, &info);
     if (st != RED_OK) return st;
+    const StreamTurn turn(dev, stream);
     Workspace ws;
     st = get_workspace(dev, stream, &ws);
     if (st != RED_OK) return st;
@@ -697,11 +700,13 @@ red_status rows_call(const float* x, size_t rows, size_t cols, size_t ld, float*
     const size_t tiles_per_row = cols / tile_elems;
     const bool want_split =
         p.split == 2 || (p.split == 0 && rows < kSplitRowsBelow && cols >= kSplitMinCols);
+    std::optional<StreamTurn> turn;  // where rows are split
     if (want_split && tiles_per_row >= 2) {
         size_t gx = (kSplitTargetWaves + rows - 1) / rows;
         if (gx > tiles_per_row) gx = tiles_per_row;
         if (gx > libred::kMaxSplitPartials / rows) gx = libred::kMaxSplitPartials / rows;
         if (gx >= 2) {
+            turn.emplace(dev, stream);
             Workspace ws;
             st = get_workspace(dev, stream, &ws);
             if (st != RED_OK) return st;
@@ -1033,8 +1038,10 @@ red_status cols_call(const float* x, size_t rows, size_t cols, size_t ld, float*
         L.order = 2;
     else
         L.order = 0;
+    std::optional<StreamTurn> turn;  // where there are partials
     L.partials = nullptr;
     if (nchunks > 1 || L.fold_m > 1 || L.rot > 0) {
+        turn.emplace(dev, stream);
         st = get_scratch(dev, stream, nchunks * cols * 8, &L.partials);
         if (st != RED_OK) return st;
     }
@@ -1089,6 +1096,7 @@ red_status red_sum_f32_noalloc(const float* x, size_t n, float* out, hipStream_t
     if (st != RED_OK) return st;
     const size_t grid = flat_grid_for(n, p, info.cu_count);
     if (grid > kNoAllocMaxPartials) return RED_ERR_SCRATCH;
+    const StreamTurn turn(dev, stream);
     double* ptr = nullptr;
     st = noalloc_scratch(dev, &ptr);
     if (st != RED_OK) return st;

@@ -3,6 +3,8 @@
 // red_tree_attention, in decode.cpp.)
 #include "serve.hpp"
 
+#include <optional>
+
 #include "decode_host.hpp"
 
 using namespace libred;
@@ -54,6 +56,7 @@ red_status plan_call(const red_plan_slots_args* a, hipStream_t stream) {
     int dev, cus;
     red_status st = host_compute_units(&dev, &cus);
     if (st != RED_OK) return st;
+    const StreamTurn turn(dev, stream);
     void* p = nullptr;
     st = host_scratch(dev, stream, (3 * (B + 1) + 4 + a->pages) * sizeof(int32_t), &p);
     if (st != RED_OK) return st;
@@ -188,6 +191,7 @@ red_status select_call(const red_select_pages_args* a, hipStream_t stream) {
     k.nodes = (int)N, k.heads = (int)H, k.group = (int)(a->q_heads / H), k.dim = (int)D, k.places = (int)a->places;
     k.budget = (int)a->budget, k.first = (int)a->first, k.last = (int)a->last;
     k.most = (int)most, k.share = (int)share, k.max_len = (int)tokens;
+    const StreamTurn turn(dev, stream);
     // Asked for where the budget takes all pages as well, so that a call provides
     // it for those of a smaller budget.
     void* p = nullptr;
@@ -253,7 +257,9 @@ red_status sample_call(const red_sample_args* a, hipStream_t stream) {
     const int probs_type = a->probs != nullptr ? a->probs_type : RED_F32;
     const size_t rows = B * S;
     size_t each = rows;
+    std::optional<StreamTurn> turn;  // where there is scratch
     if (V > kSampleRow) {
+        turn.emplace(dev, stream);
         // Rows cut into chunks, as many at a time as 256 MiB hold the bins and
         // lists of.
         const size_t chunks = (V + kSampleChunk - 1) / kSampleChunk;
