@@ -129,9 +129,11 @@ __global__ __launch_bounds__(kBoundsWaves* kWave) void page_bounds_kernel(PageBo
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float v = f[i];
-                if constexpr (C::kScaled) v *= s[u];
-                // fmin and fmax pass over a NaN.
+                // fmin and fmax pass over a quiet NaN, but of a signalling one the hardware
+                // makes a quiet one in place of what came before it. A product is quiet.
+                float v;
+                if constexpr (C::kScaled) v = f[i] * s[u];
+                else v = __builtin_canonicalizef(f[i]);
                 lo[i] = fminf(lo[i], v);
                 hi[i] = fmaxf(hi[i], v);
             }
