@@ -448,10 +448,12 @@ __global__ __launch_bounds__(kChunkThreads) void sample_bins_kernel(Sample a) {
     const Chunk<T> x(p, first, a.vocab);
     const Settings set(a, b);
     for (int i = tid; i < kGrid; i += kChunkThreads) bins[i] = 0;  // those behind are not read
-    // The largest logit; a NaN is none.
+    // The largest logit; a NaN is none. (A signalling one is made quiet first: of it the
+    // hardware's maximum makes a quiet one in place of what came before it, and bins go
+    // by their distance from the largest.)
     float top = kNone;
 #pragma unroll
-    for (int n = 0; n < kOwn; ++n) top = fmaxf(top, x.at(n));
+    for (int n = 0; n < kOwn; ++n) top = fmaxf(top, __builtin_canonicalizef(x.at(n)));
     top = group_combine<kWave>(top, [](float m, float n) { return fmaxf(m, n); });
     if (lane == 0) tops[wave] = top;
     __syncthreads();
