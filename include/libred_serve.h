@@ -185,14 +185,16 @@ red_status red_sparse_attention(const red_tree_attention_args *a, int64_t table_
  * T NULL is 1; a T of 0, below, or NaN keeps the first of the order alone. A
  * NaN counts as -inf; -inf has w = 0; where x holds +inf, those have w = 1 and
  * all others 0. A row of -inf has probabilities 0 and token -1. With r of 1 or
- * more, or NaN, the token is the last of positive w.
+ * more, or NaN, the token is the last that may be drawn.
  *
- * Weights are float64; their sums are whole multiples of 2^(ceil(log2 vocab) -
- * 62), so they do not depend on any order. Rows of more than 8192 tokens are
- * added up by bins of equal ratios of the weight, in which a weight counts to
- * within 2^-35 of itself; where all kept tokens have the largest logit the sums
- * are exact. A border or token whose target lies closer to a running sum than
- * that may be the neighbouring one, the same one every time.
+ * Weights are float64; in sums each counts as a whole number of units, so they
+ * do not depend on any order. A unit is 2^(ceil(log2 vocab) - 62), 2^-51 at the
+ * least. A weight below half a unit has its probability, but is not drawn. Rows
+ * of more than 8192 tokens are added up by bins of equal ratios of the weight,
+ * in which a weight counts to within 2^-35 of itself, those below half a unit
+ * too; where all kept tokens have the largest logit the sums are exact. A border
+ * or token whose target lies closer to a running sum than that may be the
+ * neighbouring one, the same one every time.
  *
  * type: RED_F32, RED_F16 or RED_BF16 of the logits; probs_type the same of
  * probs. tokens (with r) or probs may be NULL: not wanted. tokens and r are

@@ -654,6 +654,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) v[u] = bins[(int64_t)own_chunk * kGrid + u * kWave + lane];
     const uint64_t head = heads[own_chunk].first;
+    const uint64_t chunk_first = heads[min(tid, a.chunks - 1)].first;
     const SamplePlan plan = a.plans[blockIdx.x];
     SamplePlan& to = a.plans[blockIdx.x];
     const float r = a.r ? a.r[at] : 0.f;
@@ -706,7 +707,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     const uint64_t border = cut_border(of, set, plan, above);
     // What is kept of the list joins its chunks.
     __syncthreads();
-    if (tid == 0) s.bin = 0, s.rest = 1;  // a place in the row whatever the sums are
     if (ranges > 0)
         of.each([&](uint64_t c, auto weight) {
             // The gathering left a chunk's codes side by side: a wave has mostly those of
@@ -726,13 +726,26 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     uint64_t before = block_before(own, s, &total);
     if (tid == 0) to.border = border, to.share = row.unit / (double)total;
     if (!a.tokens) return;
+    // The chunk: the last that begins below the target, of those in which a weight counts
+    // by itself. (Its first code tells. The sums by bins hold weights of less than half a
+    // unit as well, where they are many, and are cut off to whole units.) Where that is
+    // none, the token is the first of the first of those; for r of 1, the last of the last.
     const uint64_t want = draw_target(r, total);
-    if (own > 0 && before < want && before + own >= want) s.bin = tid, s.rest = want - before;
+    const bool last = !(r < 1.f);
+    const bool counts = tid < a.chunks && chunk_first >= border && row.units(row.weight(R::C::logit(chunk_first))) > 0;
+    const uint64_t all = __ballot(counts), below = __ballot(counts && (last || before < want));
+    if (tid < a.chunks) runs[tid] = want - before;
+    if (tid < 2 * kWave && lane == 0) s.few[wave] = all, s.few_own[wave] = below;
     __syncthreads();
-    // The chunk, in which sums by weights may fall short of those by bins.
+    static_assert(kMaxVocab / kChunk <= 2 * kWave, "chunks are told by two words");
+    const bool first_one = (s.few_own[0] | s.few_own[1]) == 0;
+    const int chunk = s.few_own[1] ? 127 - __clzll(s.few_own[1]) : s.few_own[0] ? 63 - __clzll(s.few_own[0])
+                      : s.few[0]   ? __ffsll(s.few[0]) - 1
+                                   : s.few[1] ? __ffsll(s.few[1]) + 63 : 0;
+    // Its token. Sums by weights may fall short of those by bins.
     constexpr int kEach = kChunk / kThreads;
-    const int i0 = (int)s.bin * kChunk + tid * kEach;
-    const uint64_t rest = s.rest;
+    const int i0 = chunk * kChunk + tid * kEach;
+    const uint64_t rest = first_one ? 1 : last ? ~0ull : runs[chunk];
     float x[kEach];
     row.template neighbours<kEach>(i0, x);
     uint64_t w[kEach], mine = 0, whole;
@@ -743,7 +756,6 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(Sample a) {
     }
     before = block_before(mine, s, &whole);
     const uint64_t goal = rest < whole ? rest : whole;
-    if (whole == 0 && tid == 0) a.tokens[at] = R::C::token(first);  // weights that are less than a unit each
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         if (before < goal && before + w[j] >= goal) a.tokens[at] = i0 + j;
