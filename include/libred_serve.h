@@ -119,7 +119,8 @@ red_status red_page_bounds(const red_page_bounds_args *a, hipStream_t stream);
  *   score = sum max(q_d lo_d, q_d hi_d) = sum_d (U_d hi_d + D_d lo_d),
  *   U_d = sum max(q_d, 0),  D_d = sum min(q_d, 0)
  *
- * in float64. Selected are min(P, budget) pages: the first `first`, those
+ * in float64, a product of 0 being 0 whatever the bound. Selected are min(P,
+ * budget) pages: the first `first`, those
  * from floor(lens[b] / places) - last on, and of the others those of the
  * largest scores, ties to the lower page; a score that is NaN is below all
  * others. selected[b][h][i] (int32, batch x kv heads x budget) are their page
