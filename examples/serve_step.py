@@ -81,15 +81,16 @@ class Toy:
 
 
 def serve(model, requests, answer, seed=1):
-    """requests: prompts (lists of tokens). -> the answers, `answer` tokens each, and the steps taken."""
+    """requests: prompts (lists of tokens). -> the answers, `answer` tokens each (one at least), and the steps taken."""
     device, batch = model.table.device, model.batch
     g = torch.Generator(device=device).manual_seed(seed)
     settings = dict(temperature=torch.linspace(0.0, 1.2, batch, device=device), top_k=torch.full((batch,), 50, device=device, dtype=torch.int32),
                     top_p=torch.full((batch,), 0.95, device=device), min_p=torch.full((batch,), 0.01, device=device))
-    assert all(len(p) > 0 for p in requests)
+    assert all(len(p) > 0 for p in requests) and answer > 0
     queue, answers, steps = list(range(len(requests))), [[] for _ in requests], 0
     need = [-(-(len(p) + answer) // PLACES) for p in requests]
     assert max(need) <= model.free_pages.shape[0], "no request may need more pages than there are"
+    assert max(need) <= model.table.shape[1], "no request may need more pages than a row of the table has"
     who, todo, ended = [None] * batch, [[] for _ in range(batch)], [0] * batch
     while queue or any(w is not None for w in who):
         for b in range(batch):
@@ -122,7 +123,8 @@ def main():
     args = ap.parse_args()
     g = torch.Generator().manual_seed(2)
     requests = [torch.randint(0, VOCAB, (int(torch.randint(1, 300, (1,), generator=g)),), generator=g).tolist() for _ in range(args.requests)]
-    model = Toy(args.batch, 320, args.batch * 16, 8, torch.device("cuda:0"))
+    longest = max(len(p) for p in requests) + args.answer
+    model = Toy(args.batch, longest, max(args.batch * 16, -(-longest // PLACES)), 8, torch.device("cuda:0"))
     answers, steps = serve(model, requests, args.answer)
     for i, (prompt, answer) in enumerate(zip(requests, answers)):
         print(f"request {i}, {len(prompt)} tokens: {answer}")
