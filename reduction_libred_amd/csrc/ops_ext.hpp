@@ -39,7 +39,7 @@ struct MinF32 {
 //    first element equal to the kept value, making acc[3] exact;
 //  - vectors outside whole tiles find their exact index at once (fold, into
 //    acc[0]).
-// The streaming loop thus costs about two and a half vector operations per
+// The streaming loop thus costs about three and a half vector operations per
 // element and never selects a 64-bit index per element; the second read is
 // one 16-byte vector per thread.
 struct ArgExt {
@@ -59,7 +59,12 @@ struct ArgExtF32 {
     static __device__ __forceinline__ bool better(float a, float b) { return MAX ? (a > b) : (a < b); }
     // The extreme of two values; a NaN operand is ignored (NaN only if both are).
     static __device__ __forceinline__ float ext(float a, float b) { return MAX ? fmaxf(a, b) : fminf(a, b); }
-    static __device__ __forceinline__ float ext4(vec_t v) { return ext(ext(v[0], v[1]), ext(v[2], v[3])); }
+    // Of a signalling NaN the hardware makes a quiet one in place of the other operand:
+    // elements are made quiet first.
+    static __device__ __forceinline__ float quiet(float x) { return __builtin_canonicalizef(x); }
+    static __device__ __forceinline__ float ext4(vec_t v) {
+        return ext(ext(quiet(v[0]), quiet(v[1])), ext(quiet(v[2]), quiet(v[3])));
+    }
     // Does extreme e (NaN: no number) replace the running value m (NaN: none)?
     static __device__ __forceinline__ bool replaces(float e, float m) {
         return (MAX ? !(e <= m) : !(e >= m)) & (e == e);
