@@ -87,7 +87,9 @@ red_status red_plan_slots(const red_plan_slots_args *a, hipStream_t stream);
  * of lo and hi, and the cache's own type where that has 16 bits; with an 8-bit
  * cache element * scale in float32, rounded to `type`. lo and hi: element
  * (p, h, d) at p * bound_page_stride + h * bound_head_stride + d, pages and
- * heads those of the cache. The cache's v and v_scales are not read and may be
+ * heads those of the cache. (Rounded to nearest, as red_cache_read does: a key
+ * in float32 may lie outside its page's bounds by half a step of `type`, the key
+ * that is read back in `type` does not.) The cache's v and v_scales are not read and may be
  * NULL. Page numbers outside the cache are skipped. Two sequences may share
  * pages that both fill. batch <= 65535.
  */
@@ -127,6 +129,8 @@ red_status red_page_bounds(const red_page_bounds_args *a, hipStream_t stream);
  * numbers in the order of the sequence, then -1. selected_lens[b] = lens[b] -
  * places * (pages left out): lens of the sequence that has the selected pages
  * alone. A sequence without nodes has no pages selected and length 0.
+ *
+ * The score is of q . k: for an attention whose scale is below 0, -q is given.
  *
  * type RED_F16 or RED_BF16 of q, lo and hi (as red_page_bounds leaves them;
  * pages behind floor(lens / places) - last are not looked at). max_len: the

@@ -20,9 +20,9 @@
 //  5. probabilities.
 //
 // Microseconds of bins / find / gather / draw (/ probabilities): one row of 32000
-// float32, top-k 50 and top-p, 4.5 / 8.7 with the gathering / 9.6; 192 rows of 131071, top-p, 22.1 /
-// 7.6 / 18.6 / 20.4; 224 rows of bfloat16, top-p and min-p, 24.7 / 8.0 / 13.8 / 16.1 /
-// 33.4. The bins take turns at the read (the 100 MB alone 14), 22 vector
+// float32, top-k 50 and top-p, 4.6 / 8.8 with the gathering / 10.2; 192 rows of 131071, top-p, 22.8 /
+// 7.7 / 18.9 / 21.1; 224 rows of bfloat16, top-p and min-p, 25.4 / 8.2 / 13.7 / 16.7 /
+// 34.2. The bins take turns at the read (the 100 MB alone 14), 22 vector
 // instructions a logit, half of them float64 (two thirds of the cycles), and an LDS
 // atomic each (two fifths): 17 instructions a logit took 23, blocks that go through
 // several chunks with the next one's logits on their way 24 to 27. The gathering and
@@ -31,9 +31,12 @@
 // usual). Finding, gathering and drawing in one launch of a block a row: 55 instead
 // of 47 for the 192 rows, 23 instead of 20 for the one.
 //
-// Where more logits than kList are near a border (thousands of equal ones), or
-// the border is further than 64 powers of two below the largest weight, the
-// block that draws goes through the whole row instead.
+// Where more logits than kList are near a border, or the border is further than 64
+// powers of two below the largest weight, the block that draws goes through the whole
+// row instead, once for every step of every border. That is rows of thousands of equal
+// logits, and flat rows of distinct ones: logits of spread 1 and top-p 0.9 from 262144
+// tokens at temperature 3 on (1 row 580 us, at temperature 2 47) and at 2^20 tokens from
+// 0.7 on (2.2 ms at temperature 1, 48 us at 0.3); 64 rows take little longer than one.
 #include "sample_common.hpp"
 
 namespace libred {

@@ -26,8 +26,8 @@ struct PlanSlots {
     int64_t *slots, *pos;
     int32_t *starts, *granted;
     int batch, tokens, cols, places, pages;
-    // Of a sequence, in the scratch: pages it has (fewer than 0: refused), of
-    // those taken the ones before its, of those given back the ones before its.
+    // Of a sequence, in the scratch: pages it has, of those taken the ones before
+    // its, of those given back the ones before its.
     int32_t *have, *before, *back;
     int32_t* sums;   // 4: stack's height before, with the pages given back, and behind the step
     int32_t* fresh;  // the pages taken
@@ -69,7 +69,9 @@ struct SelectPages {
 constexpr int kSelectPages = 64;  // a multiple of this many pages has a block that scores them
 hipError_t launch_select_pages(int type, int vec, int lanes, const SelectPages& a, hipStream_t stream);
 
-// Sampling. A row goes through one block, or is cut into chunks.
+// Sampling. A row goes through one block, or is cut into chunks. The list holds the
+// codes near a border, 1000 of 131072 as a rule; flat rows have more (see
+// sample_split.hip).
 constexpr int kSampleChunk = 8192, kSampleGrid = 512, kSampleList = 16384;
 // Rows of up to so many logits are held by one block. (Microseconds of 1 / 192 / 1900
 // float32 rows, top-p, replayed: 4000 logits 10.4 / 11.6 / 74 by a block, 22 / 24 / 120

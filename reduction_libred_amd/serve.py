@@ -194,10 +194,10 @@ def red_select_pages(q, lo, hi, table, lens, places, budget, first=1, last=1, ma
     pages, the last ones from lens[b] // places - last on, and of the others
     those with the largest bounds of q . k, summed over the nodes and the query
     heads of a kv head, `budget` pages in all. node_count, max_len: as
-    red_tree_attention takes them. -> (selected (batch, kv heads, budget) int32:
-    page numbers in the order of the sequence, then -1, and lens (batch) int32:
-    tokens of the selected pages before the nodes), which red_sparse_attention
-    takes."""
+    red_tree_attention takes them; for a scale below 0, -q is given here.
+    -> (selected (batch, kv heads, budget) int32: page numbers in the order of
+    the sequence, then -1, and lens (batch) int32: tokens of the selected pages
+    before the nodes), which red_sparse_attention takes."""
     if stream is not None:
         return _on(stream, red_select_pages, q, lo, hi, table, lens, places, budget, first, last, max_len, node_count)
     try:
