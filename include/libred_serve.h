@@ -121,11 +121,10 @@ red_status red_page_bounds(const red_page_bounds_args *a, hipStream_t stream);
  *   score = sum max(q_d lo_d, q_d hi_d) = sum_d (U_d hi_d + D_d lo_d),
  *   U_d = sum max(q_d, 0),  D_d = sum min(q_d, 0)
  *
- * in float64, a product of 0 being 0 whatever the bound. Selected are min(P,
- * budget) pages: the first `first`, those
- * from floor(lens[b] / places) - last on, and of the others those of the
- * largest scores, ties to the lower page; a score that is NaN is below all
- * others. selected[b][h][i] (int32, batch x kv heads x budget) are their page
+ * in float64, a product of 0 and an infinite bound being 0. Selected are
+ * min(P, budget) pages: the first `first`, those from floor(lens[b] / places) -
+ * last on, and of the others those of the largest scores, ties to the lower
+ * page; a score that is NaN is below all others. selected[b][h][i] (int32, batch x kv heads x budget) are their page
  * numbers in the order of the sequence, then -1. selected_lens[b] = lens[b] -
  * places * (pages left out): lens of the sequence that has the selected pages
  * alone. A sequence without nodes has no pages selected and length 0.

@@ -194,7 +194,7 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
         }
     }
     // 0 times an infinite bound is no number, though no query takes that bound: the
-    // wave's pages again, without the products by 0. (In the loop above it takes 104
+    // wave's pages again, without these products. (In the loop above it takes 104
     // registers instead of 86, a wave a SIMD less.)
     if (!__any(none)) return;
 #pragma unroll 1
@@ -209,8 +209,9 @@ __global__ __launch_bounds__(kScoreThreads) void score_kernel(SelectPages a) {
             for (int i = 0; i < N; ++i) {
                 const int e = VEC == 8 ? in * 8 + i : in + i * kWave;
                 if (!there[i] || a.pages == 0) continue;
-                if (pu[i] != 0.0) s = __builtin_fma(pu[i], (double)T::widen(hi[at + e]), s);
-                if (pd[i] != 0.0) s = __builtin_fma(pd[i], (double)T::widen(lo[at + e]), s);
+                const double most = (double)T::widen(hi[at + e]), least = (double)T::widen(lo[at + e]);
+                if (pu[i] != 0.0 || most != most) s = __builtin_fma(pu[i], most, s);
+                if (pd[i] != 0.0 || least != least) s = __builtin_fma(pd[i], least, s);
             }
             s = group_combine<G>(s, AddF64());
             if (in == 0 && j < last) keys[j] = good ? ordered(s) : 0;

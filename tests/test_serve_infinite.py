@@ -1,5 +1,5 @@
 """Selection by bounds of pages that are infinite: a bound that no query takes does
-not count, the others make a score infinite."""
+not count, the others make a score infinite. A bound that is NaN always counts."""
 import math
 
 import pytest
@@ -22,7 +22,7 @@ def scores(q, lo, hi):
     x, l, h = (v.to(F64) for v in (q, lo, hi))
     each = torch.where(x[:, None] > 0, x[:, None] * h, torch.where(x[:, None] < 0, x[:, None] * l, 0.0))
     each = torch.where(x[:, None].isnan(), x[:, None], each)
-    return each.sum((0, 2))
+    return each.sum((0, 2)) + torch.where(l.isnan() | h.isnan(), math.nan, 0.0).sum(1)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -43,7 +43,7 @@ def test_infinite_bounds(dtype, nodes, group, dim, cols):
     hi[11, :, 0], lo[11, :, 0] = -INF, -INF           # and minus that
     hi[13, :, 0], hi[13, 0, 1], lo[13, 0, 1] = INF, INF, INF      # inf - inf: no number in head 0
     lo[15], hi[15] = INF, -INF                        # a page of NaN alone
-    hi[17, 1, 2] = math.nan                            # no number, if not taken
+    hi[17, 1, 2] = math.nan                            # no number, taken or not
     hi[19, 0, 0] = math.nan
     lo, hi, q = lo.to(dtype), hi.to(dtype), q.to(dtype)
     table = torch.randperm(cols, generator=g).to(I32)[None]
